@@ -1,0 +1,170 @@
+"""The head's loss and gradient on the GPU against the formulas in 64 bits.
+
+Error bounds (derived, per element):
+* z: bf16 products are exact in fp32 and are summed in fp32, 16 at a time:
+  |dz| <= (D / 16 + 5) 2^-23 sum_j |A_j B_j|.
+* lse: |dz| plus the exponential's and logarithm's rounding,
+  2^-20 (1 + max |z|).
+* a gradient: G is rounded to bf16 (8 significant bits: at most 2^-8 of each
+  entry) and carries the relative error of exp, |dz| + |dlse|; the product's
+  sums are fp32 and the result is rounded to bf16 once (2^-8 of it):
+  2^-8 |ref| + (2^-8 + |dz| + |dlse| + K/16 2^-23) sum |G| |B|.
+"""
+import numpy as np
+import pytest
+
+pytestmark = pytest.mark.gpu
+
+
+def make(M, vocab, d, rank, ignored=0.0, seed=0, sd=1.0):
+    import torch
+    g = torch.Generator().manual_seed(seed)
+    n = lambda *s: torch.randn(*s, generator=g)  # noqa: E731
+    x = {"h": (n(M, d) * sd).bfloat16(), "W": (n(vocab, d) * 2.0 / d ** 0.5).bfloat16(),
+         "U": (n(vocab, rank) * 0.3).bfloat16() if rank else None,
+         "V": (n(vocab, rank) * 0.3).bfloat16() if rank else None,
+         "prev": torch.randint(0, vocab, (M,), generator=g, dtype=torch.int32) if rank else None,
+         "target": torch.randint(0, vocab, (M,), generator=g, dtype=torch.int32)}
+    k = int(M * ignored)
+    x["target"][torch.randperm(M, generator=g)[:k]] = -1
+    x["dloss"] = torch.full((M,), 1.0 / max(M - k, 1))
+    return x
+
+
+def reference(x):
+    """Loss, lse, gradients in 64 bits, and the magnitudes the bounds need."""
+    import torch
+    f = torch.float64
+    ok = (x["target"] >= 0) & (x["target"] < x["W"].shape[0])
+    t = x["target"].long().clamp(0, x["W"].shape[0] - 1)
+    A, B = x["h"].to(f), x["W"].to(f)
+    if x["U"] is not None:
+        pv = x["prev"].long()
+        pv = torch.where((pv < 0) | (pv >= x["U"].shape[0]), 0, pv)
+        A = torch.cat([A, x["U"][pv].to(f)], 1)
+        B = torch.cat([B, x["V"].to(f)], 1)
+    A = torch.where(ok[:, None], A, torch.zeros((), dtype=f))
+    z = A @ B.T
+    lse = torch.logsumexp(z, 1)
+    zt = z[torch.arange(len(t)), t]
+    G = (z - lse[:, None]).exp()
+    G[torch.arange(len(t)), t] -= 1.0
+    G *= torch.where(ok, x["dloss"].to(f), 0.0)[:, None]
+    d = x["h"].shape[1]
+    D = A.shape[1]
+    dA, dB = G @ B, G.T @ A
+    mA, mB = G.abs() @ B.abs(), G.abs().T @ A.abs()
+    dz = (D / 16 + 5) * 2.0 ** -23 * (A.abs() @ B.abs().T).amax(1)     # per row
+    dl = dz + 2.0 ** -20 * (1 + z.abs().amax(1))
+    r = {"loss": torch.where(ok, lse - zt, 0.0), "lse": torch.where(ok, lse, 0.0),
+         "dh": dA[:, :d], "dW": dB[:, :d]}
+    eps = (dz + dl).amax().item() if len(dz) else 0.0
+    tol = {"loss": dz + dl, "lse": dl}
+    rel = 2.0 ** -8 + eps + max(B.shape[0], A.shape[0]) / 16 * 2.0 ** -23
+    mags = {"dh": mA[:, :d], "dW": mB[:, :d]}
+    if x["U"] is not None:
+        vocab, rank = x["U"].shape
+        r["dV"], mags["dV"] = dB[:, d:], mB[:, d:]
+        r["dU"] = torch.zeros(vocab, rank, dtype=f).index_add_(0, pv, dA[:, d:])
+        mags["dU"] = torch.zeros(vocab, rank, dtype=f).index_add_(0, pv, mA[:, d:])
+    for k, m in mags.items():
+        tol[k] = 2.0 ** -8 * r[k].abs() + rel * m
+    return r, tol
+
+
+def run(x, h=None, dh=None, stream=None, grad=True):
+    import torch
+    from speculative_decoding_draft_dspark_gb300 import head as H
+    c = {k: (v.cuda() if v is not None else None) for k, v in x.items()}
+    if h is not None:
+        c["h"] = h
+    (M, d), vocab = x["h"].shape, x["W"].shape[0]
+    rank = 0 if x["U"] is None else x["U"].shape[1]
+    full = lambda *s: torch.full(s, 7.0, dtype=torch.bfloat16, device="cuda")  # noqa: E731
+    o = {"loss": torch.full((M,), 7.0, device="cuda"), "lse": torch.full((M,), 7.0, device="cuda"),
+         "dh": full(M, d) if dh is None else dh, "dW": full(vocab, d)}
+    if rank:
+        o["dU"], o["dV"] = full(vocab, rank), full(vocab, rank)
+    ws = H.new_workspace(H.dspark_head_workspace_size(M, vocab, d, rank, True))
+    H.dspark_head_loss(c["h"], c["W"], c["U"], c["V"], c["prev"], c["target"], o["loss"], o["lse"],
+                       ws, stream=stream)
+    if grad:
+        H.dspark_head_loss_grad(c["h"], c["W"], c["U"], c["V"], c["prev"], c["target"], o["lse"],
+                                c["dloss"], o["dh"], o["dW"], o.get("dU"), o.get("dV"), ws,
+                                stream=stream)
+    torch.cuda.synchronize()
+    from speculative_decoding_draft_dspark_gb300 import dspark as D
+    o["status"] = D.dspark_read_status(ws)
+    return {k: v.cpu() if hasattr(v, "cpu") else v for k, v in o.items()}
+
+
+def check(got, ref, tol, keys=None):
+    for k in keys or ref:
+        e = (got[k].double() - ref[k]).abs()
+        bad = ~(e <= tol[k])
+        assert not bad.any(), (k, int(bad.sum()), e[bad].max().item(), (e / tol[k].clamp(min=1e-300)).max().item())
+
+
+@pytest.mark.parametrize("M,vocab,d,rank,ignored", [
+    (1, 1, 8, 0, 0.0),
+    (1, 257, 64, 16, 0.0),
+    (21, 1024, 64, 16, 0.0),
+    (130, 1000, 72, 8, 0.3),
+    (255, 511, 200, 0, 0.5),
+    (257, 2049, 136, 256, 0.1),
+    (600, 777, 520, 40, 0.4),
+    (513, 4096, 256, 64, 0.0),
+    (64, 20000, 320, 248, 0.1),
+])
+def test_against_the_formulas(M, vocab, d, rank, ignored):
+    x = make(M, vocab, d, rank, ignored, seed=M + vocab)
+    got = run(x)
+    ref, tol = reference(x)
+    assert got["status"] == 0
+    check(got, ref, tol)
+
+
+def test_several_pieces_of_the_vocabulary():
+    """Large enough that the gradient goes over the vocabulary in pieces."""
+    import torch
+    x = make(3000, 70000, 64, 16, 0.2, seed=3)
+    got = run(x)
+    c = {k: v.cuda() for k, v in x.items()}
+    with torch.device("cuda"):
+        torch.set_default_dtype(torch.float32)
+        ref, tol = _reference_cuda(c)
+    check(got, ref, tol)
+
+
+def _reference_cuda(c):
+    """reference() with its large products on the GPU, in 64 bits."""
+    import torch
+    f = torch.float64
+    ok = c["target"] >= 0
+    t = c["target"].long().clamp(min=0)
+    A = torch.cat([c["h"].to(f), c["U"][c["prev"].long()].to(f)], 1)
+    B = torch.cat([c["W"].to(f), c["V"].to(f)], 1)
+    A = torch.where(ok[:, None], A, torch.zeros((), dtype=f))
+    z = A @ B.T
+    lse = torch.logsumexp(z, 1)
+    rows = torch.arange(len(t))
+    zt = z[rows, t]
+    zmax = z.abs().amax(1)
+    dz = (A.shape[1] / 16 + 5) * 2.0 ** -23 * (A.abs() @ B.abs().T).amax(1)
+    dl = dz + 2.0 ** -20 * (1 + zmax)
+    G = (z - lse[:, None]).exp()
+    G[rows, t] -= 1.0
+    G *= torch.where(ok, c["dloss"].to(f), 0.0)[:, None]
+    d = c["h"].shape[1]
+    dA, dB, mA, mB = G @ B, G.T @ A, G.abs() @ B.abs(), G.abs().T @ A.abs()
+    pv = c["prev"].long()
+    zero = torch.zeros(c["U"].shape, dtype=f)
+    ref = {"loss": torch.where(ok, lse - zt, 0.0), "lse": torch.where(ok, lse, 0.0),
+           "dh": dA[:, :d], "dW": dB[:, :d], "dV": dB[:, d:],
+           "dU": zero.index_add(0, pv, dA[:, d:])}
+    rel = 2.0 ** -8 + (dz + dl).amax() + B.shape[0] / 16 * 2.0 ** -23
+    mags = {"dh": mA[:, :d], "dW": mB[:, :d], "dV": mB[:, d:], "dU": zero.index_add(0, pv, mA[:, d:])}
+    tol = {"loss": dz + dl, "lse": dl}
+    for k, m in mags.items():
+        tol[k] = 2.0 ** -8 * ref[k].abs() + rel * m
+    return {k: v.cpu() for k, v in ref.items()}, {k: v.cpu() for k, v in tol.items()}
