@@ -82,6 +82,73 @@ DSPARK_API dspark_status dspark_head_loss_grad(
     void *dh, int64_t dh_stride, void *dW, void *dU, void *dV,
     void *workspace, size_t workspace_bytes, dspark_stream_t stream);
 
+/* ------------------------------------------------------------------------
+ * Residual stream.  r = residual + dropout(x); y = r / sqrt(mean r^2 + eps) *
+ * gain, row by row (sums in fp32, from the unrounded r).
+ *
+ * x, residual    [M, d] of dtype (DSPARK_BF16 or DSPARK_F32), rows x_stride /
+ *                residual_stride elements apart (>= d); residual NULL = none.
+ * gain           [d] of dtype.
+ * r              out [M, d] of dtype, or NULL; may be x or residual itself.
+ * y              out [M, d]: of dtype, or DSPARK_E4M3 (one byte each, y_dtype)
+ *                with scales: group 0 = one scale for a row, group 128 = one
+ *                for each 128 columns (the last may be narrower).  scale =
+ *                max |y| / 448 over its columns (1 where that is 0), and the
+ *                byte is y / scale rounded to nearest even; scale is fp32
+ *                [M, ceil(d / 128)] or [M], contiguous.  group and scale are
+ *                not used when y is of dtype.
+ * rstd           out [M] fp32: 1 / sqrt(mean r^2 + eps), or NULL.
+ * p              probability of dropping an element of x, 0 <= p <= 1; 0 = none.
+ *                Rounded so that T = round(65536 (1 - p)) of 65536 values are
+ *                kept; what is kept is multiplied by 65536 / T.  Element (i, c)
+ *                is kept iff lane c % 8 (16 bits each, low half of a word
+ *                first) of the words of Philox4x32-10 with counter (c / 8, i,
+ *                2^31, offset) and key (seed low, seed high) is below T.  The
+ *                same (seed, offset) gives the same mask here, in the gradient
+ *                and in dspark_dropout; use a new offset for every use.
+ * Any d and alignment to the element works; rows that are 16-byte aligned with
+ * d a multiple of 8 are faster.  A NaN or infinity stays in its own row (in
+ * its own element where it is dropped).
+ * Limits: 1 <= M, 1 <= d <= 32768.
+ * ------------------------------------------------------------------------ */
+#define DSPARK_E4M3 2
+
+DSPARK_API dspark_status dspark_residual_norm(
+    const void *x, int64_t x_stride, const void *residual, int64_t residual_stride,
+    const void *gain, int32_t dtype, int32_t M, int32_t d, float eps,
+    float p, uint64_t seed, uint32_t offset,
+    void *r, int64_t r_stride, void *y, int64_t y_stride, int32_t y_dtype,
+    int32_t group, float *scale, float *rstd, dspark_stream_t stream);
+
+/* Gradient.  With a = dy gain, xh = r rstd:
+ *     dr'   = dr + rstd (a - xh mean(a xh))
+ *     dresidual = dr',  dx = dropout(dr'),  dgain = sum over rows of dy xh
+ * dy             [M, d]: derivative by y.
+ * dr             [M, d]: derivative by r from elsewhere, or NULL.
+ * r, rstd        as written by dspark_residual_norm.
+ * dx, dresidual  out [M, d], either may be NULL; dx may be dy itself and
+ *                dresidual dr itself.
+ * dgain          out [d], or NULL.
+ * workspace      >= dspark_norm_workspace_size(M, d) bytes, 256-byte aligned.
+ * All of dtype with strides as above; rstd fp32.  dgain is summed in an order
+ * fixed by M, d and dtype. */
+DSPARK_API size_t dspark_norm_workspace_size(int32_t M, int32_t d);
+
+DSPARK_API dspark_status dspark_residual_norm_grad(
+    const void *dy, int64_t dy_stride, const void *dr, int64_t dr_stride,
+    const void *r, int64_t r_stride, const void *gain, const float *rstd,
+    int32_t dtype, int32_t M, int32_t d, float p, uint64_t seed, uint32_t offset,
+    void *dx, int64_t dx_stride, void *dresidual, int64_t dresidual_stride, void *dgain,
+    void *workspace, size_t workspace_bytes, dspark_stream_t stream);
+
+/* y = residual + dropout(x), elements, mask and arguments as above; residual
+ * may be NULL, y may be x or residual itself.  Its gradient by x is
+ * dspark_dropout of dy with residual = NULL. */
+DSPARK_API dspark_status dspark_dropout(
+    const void *x, int64_t x_stride, const void *residual, int64_t residual_stride,
+    int32_t dtype, int32_t M, int32_t d, float p, uint64_t seed, uint32_t offset,
+    void *y, int64_t y_stride, dspark_stream_t stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -18,7 +18,7 @@ CSRC = os.path.join(HERE, "csrc")
 BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "libdspark.so")
 SOURCES = ["chain.cu", "lmhead.cu", "select.cu", "verify.cu", "api.cu", "chain_noalloc.cu",
-           "head_loss.cu", "head_api.cu"]
+           "head_loss.cu", "norm.cu", "head_api.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC",
          "-Xcompiler", "-fvisibility=hidden", "--expt-relaxed-constexpr"]

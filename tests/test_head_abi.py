@@ -109,3 +109,77 @@ def test_binding_checks_shapes_and_types():
                dict(h=z(64, 4).T)):
         with pytest.raises(ValueError):
             H.dspark_head_loss(**{**ok, **kw})
+
+
+# -------------------------------------------------------- residual stream
+def _norm(lib, **kw):
+    a = dict(x=FAKE, xs=64, res=FAKE, ress=64, gain=FAKE, dt=D.BF16, M=4, d=64, eps=1e-6, p=0.0,
+             seed=1, offset=0, r=FAKE, rs=64, y=FAKE, ys=64, ydt=D.BF16, group=0, scale=None,
+             rstd=FAKE, stream=None)
+    a.update(kw)
+    return lib.dspark_residual_norm(*a.values())
+
+
+def _norm_grad(lib, **kw):
+    a = dict(dy=FAKE, dys=64, dr=FAKE, drs=64, r=FAKE, rs=64, gain=FAKE, rstd=FAKE, dt=D.F32, M=4,
+             d=64, p=0.0, seed=1, offset=0, dx=FAKE, dxs=64, ds=FAKE, dss=64, dgain=FAKE, ws=FAKE,
+             wsb=1 << 30, stream=None)
+    a.update(kw)
+    return lib.dspark_residual_norm_grad(*a.values())
+
+
+def _drop(lib, **kw):
+    a = dict(x=FAKE, xs=64, res=FAKE, ress=64, dt=D.BF16, M=4, d=64, p=0.1, seed=1, offset=0, y=FAKE,
+             ys=64, stream=None)
+    a.update(kw)
+    return lib.dspark_dropout(*a.values())
+
+
+@pytest.mark.parametrize("call", [_norm, _norm_grad, _drop])
+@pytest.mark.parametrize("kw,code", [
+    (dict(dt=2), D.ERR_INVALID_ARG),
+    (dict(M=0), D.ERR_INVALID_ARG),
+    (dict(d=0), D.ERR_INVALID_ARG),
+    (dict(d=32769), D.ERR_UNSUPPORTED),
+    (dict(p=-0.1), D.ERR_INVALID_ARG),
+    (dict(p=1.5), D.ERR_INVALID_ARG),
+    (dict(p=float("nan")), D.ERR_INVALID_ARG),
+])
+def test_residual_stream_validation(lib, call, kw, code):
+    assert call(lib, **kw) == code
+
+
+@pytest.mark.parametrize("call,kw,code", [
+    (_norm, dict(x=None), D.ERR_INVALID_ARG),
+    (_norm, dict(gain=None), D.ERR_INVALID_ARG),
+    (_norm, dict(y=None), D.ERR_INVALID_ARG),
+    (_norm, dict(xs=63), D.ERR_INVALID_ARG),
+    (_norm, dict(ress=10), D.ERR_INVALID_ARG),
+    (_norm, dict(rs=63), D.ERR_INVALID_ARG),
+    (_norm, dict(ys=63), D.ERR_INVALID_ARG),
+    (_norm, dict(x=FAKE + 1), D.ERR_INVALID_ARG),
+    (_norm, dict(eps=-1.0), D.ERR_INVALID_ARG),
+    (_norm, dict(eps=float("inf")), D.ERR_INVALID_ARG),
+    (_norm, dict(ydt=D.F32), D.ERR_INVALID_ARG),
+    (_norm, dict(ydt=H.E4M3), D.ERR_INVALID_ARG),                 # no scale
+    (_norm, dict(ydt=H.E4M3, scale=FAKE, group=64), D.ERR_UNSUPPORTED),
+    (_norm_grad, dict(dy=None), D.ERR_INVALID_ARG),
+    (_norm_grad, dict(r=None), D.ERR_INVALID_ARG),
+    (_norm_grad, dict(rstd=None), D.ERR_INVALID_ARG),
+    (_norm_grad, dict(gain=FAKE + 2), D.ERR_INVALID_ARG),
+    (_norm_grad, dict(dxs=60), D.ERR_INVALID_ARG),
+    (_norm_grad, dict(ws=None), D.ERR_WORKSPACE),
+    (_norm_grad, dict(ws=FAKE + 128), D.ERR_WORKSPACE),
+    (_norm_grad, dict(wsb=256), D.ERR_WORKSPACE),
+    (_drop, dict(x=None), D.ERR_INVALID_ARG),
+    (_drop, dict(y=None), D.ERR_INVALID_ARG),
+    (_drop, dict(ys=8), D.ERR_INVALID_ARG),
+])
+def test_residual_stream_arguments(lib, call, kw, code):
+    assert call(lib, **kw) == code
+
+
+def test_norm_workspace_size(lib):
+    f = H.dspark_norm_workspace_size
+    assert f(1, 8) >= 256 + 32 and f(15360, 2048) > f(1, 2048)
+    assert f(0, 8) == f(1, 0) == f(1, 40000) == 0
