@@ -20,11 +20,11 @@ struct HeadLayout {
   int64_t piece;      // vocabulary entries handled at a time by the gradient
   int32_t splits;     // partial sums of the gradient of [h, U[prev]]
   size_t rowinfo;     // per counted row: index, target, prev, lse, weight, z_t
-  size_t position;    // per row: its place among the counted rows, or -1
   size_t a;           // bf16 [rows_pad, cols_pad]: [h, U[prev]]
-  size_t partial;     // loss: float2 [vocab / 256][rows_pad] (max, sum)
-  size_t g;           // gradient: bf16 [rows_pad, piece]
-  size_t acc;         // gradient: fp32 [splits][rows_pad][cols_pad]
+  size_t partial;     // loss: float2 [epilogue warps][rows_pad] (max, sum)
+  size_t g;           // gradient: G^T, bf16 [piece, rows_pad]
+  size_t acc;         // gradient: sums of dA^T, fp32 [splits][cols_pad][rows_pad]
+  size_t de;          // gradient: fp32 [rows_pad, rank], dA's tail by rows
   size_t total;
 };
 HeadLayout head_layout(int32_t M, int32_t vocab, int32_t d, int32_t rank, bool grad);

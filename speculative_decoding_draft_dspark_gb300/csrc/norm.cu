@@ -19,6 +19,7 @@
 #include <cmath>
 
 #include "common.cuh"
+#include "launch.cuh"
 #include "norm_internal.h"
 
 namespace dspark {
@@ -303,6 +304,8 @@ __device__ __forceinline__ void by_groups(const NormArgs &a, int64_t row, int ba
 // column 256 (i warps + w)); a CTA has as many rows as fit.
 template <bool F32, bool VEC, int NV>
 __global__ void __launch_bounds__(256) norm_kernel(const NormArgs a, int warps) {
+  allow_next_kernel();
+  wait_for_earlier_kernel();
   __shared__ float slots[2][32];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int group = warp / warps, w = warp - group * warps;
@@ -412,6 +415,8 @@ __device__ __forceinline__ void times_gain(const NormArgs &a, float rstd, int ba
 
 template <bool F32, bool VEC>
 __global__ void __launch_bounds__(WIDE_WARPS * 32) norm_wide_kernel(const NormArgs a) {
+  allow_next_kernel();
+  wait_for_earlier_kernel();
   __shared__ float slots[2][32];
   const int w = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int64_t row = blockIdx.x;
@@ -461,11 +466,39 @@ __global__ void __launch_bounds__(WIDE_WARPS * 32) norm_wide_kernel(const NormAr
 }
 
 // --------------------------------------------------------------- backward
-// A row as in the forward kernel; a CTA goes over rows and keeps dgain's sums
+// A row as in the forward kernel, with the next row's loads issued before the
+// current row's sum is waited for.  A CTA goes over rows and keeps dgain's sums
 // of its columns in registers, joins its row groups in order and writes one
 // fp32 line of partial sums.  dgain_kernel adds the lines up in order.
+template <bool F32, int NV>
+struct GradRow {
+  Raw<F32> dy[NV], r[NV], dr[NV];
+  float rstd;
+};
+
 template <bool F32, bool VEC, int NV>
-__global__ void __launch_bounds__(256) norm_grad_kernel(const NormGradArgs a, int warps) {
+__device__ __forceinline__ void load_row(const NormGradArgs &a, int64_t row, int warps, int w,
+                                         int lane, GradRow<F32, NV> &x) {
+  constexpr int E = F32 ? 4 : 2;
+  if (row >= a.M) return;
+  const uint8_t *py = static_cast<const uint8_t *>(a.dy) + row * a.dy_stride * E;
+  const uint8_t *pr = static_cast<const uint8_t *>(a.r) + row * a.r_stride * E;
+  const uint8_t *pd = static_cast<const uint8_t *>(a.dr) + row * a.dr_stride * E;
+#pragma unroll
+  for (int i = 0; i < NV; ++i) load8<F32, VEC>(py, (i * warps + w) * 256, lane, a.d, x.dy[i]);
+#pragma unroll
+  for (int i = 0; i < NV; ++i) load8<F32, VEC>(pr, (i * warps + w) * 256, lane, a.d, x.r[i]);
+  if (a.dr) {
+#pragma unroll
+    for (int i = 0; i < NV; ++i) load8<F32, VEC>(pd, (i * warps + w) * 256, lane, a.d, x.dr[i]);
+  }
+  x.rstd = a.rstd[row];
+}
+
+template <bool F32, bool VEC, int NV, int THREADS>
+__global__ void __launch_bounds__(THREADS) norm_grad_kernel(const NormGradArgs a, int warps) {
+  allow_next_kernel();
+  wait_for_earlier_kernel();
   __shared__ float slots[2][32];
   extern __shared__ float lines[];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -477,31 +510,22 @@ __global__ void __launch_bounds__(256) norm_grad_kernel(const NormGradArgs a, in
 #pragma unroll
   for (int i = 0; i < NV; ++i) load8<F32, VEC>(a.gain, (i * warps + w) * 256, lane, a.d, g[i]);
 
-  int turn = 0;
-  for (int64_t r0 = static_cast<int64_t>(blockIdx.x) * groups; r0 < a.M;
-       r0 += static_cast<int64_t>(gridDim.x) * groups, turn ^= 1) {
+  const int64_t step = static_cast<int64_t>(gridDim.x) * groups;
+  int64_t r0 = static_cast<int64_t>(blockIdx.x) * groups;
+  GradRow<F32, NV> cur, next;
+  load_row<F32, VEC, NV>(a, r0 + group, warps, w, lane, cur);
+  for (int turn = 0; r0 < a.M; r0 += step, turn ^= 1) {
     const int64_t row = r0 + group;
     const bool live = row < a.M;
-    Raw<F32> dy[NV], r[NV], dr[NV];
-    float rstd = 0.0f, dot = 0.0f;
+    load_row<F32, VEC, NV>(a, row + step, warps, w, lane, next);
+    float dot = 0.0f;
+    const float rstd = cur.rstd;
     if (live) {
-      const uint8_t *py = static_cast<const uint8_t *>(a.dy) + row * a.dy_stride * E;
-      const uint8_t *pr = static_cast<const uint8_t *>(a.r) + row * a.r_stride * E;
-      const uint8_t *pd = static_cast<const uint8_t *>(a.dr) + row * a.dr_stride * E;
-      rstd = a.rstd[row];
-#pragma unroll
-      for (int i = 0; i < NV; ++i) load8<F32, VEC>(py, (i * warps + w) * 256, lane, a.d, dy[i]);
-#pragma unroll
-      for (int i = 0; i < NV; ++i) load8<F32, VEC>(pr, (i * warps + w) * 256, lane, a.d, r[i]);
-      if (a.dr) {
-#pragma unroll
-        for (int i = 0; i < NV; ++i) load8<F32, VEC>(pd, (i * warps + w) * 256, lane, a.d, dr[i]);
-      }
 #pragma unroll
       for (int i = 0; i < NV; ++i) {
         float y[8], x[8], t[8];
-        unpack8<F32>(dy[i], y);
-        unpack8<F32>(r[i], x);
+        unpack8<F32>(cur.dy[i], y);
+        unpack8<F32>(cur.r[i], x);
         unpack8<F32>(g[i], t);
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
@@ -520,13 +544,13 @@ __global__ void __launch_bounds__(256) norm_grad_kernel(const NormGradArgs a, in
       for (int i = 0; i < NV; ++i) {
         const int base = (i * warps + w) * 256;
         float y[8], x[8], t[8], o[8];
-        unpack8<F32>(dy[i], y);
-        unpack8<F32>(r[i], x);
+        unpack8<F32>(cur.dy[i], y);
+        unpack8<F32>(cur.r[i], x);
         unpack8<F32>(g[i], t);
 #pragma unroll
         for (int e = 0; e < 8; ++e) o[e] = rstd * (y[e] * t[e] - x[e] * rstd * dot);
         if (a.dr) {
-          unpack8<F32>(dr[i], t);
+          unpack8<F32>(cur.dr[i], t);
 #pragma unroll
           for (int e = 0; e < 8; ++e) o[e] += t[e];
         }
@@ -537,6 +561,7 @@ __global__ void __launch_bounds__(256) norm_grad_kernel(const NormGradArgs a, in
         }
       }
     }
+    cur = next;
   }
   if (!a.dgain) return;
   // the row groups' sums, joined in order
@@ -568,6 +593,8 @@ __global__ void __launch_bounds__(256) norm_grad_kernel(const NormGradArgs a, in
 // shared memory, every column with one thread.
 template <bool F32, bool VEC>
 __global__ void __launch_bounds__(WIDE_WARPS * 32) norm_grad_wide_kernel(const NormGradArgs a) {
+  allow_next_kernel();
+  wait_for_earlier_kernel();
   __shared__ float slots[2][32];
   extern __shared__ float line[];
   const int w = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -643,6 +670,8 @@ __global__ void __launch_bounds__(WIDE_WARPS * 32) norm_grad_wide_kernel(const N
 template <bool F32>
 __global__ void __launch_bounds__(1024)
     dgain_kernel(const float *partial, int lines, int d, void *dgain) {
+  allow_next_kernel();
+  wait_for_earlier_kernel();
   __shared__ float part[32][33];
   const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
   const int c = blockIdx.x * 32 + lane;
@@ -667,6 +696,8 @@ __global__ void __launch_bounds__(1024)
 template <bool F32, bool VEC>
 __global__ void __launch_bounds__(256) dropout_kernel(const DropoutArgs a, int rows_per_cta,
                                                       int chunks) {
+  allow_next_kernel();
+  wait_for_earlier_kernel();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   constexpr int E = F32 ? 4 : 2;
   const int64_t r0 = static_cast<int64_t>(blockIdx.x) * rows_per_cta;
@@ -705,61 +736,84 @@ struct RowPlan {
 };
 
 constexpr int kHeldColumns = 8192;
-constexpr int kGradCtas = 152 * 4;
 
-RowPlan row_plan(int d) {
+RowPlan row_plan(int d, int nv) {
   if (d > kHeldColumns) return {0, WIDE_WARPS, 1, WIDE_WARPS * 32};
   RowPlan p;
   const int chunks = (d + 255) / 256;
-  p.nv = chunks >= 4 ? 4 : chunks >= 2 ? 2 : 1;
+  p.nv = std::min(nv, chunks >= 4 ? 4 : chunks >= 2 ? 2 : 1);
   p.warps = (chunks + p.nv - 1) / p.nv;
   p.rows_per_cta = std::max(1, 4 / p.warps);
   p.threads = p.rows_per_cta * p.warps * 32;
   return p;
 }
 
+// forward: two chunks a warp
+RowPlan norm_plan(int d) { return row_plan(d, 4); }
+
+// gradient: one chunk a warp, so that the sums and two rows fit 64 registers;
+// in the odd layout two, where addresses take more of them
+RowPlan norm_grad_plan(int d, bool vec) { return row_plan(d, vec ? 1 : 2); }
+
+// CTAs go over the rows: as many as a GB300 holds at 64 registers a thread.
 int grad_grid(int32_t M, const RowPlan &p) {
-  const int64_t most = p.nv ? kGradCtas : kGradCtas / 4;
+  const int64_t most = 152 * std::max(1, 1024 / p.threads);
   return static_cast<int>(
       std::min<int64_t>((static_cast<int64_t>(M) + p.rows_per_cta - 1) / p.rows_per_cta, most));
 }
 
 template <bool F32, bool VEC>
-void norm_launch_t(const NormArgs &a, const RowPlan &p, cudaStream_t st) {
+cudaError_t norm_launch_t(const NormArgs &a, cudaStream_t st) {
+  const RowPlan p = norm_plan(a.d);
   const unsigned grid = (static_cast<int64_t>(a.M) + p.rows_per_cta - 1) / p.rows_per_cta;
   switch (p.nv) {
-    case 0: norm_wide_kernel<F32, VEC><<<grid, p.threads, 0, st>>>(a); break;
-    case 1: norm_kernel<F32, VEC, 1><<<grid, p.threads, 0, st>>>(a, p.warps); break;
-    case 2: norm_kernel<F32, VEC, 2><<<grid, p.threads, 0, st>>>(a, p.warps); break;
-    default: norm_kernel<F32, VEC, 4><<<grid, p.threads, 0, st>>>(a, p.warps); break;
+    case 0: return launch_overlapped(norm_wide_kernel<F32, VEC>, grid, p.threads, 0, st, a);
+    case 1: return launch_overlapped(norm_kernel<F32, VEC, 1>, grid, p.threads, 0, st, a, p.warps);
+    case 2: return launch_overlapped(norm_kernel<F32, VEC, 2>, grid, p.threads, 0, st, a, p.warps);
+    default: return launch_overlapped(norm_kernel<F32, VEC, 4>, grid, p.threads, 0, st, a, p.warps);
   }
 }
 
 template <bool F32, bool VEC>
-cudaError_t norm_grad_launch_t(const NormGradArgs &a, const RowPlan &p, int grid,
-                               cudaStream_t st) {
+cudaError_t norm_grad_launch_t(const NormGradArgs &a, cudaStream_t st) {
+  const RowPlan p = norm_grad_plan(a.d, VEC);
+  const int grid = grad_grid(a.M, p);
   const size_t line = static_cast<size_t>(a.d) * 4;
   const size_t sm = p.rows_per_cta > 1 ? line : 0;
-  switch (p.nv) {
-    case 0: {
-      const cudaError_t e =
-          cudaFuncSetAttribute(norm_grad_wide_kernel<F32, VEC>,
-                               cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxNormColumns * 4);
-      if (e != cudaSuccess) return e;
-      norm_grad_wide_kernel<F32, VEC><<<grid, p.threads, a.dgain ? line : 0, st>>>(a);
-      break;
-    }
-    case 1: norm_grad_kernel<F32, VEC, 1><<<grid, p.threads, sm, st>>>(a, p.warps); break;
-    case 2: norm_grad_kernel<F32, VEC, 2><<<grid, p.threads, sm, st>>>(a, p.warps); break;
-    default: norm_grad_kernel<F32, VEC, 4><<<grid, p.threads, sm, st>>>(a, p.warps); break;
+  cudaError_t e;
+  if (p.nv == 0) {
+    const auto kernel = norm_grad_wide_kernel<F32, VEC>;
+    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             kMaxNormColumns * 4);
+    if (e == cudaSuccess)
+      e = launch_overlapped(kernel, grid, p.threads, a.dgain ? line : 0, st, a);
+  } else if (p.nv == 1) {
+    e = launch_overlapped(norm_grad_kernel<F32, VEC, 1, 1024>, grid, p.threads, sm, st, a, p.warps);
+  } else {
+    e = launch_overlapped(norm_grad_kernel<F32, VEC, 2, 512>, grid, p.threads, sm, st, a, p.warps);
   }
-  return cudaSuccess;
+  if (e != cudaSuccess || !a.dgain) return e;
+  return launch_overlapped(dgain_kernel<F32>, (a.d + 31) / 32, 1024, 0, st,
+                           static_cast<const float *>(a.partial), grid, a.d, a.dgain);
 }
+
+template <bool F32, bool VEC>
+cudaError_t dropout_launch_t(const DropoutArgs &a, cudaStream_t st) {
+  const int chunks = (a.d + 255) / 256;
+  const int rows = std::max(1, 16 / chunks);
+  const unsigned grid = (static_cast<int64_t>(a.M) + rows - 1) / rows;
+  return launch_overlapped(dropout_kernel<F32, VEC>, grid, 256, 0, st, a, rows, chunks);
+}
+
+dspark_status result(cudaError_t e) { return e == cudaSuccess ? DSPARK_OK : DSPARK_ERR_CUDA; }
 
 }  // namespace
 
 size_t norm_workspace_bytes(int32_t M, int32_t d) {
-  return kNormPartialOffset + static_cast<size_t>(grad_grid(M, row_plan(d))) * d * 4;
+  // either layout's lines
+  const int lines =
+      std::max(grad_grid(M, norm_grad_plan(d, true)), grad_grid(M, norm_grad_plan(d, false)));
+  return kNormPartialOffset + static_cast<size_t>(lines) * d * 4;
 }
 
 dspark_status norm_launch(const NormArgs &a, cudaStream_t st) {
@@ -768,12 +822,8 @@ dspark_status norm_launch(const NormArgs &a, cudaStream_t st) {
                    wide(a.residual, a.residual_stride, e, 16) && wide(a.r, a.r_stride, e, 16) &&
                    wide(a.gain, 0, e, 16) &&
                    wide(a.y, a.y_stride, a.e4m3 ? 1 : e, a.e4m3 ? 8 : 16);
-  const RowPlan p = row_plan(a.d);
-  if (a.f32)
-    vec ? norm_launch_t<true, true>(a, p, st) : norm_launch_t<true, false>(a, p, st);
-  else
-    vec ? norm_launch_t<false, true>(a, p, st) : norm_launch_t<false, false>(a, p, st);
-  return cudaGetLastError() == cudaSuccess ? DSPARK_OK : DSPARK_ERR_CUDA;
+  if (a.f32) return result(vec ? norm_launch_t<true, true>(a, st) : norm_launch_t<true, false>(a, st));
+  return result(vec ? norm_launch_t<false, true>(a, st) : norm_launch_t<false, false>(a, st));
 }
 
 dspark_status norm_grad_launch(const NormGradArgs &a, cudaStream_t st) {
@@ -782,40 +832,18 @@ dspark_status norm_grad_launch(const NormGradArgs &a, cudaStream_t st) {
                    wide(a.dr, a.dr_stride, e, 16) && wide(a.r, a.r_stride, e, 16) &&
                    wide(a.gain, 0, e, 16) && wide(a.dx, a.dx_stride, e, 16) &&
                    wide(a.dresidual, a.dresidual_stride, e, 16);
-  const RowPlan p = row_plan(a.d);
-  const int grid = grad_grid(a.M, p);
-  cudaError_t err;
   if (a.f32)
-    err = vec ? norm_grad_launch_t<true, true>(a, p, grid, st)
-              : norm_grad_launch_t<true, false>(a, p, grid, st);
-  else
-    err = vec ? norm_grad_launch_t<false, true>(a, p, grid, st)
-              : norm_grad_launch_t<false, false>(a, p, grid, st);
-  if (err != cudaSuccess) return DSPARK_ERR_CUDA;
-  if (a.dgain) {
-    const int blocks = (a.d + 31) / 32;
-    if (a.f32)
-      dgain_kernel<true><<<blocks, 1024, 0, st>>>(a.partial, grid, a.d, a.dgain);
-    else
-      dgain_kernel<false><<<blocks, 1024, 0, st>>>(a.partial, grid, a.d, a.dgain);
-  }
-  return cudaGetLastError() == cudaSuccess ? DSPARK_OK : DSPARK_ERR_CUDA;
+    return result(vec ? norm_grad_launch_t<true, true>(a, st) : norm_grad_launch_t<true, false>(a, st));
+  return result(vec ? norm_grad_launch_t<false, true>(a, st) : norm_grad_launch_t<false, false>(a, st));
 }
 
 dspark_status dropout_launch(const DropoutArgs &a, cudaStream_t st) {
   const int e = a.f32 ? 4 : 2;
   const bool vec = a.d % 8 == 0 && wide(a.x, a.x_stride, e, 16) &&
                    wide(a.residual, a.residual_stride, e, 16) && wide(a.y, a.y_stride, e, 16);
-  const int chunks = (a.d + 255) / 256;
-  const int rows = std::max(1, 16 / chunks);
-  const int64_t grid = (a.M + rows - 1) / rows;
   if (a.f32)
-    vec ? dropout_kernel<true, true><<<grid, 256, 0, st>>>(a, rows, chunks)
-        : dropout_kernel<true, false><<<grid, 256, 0, st>>>(a, rows, chunks);
-  else
-    vec ? dropout_kernel<false, true><<<grid, 256, 0, st>>>(a, rows, chunks)
-        : dropout_kernel<false, false><<<grid, 256, 0, st>>>(a, rows, chunks);
-  return cudaGetLastError() == cudaSuccess ? DSPARK_OK : DSPARK_ERR_CUDA;
+    return result(vec ? dropout_launch_t<true, true>(a, st) : dropout_launch_t<true, false>(a, st));
+  return result(vec ? dropout_launch_t<false, true>(a, st) : dropout_launch_t<false, false>(a, st));
 }
 
 }  // namespace dspark

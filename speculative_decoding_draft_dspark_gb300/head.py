@@ -12,9 +12,11 @@ import ctypes
 import os
 import re
 
+import torch
+
 from . import dspark as _d
-from .dspark import (BF16, F32, _F, _I32, _I64, _P, _SZ, _U32, _check, _nbytes,
-                     _ptr, _stream, new_workspace)
+from .dspark import (BF16, F32, DsparkError, _F, _I32, _I64, _P, _SZ, _U32, _nbytes,
+                     new_workspace)
 
 HEADER = os.path.join(os.path.dirname(_d.HERE), "include", "dspark_head.h")
 
@@ -63,22 +65,66 @@ def load() -> ctypes.CDLL:
     return _lib
 
 
-def _want(name, t, shape, dtype, rows_strided=False):
-    """t is a tensor of this shape and type, contiguous (or, where rows may
-    be apart, with contiguous rows)."""
+def _refuse(name, t, shape, dtype):
     if t is None:
         raise ValueError(f"{name} is required")
-    if tuple(t.shape) != tuple(shape) or t.dtype != dtype:
-        raise ValueError(f"{name} must be {tuple(shape)} {dtype}, got "
-                         f"{tuple(t.shape)} {t.dtype}")
-    ok = t.stride(-1) == 1 or t.shape[-1] == 1 if rows_strided else t.is_contiguous()
-    if not ok:
-        raise ValueError(f"{name} must be contiguous" + (" along its rows" if rows_strided else ""))
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be on the GPU")
+    if t.shape != shape or t.dtype is not dtype:
+        raise ValueError(f"{name} must be {tuple(shape)} {dtype}, got {tuple(t.shape)} {t.dtype}")
+    raise ValueError(f"{name} must be contiguous (a matrix: along its rows)")
 
 
-def _row_stride(t):
+def _flat(name, t, shape, dtype):
+    """Pointer of a contiguous tensor of this shape and type."""
+    if (t is None or t.dtype is not dtype or t.shape != shape or not t.is_contiguous()
+            or not t.is_cuda):
+        _refuse(name, t, shape, dtype)
+    return t.data_ptr()
+
+
+def _rows(name, t, shape, dtype):
+    """(pointer, row stride) of a matrix of this shape and type whose rows are
+    contiguous; (None, 0) for None."""
+    if t is None:
+        return None, 0
+    if t.dtype is not dtype or t.shape != shape or not t.is_cuda:
+        _refuse(name, t, shape, dtype)
+    s, one = t.stride()
+    if one != 1 and shape[1] > 1:
+        _refuse(name, t, shape, dtype)
     # the stride of a dimension with one entry means nothing
-    return t.stride(0) if t.shape[0] > 1 else max(t.stride(0), t.shape[1])
+    return t.data_ptr(), s if shape[0] > 1 else max(s, shape[1])
+
+
+def _matrix(name, t):
+    if t is None or t.dim() != 2:
+        raise ValueError(f"{name} must be 2-D")
+    return t.shape
+
+
+_TYPES = {torch.bfloat16: BF16, torch.float32: F32}
+
+
+def _dtype(name, t):
+    dt = _TYPES.get(t.dtype)
+    if dt is None:
+        raise ValueError(f"{name} must be bfloat16 or float32, got {t.dtype}")
+    return dt
+
+
+def _stream(stream):
+    # the current stream's handle without the Stream object around it: the
+    # object costs as long as a small call's kernel
+    if stream is None:
+        return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
+    return stream if isinstance(stream, int) else stream.cuda_stream
+
+
+def _done(name, code, raise_on_error):
+    if code and raise_on_error:
+        raise DsparkError(name, code)
+    return code
 
 
 # ------------------------------------------------------------------- loss
@@ -86,20 +132,20 @@ def dspark_head_workspace_size(M: int, vocab: int, d: int, rank: int, grad: bool
     return int(load().dspark_head_workspace_size(M, vocab, d, rank, int(bool(grad))))
 
 
-def _head_dims(h, W, U, V, prev, target):
-    import torch
-    if h.dim() != 2 or W.dim() != 2:
-        raise ValueError("h and W must be 2-D")
-    (M, d), vocab = h.shape, W.shape[0]
-    rank = 0 if V is None else V.shape[1]
-    _want("h", h, (M, d), torch.bfloat16, rows_strided=True)
-    _want("W", W, (vocab, d), torch.bfloat16)
+def _head_inputs(h, W, U, V, prev, target):
+    M, d = _matrix("h", h)
+    vocab, dw = _matrix("W", W)
+    rank = 0 if V is None else _matrix("V", V)[1]
+    bf16, i32 = torch.bfloat16, torch.int32
+    ph, sh = _rows("h", h, (M, dw), bf16)
+    pw = _flat("W", W, (vocab, dw), bf16)
+    pu = pv = pp = None
     if rank:
-        _want("U", U, (vocab, rank), torch.bfloat16)
-        _want("V", V, (vocab, rank), torch.bfloat16)
-        _want("prev", prev, (M,), torch.int32)
-    _want("target", target, (M,), torch.int32)
-    return M, vocab, d, rank
+        pu = _flat("U", U, (vocab, rank), bf16)
+        pv = _flat("V", V, (vocab, rank), bf16)
+        pp = _flat("prev", prev, (M,), i32)
+    pt = _flat("target", target, (M,), i32)
+    return (ph, sh, pw, pu, pv, pp, pt), (M, vocab, d, rank)
 
 
 def dspark_head_loss(h, W, U, V, prev, target, loss, lse, workspace, *,
@@ -107,15 +153,13 @@ def dspark_head_loss(h, W, U, V, prev, target, loss, lse, workspace, *,
     """h [M, d] bf16 (rows may be apart), W [vocab, d] bf16, U/V [vocab, rank]
     bf16 or None, prev/target [M] int32 (target < 0: ignored), loss/lse [M]
     fp32 (out), workspace of dspark_head_workspace_size bytes."""
-    import torch
-    M, vocab, d, rank = _head_dims(h, W, U, V, prev, target)
-    _want("loss", loss, (M,), torch.float32)
-    _want("lse", lse, (M,), torch.float32)
-    code = load().dspark_head_loss(
-        _ptr(h), _row_stride(h), _ptr(W), _ptr(U), _ptr(V), _ptr(prev),
-        _ptr(target), M, vocab, d, rank, _ptr(loss), _ptr(lse),
-        _ptr(workspace), _nbytes(workspace), _stream(stream))
-    return _check("dspark_head_loss", code, raise_on_error)
+    x, dims = _head_inputs(h, W, U, V, prev, target)
+    rows = (dims[0],)
+    code = (_lib or load()).dspark_head_loss(
+        *x, *dims, _flat("loss", loss, rows, torch.float32),
+        _flat("lse", lse, rows, torch.float32), workspace.data_ptr(),
+        _nbytes(workspace), _stream(stream))
+    return _done("dspark_head_loss", code, raise_on_error)
 
 
 def dspark_head_loss_grad(h, W, U, V, prev, target, lse, dloss, dh, dW, dU, dV,
@@ -123,47 +167,23 @@ def dspark_head_loss_grad(h, W, U, V, prev, target, lse, dloss, dh, dW, dU, dV,
     """Gradients of sum_i dloss_i loss_i: dh [M, d] (rows may be apart), dW
     [vocab, d], dU/dV [vocab, rank] or None, all bf16 and written in full; lse
     [M] as written by dspark_head_loss, dloss [M] fp32."""
-    import torch
-    M, vocab, d, rank = _head_dims(h, W, U, V, prev, target)
-    _want("lse", lse, (M,), torch.float32)
-    _want("dloss", dloss, (M,), torch.float32)
-    _want("dh", dh, (M, d), torch.bfloat16, rows_strided=True)
-    _want("dW", dW, (vocab, d), torch.bfloat16)
+    x, dims = _head_inputs(h, W, U, V, prev, target)
+    M, vocab, d, rank = dims
+    bf16 = torch.bfloat16
+    pdh, sdh = _rows("dh", dh, (M, d), bf16)
+    pdu = pdv = None
     if rank:
-        _want("dU", dU, (vocab, rank), torch.bfloat16)
-        _want("dV", dV, (vocab, rank), torch.bfloat16)
-    code = load().dspark_head_loss_grad(
-        _ptr(h), _row_stride(h), _ptr(W), _ptr(U), _ptr(V), _ptr(prev),
-        _ptr(target), _ptr(lse), _ptr(dloss), M, vocab, d, rank, _ptr(dh),
-        _row_stride(dh), _ptr(dW), _ptr(dU), _ptr(dV), _ptr(workspace),
+        pdu = _flat("dU", dU, (vocab, rank), bf16)
+        pdv = _flat("dV", dV, (vocab, rank), bf16)
+    code = (_lib or load()).dspark_head_loss_grad(
+        *x, _flat("lse", lse, (M,), torch.float32),
+        _flat("dloss", dloss, (M,), torch.float32), *dims, pdh, sdh,
+        _flat("dW", dW, (vocab, d), bf16), pdu, pdv, workspace.data_ptr(),
         _nbytes(workspace), _stream(stream))
-    return _check("dspark_head_loss_grad", code, raise_on_error)
+    return _done("dspark_head_loss_grad", code, raise_on_error)
 
 
 # -------------------------------------------------------- residual stream
-def _dtype(name, t):
-    import torch
-    if t.dtype == torch.bfloat16:
-        return BF16
-    if t.dtype == torch.float32:
-        return F32
-    raise ValueError(f"{name} must be bfloat16 or float32, got {t.dtype}")
-
-
-def _rows(name, t, like, required=False):
-    """(pointer, row stride) of a [M, d] tensor of like's type, or of None."""
-    if t is None and not required:
-        return None, 0
-    _want(name, t, like.shape, like.dtype, rows_strided=True)
-    return _ptr(t), _row_stride(t)
-
-
-def _matrix(name, t):
-    if t.dim() != 2:
-        raise ValueError(f"{name} must be 2-D")
-    return t.shape
-
-
 def dspark_residual_norm(x, residual, gain, r, y, scale=None, rstd=None, *, eps,
                          group=0, p=0.0, seed=0, offset=0, stream=None,
                          raise_on_error=True) -> int:
@@ -171,30 +191,24 @@ def dspark_residual_norm(x, residual, gain, r, y, scale=None, rstd=None, *, eps,
     and r (or None) [M, d] bf16 or fp32 (rows may be apart), gain [d]; y of the
     same type, or float8_e4m3fn with scale [M, 1] (group 0) or [M, ceil(d /
     128)] (group 128) fp32; rstd [M] fp32 or None."""
-    import torch
-    M, d = _matrix("x", x)
-    dt = _dtype("x", x)
-    px, sx = _rows("x", x, x)
-    pres, sres = _rows("residual", residual, x)
-    pr, sr = _rows("r", r, x)
-    _want("gain", gain, (d,), x.dtype)
-    if rstd is not None:
-        _want("rstd", rstd, (M,), torch.float32)
-    ydt = dt
-    if y is not None and y.dtype == torch.float8_e4m3fn:
-        ydt = E4M3
-        _want("y", y, (M, d), y.dtype, rows_strided=True)
+    shape = M, d = _matrix("x", x)
+    ydt = dt = _dtype("x", x)
+    ty = t = x.dtype
+    px, sx = _rows("x", x, shape, t)
+    ps, ss = _rows("residual", residual, shape, t)
+    pr, sr = _rows("r", r, shape, t)
+    pscale = prstd = None
+    if y is not None and y.dtype is torch.float8_e4m3fn:
+        ydt, ty = E4M3, y.dtype
         n = -(-d // group) if group > 0 else 1
-        if scale is None or scale.dim() != 2:
-            raise ValueError("scale must be 2-D with an 8-bit y")
-        _want("scale", scale, (M, n), torch.float32)
-    else:
-        _rows("y", y, x, required=True)
-    code = load().dspark_residual_norm(
-        px, sx, pres, sres, _ptr(gain), dt, M, d, float(eps), float(p), int(seed),
-        int(offset), pr, sr, _ptr(y), _row_stride(y), ydt, int(group), _ptr(scale),
-        _ptr(rstd), _stream(stream))
-    return _check("dspark_residual_norm", code, raise_on_error)
+        pscale = _flat("scale", scale, (M, n), torch.float32)
+    py, sy = _rows("y", y, shape, ty)
+    if rstd is not None:
+        prstd = _flat("rstd", rstd, (M,), torch.float32)
+    code = (_lib or load()).dspark_residual_norm(
+        px, sx, ps, ss, _flat("gain", gain, (d,), t), dt, M, d, eps, p, seed, offset,
+        pr, sr, py, sy, ydt, group, pscale, prstd, _stream(stream))
+    return _done("dspark_residual_norm", code, raise_on_error)
 
 
 def dspark_norm_workspace_size(M: int, d: int) -> int:
@@ -208,34 +222,26 @@ def dspark_residual_norm_grad(dy, dr, r, gain, rstd, dx, dresidual, dgain, works
     dropout(dr'), dgain = the gain's gradient.  dr, dx, dresidual and dgain may
     be None; everything of r's type but rstd [M] fp32 (as written by
     dspark_residual_norm)."""
-    import torch
-    M, d = _matrix("r", r)
-    dt = _dtype("r", r)
-    pdy, sdy = _rows("dy", dy, r, required=True)
-    pdr, sdr = _rows("dr", dr, r)
-    pr, sr = _rows("r", r, r)
-    pdx, sdx = _rows("dx", dx, r)
-    pds, sds = _rows("dresidual", dresidual, r)
-    _want("gain", gain, (d,), r.dtype)
-    _want("rstd", rstd, (M,), torch.float32)
-    if dgain is not None:
-        _want("dgain", dgain, (d,), r.dtype)
-    code = load().dspark_residual_norm_grad(
-        pdy, sdy, pdr, sdr, pr, sr, _ptr(gain), _ptr(rstd), dt, M, d, float(p),
-        int(seed), int(offset), pdx, sdx, pds, sds, _ptr(dgain), _ptr(workspace),
+    shape = M, d = _matrix("r", r)
+    dt, t = _dtype("r", r), r.dtype
+    pg = None if dgain is None else _flat("dgain", dgain, (d,), t)
+    code = (_lib or load()).dspark_residual_norm_grad(
+        *_rows("dy", dy, shape, t), *_rows("dr", dr, shape, t), *_rows("r", r, shape, t),
+        _flat("gain", gain, (d,), t), _flat("rstd", rstd, (M,), torch.float32),
+        dt, M, d, p, seed, offset, *_rows("dx", dx, shape, t),
+        *_rows("dresidual", dresidual, shape, t), pg, workspace.data_ptr(),
         _nbytes(workspace), _stream(stream))
-    return _check("dspark_residual_norm_grad", code, raise_on_error)
+    return _done("dspark_residual_norm_grad", code, raise_on_error)
 
 
 def dspark_dropout(x, residual, y, *, p, seed, offset, stream=None,
                    raise_on_error=True) -> int:
     """y = residual + dropout(x) ([M, d] bf16 or fp32; residual may be None);
     seed (uint64) and offset (uint32) as in include/dspark_head.h."""
-    M, d = _matrix("x", x)
-    dt = _dtype("x", x)
-    px, sx = _rows("x", x, x)
-    pres, sres = _rows("residual", residual, x)
-    py, sy = _rows("y", y, x, required=True)
-    code = load().dspark_dropout(px, sx, pres, sres, dt, M, d, float(p), int(seed),
-                                 int(offset), py, sy, _stream(stream))
-    return _check("dspark_dropout", code, raise_on_error)
+    shape = M, d = _matrix("x", x)
+    t = x.dtype
+    code = (_lib or load()).dspark_dropout(
+        *_rows("x", x, shape, t), *_rows("residual", residual, shape, t),
+        _dtype("x", x), M, d, p, seed, offset, *_rows("y", y, shape, t),
+        _stream(stream))
+    return _done("dspark_dropout", code, raise_on_error)
