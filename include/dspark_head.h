@@ -109,7 +109,7 @@ DSPARK_API dspark_status dspark_head_loss_grad(
  * Any d and alignment to the element works; rows that are 16-byte aligned with
  * d a multiple of 8 are faster.  A NaN or infinity stays in its own row (in
  * its own element where it is dropped).
- * Limits: 1 <= M, 1 <= d <= 32768.
+ * Limits: 1 <= M <= 2^30, 1 <= d <= 32768.
  * ------------------------------------------------------------------------ */
 #define DSPARK_E4M3 2
 

@@ -54,15 +54,15 @@ dspark_status check_norm_dims(int32_t dtype, int32_t M, int32_t d, float p) {
   if (dtype != DSPARK_BF16 && dtype != DSPARK_F32) return DSPARK_ERR_INVALID_ARG;
   if (M <= 0 || d <= 0) return DSPARK_ERR_INVALID_ARG;
   if (!(p >= 0.0f && p <= 1.0f)) return DSPARK_ERR_INVALID_ARG;
-  if (d > kMaxNormColumns) return DSPARK_ERR_UNSUPPORTED;
+  if (d > kMaxNormColumns || M > (1 << 30)) return DSPARK_ERR_UNSUPPORTED;
   return DSPARK_OK;
 }
 
 DropArgs drop_args(float p, uint64_t seed, uint32_t offset) {
   DropArgs a = {};
   const double keep = std::floor((1.0 - static_cast<double>(p)) * 65536.0 + 0.5);
-  a.on = p > 0.0f;
-  a.keep = static_cast<uint32_t>(keep);
+  a.on = keep < 65536.0;
+  a.keep_hi = static_cast<uint32_t>(keep) << 16;
   a.scale = keep > 0.0 ? static_cast<float>(65536.0 / keep) : 0.0f;
   a.seed_lo = static_cast<uint32_t>(seed);
   a.seed_hi = static_cast<uint32_t>(seed >> 32);
@@ -185,6 +185,7 @@ dspark_status dspark_residual_norm(const void *x, int64_t x_stride, const void *
   a.M = M;
   a.d = d;
   a.eps = eps;
+  a.inv_d = 1.0f / static_cast<float>(d);
   a.drop = drop_args(p, seed, offset);
   a.r = r;
   a.y = y;
@@ -235,6 +236,7 @@ dspark_status dspark_residual_norm_grad(const void *dy, int64_t dy_stride, const
   a.f32 = dtype == DSPARK_F32;
   a.M = M;
   a.d = d;
+  a.inv_d = 1.0f / static_cast<float>(d);
   a.drop = drop_args(p, seed, offset);
   a.dx = dx;
   a.dresidual = dresidual;

@@ -31,25 +31,21 @@ struct Philox4 {
   uint32_t w[4];
 };
 
-__device__ __forceinline__ Philox4 philox4x32_10(uint32_t c0, uint32_t c1, uint32_t c2,
-                                                 uint32_t c3, uint32_t k0, uint32_t k1) {
+__device__ __forceinline__ Philox4 drop_words(const DropArgs &d, int group, int row) {
+  uint32_t c0 = static_cast<uint32_t>(group), c1 = static_cast<uint32_t>(row);
+  uint32_t c2 = 0x80000000u, c3 = d.offset, k0 = d.seed_lo, k1 = d.seed_hi;
 #pragma unroll
   for (int i = 0; i < 10; ++i) {
-    const uint32_t h0 = __umulhi(0xD2511F53u, c0), l0 = 0xD2511F53u * c0;
-    const uint32_t h1 = __umulhi(0xCD9E8D57u, c2), l1 = 0xCD9E8D57u * c2;
-    c0 = h1 ^ c1 ^ k0;
-    c1 = l1;
-    c2 = h0 ^ c3 ^ k1;
-    c3 = l0;
+    const uint64_t p0 = static_cast<uint64_t>(0xD2511F53u) * c0;
+    const uint64_t p1 = static_cast<uint64_t>(0xCD9E8D57u) * c2;
+    c0 = static_cast<uint32_t>(p1 >> 32) ^ c1 ^ k0;
+    c2 = static_cast<uint32_t>(p0 >> 32) ^ c3 ^ k1;
+    c1 = static_cast<uint32_t>(p1);
+    c3 = static_cast<uint32_t>(p0);
     k0 += 0x9E3779B9u;
     k1 += 0xBB67AE85u;
   }
   return {{c0, c1, c2, c3}};
-}
-
-__device__ __forceinline__ Philox4 drop_words(const DropArgs &d, int group, int row) {
-  return philox4x32_10(static_cast<uint32_t>(group), static_cast<uint32_t>(row), 0x80000000u,
-                       d.offset, d.seed_lo, d.seed_hi);
 }
 
 // ----------------------------------------------------- eight columns a lane
@@ -73,6 +69,45 @@ __device__ __forceinline__ uint16_t to_bf16(float v) {
   uint16_t r;
   asm("cvt.rn.bf16.f32 %0, %1;" : "=h"(r) : "f"(v));
   return r;
+}
+
+// Eight values as four pairs: the packed fp32 instructions do two at once.
+struct V8 {
+  uint64_t p[4];
+};
+
+__device__ __forceinline__ uint64_t pair(float lo, float hi) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
+  return r;
+}
+__device__ __forceinline__ void halves(uint64_t v, float &lo, float &hi) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(v));
+}
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ void split8(const V8 &v, float (&f)[8]) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) halves(v.p[i], f[2 * i], f[2 * i + 1]);
+}
+__device__ __forceinline__ V8 join8(const float (&f)[8]) {
+  V8 v;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) v.p[i] = pair(f[2 * i], f[2 * i + 1]);
+  return v;
 }
 
 // eight values as they lie in memory
@@ -118,22 +153,19 @@ __device__ __forceinline__ void load8(const void *row, int base, int lane, int d
 }
 
 template <bool F32>
-__device__ __forceinline__ void unpack8(const Raw<F32> &r, float (&v)[8]) {
-  if (F32) {
+__device__ __forceinline__ V8 unpack8(const Raw<F32> &r) {
+  V8 v;
 #pragma unroll
-    for (int e = 0; e < 8; ++e) v[e] = __uint_as_float(r.w[e]);
-  } else {
-#pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      v[2 * e] = bf16_lo(r.w[e]);
-      v[2 * e + 1] = bf16_hi(r.w[e]);
-    }
-  }
+  for (int i = 0; i < 4; ++i)
+    v.p[i] = F32 ? pair(__uint_as_float(r.w[F32 ? 2 * i : 0]), __uint_as_float(r.w[F32 ? 2 * i + 1 : 0]))
+                 : pair(bf16_lo(r.w[i]), bf16_hi(r.w[i]));
+  return v;
 }
 
 template <bool F32, bool VEC>
-__device__ __forceinline__ void store8(void *row, int base, int lane, int d,
-                                       const float (&v)[8]) {
+__device__ __forceinline__ void store8(void *row, int base, int lane, int d, const V8 &x) {
+  float v[8];
+  split8(x, v);
   if (VEC) {
     const int c = base + lane * 8;
     if (c >= d) return;
@@ -162,21 +194,14 @@ __device__ __forceinline__ void store8(void *row, int base, int lane, int d,
   }
 }
 
-// v = dropout(v); a select, so that what a dropped element holds (NaN,
-// infinity) is gone
+// The Philox words of a lane's eight columns, two 16-bit lanes each.
 template <bool VEC>
-__device__ __forceinline__ void drop8(const DropArgs &dr, int base, int lane, int row,
-                                      float (&v)[8]) {
-  const Philox4 p = drop_words(dr, base / 8 + lane, row);
-  if (VEC) {
-#pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      const uint32_t x = (p.w[e >> 1] >> (16 * (e & 1))) & 0xFFFFu;
-      v[e] = x < dr.keep ? v[e] * dr.scale : 0.0f;
-    }
-  } else {
+__device__ __forceinline__ Philox4 drop8_words(const DropArgs &dr, int base, int lane, int row) {
+  Philox4 p = drop_words(dr, base / 8 + lane, row);
+  if (!VEC) {
     // lane l drew the words of columns 8l .. 8l+7; column 32e + l is lane
     // (l % 8) of group 4e + l / 8
+    Philox4 q = {};
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
       const int src = 4 * e + (lane >> 3);
@@ -186,10 +211,30 @@ __device__ __forceinline__ void drop8(const DropArgs &dr, int base, int lane, in
       const uint32_t f = __shfl_sync(0xFFFFFFFFu, p.w[3], src);
       const uint32_t lo = lane & 2 ? b : a, hi = lane & 2 ? f : c;
       const uint32_t w = lane & 4 ? hi : lo;
-      const uint32_t x = (lane & 1 ? w >> 16 : w) & 0xFFFFu;
-      v[e] = x < dr.keep ? v[e] * dr.scale : 0.0f;
+      const uint32_t half = lane & 1 ? w >> 16 : w & 0xFFFFu;
+      q.w[e >> 1] |= half << (16 * (e & 1));
     }
+    p = q;
   }
+  return p;
+}
+
+// dropout(x); a select, so that what a dropped element holds (NaN, infinity)
+// is gone.  A 16-bit lane is kept iff it is below T: the upper half of a word
+// compares with T in the upper half, the lower one once shifted there.
+__device__ __forceinline__ V8 drop8(const DropArgs &dr, const Philox4 &p, const V8 &x) {
+  const uint64_t s = pair(dr.scale, dr.scale);
+  V8 y;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) y.p[i] = mul2(x.p[i], s);
+  float v[8];
+  split8(y, v);
+#pragma unroll
+  for (int e = 0; e < 8; e += 2) {
+    v[e] = (p.w[e >> 1] << 16) < dr.keep_hi ? v[e] : 0.0f;
+    v[e + 1] = p.w[e >> 1] < dr.keep_hi ? v[e + 1] : 0.0f;
+  }
+  return join8(v);
 }
 
 __device__ __forceinline__ float warp_sum(float v) {
@@ -210,18 +255,14 @@ __device__ __forceinline__ float row_sum(float v, float *slots, int w, int warps
   if (warps == 1) return v;
   if (lane == 0) slots[w] = v;
   __syncthreads();
-  float s = 0.0f;
-  for (int i = 0; i < warps; ++i) s += slots[i];
-  return s;
+  return warp_sum(lane < warps ? slots[lane] : 0.0f);
 }
 __device__ __forceinline__ float row_max_nan(float v, float *slots, int w, int warps, int lane) {
   v = warp_max_nan(v);
   if (warps == 1) return v;
   if (lane == 0) slots[w] = v;
   __syncthreads();
-  float s = 0.0f;
-  for (int i = 0; i < warps; ++i) s = fmax_nan(s, slots[i]);
-  return s;
+  return warp_max_nan(lane < warps ? slots[lane] : 0.0f);
 }
 
 // eight e4m3 numbers of y / scale
@@ -239,20 +280,26 @@ __device__ __forceinline__ float scale_of(float top) {
 
 // q = y / scale.  The product with the reciprocal is within an ulp of it, and
 // e4m3 keeps 4 bits; where the reciprocal would overflow it divides.
-__device__ __forceinline__ void over_scale(float (&y)[8], float scale) {
+__device__ __forceinline__ void over_scale(V8 &y, float scale) {
   if (scale > 1e-35f || scale != scale) {
     const float inv = 1.0f / scale;
+    const uint64_t i2 = pair(inv, inv);
 #pragma unroll
-    for (int e = 0; e < 8; ++e) y[e] *= inv;
+    for (int i = 0; i < 4; ++i) y.p[i] = mul2(y.p[i], i2);
   } else {
+    float v[8];
+    split8(y, v);
 #pragma unroll
-    for (int e = 0; e < 8; ++e) y[e] /= scale;
+    for (int e = 0; e < 8; ++e) v[e] /= scale;
+    y = join8(v);
   }
 }
 
 template <bool VEC>
 __device__ __forceinline__ void store8_e4m3(uint8_t *row, int base, int lane, int d,
-                                            const float (&q)[8]) {
+                                            const V8 &x) {
+  float q[8];
+  split8(x, q);
   if (VEC) {
     const int c = base + lane * 8;
     if (c >= d) return;
@@ -271,12 +318,14 @@ __device__ __forceinline__ void store8_e4m3(uint8_t *row, int base, int lane, in
 // neighbours, else the warp's first or last four
 template <bool VEC>
 __device__ __forceinline__ void by_groups(const NormArgs &a, int64_t row, int base, int lane,
-                                          float (&y)[8]) {
+                                          V8 &y) {
+  float v[8];
+  split8(y, v);
   float t0 = 0.0f, t1 = 0.0f;
 #pragma unroll
-  for (int e = 0; e < 4; ++e) t0 = fmax_nan(t0, fabsf(y[e]));
+  for (int e = 0; e < 4; ++e) t0 = fmax_nan(t0, fabsf(v[e]));
 #pragma unroll
-  for (int e = 4; e < 8; ++e) t1 = fmax_nan(t1, fabsf(y[e]));
+  for (int e = 4; e < 8; ++e) t1 = fmax_nan(t1, fabsf(v[e]));
   if (VEC) {
     t0 = fmax_nan(t0, t1);
 #pragma unroll
@@ -289,14 +338,40 @@ __device__ __forceinline__ void by_groups(const NormArgs &a, int64_t row, int ba
     const float s0 = scale_of(warp_max_nan(t0)), s1 = scale_of(warp_max_nan(t1));
     if (lane == 0 && base < a.d) a.scale[row * a.groups + base / 128] = s0;
     if (lane == 0 && base + 128 < a.d) a.scale[row * a.groups + base / 128 + 1] = s1;
-    float q[8];
-#pragma unroll
-    for (int e = 0; e < 8; ++e) q[e] = y[e];
+    V8 q = y;
     over_scale(q, s0);
     over_scale(y, s1);
-#pragma unroll
-    for (int e = 0; e < 4; ++e) y[e] = q[e];
+    y.p[0] = q.p[0];
+    y.p[1] = q.p[1];
   }
+}
+
+__device__ __forceinline__ float top8(float top, const V8 &y) {
+  float v[8];
+  split8(y, v);
+#pragma unroll
+  for (int e = 0; e < 8; ++e) top = fmax_nan(top, fabsf(v[e]));
+  return top;
+}
+
+// sum of squares, two running sums
+__device__ __forceinline__ void squares8(const V8 &r, uint64_t &sum) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) sum = fma2(r.p[i], r.p[i], sum);
+}
+
+// r rstd gain
+template <bool F32, bool VEC>
+__device__ __forceinline__ V8 times_gain(const void *gain, float rstd, int base, int lane, int d,
+                                         const V8 &r) {
+  Raw<F32> raw;
+  load8<F32, VEC>(gain, base, lane, d, raw);
+  const V8 g = unpack8<F32>(raw);
+  const uint64_t s = pair(rstd, rstd);
+  V8 y;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) y.p[i] = mul2(mul2(r.p[i], s), g.p[i]);
+  return y;
 }
 
 // ---------------------------------------------------------------- forward
@@ -316,8 +391,8 @@ __global__ void __launch_bounds__(256) norm_kernel(const NormArgs a, int warps) 
   const uint8_t *x = static_cast<const uint8_t *>(a.x) + row * a.x_stride * E;
   const uint8_t *res = static_cast<const uint8_t *>(a.residual) + row * a.residual_stride * E;
 
-  float r[NV][8];
-  float sum = 0.0f;
+  V8 r[NV];
+  uint64_t sum2 = 0;
   if (live) {
     Raw<F32> rx[NV], rr[NV];
 #pragma unroll
@@ -328,20 +403,22 @@ __global__ void __launch_bounds__(256) norm_kernel(const NormArgs a, int warps) 
     }
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
-      unpack8<F32>(rx[i], r[i]);
-      if (a.drop.on) drop8<VEC>(a.drop, (i * warps + w) * 256, lane, static_cast<int>(row), r[i]);
+      r[i] = unpack8<F32>(rx[i]);
+      if (a.drop.on)
+        r[i] = drop8(a.drop,
+                     drop8_words<VEC>(a.drop, (i * warps + w) * 256, lane, static_cast<int>(row)), r[i]);
       if (a.residual) {
-        float t[8];
-        unpack8<F32>(rr[i], t);
+        const V8 t = unpack8<F32>(rr[i]);
 #pragma unroll
-        for (int e = 0; e < 8; ++e) r[i][e] += t[e];
+        for (int e = 0; e < 4; ++e) r[i].p[e] = add2(r[i].p[e], t.p[e]);
       }
-#pragma unroll
-      for (int e = 0; e < 8; ++e) sum = fmaf(r[i][e], r[i][e], sum);
+      squares8(r[i], sum2);
     }
   }
-  sum = row_sum(sum, slots[0] + group * warps, w, warps, lane);
-  const float rstd = rsqrtf(sum / static_cast<float>(a.d) + a.eps);
+  float lo, hi;
+  halves(sum2, lo, hi);
+  const float sum = row_sum(lo + hi, slots[0] + group * warps, w, warps, lane);
+  const float rstd = rsqrtf(fmaf(sum, a.inv_d, a.eps));
   float top = 0.0f;
   if (live) {
     if (a.rstd && w == 0 && lane == 0) a.rstd[row] = rstd;
@@ -351,17 +428,11 @@ __global__ void __launch_bounds__(256) norm_kernel(const NormArgs a, int warps) 
     for (int i = 0; i < NV; ++i) {
       const int base = (i * warps + w) * 256;
       if (a.r) store8<F32, VEC>(ro, base, lane, a.d, r[i]);
-      Raw<F32> g;
-      float t[8];
-      load8<F32, VEC>(a.gain, base, lane, a.d, g);
-      unpack8<F32>(g, t);
-#pragma unroll
-      for (int e = 0; e < 8; ++e) r[i][e] = r[i][e] * rstd * t[e];
+      r[i] = times_gain<F32, VEC>(a.gain, rstd, base, lane, a.d, r[i]);
       if (!a.e4m3) {
         store8<F32, VEC>(yo, base, lane, a.d, r[i]);
       } else if (a.group == 0) {
-#pragma unroll
-        for (int e = 0; e < 8; ++e) top = fmax_nan(top, fabsf(r[i][e]));
+        top = top8(top, r[i]);
       } else {
         by_groups<VEC>(a, row, base, lane, r[i]);
         store8_e4m3<VEC>(yo, base, lane, a.d, r[i]);
@@ -387,30 +458,19 @@ __global__ void __launch_bounds__(256) norm_kernel(const NormArgs a, int warps) 
 constexpr int WIDE_WARPS = 16;
 
 template <bool F32, bool VEC>
-__device__ __forceinline__ void stream8(const NormArgs &a, const uint8_t *x, const uint8_t *res,
-                                        int64_t row, int base, int lane, float (&r)[8]) {
+__device__ __forceinline__ V8 stream8(const NormArgs &a, const uint8_t *x, const uint8_t *res,
+                                      int64_t row, int base, int lane) {
   Raw<F32> rx, rr;
   load8<F32, VEC>(x, base, lane, a.d, rx);
   if (a.residual) load8<F32, VEC>(res, base, lane, a.d, rr);
-  unpack8<F32>(rx, r);
-  if (a.drop.on) drop8<VEC>(a.drop, base, lane, static_cast<int>(row), r);
+  V8 r = unpack8<F32>(rx);
+  if (a.drop.on) r = drop8(a.drop, drop8_words<VEC>(a.drop, base, lane, static_cast<int>(row)), r);
   if (a.residual) {
-    float t[8];
-    unpack8<F32>(rr, t);
+    const V8 t = unpack8<F32>(rr);
 #pragma unroll
-    for (int e = 0; e < 8; ++e) r[e] += t[e];
+    for (int e = 0; e < 4; ++e) r.p[e] = add2(r.p[e], t.p[e]);
   }
-}
-
-template <bool F32, bool VEC>
-__device__ __forceinline__ void times_gain(const NormArgs &a, float rstd, int base, int lane,
-                                           float (&r)[8]) {
-  Raw<F32> g;
-  float t[8];
-  load8<F32, VEC>(a.gain, base, lane, a.d, g);
-  unpack8<F32>(g, t);
-#pragma unroll
-  for (int e = 0; e < 8; ++e) r[e] = r[e] * rstd * t[e];
+  return r;
 }
 
 template <bool F32, bool VEC>
@@ -423,25 +483,20 @@ __global__ void __launch_bounds__(WIDE_WARPS * 32) norm_wide_kernel(const NormAr
   constexpr int E = F32 ? 4 : 2;
   const uint8_t *x = static_cast<const uint8_t *>(a.x) + row * a.x_stride * E;
   const uint8_t *res = static_cast<const uint8_t *>(a.residual) + row * a.residual_stride * E;
-  float sum = 0.0f;
-  for (int base = w * 256; base < a.d; base += WIDE_WARPS * 256) {
-    float r[8];
-    stream8<F32, VEC>(a, x, res, row, base, lane, r);
-#pragma unroll
-    for (int e = 0; e < 8; ++e) sum = fmaf(r[e], r[e], sum);
-  }
-  sum = row_sum(sum, slots[0], w, WIDE_WARPS, lane);
-  const float rstd = rsqrtf(sum / static_cast<float>(a.d) + a.eps);
+  uint64_t sum2 = 0;
+  for (int base = w * 256; base < a.d; base += WIDE_WARPS * 256)
+    squares8(stream8<F32, VEC>(a, x, res, row, base, lane), sum2);
+  float lo, hi;
+  halves(sum2, lo, hi);
+  const float sum = row_sum(lo + hi, slots[0], w, WIDE_WARPS, lane);
+  const float rstd = rsqrtf(fmaf(sum, a.inv_d, a.eps));
   if (a.rstd && threadIdx.x == 0) a.rstd[row] = rstd;
   float s = 1.0f;
   if (a.e4m3 && a.group == 0) {
     float top = 0.0f;
     for (int base = w * 256; base < a.d; base += WIDE_WARPS * 256) {
-      float r[8];
-      stream8<F32, VEC>(a, x, res, row, base, lane, r);
-      times_gain<F32, VEC>(a, rstd, base, lane, r);
-#pragma unroll
-      for (int e = 0; e < 8; ++e) top = fmax_nan(top, fabsf(r[e]));
+      const V8 r = stream8<F32, VEC>(a, x, res, row, base, lane);
+      top = top8(top, times_gain<F32, VEC>(a.gain, rstd, base, lane, a.d, r));
     }
     s = scale_of(row_max_nan(top, slots[1], w, WIDE_WARPS, lane));
     if (threadIdx.x == 0) a.scale[row] = s;
@@ -449,156 +504,334 @@ __global__ void __launch_bounds__(WIDE_WARPS * 32) norm_wide_kernel(const NormAr
   uint8_t *ro = static_cast<uint8_t *>(a.r) + row * a.r_stride * E;
   uint8_t *yo = static_cast<uint8_t *>(a.y) + row * a.y_stride * (a.e4m3 ? 1 : E);
   for (int base = w * 256; base < a.d; base += WIDE_WARPS * 256) {
-    float r[8];
-    stream8<F32, VEC>(a, x, res, row, base, lane, r);
+    const V8 r = stream8<F32, VEC>(a, x, res, row, base, lane);
     if (a.r) store8<F32, VEC>(ro, base, lane, a.d, r);
-    times_gain<F32, VEC>(a, rstd, base, lane, r);
+    V8 y = times_gain<F32, VEC>(a.gain, rstd, base, lane, a.d, r);
     if (!a.e4m3) {
-      store8<F32, VEC>(yo, base, lane, a.d, r);
+      store8<F32, VEC>(yo, base, lane, a.d, y);
       continue;
     }
     if (a.group == 0)
-      over_scale(r, s);
+      over_scale(y, s);
     else
-      by_groups<VEC>(a, row, base, lane, r);
-    store8_e4m3<VEC>(yo, base, lane, a.d, r);
+      by_groups<VEC>(a, row, base, lane, y);
+    store8_e4m3<VEC>(yo, base, lane, a.d, y);
   }
 }
 
 // --------------------------------------------------------------- backward
-// A row as in the forward kernel, with the next row's loads issued before the
-// current row's sum is waited for.  A CTA goes over rows and keeps dgain's sums
-// of its columns in registers, joins its row groups in order and writes one
-// fp32 line of partial sums.  dgain_kernel adds the lines up in order.
-template <bool F32, int NV>
+// A row as in the forward kernel, one chunk of 256 columns a warp.  A CTA goes
+// over rows and keeps dgain's sums of its columns in registers, joins its row
+// groups in order and writes one fp32 line of partial sums.  dgain_kernel adds
+// the lines up in order.
+template <bool F32>
 struct GradRow {
-  Raw<F32> dy[NV], r[NV], dr[NV];
+  Raw<F32> dy, r, dr;
   float rstd;
 };
 
-template <bool F32, bool VEC, int NV>
-__device__ __forceinline__ void load_row(const NormGradArgs &a, int64_t row, int warps, int w,
-                                         int lane, GradRow<F32, NV> &x) {
+template <bool F32, bool VEC>
+__device__ __forceinline__ void load_row(const NormGradArgs &a, int64_t row, int base, int lane,
+                                         GradRow<F32> &x) {
   constexpr int E = F32 ? 4 : 2;
-  if (row >= a.M) return;
-  const uint8_t *py = static_cast<const uint8_t *>(a.dy) + row * a.dy_stride * E;
-  const uint8_t *pr = static_cast<const uint8_t *>(a.r) + row * a.r_stride * E;
-  const uint8_t *pd = static_cast<const uint8_t *>(a.dr) + row * a.dr_stride * E;
-#pragma unroll
-  for (int i = 0; i < NV; ++i) load8<F32, VEC>(py, (i * warps + w) * 256, lane, a.d, x.dy[i]);
-#pragma unroll
-  for (int i = 0; i < NV; ++i) load8<F32, VEC>(pr, (i * warps + w) * 256, lane, a.d, x.r[i]);
-  if (a.dr) {
-#pragma unroll
-    for (int i = 0; i < NV; ++i) load8<F32, VEC>(pd, (i * warps + w) * 256, lane, a.d, x.dr[i]);
-  }
+  load8<F32, VEC>(static_cast<const uint8_t *>(a.dy) + row * a.dy_stride * E, base, lane, a.d, x.dy);
+  load8<F32, VEC>(static_cast<const uint8_t *>(a.r) + row * a.r_stride * E, base, lane, a.d, x.r);
+  if (a.dr)
+    load8<F32, VEC>(static_cast<const uint8_t *>(a.dr) + row * a.dr_stride * E, base, lane, a.d,
+                    x.dr);
   x.rstd = a.rstd[row];
 }
 
-template <bool F32, bool VEC, int NV, int THREADS>
-__global__ void __launch_bounds__(THREADS) norm_grad_kernel(const NormGradArgs a, int warps) {
-  allow_next_kernel();
-  wait_for_earlier_kernel();
-  __shared__ float slots[2][32];
-  extern __shared__ float lines[];
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int group = warp / warps, w = warp - group * warps;
-  const int groups = (blockDim.x >> 5) / warps;
+// a row's lines on their way to L2
+template <bool F32>
+__device__ __forceinline__ void row_to_l2(const NormGradArgs &a, int64_t row, int base, int lane) {
   constexpr int E = F32 ? 4 : 2;
-  float dg[NV][8] = {};
-  Raw<F32> g[NV];
-#pragma unroll
-  for (int i = 0; i < NV; ++i) load8<F32, VEC>(a.gain, (i * warps + w) * 256, lane, a.d, g[i]);
+  const int c = base + lane * (128 / E);
+  if (row >= a.M || lane >= 2 * E || c >= a.d) return;
+  asm volatile("prefetch.global.L2 [%0];" ::"l"(static_cast<const uint8_t *>(a.dy) +
+                                                (row * a.dy_stride + c) * E));
+  asm volatile("prefetch.global.L2 [%0];" ::"l"(static_cast<const uint8_t *>(a.r) +
+                                                (row * a.r_stride + c) * E));
+  if (a.dr)
+    asm volatile("prefetch.global.L2 [%0];" ::"l"(static_cast<const uint8_t *>(a.dr) +
+                                                  (row * a.dr_stride + c) * E));
+}
 
-  const int64_t step = static_cast<int64_t>(gridDim.x) * groups;
-  int64_t r0 = static_cast<int64_t>(blockIdx.x) * groups;
-  GradRow<F32, NV> cur, next;
-  load_row<F32, VEC, NV>(a, r0 + group, warps, w, lane, cur);
-  for (int turn = 0; r0 < a.M; r0 += step, turn ^= 1) {
-    const int64_t row = r0 + group;
-    const bool live = row < a.M;
-    load_row<F32, VEC, NV>(a, row + step, warps, w, lane, next);
-    float dot = 0.0f;
-    const float rstd = cur.rstd;
-    if (live) {
+// What a row keeps between its sum and its use: xh = r rstd and a = dy gain.
+struct GradHalf {
+  V8 xh, a;
+};
+
+// dg += dy xh, dot += a xh
+template <bool F32>
+__device__ __forceinline__ GradHalf grad_dot(const GradRow<F32> &x, const Raw<F32> &gain, V8 &dg,
+                                             uint64_t &dot) {
+  const V8 y = unpack8<F32>(x.dy), r = unpack8<F32>(x.r), g = unpack8<F32>(gain);
+  const uint64_t rs = pair(x.rstd, x.rstd);
+  GradHalf h;
 #pragma unroll
-      for (int i = 0; i < NV; ++i) {
-        float y[8], x[8], t[8];
-        unpack8<F32>(cur.dy[i], y);
-        unpack8<F32>(cur.r[i], x);
-        unpack8<F32>(g[i], t);
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          const float s = y[e] * (x[e] * rstd);
-          dg[i][e] += s;
-          dot = fmaf(s, t[e], dot);
-        }
-      }
-    }
-    // two sets of slots: a row's sums are read while the next row's are written
-    dot = row_sum(dot, slots[turn] + group * warps, w, warps, lane) / static_cast<float>(a.d);
-    if (live) {
-      uint8_t *px = static_cast<uint8_t *>(a.dx) + row * a.dx_stride * E;
-      uint8_t *ps = static_cast<uint8_t *>(a.dresidual) + row * a.dresidual_stride * E;
-#pragma unroll
-      for (int i = 0; i < NV; ++i) {
-        const int base = (i * warps + w) * 256;
-        float y[8], x[8], t[8], o[8];
-        unpack8<F32>(cur.dy[i], y);
-        unpack8<F32>(cur.r[i], x);
-        unpack8<F32>(g[i], t);
-#pragma unroll
-        for (int e = 0; e < 8; ++e) o[e] = rstd * (y[e] * t[e] - x[e] * rstd * dot);
-        if (a.dr) {
-          unpack8<F32>(cur.dr[i], t);
-#pragma unroll
-          for (int e = 0; e < 8; ++e) o[e] += t[e];
-        }
-        if (a.dresidual) store8<F32, VEC>(ps, base, lane, a.d, o);
-        if (a.dx) {
-          if (a.drop.on) drop8<VEC>(a.drop, base, lane, static_cast<int>(row), o);
-          store8<F32, VEC>(px, base, lane, a.d, o);
-        }
-      }
-    }
-    cur = next;
+  for (int e = 0; e < 4; ++e) {
+    h.xh.p[e] = mul2(r.p[e], rs);
+    h.a.p[e] = mul2(y.p[e], g.p[e]);
+    dg.p[e] = fma2(y.p[e], h.xh.p[e], dg.p[e]);
+    dot = fma2(h.a.p[e], h.xh.p[e], dot);
   }
-  if (!a.dgain) return;
-  // the row groups' sums, joined in order
+  return h;
+}
+
+// dr' = rstd (a - xh mean) + dr
+template <bool F32>
+__device__ __forceinline__ V8 grad_sum(const Raw<F32> *dr, const GradHalf &h, float rstd,
+                                       float mean) {
+  const uint64_t rs = pair(rstd, rstd), m = pair(-mean, -mean);
+  V8 o = {};
+  if (dr) o = unpack8<F32>(*dr);
+#pragma unroll
+  for (int e = 0; e < 4; ++e) o.p[e] = fma2(fma2(h.xh.p[e], m, h.a.p[e]), rs, o.p[e]);
+  return o;
+}
+
+template <bool F32, bool VEC>
+__device__ __forceinline__ void grad_out(const NormGradArgs &a, int64_t row, int base, int lane,
+                                         const GradRow<F32> &x, const GradHalf &h, float mean,
+                                         const Philox4 &words) {
+  constexpr int E = F32 ? 4 : 2;
+  V8 o = grad_sum<F32>(a.dr ? &x.dr : nullptr, h, x.rstd, mean);
+  if (a.dresidual)
+    store8<F32, VEC>(static_cast<uint8_t *>(a.dresidual) + row * a.dresidual_stride * E, base, lane,
+                     a.d, o);
+  if (a.dx) {
+    if (a.drop.on) o = drop8(a.drop, words, o);
+    store8<F32, VEC>(static_cast<uint8_t *>(a.dx) + row * a.dx_stride * E, base, lane, a.d, o);
+  }
+}
+
+// a CTA's line of dgain: the row groups' sums, joined in order
+template <bool VEC>
+__device__ __forceinline__ void write_line(const NormGradArgs &a, float *lines, int group,
+                                           int groups, int base, int lane, const V8 &dg) {
   float *line = a.partial + static_cast<int64_t>(blockIdx.x) * a.d;
+  float sums[8];
+  split8(dg, sums);
   for (int k = 0; k < groups; ++k) {
     if (group == k) {
 #pragma unroll
-      for (int i = 0; i < NV; ++i)
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          const int c = column<VEC>((i * warps + w) * 256, lane, e);
-          if (c < a.d) {
-            if (groups == 1)
-              line[c] = dg[i][e];
-            else if (k == 0)
-              lines[c] = dg[i][e];
-            else if (k < groups - 1)
-              lines[c] += dg[i][e];
-            else
-              line[c] = lines[c] + dg[i][e];
-          }
+      for (int e = 0; e < 8; ++e) {
+        const int c = column<VEC>(base, lane, e);
+        if (c < a.d) {
+          if (groups == 1)
+            line[c] = sums[e];
+          else if (k == 0)
+            lines[c] = sums[e];
+          else if (k < groups - 1)
+            lines[c] += sums[e];
+          else
+            line[c] = lines[c] + sums[e];
         }
+      }
     }
     __syncthreads();
   }
+}
+
+// Aligned rows, NV chunks a warp.  Every thread copies its own columns of the
+// next rows into shared memory, `ahead` rows before it reads them, and no other
+// thread's: the copies need no barrier and hold no registers.
+template <bool F32, int NV>
+__global__ void __launch_bounds__(NV == 1 ? 1024 : 512)
+    norm_grad_kernel(const NormGradArgs a, int warps, int ahead) {
+  __shared__ float slots[2][32];
+  extern __shared__ __align__(16) uint8_t dyn[];
+  constexpr int E = F32 ? 4 : 2, PARTS = F32 ? 2 : 1;  // 16-byte parts of eight columns
+  wait_for_earlier_kernel();
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int group = warp / warps, w = warp - group * warps;
+  const int groups = (blockDim.x >> 5) / warps;
+  const int c = w * 256 + lane * 8, chunk = warps * 256;  // chunk i: c + i * chunk
+  V8 dg[NV] = {};
+
+  const int step = gridDim.x * groups;
+  int row = blockIdx.x * groups + group;
+  const int rounds = (a.M - static_cast<int>(blockIdx.x) * groups + step - 1) / step;
+  auto at = [&](const void *p, int64_t stride) {
+    return static_cast<const uint8_t *>(p) + (row * stride + c) * E;
+  };
+  const uint8_t *dy = at(a.dy, a.dy_stride), *r = at(a.r, a.r_stride), *dr = at(a.dr, a.dr_stride);
+  const int64_t dy_step = step * a.dy_stride * E, r_step = step * a.r_stride * E,
+                dr_step = step * a.dr_stride * E;
+  uint8_t *dx = const_cast<uint8_t *>(at(a.dx, a.dx_stride)),
+          *ds = const_cast<uint8_t *>(at(a.dresidual, a.dresidual_stride));
+  const int64_t dx_step = step * a.dx_stride * E, ds_step = step * a.dresidual_stride * E;
+
+  // a stage: dy, r and dr, each NV x PARTS parts of 16 bytes a thread, and rstd
+  const uint32_t part = blockDim.x * 16, tensor = NV * PARTS * part;
+  const uint32_t stage = 3 * tensor + part / 4;
+  const uint32_t mine = smem_u32(dyn) + threadIdx.x * 16;
+  const uint32_t rstd_at = 3 * tensor - threadIdx.x * 12;
+  uint32_t fill = mine, use = mine;
+  const uint32_t end = mine + (ahead + 1) * stage;
+  int fill_row = row;
+  // the gain's columns, behind the stages
+#pragma unroll
+  for (int i = 0; i < NV; ++i) {
+    if (c + i * chunk < a.d) {
+#pragma unroll
+      for (int j = 0; j < PARTS; ++j)
+        cp_async_16(end + (i * PARTS + j) * part, static_cast<const uint8_t *>(a.gain) +
+                                                      static_cast<size_t>(c + i * chunk) * E + j * 16);
+    }
+  }
+  auto copy_row = [&] {
+    if (fill_row < a.M) {
+#pragma unroll
+      for (int i = 0; i < NV; ++i) {
+        if (c + i * chunk < a.d) {
+#pragma unroll
+          for (int j = 0; j < PARTS; ++j) {
+            const uint32_t to = fill + (i * PARTS + j) * part;
+            const int from = i * chunk * E + j * 16;
+            cp_async_16(to, dy + from);
+            cp_async_16(to + tensor, r + from);
+            if (a.dr) cp_async_16(to + 2 * tensor, dr + from);
+          }
+        }
+      }
+      cp_async_4(fill + rstd_at, a.rstd + fill_row);
+    }
+    cp_async_commit();
+    dy += dy_step;
+    r += r_step;
+    dr += dr_step;
+    fill_row += step;
+    fill += stage;
+    if (fill == end) fill = mine;
+  };
+  auto get = [&](uint32_t from, Raw<F32> &x) {
+#pragma unroll
+    for (int j = 0; j < PARTS; ++j) {
+      const uint4 v = ld_shared_v4(from + j * part);
+      x.w[4 * j] = v.x;
+      x.w[4 * j + 1] = v.y;
+      x.w[4 * j + 2] = v.z;
+      x.w[4 * j + 3] = v.w;
+    }
+  };
+  for (int i = 0; i < ahead; ++i) copy_row();
+
+  for (int k = 0; k < rounds; ++k, row += step) {
+    copy_row();
+    if (ahead == 2)
+      cp_async_wait<2>();
+    else
+      cp_async_wait<1>();
+    const bool live = row < a.M;
+    uint64_t dot2 = 0;
+    float rstd = 0.0f;
+    GradHalf h[NV];
+    if (live) {
+      asm volatile("ld.shared.f32 %0, [%1];" : "=f"(rstd) : "r"(use + rstd_at));
+#pragma unroll
+      for (int i = 0; i < NV; ++i) {
+        if (c + i * chunk < a.d) {
+          GradRow<F32> x;
+          Raw<F32> g;
+          x.rstd = rstd;
+          get(use + i * PARTS * part, x.dy);
+          get(use + tensor + i * PARTS * part, x.r);
+          get(end + i * PARTS * part, g);
+          h[i] = grad_dot<F32>(x, g, dg[i], dot2);
+        }
+      }
+    }
+    float lo, hi;
+    halves(dot2, lo, hi);
+    // the mask needs none of the data: drawn before the sum is waited for
+    Philox4 words[NV];
+    if (a.drop.on && a.dx) {
+#pragma unroll
+      for (int i = 0; i < NV; ++i) words[i] = drop_words(a.drop, (c + i * chunk) / 8, row);
+    }
+    // two sets of slots: a row's sums are read while the next row's are written
+    const float mean = row_sum(lo + hi, slots[k & 1] + group * warps, w, warps, lane) * a.inv_d;
+    if (live) {
+#pragma unroll
+      for (int i = 0; i < NV; ++i) {
+        if (c + i * chunk < a.d) {
+          Raw<F32> t;
+          if (a.dr) get(use + 2 * tensor + i * PARTS * part, t);
+          V8 o = grad_sum<F32>(a.dr ? &t : nullptr, h[i], rstd, mean);
+          // (column 0 of a row that begins at these columns)
+          if (a.dresidual) store8<F32, true>(ds + i * chunk * E, -lane * 8, lane, 1, o);
+          if (a.dx) {
+            if (a.drop.on) o = drop8(a.drop, words[i], o);
+            store8<F32, true>(dx + i * chunk * E, -lane * 8, lane, 1, o);
+          }
+        }
+      }
+    }
+    dx += dx_step;
+    ds += ds_step;
+    use += stage;
+    if (use == end) use = mine;
+  }
+  // not before: CTAs that wait here for the rows' end take the place of ones
+  // that work (70 us instead of 59 at 15360 x 2048)
+  allow_next_kernel();
+  if (!a.dgain) return;
+  __syncthreads();
+#pragma unroll
+  for (int i = 0; i < NV; ++i)
+    write_line<true>(a, reinterpret_cast<float *>(dyn), group, groups, w * 256 + i * chunk, lane,
+                     dg[i]);
+}
+
+// Rows of any alignment: the next row's lines are sent to L2 instead.
+template <bool F32>
+__global__ void __launch_bounds__(1024) norm_grad_odd_kernel(const NormGradArgs a, int warps) {
+  __shared__ float slots[2][32];
+  extern __shared__ __align__(16) uint8_t dyn[];
+  allow_next_kernel();
+  wait_for_earlier_kernel();
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int group = warp / warps, w = warp - group * warps;
+  const int groups = (blockDim.x >> 5) / warps;
+  const int base = w * 256;
+  V8 dg = {};
+  Raw<F32> g;
+  load8<F32, false>(a.gain, base, lane, a.d, g);
+  const int64_t step = static_cast<int64_t>(gridDim.x) * groups;
+  int turn = 0;
+  for (int64_t r0 = static_cast<int64_t>(blockIdx.x) * groups; r0 < a.M; r0 += step, turn ^= 1) {
+    const int64_t row = r0 + group;
+    const bool live = row < a.M;
+    uint64_t dot2 = 0;
+    GradHalf h;
+    GradRow<F32> x;
+    if (live) {
+      load_row<F32, false>(a, row, base, lane, x);
+      row_to_l2<F32>(a, row + step, base, lane);
+      h = grad_dot<F32>(x, g, dg, dot2);
+    }
+    float lo, hi;
+    halves(dot2, lo, hi);
+    Philox4 words = {};
+    if (a.drop.on && a.dx) words = drop8_words<false>(a.drop, base, lane, static_cast<int>(row));
+    const float mean = row_sum(lo + hi, slots[turn] + group * warps, w, warps, lane) * a.inv_d;
+    if (live) grad_out<F32, false>(a, row, base, lane, x, h, mean, words);
+  }
+  if (!a.dgain) return;
+  write_line<false>(a, reinterpret_cast<float *>(dyn), group, groups, base, lane, dg);
 }
 
 // Rows too wide to hold: a CTA to a row, read twice; dgain's sums stay in
 // shared memory, every column with one thread.
 template <bool F32, bool VEC>
 __global__ void __launch_bounds__(WIDE_WARPS * 32) norm_grad_wide_kernel(const NormGradArgs a) {
-  allow_next_kernel();
-  wait_for_earlier_kernel();
   __shared__ float slots[2][32];
   extern __shared__ float line[];
+  allow_next_kernel();
+  wait_for_earlier_kernel();
   const int w = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  constexpr int E = F32 ? 4 : 2;
   if (a.dgain)
     for (int base = w * 256; base < a.d; base += WIDE_WARPS * 256)
 #pragma unroll
@@ -608,53 +841,35 @@ __global__ void __launch_bounds__(WIDE_WARPS * 32) norm_grad_wide_kernel(const N
       }
   int turn = 0;
   for (int64_t row = blockIdx.x; row < a.M; row += gridDim.x, turn ^= 1) {
-    const uint8_t *py = static_cast<const uint8_t *>(a.dy) + row * a.dy_stride * E;
-    const uint8_t *pr = static_cast<const uint8_t *>(a.r) + row * a.r_stride * E;
-    const uint8_t *pd = static_cast<const uint8_t *>(a.dr) + row * a.dr_stride * E;
-    const float rstd = a.rstd[row];
-    float dot = 0.0f;
+    uint64_t dot2 = 0;
     for (int base = w * 256; base < a.d; base += WIDE_WARPS * 256) {
-      Raw<F32> raw;
-      float y[8], x[8], t[8];
-      load8<F32, VEC>(py, base, lane, a.d, raw);
-      unpack8<F32>(raw, y);
-      load8<F32, VEC>(pr, base, lane, a.d, raw);
-      unpack8<F32>(raw, x);
-      load8<F32, VEC>(a.gain, base, lane, a.d, raw);
-      unpack8<F32>(raw, t);
+      GradRow<F32> x;
+      Raw<F32> g;
+      load8<F32, VEC>(a.gain, base, lane, a.d, g);
+      load_row<F32, VEC>(a, row, base, lane, x);
+      V8 dg = {};
+      grad_dot<F32>(x, g, dg, dot2);
+      float s[8];
+      split8(dg, s);
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
-        const float s = y[e] * (x[e] * rstd);
         const int c = column<VEC>(base, lane, e);
-        if (a.dgain && c < a.d) line[c] += s;
-        dot = fmaf(s, t[e], dot);
+        if (a.dgain && c < a.d) line[c] += s[e];
       }
     }
-    dot = row_sum(dot, slots[turn], w, WIDE_WARPS, lane) / static_cast<float>(a.d);
-    uint8_t *px = static_cast<uint8_t *>(a.dx) + row * a.dx_stride * E;
-    uint8_t *ps = static_cast<uint8_t *>(a.dresidual) + row * a.dresidual_stride * E;
+    float lo, hi;
+    halves(dot2, lo, hi);
+    const float mean = row_sum(lo + hi, slots[turn], w, WIDE_WARPS, lane) * a.inv_d;
     for (int base = w * 256; base < a.d; base += WIDE_WARPS * 256) {
-      Raw<F32> raw;
-      float y[8], x[8], o[8];
-      load8<F32, VEC>(a.gain, base, lane, a.d, raw);
-      unpack8<F32>(raw, o);
-      load8<F32, VEC>(py, base, lane, a.d, raw);
-      unpack8<F32>(raw, y);
-      load8<F32, VEC>(pr, base, lane, a.d, raw);
-      unpack8<F32>(raw, x);
-#pragma unroll
-      for (int e = 0; e < 8; ++e) o[e] = rstd * (y[e] * o[e] - x[e] * rstd * dot);
-      if (a.dr) {
-        load8<F32, VEC>(pd, base, lane, a.d, raw);
-        unpack8<F32>(raw, y);
-#pragma unroll
-        for (int e = 0; e < 8; ++e) o[e] += y[e];
-      }
-      if (a.dresidual) store8<F32, VEC>(ps, base, lane, a.d, o);
-      if (a.dx) {
-        if (a.drop.on) drop8<VEC>(a.drop, base, lane, static_cast<int>(row), o);
-        store8<F32, VEC>(px, base, lane, a.d, o);
-      }
+      GradRow<F32> x;
+      Raw<F32> g;
+      load8<F32, VEC>(a.gain, base, lane, a.d, g);
+      load_row<F32, VEC>(a, row, base, lane, x);
+      V8 dg = {};
+      const GradHalf h = grad_dot<F32>(x, g, dg, dot2);
+      Philox4 words = {};
+      if (a.drop.on && a.dx) words = drop8_words<VEC>(a.drop, base, lane, static_cast<int>(row));
+      grad_out<F32, VEC>(a, row, base, lane, x, h, mean, words);
     }
   }
   if (!a.dgain) return;
@@ -667,22 +882,34 @@ __global__ void __launch_bounds__(WIDE_WARPS * 32) norm_grad_wide_kernel(const N
     }
 }
 
+// Eight columns (a sector) of 128 lines at a time; the order is fixed.
+constexpr int DGAIN_COLS = 8;
+
 template <bool F32>
 __global__ void __launch_bounds__(1024)
     dgain_kernel(const float *partial, int lines, int d, void *dgain) {
+  __shared__ float part[32][DGAIN_COLS];
   allow_next_kernel();
   wait_for_earlier_kernel();
-  __shared__ float part[32][33];
   const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
-  const int c = blockIdx.x * 32 + lane;
+  const int c = blockIdx.x * DGAIN_COLS + (lane & 7);
   float s = 0.0f;
-  if (c < d)
-    for (int i = w; i < lines; i += 32) s += partial[static_cast<int64_t>(i) * d + c];
-  part[w][lane] = s;
+  if (c < d) {
+#pragma unroll 8
+    for (int i = w * 4 + (lane >> 3); i < lines; i += 128)
+      s += partial[static_cast<int64_t>(i) * d + c];
+  }
+  s += __shfl_xor_sync(0xFFFFFFFFu, s, 8);
+  s += __shfl_xor_sync(0xFFFFFFFFu, s, 16);
+  if (lane < DGAIN_COLS) part[w][lane] = s;
   __syncthreads();
-  if (w == 0 && c < d) {
-    s = 0.0f;
-    for (int i = 0; i < 32; ++i) s += part[i][lane];
+  if (w > 0) return;
+  s = 0.0f;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) s += part[(lane >> 3) * 8 + i][lane & 7];
+  s += __shfl_xor_sync(0xFFFFFFFFu, s, 8);
+  s += __shfl_xor_sync(0xFFFFFFFFu, s, 16);
+  if (lane < DGAIN_COLS && c < d) {
     if (F32)
       static_cast<float *>(dgain)[c] = s;
     else
@@ -710,14 +937,12 @@ __global__ void __launch_bounds__(256) dropout_kernel(const DropoutArgs a, int r
     if (a.residual)
       load8<F32, VEC>(static_cast<const uint8_t *>(a.residual) + row * a.residual_stride * E, base,
                       lane, a.d, rs);
-    float v[8];
-    unpack8<F32>(rx, v);
-    if (a.drop.on) drop8<VEC>(a.drop, base, lane, static_cast<int>(row), v);
+    V8 v = unpack8<F32>(rx);
+    if (a.drop.on) v = drop8(a.drop, drop8_words<VEC>(a.drop, base, lane, static_cast<int>(row)), v);
     if (a.residual) {
-      float t[8];
-      unpack8<F32>(rs, t);
+      const V8 t = unpack8<F32>(rs);
 #pragma unroll
-      for (int e = 0; e < 8; ++e) v[e] += t[e];
+      for (int e = 0; e < 4; ++e) v.p[e] = add2(v.p[e], t.p[e]);
     }
     store8<F32, VEC>(static_cast<uint8_t *>(a.y) + row * a.y_stride * E, base, lane, a.d, v);
   }
@@ -736,6 +961,7 @@ struct RowPlan {
 };
 
 constexpr int kHeldColumns = 8192;
+constexpr int kGradShared = 226 * 1024;
 
 RowPlan row_plan(int d, int nv) {
   if (d > kHeldColumns) return {0, WIDE_WARPS, 1, WIDE_WARPS * 32};
@@ -748,16 +974,23 @@ RowPlan row_plan(int d, int nv) {
   return p;
 }
 
-// forward: two chunks a warp
 RowPlan norm_plan(int d) { return row_plan(d, 4); }
 
-// gradient: one chunk a warp, so that the sums and two rows fit 64 registers;
-// in the odd layout two, where addresses take more of them
-RowPlan norm_grad_plan(int d, bool vec) { return row_plan(d, vec ? 1 : 2); }
+// Gradient.  Aligned bf16 rows: two chunks a warp, as what a warp does once for
+// a row (its sum, pointers, branches) costs a third of what it does for a chunk.
+// Rows of other alignments and fp32: one, so that 64 registers hold it.  Aligned
+// fp32 rows are held while two of them (dy, r, dr) and the gain fit shared memory.
+constexpr int kHeldGradF32 = 7168;
 
-// CTAs go over the rows: as many as a GB300 holds at 64 registers a thread.
+RowPlan norm_grad_plan(int d, bool f32, bool vec) {
+  if (!vec) return row_plan(d, 1);
+  return row_plan(f32 && d > kHeldGradF32 ? kHeldColumns + 1 : d, f32 ? 1 : 2);
+}
+
+// CTAs go over the rows: as many as a GB300 holds at 64 registers a thread (112
+// with two chunks a warp).
 int grad_grid(int32_t M, const RowPlan &p) {
-  const int64_t most = 152 * std::max(1, 1024 / p.threads);
+  const int64_t most = 152 * std::max(1, (p.nv == 2 ? 512 : 1024) / p.threads);
   return static_cast<int>(
       std::min<int64_t>((static_cast<int64_t>(M) + p.rows_per_cta - 1) / p.rows_per_cta, most));
 }
@@ -776,7 +1009,7 @@ cudaError_t norm_launch_t(const NormArgs &a, cudaStream_t st) {
 
 template <bool F32, bool VEC>
 cudaError_t norm_grad_launch_t(const NormGradArgs &a, cudaStream_t st) {
-  const RowPlan p = norm_grad_plan(a.d, VEC);
+  const RowPlan p = norm_grad_plan(a.d, F32, VEC);
   const int grid = grad_grid(a.M, p);
   const size_t line = static_cast<size_t>(a.d) * 4;
   const size_t sm = p.rows_per_cta > 1 ? line : 0;
@@ -787,13 +1020,21 @@ cudaError_t norm_grad_launch_t(const NormGradArgs &a, cudaStream_t st) {
                              kMaxNormColumns * 4);
     if (e == cudaSuccess)
       e = launch_overlapped(kernel, grid, p.threads, a.dgain ? line : 0, st, a);
-  } else if (p.nv == 1) {
-    e = launch_overlapped(norm_grad_kernel<F32, VEC, 1, 1024>, grid, p.threads, sm, st, a, p.warps);
+  } else if (VEC) {
+    // two rows ahead where three stages fit (they do but for the widest fp32)
+    const size_t part = static_cast<size_t>(p.threads) * 16 * p.nv * (F32 ? 2 : 1);
+    const size_t stage = 3 * part + static_cast<size_t>(p.threads) * 4;
+    const int ahead = 3 * stage + part <= kGradShared ? 2 : 1;
+    const size_t bytes = std::max((ahead + 1) * stage + part, sm);
+    const auto kernel = p.nv == 1 ? norm_grad_kernel<F32, 1> : norm_grad_kernel<F32, 2>;
+    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kGradShared);
+    if (e == cudaSuccess)
+      e = launch_overlapped(kernel, grid, p.threads, bytes, st, a, p.warps, ahead);
   } else {
-    e = launch_overlapped(norm_grad_kernel<F32, VEC, 2, 512>, grid, p.threads, sm, st, a, p.warps);
+    e = launch_overlapped(norm_grad_odd_kernel<F32>, grid, p.threads, sm, st, a, p.warps);
   }
   if (e != cudaSuccess || !a.dgain) return e;
-  return launch_overlapped(dgain_kernel<F32>, (a.d + 31) / 32, 1024, 0, st,
+  return launch_overlapped(dgain_kernel<F32>, (a.d + DGAIN_COLS - 1) / DGAIN_COLS, 1024, 0, st,
                            static_cast<const float *>(a.partial), grid, a.d, a.dgain);
 }
 
@@ -810,9 +1051,10 @@ dspark_status result(cudaError_t e) { return e == cudaSuccess ? DSPARK_OK : DSPA
 }  // namespace
 
 size_t norm_workspace_bytes(int32_t M, int32_t d) {
-  // either layout's lines
-  const int lines =
-      std::max(grad_grid(M, norm_grad_plan(d, true)), grad_grid(M, norm_grad_plan(d, false)));
+  // any type's and alignment's lines
+  const int lines = std::max({grad_grid(M, norm_grad_plan(d, false, true)),
+                              grad_grid(M, norm_grad_plan(d, true, true)),
+                              grad_grid(M, norm_grad_plan(d, false, false))});
   return kNormPartialOffset + static_cast<size_t>(lines) * d * 4;
 }
 

@@ -10,9 +10,9 @@
 namespace dspark {
 
 struct DropArgs {
-  int32_t on;       // p > 0
-  uint32_t keep;    // an element is kept iff its 16-bit lane is below this
-  float scale;      // 65536 / keep
+  int32_t on;         // something is dropped
+  uint32_t keep_hi;   // T 65536: kept iff the 16-bit lane, in a word's upper half, is below
+  float scale;        // 65536 / T
   uint32_t seed_lo, seed_hi, offset;
 };
 
@@ -20,7 +20,7 @@ struct NormArgs {
   const void *x, *residual, *gain;
   int64_t x_stride, residual_stride;  // elements
   int32_t f32, M, d;
-  float eps;
+  float eps, inv_d;
   DropArgs drop;
   void *r, *y;
   int64_t r_stride, y_stride;
@@ -33,6 +33,7 @@ struct NormGradArgs {
   int64_t dy_stride, dr_stride, r_stride;
   const float *rstd;
   int32_t f32, M, d;
+  float inv_d;
   DropArgs drop;
   void *dx, *dresidual, *dgain;
   int64_t dx_stride, dresidual_stride;
