@@ -24,20 +24,20 @@ namespace dspark {
 
 namespace {
 
-constexpr int HT = 256;        // rows of a pair's tile, and its columns at most
+constexpr int HT = 256;        // rows of a pair's tile
+constexpr int HW = 512;        // its columns at most, in two halves
 constexpr int HU = 32;         // a tile's rows of A come in units of this
 constexpr int HK = 64;         // reduction entries of a stage (128 bytes)
-constexpr int H_STAGES = 6;
 constexpr int H_BOX = 64 * 128;             // a 64 x 64 bf16 box
-constexpr int H_OPERAND = 2 * H_BOX;        // a CTA's 128 rows of one operand
-constexpr int H_STAGE = 2 * H_OPERAND;
+constexpr int H_OPERAND = 2 * H_BOX;        // 128 rows of an operand
+constexpr int H_RING = 12 * H_OPERAND;      // 6 stages of 32 KB or 4 of 48 KB
+constexpr int H_MAX_STAGES = 6;
+constexpr int H_EPI_WARPS = 8;
 constexpr int H_OUT_BOX = 32 * 128;         // a warp's 32 rows of 128 bytes at most
-constexpr int H_OUT = 4 * 2 * H_OUT_BOX;    // four warps, two boxes each
-constexpr int H_OUT_OFF = H_STAGES * H_STAGE;
-constexpr int H_BAR_OFF = H_OUT_OFF + H_OUT;
-constexpr int H_BARS = 2 * H_STAGES + 2 + 2 + 1;
+constexpr int H_BAR_OFF = H_RING + H_EPI_WARPS * H_OUT_BOX;
+constexpr int H_BARS = 2 * H_MAX_STAGES + 2 + 2 + 1;
 constexpr int H_SMEM = H_BAR_OFF + H_BARS * 8 + 16 + 1024;
-constexpr int H_THREADS = 256;
+constexpr int H_THREADS = (4 + H_EPI_WARPS) * 32;
 constexpr int kPairs = 76;                  // CTA pairs of a GB300: the layout is planned for it
 constexpr uint32_t H_TMEM = 512;            // two accumulators of 256 columns
 static_assert(H_SMEM <= 232448, "shared memory budget");
@@ -220,17 +220,22 @@ __global__ void __launch_bounds__(PACK_THREADS) head_pack_kernel(const PackParam
 
 // -------------------------------------------------------------- products
 // Three kernels on one main loop.  A cluster of two CTAs computes a tile of
-// 256 rows with tcgen05.mma.cta_group::2: each CTA stages 128 of them and half
-// of the columns, 64 deep, and holds its 128 rows of the accumulator, so an
-// operand byte is read from L2 once for 256 entries of the other one.
+// 256 rows and up to 512 columns with tcgen05.mma.cta_group::2: each CTA stages
+// 128 of the rows and half of the columns, 64 deep, and holds its 128 rows of
+// the accumulators.
 //
 //   LSE    z^T tile, 256 vocabulary entries x up to 256 rows of A
 //          -> per row of A (max, sum exp), and z at the target
 //   PROB   z^T tile -> G^T, bf16
-//   GRAD   dA^T tiles (256 columns of A x up to 256 rows; reduction over a
+//   GRAD   dA^T tiles (256 columns of A x up to 512 rows; reduction over a
 //          piece of the vocabulary, added up in fp32 by TMA) and dB tiles (256
-//          vocabulary entries x 256 columns; reduction over the rows, bf16),
-//          in one launch so that the ones fill the others' last wave
+//          vocabulary entries x up to 512 columns; reduction over the rows,
+//          bf16), in one launch so that the ones fill the others' last wave
+//
+// 512 columns are two halves, both accumulators, for one read of the rows'
+// operand.  The epilogue of a half runs while the other one is still
+// multiplied, and at a tile's start the first half gets ahead as far as the ring
+// holds.  With 256 columns the accumulators are two tiles' in turn.
 //
 // The rows of A are always the tile's columns or the reduction: those come in
 // steps of 32 and 16, where a tile's rows are always 256, so that 403 rows cost
@@ -239,14 +244,20 @@ __global__ void __launch_bounds__(PACK_THREADS) head_pack_kernel(const PackParam
 // descriptors say that the other index is the contiguous one.
 enum HeadKind { kLse = 0, kProb = 1, kGrad = 2 };
 
+// The tensor maps.  Boxes are 64 entries (128 bytes) wide.  "rows": many rows,
+// for an operand whose reduction index is contiguous.  "wide": two neighbouring
+// 64 x 64 blocks as one copy (a third dimension over the blocks), for the
+// others: a copy costs some 30 to 50 cycles of the TMA unit beside its bytes.
 struct HeadMaps {
-  CUtensorMap a;      // packed A, 64 x 64 boxes
-  CUtensorMap w, v;   // W and V, 64 x 64 boxes
-  CUtensorMap a_rows, w_rows, v_rows;  // the same, 128 rows x 64 boxes
-  CUtensorMap g;      // G^T, 64 x 64 boxes
-  CUtensorMap g_out;  // G^T, 32 x 32 boxes
-  CUtensorMap dw, dv; // dW and dV, 32 rows x 64 boxes
-  CUtensorMap acc;    // fp32 sums of dA^T, 32 x 32 boxes
+  CUtensorMap a_rows;        // packed A, 128 rows
+  CUtensorMap w_rows, v_rows;  // W and V, 128 rows
+  CUtensorMap a, a_wide;
+  CUtensorMap w, v, w_wide, v_wide;
+  CUtensorMap g;             // G^T
+  CUtensorMap g_rows;        // 128 rows
+  CUtensorMap g_out;         // 32 x 32
+  CUtensorMap dw, dv;        // dW and dV, 32 rows
+  CUtensorMap acc;           // fp32 sums of dA^T, 32 x 32
 };
 
 struct HeadParams {
@@ -255,10 +266,10 @@ struct HeadParams {
   int32_t kd, kr;       // 64-column blocks of d and of rank
   int32_t v0;           // first vocabulary entry of the piece
   int32_t v_tiles;      // 256-entry tiles of the piece
-  int32_t d_tiles;      // 256-column tiles of A
   int32_t splits;
   int32_t first_piece;
   int32_t d, rank;
+  int32_t w_whole, v_whole;  // d and rank are multiples of 64: the wide maps hold
   float2 *partial;
   uint32_t *status;
 };
@@ -266,78 +277,149 @@ struct HeadParams {
 struct HeadTile {
   int da;       // GRAD: a dA tile
   int m, n;     // first row and column of the output tile
-  int cols;     // its columns
+  int cols[2];  // columns of its halves; the second may have none
   int k0, nk;   // range of the reduction, in 64-entry blocks
   int split;
 };
 
-// The rows of A in tiles: units of 32, spread evenly over as few tiles of at
-// most 256 as hold them.
-__device__ __forceinline__ int row_tiles(int n_valid) { return (n_valid + HT - 1) / HT; }
-
-__device__ __forceinline__ void row_tile(int n_valid, int i, int &first, int &count) {
-  const int nt = row_tiles(n_valid), units = (n_valid + HU - 1) / HU;
-  const int lo = static_cast<int>(static_cast<int64_t>(units) * i / nt);
-  const int hi = static_cast<int>(static_cast<int64_t>(units) * (i + 1) / nt);
-  first = lo * HU;
-  count = (hi - lo) * HU;
+// `units` of `unit` columns, spread evenly over as few tiles of at most `width`
+// as hold them: tile i of them, the first half as wide as it can be.
+__device__ __forceinline__ void spread(int units, int unit, int width, int tiles, int i,
+                                       HeadTile &x) {
+  const int lo = static_cast<int>(static_cast<int64_t>(units) * i / tiles);
+  const int n = static_cast<int>(static_cast<int64_t>(units) * (i + 1) / tiles) - lo;
+  x.n = lo * unit;
+  x.cols[0] = min(n * unit, HT);
+  x.cols[1] = n * unit - x.cols[0];
 }
 
-template <int KIND>
-__device__ __forceinline__ int head_tiles(const HeadParams &p, int n_valid) {
-  const int nt = row_tiles(n_valid);
-  if (KIND != kGrad) return nt * p.v_tiles;
-  return nt * p.d_tiles * p.splits + p.v_tiles * p.d_tiles;
+__device__ __forceinline__ int row_tiles(int n_valid, int width) {
+  return (n_valid + width - 1) / width;
 }
 
+__device__ __forceinline__ void row_tile(int n_valid, int width, int i, HeadTile &x) {
+  spread((n_valid + HU - 1) / HU, HU, width, row_tiles(n_valid, width), i, x);
+}
+
+// Width of the tiles whose columns are rows of A.  z^T tiles have both
+// accumulators in turn, one half each: their epilogues (an exponential for each
+// entry) take a fifth of a tile's time and hide only behind another tile (512
+// columns: 1280 us instead of 1190 at 1613 rows x 262144 x 2304).  dA^T tiles
+// have a long reduction and a short epilogue (256 columns: 19.8 ms instead of
+// 18.9 for 6452 rows, loss and gradient).
 template <int KIND>
-__device__ __forceinline__ HeadTile head_tile(const HeadParams &p, int n_valid, int t) {
-  const int nt = row_tiles(n_valid);
-  HeadTile x;
+__device__ __forceinline__ int row_width(int n_valid) {
+  return KIND == kGrad && n_valid > HT ? HW : HT;
+}
+
+// dB tiles: 512 columns where the reduction over the rows is as long (256: 20.0
+// ms instead of 18.9 for 6452 rows); for few rows 256, whose epilogue hides
+// behind the next tile (512: 835 us instead of 790 for 403 rows).
+__device__ __forceinline__ int weight_width(int n_valid) { return n_valid > 1024 ? HW : HT; }
+
+// What a pair does: tiles t = first, first + step, ... < end of its list.  dA
+// tiles go round over the pairs, and each pair gets a run of dB tiles, shorter
+// where it has one dA tile more, so that all have the same to do.
+struct HeadWork {
+  int width;             // of tiles whose columns are rows of A
+  int nt;                // and how many there are side by side
+  int da_tiles, db_lo, db_hi;
+};
+
+template <int KIND>
+__device__ __forceinline__ HeadWork head_work(const HeadParams &p, int n_valid, int pair,
+                                              int pairs) {
+  HeadWork w;
+  w.width = row_width<KIND>(n_valid);
+  const int nt = w.nt = row_tiles(n_valid, w.width);
+  if (KIND != kGrad) {
+    w.da_tiles = nt * p.v_tiles;
+    w.db_lo = w.db_hi = 0;
+    return w;
+  }
+  const int d_tiles = (p.cols_pad + HT - 1) / HT;
+  w.da_tiles = nt * d_tiles * p.splits;
+  const int width = weight_width(n_valid);
+  const int n_db = p.v_tiles * ((p.cols_pad + width - 1) / width);
+  // times in 64-entry blocks of 256 columns; a dB tile's stores take about as
+  // long as three of them
+  const float t_da = static_cast<float>(p.v_tiles) * (HT / HK) / p.splits *
+                     (static_cast<float>(n_valid) / (HT * (nt > 0 ? nt : 1)));
+  const float t_db = ((n_valid + HK - 1) / HK + 3) * static_cast<float>(p.cols_pad) * p.v_tiles /
+                     (static_cast<float>(HT) * n_db);
+  const int more = w.da_tiles % pairs;  // pairs with one dA tile more
+  const float gap = t_da / t_db;
+  float x = (n_db - (pairs - more) * gap) / pairs, y = x + gap;
+  if (x < 0.0f) {
+    x = 0.0f;
+    y = static_cast<float>(n_db) / (pairs - more);
+  }
+  if (more == 0) y = static_cast<float>(n_db) / pairs;
+  auto start = [&](int q) {
+    if (q >= pairs) return n_db;
+    // unfused, so that neighbours agree on where the one ends and the other begins
+    const float at = __fadd_rn(__fmul_rn(x, static_cast<float>(min(q, more))),
+                               __fmul_rn(y, static_cast<float>(max(q - more, 0))));
+    return min(n_db, static_cast<int>(at));
+  };
+  w.db_lo = start(pair);
+  w.db_hi = start(pair + 1);
+  return w;
+}
+
+// The i-th tile of a pair; false after the last.
+template <int KIND>
+__device__ __forceinline__ bool head_tile(const HeadParams &p, const HeadWork &w, int n_valid,
+                                          int pair, int pairs, int i, HeadTile &x) {
+  const int nt = w.nt;
+  int t = pair + i * pairs;
   x.da = 0;
   x.split = 0;
-  if (KIND != kGrad) {
-    x.m = (t / nt) * HT;
-    row_tile(n_valid, t % nt, x.n, x.cols);
-    x.k0 = 0;
-    x.nk = p.kd + p.kr;
-    return x;
-  }
-  const int n_da = nt * p.d_tiles * p.splits;
-  if (t < n_da) {
+  if (t < w.da_tiles) {
+    if (KIND != kGrad) {
+      x.m = (t / nt) * HT;
+      row_tile(n_valid, w.width, t % nt, x);
+      x.k0 = 0;
+      x.nk = p.kd + p.kr;
+      return true;
+    }
+    const int d_tiles = (p.cols_pad + HT - 1) / HT;
     x.da = 1;
-    x.m = (t % p.d_tiles) * HT;
-    const int u = t / p.d_tiles;
-    row_tile(n_valid, u % nt, x.n, x.cols);
+    x.m = (t % d_tiles) * HT;
+    const int u = t / d_tiles;
+    row_tile(n_valid, w.width, u % nt, x);
     x.split = u / nt;
     const int kb = p.v_tiles * (HT / HK);
     x.k0 = static_cast<int>(static_cast<int64_t>(kb) * x.split / p.splits);
     x.nk = static_cast<int>(static_cast<int64_t>(kb) * (x.split + 1) / p.splits) - x.k0;
-  } else {
-    t -= n_da;
-    x.n = (t % p.d_tiles) * HT;
-    x.cols = HT;
-    x.m = (t / p.d_tiles) * HT;
-    x.k0 = 0;
-    x.nk = (n_valid + HK - 1) / HK;
+    return true;
   }
-  return x;
+  if (KIND != kGrad) return false;
+  const int da = w.da_tiles > pair ? (w.da_tiles - pair + pairs - 1) / pairs : 0;
+  t = w.db_lo + i - da;
+  if (t >= w.db_hi) return false;
+  const int width = weight_width(n_valid), tiles = (p.cols_pad + width - 1) / width;
+  spread(p.cols_pad / 64, 64, width, tiles, t % tiles, x);
+  x.m = (t / tiles) * HT;
+  x.k0 = 0;
+  x.nk = (n_valid + HK - 1) / HK;
+  return true;
 }
 
-// K-major operand (the reduction index contiguous): common.cuh's descriptor.
-// Otherwise the 128-byte rows run along the other index, 64 entries each; one
-// row per reduction index, 8 rows (1024 bytes) an atom, atoms 1024 bytes apart
-// along the reduction (bits 32-45) and a box apart along the other index
-// (bits 16-29).
-__device__ __forceinline__ uint64_t sw128_mnmajor_desc(uint32_t smem_addr) {
-  uint64_t d = 0;
-  d |= static_cast<uint64_t>((smem_addr & 0x3FFFFu) >> 4);
-  d |= static_cast<uint64_t>(H_BOX >> 4) << 16;
-  d |= static_cast<uint64_t>(1024u >> 4) << 32;
-  d |= static_cast<uint64_t>(1u) << 46;
-  d |= static_cast<uint64_t>(2u) << 61;
-  return d;
+// Operand descriptors, as in common.cuh, in halves.  K-major operand (the
+// reduction index contiguous): 8-row atoms of 1024 bytes.  Otherwise the
+// 128-byte rows run along the other index, 64 entries each; one row per
+// reduction index, 8 rows (1024 bytes) an atom, atoms 1024 bytes apart along
+// the reduction (bits 32-45) and a box apart along the other index (bits
+// 16-29).  The upper half is the same; 16 reduction entries on, the address is
+// 32 bytes further in the one, two atoms in the other (in units of 16 bytes).
+constexpr uint32_t kDescHi = (1024u >> 4) | (1u << 14) | (2u << 29);
+
+__device__ __forceinline__ uint32_t desc_lo(uint32_t smem_addr, bool mn_major) {
+  return ((smem_addr & 0x3FFFFu) >> 4) | (mn_major ? static_cast<uint32_t>(H_BOX >> 4) << 16
+                                                   : 1u << 16);
 }
+__device__ __forceinline__ uint32_t desc_step(bool mn_major) { return mn_major ? 128u : 2u; }
 
 __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
   uint32_t r;
@@ -352,36 +434,107 @@ __device__ __forceinline__ float ex2(float x) {
 }
 
 // ------------------------------------------------------------- epilogues
-// A warp has 32 rows of the accumulator, a lane one of them, 32 columns at a
-// time.  What goes to memory is laid out in a box of shared memory (the
-// swizzle of its tensor map) and stored by TMA; two boxes alternate.
-__device__ __forceinline__ uint32_t next_box(uint32_t out, int &boxes, int lane) {
-  if (lane == 0) bulk_wait_read<1>();  // the box's last store has read it
+// A warp has 32 rows of the accumulator, a lane one of them; two warps share
+// the rows and take every second block of a half's columns (`part` 0 or 1; the
+// half begins at column n and has `cols`).  The next 32 columns are on their
+// way from tensor memory while the ones before are used, and the accumulator
+// is given back as soon as its last are in registers.  What goes to memory is
+// laid out in the warp's box of shared memory (the swizzle of its tensor map)
+// and stored by TMA.
+struct HalfTile {
+  int n, cols, part;
+  bool empty;         // no reduction: all zero, and no accumulator
+  uint32_t acc, box;  // tensor memory, shared memory
+  uint32_t acc_empty; // barrier, in the cluster's window
+  int lane;
+};
+
+__device__ __forceinline__ void give_back(const HalfTile &t) {
+  if (t.empty) return;
+  tc_fence_before();
   __syncwarp();
-  return out + (boxes++ & 1) * H_OUT_BOX;
+  if (t.lane == 0) mbar_arrive_cluster(t.acc_empty);
 }
 
-// LSE: lanes are vocabulary entries, columns rows of A.  The 32 x 32 block is
+// use(b, column, values) for each block b of 32 columns; WIDE: blocks come in
+// twos, 64 columns a part
+template <bool WIDE, class F>
+__device__ __forceinline__ void each_block(const HalfTile &t, F use) {
+  auto column = [&](int b) {
+    return WIDE ? t.part * 64 + (b >> 1) * 128 + (b & 1) * 32 : t.part * 32 + b * 64;
+  };
+  uint32_t v[2][32];
+  if (t.empty) {
+#pragma unroll
+    for (int e = 0; e < 32; ++e) v[0][e] = 0u;
+    for (int b = 0; b < 4; ++b)
+      if (column(b) < t.cols) use(b, column(b), v[0]);
+    return;
+  }
+  if (column(0) >= t.cols) {
+    give_back(t);
+    return;
+  }
+  tmem_ld_32x32b_x32(t.acc + column(0), v[0]);
+#pragma unroll
+  for (int b = 0; b < 4; ++b) {
+    if (column(b) >= t.cols) break;
+    tmem_ld_wait(v[b & 1]);
+    if (b < 3 && column(b + 1) < t.cols)
+      tmem_ld_32x32b_x32(t.acc + column(b + 1), v[(b + 1) & 1]);
+    else
+      give_back(t);
+    use(b, column(b), v[b & 1]);
+  }
+}
+
+__device__ __forceinline__ void box_is_free(int lane) {
+  if (lane == 0) bulk_wait_read<0>();  // the last store has read it
+  __syncwarp();
+}
+
+__device__ __forceinline__ void put4(uint32_t at, const float *g) {
+  st_shared_v4(at, make_uint4(pack_bf16(g[0], g[1]), pack_bf16(g[2], g[3]),
+                              pack_bf16(g[4], g[5]), pack_bf16(g[6], g[7])));
+}
+
+// LSE: lanes are vocabulary entries, columns rows of A.  A 32 x 32 block is
 // turned in shared memory, so that a lane has 32 entries of its own row of A
-// and needs no other lane for their maximum and sum.
-__device__ __forceinline__ void lse_tile(const HeadParams &p, const HeadTile &x, uint32_t acc_at,
-                                         int v_first, float2 *slot, uint32_t out, int lane) {
+// and needs no other lane for their maximum and sum.  A row's running pair and
+// target are read before the accumulator is waited for.
+struct LseRows {
+  float2 run[4];
+  int target[4];
+};
+
+__device__ __forceinline__ LseRows lse_rows(const HeadParams &p, const float2 *slot, int n,
+                                            int cols, int part, int lane) {
+  LseRows r;
+#pragma unroll
+  for (int b = 0; b < 4; ++b) {
+    const int c = part * 32 + b * 64;
+    if (c < cols) {
+      r.run[b] = slot[n + c + lane];
+      r.target[b] = p.rows.target[n + c + lane];
+    }
+  }
+  return r;
+}
+
+__device__ __forceinline__ void lse_tile(const HeadParams &p, const HalfTile &t, int v_first,
+                                         const LseRows &rows, float2 *slot) {
+  const int lane = t.lane;
   const bool beyond = v_first + lane >= p.vocab;
-  for (int c0 = 0; c0 < x.cols; c0 += 32) {
-    const int row = x.n + c0 + lane;
-    const float2 old = slot[row];
-    const int at = p.rows.target[row] - v_first;
-    uint32_t acc[32];
-    tmem_ld_32x32b_x32(acc_at + c0, acc);
-    tmem_ld_wait(acc);
+  each_block<false>(t, [&](int b, int c0, uint32_t (&acc)[32]) {
+    const int row = t.n + c0 + lane;
     if (beyond) {
 #pragma unroll
       for (int e = 0; e < 32; ++e) acc[e] = 0xFF800000u;  // -infinity
     }
-    const uint32_t box = out + ((c0 >> 5) & 1) * H_OUT_BOX;
+    __syncwarp();  // the block before has been read
 #pragma unroll
     for (int c = 0; c < 8; ++c)
-      st_shared_v4(box + lane * 128 + ((c ^ (lane & 7)) << 4),
+      st_shared_v4(t.box + lane * 128 + ((c ^ (lane & 7)) << 4),
                    make_uint4(acc[4 * c], acc[4 * c + 1], acc[4 * c + 2], acc[4 * c + 3]));
     __syncwarp();
     float z[32];
@@ -390,18 +543,21 @@ __device__ __forceinline__ void lse_tile(const HeadParams &p, const HeadTile &x,
       uint32_t w;
       asm volatile("ld.shared.u32 %0, [%1];"
                    : "=r"(w)
-                   : "r"(box + v * 128 + (((lane >> 2) ^ (v & 7)) << 4) + (lane & 3) * 4));
+                   : "r"(t.box + v * 128 + (((lane >> 2) ^ (v & 7)) << 4) + (lane & 3) * 4));
       z[v] = __uint_as_float(w);
     }
+    const int at = rows.target[b] - v_first;
     if (static_cast<uint32_t>(at) < 32u) {
       float zt = 0.0f;
 #pragma unroll
       for (int v = 0; v < 32; ++v) zt = v == at ? z[v] : zt;
       p.rows.z_target[row] = zt;
     }
-    float top = old.x;
+    const float2 old = rows.run[b];
+    float m[4] = {old.x, z[0], z[1], z[2]};
 #pragma unroll
-    for (int v = 0; v < 32; ++v) top = fmaxf(top, z[v]);
+    for (int v = 3; v < 32; ++v) m[v & 3] = fmaxf(m[v & 3], z[v]);
+    const float top = fmaxf(fmaxf(m[0], m[1]), fmaxf(m[2], m[3]));
     // a row of -infinity keeps a finite reference: its sum is 0
     const float ref = top == -INFINITY ? 0.0f : top * kLog2e;
     float part[4] = {0.0f, 0.0f, 0.0f, 0.0f};
@@ -410,23 +566,19 @@ __device__ __forceinline__ void lse_tile(const HeadParams &p, const HeadTile &x,
     const float sum =
         fmaf(old.y, ex2(fmaf(old.x, kLog2e, -ref)), (part[0] + part[1]) + (part[2] + part[3]));
     slot[row] = make_float2(top, sum);
-  }
+  });
 }
 
 // PROB: lanes are vocabulary entries, columns rows of A.
 __device__ __forceinline__ void prob_tile(const HeadParams &p, const CUtensorMap &g_out,
-                                          const HeadTile &x, uint32_t acc_at, int row0,
-                                          uint32_t out, int &boxes, int lane) {
-  const int v_first = p.v0 + row0;
+                                          const HalfTile &t, int row0) {
+  const int lane = t.lane, v_first = p.v0 + row0;
   const bool beyond = v_first + lane >= p.vocab;
-  for (int c0 = 0; c0 < x.cols; c0 += 32) {
-    const float4 *lse2 = reinterpret_cast<const float4 *>(p.rows.lse2 + x.n + c0);
-    const float4 *weight = reinterpret_cast<const float4 *>(p.rows.weight + x.n + c0);
-    const int at = p.rows.target[x.n + c0 + lane] - v_first;
-    uint32_t hits = __ballot_sync(0xFFFFFFFFu, static_cast<uint32_t>(at) < 32u);
-    uint32_t acc[32];
-    tmem_ld_32x32b_x32(acc_at + c0, acc);
-    tmem_ld_wait(acc);
+  each_block<false>(t, [&](int b, int c0, uint32_t (&acc)[32]) {
+    const float4 *lse2 = reinterpret_cast<const float4 *>(p.rows.lse2 + t.n + c0);
+    const float4 *weight = reinterpret_cast<const float4 *>(p.rows.weight + t.n + c0);
+    const int at = p.rows.target[t.n + c0 + lane] - v_first;
+    const uint32_t hits = __ballot_sync(0xFFFFFFFFu, static_cast<uint32_t>(at) < 32u);
     float g[32];
 #pragma unroll
     for (int e = 0; e < 32; e += 4) {
@@ -437,7 +589,7 @@ __device__ __forceinline__ void prob_tile(const HeadParams &p, const CUtensorMap
       g[e + 3] = ex2(fmaf(__uint_as_float(acc[e + 3]), kLog2e, -l.w)) * w.w;
     }
     if (hits) {
-      const float own = p.rows.weight[x.n + c0 + lane];
+      const float own = p.rows.weight[t.n + c0 + lane];
 #pragma unroll
       for (int e = 0; e < 32; ++e) {
         const int v = __shfl_sync(0xFFFFFFFFu, at, e);
@@ -449,99 +601,75 @@ __device__ __forceinline__ void prob_tile(const HeadParams &p, const CUtensorMap
 #pragma unroll
       for (int e = 0; e < 32; ++e) g[e] = 0.0f;
     }
-    const uint32_t box = next_box(out, boxes, lane);
+    // two boxes of 2 KB in turn: the one before the last store's is free
+    const uint32_t box = t.box + (b & 1) * (H_OUT_BOX / 2);
+    if (lane == 0) bulk_wait_read<1>();
+    __syncwarp();
     // rows of 64 bytes, 64-byte swizzle
 #pragma unroll
     for (int c = 0; c < 4; ++c)
-      st_shared_v4(box + lane * 64 + ((c ^ ((lane >> 1) & 3)) << 4),
-                   make_uint4(pack_bf16(g[8 * c], g[8 * c + 1]),
-                              pack_bf16(g[8 * c + 2], g[8 * c + 3]),
-                              pack_bf16(g[8 * c + 4], g[8 * c + 5]),
-                              pack_bf16(g[8 * c + 6], g[8 * c + 7])));
+      put4(box + lane * 64 + ((c ^ ((lane >> 1) & 3)) << 4), g + 8 * c);
     fence_proxy_async_smem();
     __syncwarp();
     if (lane == 0) {
-      tma_store_2d(&g_out, box, x.n + c0, row0);
+      tma_store_2d(&g_out, box, t.n + c0, row0);
       bulk_commit();
     }
-  }
+  });
 }
 
 // dA^T: lanes are columns of A, columns its rows; fp32, one addition a piece.
 __device__ __forceinline__ void sum_tile(const HeadParams &p, const CUtensorMap &acc_map,
-                                         const HeadTile &x, uint32_t acc_at, int row0,
-                                         uint32_t out, int &boxes, int lane) {
-  if (row0 >= p.cols_pad) return;
-  for (int c0 = 0; c0 < x.cols; c0 += 32) {
-    uint32_t acc[32];
-    if (x.nk > 0) {
-      tmem_ld_32x32b_x32(acc_at + c0, acc);
-      tmem_ld_wait(acc);
-    } else {
-#pragma unroll
-      for (int e = 0; e < 32; ++e) acc[e] = 0u;
-    }
-    const uint32_t box = next_box(out, boxes, lane);
+                                         const HalfTile &t, int split, int row0) {
+  const int lane = t.lane;
+  each_block<false>(t, [&](int, int c0, uint32_t (&acc)[32]) {
+    if (row0 >= p.cols_pad) return;
+    box_is_free(lane);
 #pragma unroll
     for (int c = 0; c < 8; ++c)
-      st_shared_v4(box + lane * 128 + ((c ^ (lane & 7)) << 4),
+      st_shared_v4(t.box + lane * 128 + ((c ^ (lane & 7)) << 4),
                    make_uint4(acc[4 * c], acc[4 * c + 1], acc[4 * c + 2], acc[4 * c + 3]));
     fence_proxy_async_smem();
     __syncwarp();
     if (lane == 0) {
-      const int y = x.split * p.cols_pad + row0;
+      const int y = split * p.cols_pad + row0;
       if (p.first_piece)
-        tma_store_2d(&acc_map, box, x.n + c0, y);
+        tma_store_2d(&acc_map, t.box, t.n + c0, y);
       else
-        tma_reduce_add_2d(&acc_map, box, x.n + c0, y);
+        tma_reduce_add_2d(&acc_map, t.box, t.n + c0, y);
       bulk_commit();
     }
-  }
+  });
 }
 
 // dB: lanes are vocabulary entries, columns those of [W, V].
 __device__ __forceinline__ void weight_tile(const HeadParams &p, const HeadMaps &maps,
-                                            const HeadTile &x, uint32_t acc_at, int row0,
-                                            uint32_t out, int &boxes, int lane) {
-  if (p.v0 + row0 >= p.vocab) return;
+                                            const HalfTile &t, int row0) {
+  const int lane = t.lane;
   const float scale = *p.rows.scale;
-  for (int c0 = 0; c0 < x.cols; c0 += 64) {
-    const int col = x.n + c0;
+  each_block<true>(t, [&](int b, int c0, uint32_t (&acc)[32]) {
+    const int half = (b & 1) * 32, col = t.n + c0 - half;
     const bool in_d = col < p.kd * HK;
     const int left = in_d ? p.d - col : p.rank - (col - p.kd * HK);
-    if (left <= 0) continue;
-    const uint32_t box = next_box(out, boxes, lane);
+    if (left <= 0 || p.v0 + row0 >= p.vocab) return;
+    if (half == 0) box_is_free(lane);
+    float g[32];
 #pragma unroll
-    for (int half = 0; half < 64; half += 32) {
-      uint32_t acc[32];
-      if (x.nk > 0) {
-        tmem_ld_32x32b_x32(acc_at + c0 + half, acc);
-        tmem_ld_wait(acc);
-      } else {
+    for (int e = 0; e < 32; ++e) g[e] = __uint_as_float(acc[e]) * scale;
 #pragma unroll
-        for (int e = 0; e < 32; ++e) acc[e] = 0u;
-      }
-      float g[32];
-#pragma unroll
-      for (int e = 0; e < 32; ++e) g[e] = __uint_as_float(acc[e]) * scale;
-#pragma unroll
-      for (int c = 0; c < 4; ++c)
-        st_shared_v4(box + lane * 128 + (((half / 8 + c) ^ (lane & 7)) << 4),
-                     make_uint4(pack_bf16(g[8 * c], g[8 * c + 1]),
-                                pack_bf16(g[8 * c + 2], g[8 * c + 3]),
-                                pack_bf16(g[8 * c + 4], g[8 * c + 5]),
-                                pack_bf16(g[8 * c + 6], g[8 * c + 7])));
-    }
+    for (int c = 0; c < 4; ++c)
+      put4(t.box + lane * 128 + (((half / 8 + c) ^ (lane & 7)) << 4), g + 8 * c);
+    if (half == 0) return;
     fence_proxy_async_smem();
     __syncwarp();
     if (lane == 0) {
       if (in_d)
-        tma_store_2d(&maps.dw, box, col, p.v0 + row0);
+        tma_store_2d(&maps.dw, t.box, col, p.v0 + row0);
       else
-        tma_store_2d(&maps.dv, box, col - p.kd * HK, p.v0 + row0);
+        tma_store_2d(&maps.dv, t.box, col - p.kd * HK, p.v0 + row0);
       bulk_commit();
     }
-  }
+  });
 }
 
 template <int KIND>
@@ -551,25 +679,25 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(H_THREADS, 1)
   const uint32_t raw_addr = smem_u32(smem_raw);
   uint8_t *smem = smem_raw + ((1024u - (raw_addr & 1023u)) & 1023u);
   uint64_t *full = reinterpret_cast<uint64_t *>(smem + H_BAR_OFF);
-  uint64_t *empty = full + H_STAGES;
-  uint64_t *acc_full = empty + H_STAGES;
+  uint64_t *empty = full + H_MAX_STAGES;
+  uint64_t *acc_full = empty + H_MAX_STAGES;
   uint64_t *acc_empty = acc_full + 2;
   uint64_t *mma_done = acc_empty + 2;
   uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(full + H_BARS);
   volatile uint32_t *abort_flag = tmem_slot + 1;
 
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = __shfl_sync(0xFFFFFFFFu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
   const int cta = static_cast<int>(cluster_ctarank());
   const int pair = blockIdx.x >> 1, pairs = gridDim.x >> 1;
 
   if (threadIdx.x == 0) {
-    for (int i = 0; i < H_STAGES; ++i) {
+    for (int i = 0; i < H_MAX_STAGES; ++i) {
       mbar_init(&full[i], 1);
       mbar_init(&empty[i], 1);
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(&acc_full[i], 1);
-      mbar_init(&acc_empty[i], 8);  // four epilogue warps of either CTA
+      mbar_init(&acc_empty[i], 2 * H_EPI_WARPS);  // of either CTA
     }
     mbar_init(mma_done, 1);
     *abort_flag = 0u;
@@ -587,150 +715,236 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(H_THREADS, 1)
   allow_next_kernel();
   wait_for_earlier_kernel();
   const uint32_t tmem_base = *tmem_slot;
-  const int n_valid = *p.rows.n_valid;
-  const int tiles = head_tiles<KIND>(p, n_valid);
+  const int n_valid = __shfl_sync(0xFFFFFFFFu, *p.rows.n_valid, 0);
+  const HeadWork work = head_work<KIND>(p, n_valid, pair, pairs);
+  // a stage holds 128 rows and up to 128 columns of one half or of two
+  const bool wide = work.width == HW || (KIND == kGrad && weight_width(n_valid) == HW);
+  const int stages = wide ? 4 : 6;
+  const int stage_bytes = wide ? 3 * H_OPERAND : 2 * H_OPERAND;
+  HeadTile x;
 
   if (warp == 0) {
     // ---------------------------------------------------------- loads
-    if (lane == 0) {
-      const uint32_t full0 = mapa_u32(smem_u32(full), 0);
-      bool ok = true;
-      int it = 0;
-      for (int t = pair; t < tiles && ok; t += pairs) {
-        const HeadTile x = head_tile<KIND>(p, n_valid, t);
-        for (int kb = x.k0; kb < x.k0 + x.nk; ++kb, ++it) {
-          const int s = it % H_STAGES;
-          if (!(ok = wait_bounded(&empty[s], ((it / H_STAGES) & 1) ^ 1u, abort_flag, p.status)))
-            break;
-          const uint32_t bar = full0 + s * 8;
-          uint8_t *sa = smem + s * H_STAGE, *sb = sa + H_OPERAND;
-          if (KIND != kGrad) {
-            // whole 64-row boxes, also for fewer rows: 16-row boxes, eight a
-            // stage, took 1.6 times as long (2080 us against 1289 us at 1613 rows)
-            const int slabs = (x.cols / 2 + 63) / 64;
-            if (cta == 0) mbar_arrive_expect_tx(&full[s], 2 * (H_OPERAND + slabs * H_BOX));
-            const bool in_d = kb < p.kd;
-            tma_load_2d_pair(sa, in_d ? &maps.w_rows : &maps.v_rows, bar,
-                             (in_d ? kb : kb - p.kd) * HK, p.v0 + x.m + cta * 128);
-            tma_load_2d_pair(sb, slabs == 2 ? &maps.a_rows : &maps.a, bar, kb * HK,
-                             x.n + cta * (x.cols / 2));
-          } else if (x.da) {
-            const int slabs = (x.cols / 2 + 63) / 64;
-            if (cta == 0) mbar_arrive_expect_tx(&full[s], 2 * (H_OPERAND + slabs * H_BOX));
+    const uint32_t one = elect_one();
+    const uint32_t full0 = mapa_u32(smem_u32(full), 0), ring = smem_u32(smem);
+    bool ok = true;
+    int s = 0;
+    uint32_t phase = 1u;
+    for (int i = 0; ok && head_tile<KIND>(p, work, n_valid, pair, pairs, i, x); ++i) {
+      // this CTA's half of each half's columns, in whole blocks of 64
+      const int mine[2] = {x.cols[0] / 2, x.cols[1] / 2};
+      const int col0[2] = {x.n + cta * mine[0], x.n + x.cols[0] + cta * mine[1]};
+      const int blocks[2] = {(mine[0] + 63) / 64, (mine[1] + 63) / 64};
+      const uint32_t bytes = 2 * (H_OPERAND + (blocks[0] + blocks[1]) * H_BOX);
+      for (int kb = x.k0; kb < x.k0 + x.nk; ++kb) {
+        ok = __all_sync(0xFFFFFFFFu, wait_bounded(&empty[s], phase, abort_flag, p.status));
+        if (!ok) break;
+        if (cta == 0 && one) mbar_arrive_expect_tx(&full[s], bytes);
+        __syncwarp();
+        const uint32_t bar = full0 + s * 8;
+        const uint32_t sa = ring + s * stage_bytes, sb = sa + H_OPERAND;
+        if (KIND != kGrad) {
+          const bool in_d = kb < p.kd;
+          tma_load_2d_pair(one, sa, in_d ? &maps.w_rows : &maps.v_rows, bar,
+                           (in_d ? kb : kb - p.kd) * HK, p.v0 + x.m + cta * 128);
+          // few and large copies, also of fewer rows: exact ones of 64, 32 and
+          // 16 rows instead took up to 1.3 times as long
 #pragma unroll
-            for (int j = 0; j < 2; ++j) {
-              const int cb = (x.m + cta * 128) / HK + j;
-              const bool in_d = cb < p.kd || p.kr == 0;
-              tma_load_2d_pair(sa + j * H_BOX, in_d ? &maps.w : &maps.v, bar,
-                               (in_d ? cb : cb - p.kd) * HK, p.v0 + kb * HK);
-            }
-            for (int j = 0; j < slabs; ++j)
-              tma_load_2d_pair(sb + j * H_BOX, &maps.g, bar, x.n + cta * (x.cols / 2) + j * 64,
-                               kb * HK);
+          for (int h = 0; h < 2; ++h)
+            if (blocks[h])
+              tma_load_2d_pair(one, sb + h * H_OPERAND, blocks[h] == 2 ? &maps.a_rows : &maps.a,
+                               bar, kb * HK, col0[h]);
+        } else if (x.da) {
+          const int cb = (x.m + cta * 128) / HK;
+          const bool in_d = cb < p.kd || p.kr == 0, both = in_d == (cb + 1 < p.kd || p.kr == 0);
+          if (both && (in_d ? p.w_whole : p.v_whole)) {
+            tma_load_3d_pair(one, sa, in_d ? &maps.w_wide : &maps.v_wide, bar, 0, p.v0 + kb * HK,
+                             in_d ? cb : cb - p.kd);
           } else {
-            if (cta == 0) mbar_arrive_expect_tx(&full[s], 2 * H_STAGE);
 #pragma unroll
             for (int j = 0; j < 2; ++j) {
-              const int r = cta * 128 + j * 64;
-              tma_load_2d_pair(sa + j * H_BOX, &maps.g, bar, kb * HK, x.m + r);
-              tma_load_2d_pair(sb + j * H_BOX, &maps.a, bar, x.n + r, kb * HK);
+              const bool d = cb + j < p.kd || p.kr == 0;
+              tma_load_2d_pair(one, sa + j * H_BOX, d ? &maps.w : &maps.v, bar,
+                               (d ? cb + j : cb + j - p.kd) * HK, p.v0 + kb * HK);
+            }
+          }
+          // G^T's columns: any 16 of them begin a block
+#pragma unroll
+          for (int h = 0; h < 2; ++h)
+#pragma unroll
+            for (int j = 0; j < 2; ++j)
+              if (j < blocks[h])
+                tma_load_2d_pair(one, sb + h * H_OPERAND + j * H_BOX, &maps.g, bar,
+                                 col0[h] + j * 64, kb * HK);
+        } else {
+          tma_load_2d_pair(one, sa, &maps.g_rows, bar, kb * HK, x.m + cta * 128);
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            if (mine[h] == 128) {
+              tma_load_3d_pair(one, sb + h * H_OPERAND, &maps.a_wide, bar, 0, kb * HK,
+                               col0[h] / 64);
+            } else {
+#pragma unroll
+              for (int j = 0; j < 2; ++j)
+                if (j < blocks[h])
+                  tma_load_2d_pair(one, sb + h * H_OPERAND + j * H_BOX, &maps.a, bar,
+                                   col0[h] + j * 64, kb * HK);
             }
           }
         }
+        if (++s == stages) {
+          s = 0;
+          phase ^= 1u;
+        }
       }
-      if (!ok) {
-        // copies in flight land before the shared memory is given back
-        const uint64_t t0 = global_timer_ns();
-        while (global_timer_ns() - t0 < 20000000ull) __nanosleep(1000);
-      }
+    }
+    if (!ok) {
+      // copies in flight land before the shared memory is given back
+      const uint64_t t0 = global_timer_ns();
+      while (global_timer_ns() - t0 < 20000000ull) __nanosleep(1000);
     }
     __syncwarp();
   } else if (warp == 1) {
     // ------------------------------------------------------------ MMA
-    if (cta == 0 && lane == 0) {
+    if (cta == 0) {
+      const uint32_t one = elect_one();
       const uint32_t base = smem_u32(smem);
+      const uint32_t empty0 = smem_u32(empty), acc_full0 = smem_u32(acc_full);
       bool ok = true;
-      int it = 0, ig = 0;
-      for (int t = pair; t < tiles && ok; t += pairs) {
-        const HeadTile x = head_tile<KIND>(p, n_valid, t);
+      int s = 0, ig = 0;
+      uint32_t phase = 0u;
+      for (int i = 0; ok && head_tile<KIND>(p, work, n_valid, pair, pairs, i, x); ++i) {
         if (x.nk == 0) continue;
         const bool a_mn = KIND == kGrad && x.da, b_mn = KIND == kGrad;
-        const uint32_t idesc = umma_idesc_bf16_f32(HT, static_cast<uint32_t>(x.cols)) |
-                               (a_mn ? 1u << 15 : 0u) | (b_mn ? 1u << 16 : 0u);
-        const int buf = ig & 1;
-        if (!(ok = wait_bounded(&acc_empty[buf], ((ig >> 1) & 1) ^ 1u, abort_flag, p.status)))
-          break;
-        tc_fence_after();
-        const uint32_t d_tmem = tmem_base + static_cast<uint32_t>(buf * HT);
-        for (int kb = 0; kb < x.nk; ++kb, ++it) {
-          const int s = it % H_STAGES;
-          if (!(ok = wait_bounded(&full[s], (it / H_STAGES) & 1, abort_flag, p.status))) break;
-          tc_fence_after();
-          const uint32_t sa = base + s * H_STAGE, sb = sa + H_OPERAND;
+        const uint32_t a_step = desc_step(a_mn), b_step = desc_step(b_mn);
+        const uint32_t a_lo = desc_lo(base, a_mn);
+        const uint32_t majors = (a_mn ? 1u << 15 : 0u) | (b_mn ? 1u << 16 : 0u);
+        const uint32_t idesc[2] = {
+            umma_idesc_bf16_f32(HT, static_cast<uint32_t>(x.cols[0])) | majors,
+            umma_idesc_bf16_f32(HT, static_cast<uint32_t>(x.cols[1])) | majors};
+        const uint32_t d_tmem[2] = {tmem_base + static_cast<uint32_t>((ig & 1) * HT),
+                                    tmem_base + static_cast<uint32_t>((~ig & 1) * HT)};
+        const uint32_t b_lo[2] = {desc_lo(base + H_OPERAND, b_mn),
+                                  desc_lo(base + 2 * H_OPERAND, b_mn)};
+        auto multiply = [&](int half, int stage, int kb) {
+          const uint32_t at = static_cast<uint32_t>(stage * stage_bytes) >> 4;
+          const uint32_t a = a_lo + at, b = b_lo[half] + at;
           // dB's reduction ends with the rows: no 16 of them are multiplied
           // that hold none (nor were written)
-          const int steps = KIND == kGrad && !x.da
-                                ? min(HK / 16, (n_valid - kb * HK + 15) / 16)
-                                : HK / 16;
+          const int left = KIND == kGrad && !x.da ? n_valid - kb * HK : HK;
 #pragma unroll
-          for (int kk = 0; kk < HK / 16; ++kk) {
-            if (kk >= steps) break;
-            const uint64_t ad = a_mn ? sw128_mnmajor_desc(sa + kk * 2048)
-                                     : sw128_kmajor_desc(sa + kk * 32);
-            const uint64_t bd = b_mn ? sw128_mnmajor_desc(sb + kk * 2048)
-                                     : sw128_kmajor_desc(sb + kk * 32);
-            umma_bf16_pair(d_tmem, ad, bd, idesc, (kb | kk) != 0 ? 1u : 0u);
+          for (int kk = 0; kk < HK / 16; ++kk)
+            umma_bf16_pair(left > kk * 16 ? one : 0u, d_tmem[half], a + kk * a_step,
+                           b + kk * b_step, kDescHi, idesc[half], kb | kk);
+        };
+        auto acc_free = [&](int g) {
+          ok = __all_sync(0xFFFFFFFFu, wait_bounded(&acc_empty[g & 1], ((g >> 1) & 1) ^ 1u,
+                                                    abort_flag, p.status));
+          tc_fence_after();
+          return ok;
+        };
+        auto arrived = [&] {
+          ok = __all_sync(0xFFFFFFFFu, wait_bounded(&full[s], phase, abort_flag, p.status));
+          tc_fence_after();
+          return ok;
+        };
+        auto advance = [&] {
+          if (++s == stages) {
+            s = 0;
+            phase ^= 1u;
           }
-          umma_commit_pair(&empty[s]);
+        };
+        const bool two = x.cols[1] > 0;
+        if (!acc_free(ig)) break;
+        int kb = 0;
+        if (two) {
+          // the first half alone, until the second one's accumulator is free
+          const int s0 = s;
+          const int ahead = min(stages - 1, x.nk);
+          for (; kb < ahead; ++kb) {
+            if (!arrived()) break;
+            multiply(0, s, kb);
+            advance();
+          }
+          if (!ok) break;
+          if (ahead == x.nk) umma_commit_pair(one, acc_full0 + (ig & 1) * 8);
+          if (!acc_free(ig + 1)) break;
+          for (int k = 0, t = s0; k < ahead; ++k) {
+            multiply(1, t, k);
+            umma_commit_pair(one, empty0 + t * 8);
+            t = t + 1 == stages ? 0 : t + 1;
+          }
+        }
+        for (; kb < x.nk; ++kb) {
+          if (!arrived()) break;
+          multiply(0, s, kb);
+          if (kb == x.nk - 1) umma_commit_pair(one, acc_full0 + (ig & 1) * 8);
+          if (two) multiply(1, s, kb);
+          umma_commit_pair(one, empty0 + s * 8);
+          advance();
         }
         if (!ok) break;
-        umma_commit_pair(&acc_full[buf]);
-        ++ig;
+        if (two) umma_commit_pair(one, acc_full0 + ((ig + 1) & 1) * 8);
+        ig += two ? 2 : 1;
       }
-      umma_commit_pair(mma_done);
+      umma_commit_pair(one, smem_u32(mma_done));
     }
     __syncwarp();
   } else if (warp >= 4) {
     // ------------------------------------------------------- epilogue
-    const int q = warp & 3;
+    const int q = warp & 3, part = (warp - 4) >> 2;
     const uint32_t acc_empty0 = mapa_u32(smem_u32(acc_empty), 0);
     const uint32_t lane_base = tmem_base + (static_cast<uint32_t>(q * 32) << 16);
-    uint8_t *out = smem + H_OUT_OFF + q * 2 * H_OUT_BOX;
-    const uint32_t out_addr = smem_u32(out);
-    int ig = 0, boxes = 0;
+    const uint32_t box = smem_u32(smem + H_RING + (warp - 4) * H_OUT_BOX);
+    int ig = 0;
     bool ok = true;
     float2 *slot = nullptr;
     if (KIND == kLse) {
-      // the warp's own running pairs, one for a row of A
+      // the running pairs of these 32 lanes' entries, one for a row of A; each
+      // of the two warps has the rows that it will meet
       slot = p.partial + static_cast<int64_t>(blockIdx.x * 4 + q) * p.rows_pad;
-      for (int i = lane; i < (n_valid + HU - 1) / HU * HU; i += 32)
-        slot[i] = make_float2(-INFINITY, 0.0f);
+      for (int i = 0; i < work.nt; ++i) {
+        row_tile(n_valid, work.width, i, x);
+        for (int h = 0; h < 2; ++h)
+          for (int c0 = part * 32; c0 < x.cols[h]; c0 += 64)
+            slot[x.n + h * x.cols[0] + c0 + lane] = make_float2(-INFINITY, 0.0f);
+      }
     }
-    for (int t = pair; t < tiles && ok; t += pairs) {
-      const HeadTile x = head_tile<KIND>(p, n_valid, t);
-      const int buf = ig & 1;
-      if (x.nk > 0) {
-        ok = __all_sync(0xFFFFFFFFu,
-                        wait_bounded(&acc_full[buf], (ig >> 1) & 1, abort_flag, p.status));
-        if (!ok) break;
-        tc_fence_after();
-      }
-      const uint32_t acc_at = lane_base + static_cast<uint32_t>(buf * HT);
+    for (int i = 0; ok && head_tile<KIND>(p, work, n_valid, pair, pairs, i, x); ++i) {
       const int row0 = x.m + cta * 128 + q * 32;  // the warp's first output row
+      LseRows rows[2];
       if (KIND == kLse) {
-        lse_tile(p, x, acc_at, p.v0 + row0, slot, out_addr, lane);
-      } else if (KIND == kProb) {
-        prob_tile(p, maps.g_out, x, acc_at, row0, out_addr, boxes, lane);
-      } else if (x.da) {
-        sum_tile(p, maps.acc, x, acc_at, row0, out_addr, boxes, lane);
-      } else {
-        weight_tile(p, maps, x, acc_at, row0, out_addr, boxes, lane);
+        rows[0] = lse_rows(p, slot, x.n, x.cols[0], part, lane);
+        rows[1] = lse_rows(p, slot, x.n + x.cols[0], x.cols[1], part, lane);
       }
-      if (x.nk > 0) {
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive_cluster(acc_empty0 + buf * 8);
-        ++ig;
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        if (x.cols[h] == 0) break;
+        const int buf = ig & 1;
+        if (x.nk > 0) {
+          ok = __all_sync(0xFFFFFFFFu,
+                          wait_bounded(&acc_full[buf], (ig >> 1) & 1, abort_flag, p.status));
+          if (!ok) break;
+          tc_fence_after();
+          ++ig;
+        }
+        HalfTile t;
+        t.n = x.n + h * x.cols[0];
+        t.cols = x.cols[h];
+        t.part = part;
+        t.empty = x.nk == 0;
+        t.acc = lane_base + static_cast<uint32_t>(buf * HT);
+        t.box = box;
+        t.acc_empty = acc_empty0 + buf * 8;
+        t.lane = lane;
+        if (KIND == kLse)
+          lse_tile(p, t, p.v0 + row0, rows[h], slot);
+        else if (KIND == kProb)
+          prob_tile(p, maps.g_out, t, row0);
+        else if (x.da)
+          sum_tile(p, maps.acc, t, x.split, row0);
+        else
+          weight_tile(p, maps, t, row0);
       }
     }
     if (lane == 0) bulk_wait_all();
@@ -902,16 +1116,33 @@ bool g_head_attr[128];
 
 bool encode_2d(CUtensorMap *m, CUtensorMapDataType type, int esz, const void *base, int64_t cols,
                int64_t rows, int64_t pitch, int box_cols, int box_rows) {
+  EncodeTiledFn enc = encode_tiled_fn();
   // the swizzle is as wide as the box's rows
   const auto swizzle =
       box_cols * esz == 64 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B;
-  EncodeTiledFn enc = encode_tiled_fn();
   cuuint64_t dims[2] = {static_cast<cuuint64_t>(cols), static_cast<cuuint64_t>(rows)};
   cuuint64_t strides[1] = {static_cast<cuuint64_t>(pitch) * esz};
   cuuint32_t box[2] = {static_cast<cuuint32_t>(box_cols), static_cast<cuuint32_t>(box_rows)};
   cuuint32_t es[2] = {1, 1};
   return enc(m, type, 2, const_cast<void *>(base), dims, strides, box, es,
-             CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle,
+             CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+bool encode_bf16(CUtensorMap *m, const void *base, int64_t cols, int64_t rows, int box_rows) {
+  return encode_2d(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, base, cols, rows, cols, 64, box_rows);
+}
+
+// [rows, cols] of bf16 as 64-column blocks: boxes of 64 rows in two neighbouring
+// blocks.  cols is a multiple of 64.
+bool encode_wide(CUtensorMap *m, const void *base, int64_t cols, int64_t rows) {
+  EncodeTiledFn enc = encode_tiled_fn();
+  cuuint64_t dims[3] = {64, static_cast<cuuint64_t>(rows), static_cast<cuuint64_t>(cols / 64)};
+  cuuint64_t strides[2] = {static_cast<cuuint64_t>(cols) * 2, 128};
+  cuuint32_t box[3] = {64, 64, 2};
+  cuuint32_t es[3] = {1, 1, 1};
+  return enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void *>(base), dims, strides, box,
+             es, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
              CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
@@ -943,22 +1174,28 @@ dspark_status head_plan(const HeadArgs &a, bool grad, HeadPlan &o) {
   }
   const HeadLayout &l = o.lay = head_layout(a.M, a.vocab, a.d, a.rank, grad);
   uint8_t *ws = a.workspace;
-  const auto bf16 = CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
   const int64_t vr = a.rank ? a.rank : a.d;
   const void *V = a.rank ? a.V : a.W;
-  const void *A = ws + l.a;
-  bool ok = encode_2d(&o.maps.a, bf16, 2, A, l.cols_pad, l.rows_pad, l.cols_pad, 64, 64) &&
-            encode_2d(&o.maps.w, bf16, 2, a.W, a.d, a.vocab, a.d, 64, 64) &&
-            encode_2d(&o.maps.v, bf16, 2, V, vr, a.vocab, vr, 64, 64) &&
-            encode_2d(&o.maps.a_rows, bf16, 2, A, l.cols_pad, l.rows_pad, l.cols_pad, 64, 128) &&
-            encode_2d(&o.maps.w_rows, bf16, 2, a.W, a.d, a.vocab, a.d, 64, 128) &&
-            encode_2d(&o.maps.v_rows, bf16, 2, V, vr, a.vocab, vr, 64, 128);
+  const void *A = ws + l.a, *G = ws + l.g;
+  o.p.w_whole = a.d % 64 == 0;
+  o.p.v_whole = vr % 64 == 0;
+  HeadMaps &m = o.maps;
+  bool ok = encode_bf16(&m.w_rows, a.W, a.d, a.vocab, 128) &&
+            encode_bf16(&m.v_rows, V, vr, a.vocab, 128) &&
+            encode_bf16(&m.a_rows, A, l.cols_pad, l.rows_pad, 128) &&
+            encode_bf16(&m.a, A, l.cols_pad, l.rows_pad, 64);
   if (grad) {
-    ok = ok && encode_2d(&o.maps.g, bf16, 2, ws + l.g, l.rows_pad, l.piece, l.rows_pad, 64, 64) &&
-         encode_2d(&o.maps.g_out, bf16, 2, ws + l.g, l.rows_pad, l.piece, l.rows_pad, 32, 32) &&
-         encode_2d(&o.maps.dw, bf16, 2, a.dW, a.d, a.vocab, a.d, 64, 32) &&
-         encode_2d(&o.maps.dv, bf16, 2, a.rank ? a.dV : a.dW, vr, a.vocab, vr, 64, 32) &&
-         encode_2d(&o.maps.acc, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 4, ws + l.acc, l.rows_pad,
+    ok = ok && encode_wide(&m.a_wide, A, l.cols_pad, l.rows_pad) &&
+         encode_bf16(&m.w, a.W, a.d, a.vocab, 64) && encode_bf16(&m.v, V, vr, a.vocab, 64) &&
+         (!o.p.w_whole || encode_wide(&m.w_wide, a.W, a.d, a.vocab)) &&
+         (!o.p.v_whole || encode_wide(&m.v_wide, V, vr, a.vocab)) &&
+         encode_bf16(&m.g, G, l.rows_pad, l.piece, 64) &&
+         encode_bf16(&m.g_rows, G, l.rows_pad, l.piece, 128) &&
+         encode_2d(&m.g_out, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, G, l.rows_pad, l.piece,
+                   l.rows_pad, 32, 32) &&
+         encode_bf16(&m.dw, a.dW, a.d, a.vocab, 32) &&
+         encode_bf16(&m.dv, a.rank ? a.dV : a.dW, vr, a.vocab, 32) &&
+         encode_2d(&m.acc, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 4, ws + l.acc, l.rows_pad,
                    l.cols_pad * l.splits, l.rows_pad, 32, 32);
   }
   if (!ok) return DSPARK_ERR_INVALID_ARG;
@@ -970,7 +1207,6 @@ dspark_status head_plan(const HeadArgs &a, bool grad, HeadPlan &o) {
   p.vocab = a.vocab;
   p.kd = (a.d + HK - 1) / HK;
   p.kr = (a.rank + HK - 1) / HK;
-  p.d_tiles = static_cast<int32_t>((l.cols_pad + HT - 1) / HT);
   p.splits = l.splits;
   p.v0 = 0;
   p.v_tiles = (a.vocab + HT - 1) / HT;
@@ -1010,9 +1246,9 @@ dspark_status head_plan(const HeadArgs &a, bool grad, HeadPlan &o) {
 // no more pairs than there can be tiles
 template <int KIND>
 int head_pairs(const HeadPlan &o, const HeadParams &p) {
-  const int64_t nt = o.lay.rows_pad / HT;
-  const int64_t tiles = KIND == kGrad ? nt * p.d_tiles * p.splits + int64_t(p.v_tiles) * p.d_tiles
-                                      : nt * p.v_tiles;
+  const int64_t nt = (o.lay.rows_pad + HW - 1) / HW, dt = (o.lay.cols_pad + HT - 1) / HT;
+  const int64_t tiles =
+      KIND == kGrad ? dt * (nt * p.splits + p.v_tiles) : nt * int64_t(p.v_tiles);
   return static_cast<int>(std::min<int64_t>(std::min(o.sms / 2, kPairs), tiles));
 }
 
@@ -1040,14 +1276,14 @@ HeadLayout head_layout(int32_t M, int32_t vocab, int32_t d, int32_t rank, bool g
   const int64_t v_pad = up(vocab, HT);
   l.splits = 1;
   if (!grad) {
-    const int64_t pairs = std::min<int64_t>(kPairs, l.rows_pad / HT * (v_pad / HT));
+    const int64_t pairs = std::min<int64_t>(kPairs, (l.rows_pad + HW - 1) / HW * (v_pad / HT));
     l.partial = take(static_cast<size_t>(pairs) * 8 * l.rows_pad * 8);
   } else {
     constexpr int64_t kPieceBytes = 192ll << 20;
     const int64_t most = std::max<int64_t>(4096, kPieceBytes / (2 * l.rows_pad) / HT * HT);
     const int64_t pieces = (v_pad + most - 1) / most;
     l.piece = up((v_pad + pieces - 1) / pieces, HT);
-    const int64_t tiles = l.rows_pad / HT * ((l.cols_pad + HT - 1) / HT);
+    const int64_t tiles = (l.rows_pad + HW - 1) / HW * ((l.cols_pad + HT - 1) / HT);
     const int64_t deep = l.piece / HK;  // 64-entry blocks of the reduction
     l.splits = static_cast<int32_t>(
         std::max<int64_t>(1, std::min<int64_t>({kPairs / tiles, deep / 8, 16})));

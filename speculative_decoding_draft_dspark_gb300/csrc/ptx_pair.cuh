@@ -32,15 +32,42 @@ __device__ __forceinline__ void mbar_arrive_cluster(uint32_t cluster_addr) {
                : "memory");
 }
 
-// -------------------------------------------------------------- TMA, pair
-// 2-D tile into this CTA's shared memory; the bytes are counted on a barrier
-// of either CTA of the pair (`bar`: its address in the cluster's window)
-__device__ __forceinline__ void tma_load_2d_pair(void *dst, const CUtensorMap *m, uint32_t bar,
-                                                 int32_t c0, int32_t c1) {
+// ----------------------------------------------------------- one of a warp
+// TMA copies, tcgen05 instructions and commits take their operands from uniform
+// registers.  Issued from code that only one lane runs, each operand is moved
+// there first, every time (an mma then costs its thread about 120 cycles,
+// whatever its shape); so the whole warp runs that code, and the instruction
+// itself is predicated on `one`, which is 1 in one lane.
+__device__ __forceinline__ uint32_t elect_one() {
+  uint32_t one;
   asm volatile(
-      "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::"
-      "bytes [%0], [%1, {%3, %4}], [%2];" ::"r"(smem_u32(dst)),
-      "l"(reinterpret_cast<uint64_t>(m)), "r"(bar), "r"(c0), "r"(c1)
+      "{\n\t.reg .pred p;\n\t"
+      "elect.sync _|p, 0xffffffff;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(one));
+  return one;
+}
+
+// -------------------------------------------------------------- TMA, pair
+// tile into this CTA's shared memory; the bytes are counted on a barrier of
+// either CTA of the pair (`bar`: its address in the cluster's window)
+__device__ __forceinline__ void tma_load_2d_pair(uint32_t one, uint32_t dst, const CUtensorMap *m,
+                                                 uint32_t bar, int32_t c0, int32_t c1) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %5, 0;\n\t"
+      "@p cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::"
+      "bytes [%0], [%1, {%3, %4}], [%2];\n\t}" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(m)), "r"(bar), "r"(c0), "r"(c1), "r"(one)
+      : "memory");
+}
+__device__ __forceinline__ void tma_load_3d_pair(uint32_t one, uint32_t dst, const CUtensorMap *m,
+                                                 uint32_t bar, int32_t c0, int32_t c1,
+                                                 int32_t c2) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %6, 0;\n\t"
+      "@p cp.async.bulk.tensor.3d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::"
+      "bytes [%0], [%1, {%3, %4, %5}], [%2];\n\t}" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(m)), "r"(bar), "r"(c0), "r"(c1), "r"(c2), "r"(one)
       : "memory");
 }
 
@@ -93,26 +120,31 @@ __device__ __forceinline__ void tmem_dealloc_pair(uint32_t taddr, uint32_t ncols
                : "memory");
 }
 
-// D (+)= A B^T over both CTAs' shared memory and tensor memory; issued by one
-// thread of the pair's first CTA
-__device__ __forceinline__ void umma_bf16_pair(uint32_t d_tmem, uint64_t adesc,
-                                               uint64_t bdesc, uint32_t idesc,
+// D (+)= A B^T over both CTAs' shared memory and tensor memory; issued by the
+// pair's first CTA.  The descriptors come in halves, of which only the lower
+// ones (with the addresses) change.
+__device__ __forceinline__ void umma_bf16_pair(uint32_t one, uint32_t d_tmem, uint32_t a_lo,
+                                               uint32_t b_lo, uint32_t hi, uint32_t idesc,
                                                uint32_t accumulate) {
   asm volatile(
-      "{\n\t.reg .pred p;\n\t"
-      "setp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
-      "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate)
+      "{\n\t.reg .pred p, q;\n\t.reg .b64 a, b;\n\t"
+      "setp.ne.b32 p, %5, 0;\n\t"
+      "setp.ne.b32 q, %6, 0;\n\t"
+      "mov.b64 a, {%1, %3};\n\t"
+      "mov.b64 b, {%2, %3};\n\t"
+      "@q tcgen05.mma.cta_group::2.kind::f16 [%0], a, b, %4, p;\n\t}" ::"r"(d_tmem),
+      "r"(a_lo), "r"(b_lo), "r"(hi), "r"(idesc), "r"(accumulate), "r"(one)
       : "memory");
 }
 
 // arrive once on the barrier at this offset in both CTAs when every tcgen05
 // operation issued so far by this thread has completed
-__device__ __forceinline__ void umma_commit_pair(uint64_t *bar) {
+__device__ __forceinline__ void umma_commit_pair(uint32_t one, uint32_t bar) {
   asm volatile(
-      "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster."
-      "b64 [%0], %1;" ::"r"(smem_u32(bar)),
-      "h"(static_cast<uint16_t>(3))
+      "{\n\t.reg .pred q;\n\tsetp.ne.b32 q, %2, 0;\n\t"
+      "@q tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster."
+      "b64 [%0], %1;\n\t}" ::"r"(bar),
+      "h"(static_cast<uint16_t>(3)), "r"(one)
       : "memory");
 }
 
