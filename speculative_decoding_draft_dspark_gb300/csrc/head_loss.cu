@@ -30,8 +30,8 @@ constexpr int HU = 32;         // a tile's rows of A come in units of this
 constexpr int HK = 64;         // reduction entries of a stage (128 bytes)
 constexpr int H_BOX = 64 * 128;             // a 64 x 64 bf16 box
 constexpr int H_OPERAND = 2 * H_BOX;        // 128 rows of an operand
-constexpr int H_RING = 12 * H_OPERAND;      // 6 stages of 32 KB or 4 of 48 KB
-constexpr int H_MAX_STAGES = 6;
+constexpr int H_RING = 12 * H_OPERAND;      // 8 stages of 24 KB, 6 of 32 or 4 of 48
+constexpr int H_MAX_STAGES = 8;
 constexpr int H_EPI_WARPS = 8;
 constexpr int H_OUT_BOX = 32 * 128;         // a warp's 32 rows of 128 bytes at most
 constexpr int H_BAR_OFF = H_RING + H_EPI_WARPS * H_OUT_BOX;
@@ -69,6 +69,19 @@ __host__ __device__ inline RowInfo row_info(uint8_t *at, int64_t rows_pad) {
   r.weight = reinterpret_cast<float *>(p + 4 * rows_pad);
   r.z_target = reinterpret_cast<float *>(p + 5 * rows_pad);
   return r;
+}
+
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+// What is subtracted from scores (in base 2) under their maximum.  An infinite
+// maximum is not subtracted from itself: scores of -infinity alone sum to 0, one
+// of +infinity makes the sum infinite.
+__device__ __forceinline__ float reference(float top) {
+  return fabsf(top) == INFINITY ? 0.0f : top * kLog2e;
 }
 
 // ------------------------------------------------------------------ pack
@@ -121,6 +134,12 @@ __global__ void __launch_bounds__(PACK_THREADS) head_pack_kernel(const PackParam
   for (int j = warp; j < n; j += PACK_WARPS) {
     const uint16_t *hr = p.h + static_cast<int64_t>(r0 + j) * p.h_stride;
     if (lane * 64 < p.d) asm volatile("prefetch.global.L2 [%0];" ::"l"(hr + lane * 64));
+    if (lane * 64 < p.rank) {
+      const int32_t pv = p.prev[r0 + j];
+      if (counts(pv, p.vocab))
+        asm volatile("prefetch.global.L2 [%0];" ::"l"(p.U + static_cast<int64_t>(pv) * p.rank +
+                                                      lane * 64));
+    }
   }
   int before = 0, total = 0;
   float top = 0.0f;
@@ -256,7 +275,7 @@ struct HeadMaps {
   CUtensorMap g;             // G^T
   CUtensorMap g_rows;        // 128 rows
   CUtensorMap g_out;         // 32 x 32
-  CUtensorMap dw, dv;        // dW and dV, 32 rows
+  CUtensorMap dw, dv;        // dW and dV, 32 x 32
   CUtensorMap acc;           // fp32 sums of dA^T, 32 x 32
 };
 
@@ -427,12 +446,6 @@ __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
   return r;
 }
 
-__device__ __forceinline__ float ex2(float x) {
-  float y;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
-
 // ------------------------------------------------------------- epilogues
 // A warp has 32 rows of the accumulator, a lane one of them; two warps share
 // the rows and take every second block of a half's columns (`part` 0 or 1; the
@@ -456,13 +469,10 @@ __device__ __forceinline__ void give_back(const HalfTile &t) {
   if (t.lane == 0) mbar_arrive_cluster(t.acc_empty);
 }
 
-// use(b, column, values) for each block b of 32 columns; WIDE: blocks come in
-// twos, 64 columns a part
-template <bool WIDE, class F>
+// use(b, column, values) for each block b of 32 columns
+template <class F>
 __device__ __forceinline__ void each_block(const HalfTile &t, F use) {
-  auto column = [&](int b) {
-    return WIDE ? t.part * 64 + (b >> 1) * 128 + (b & 1) * 32 : t.part * 32 + b * 64;
-  };
+  auto column = [&](int b) { return t.part * 32 + b * 64; };
   uint32_t v[2][32];
   if (t.empty) {
 #pragma unroll
@@ -493,9 +503,21 @@ __device__ __forceinline__ void box_is_free(int lane) {
   __syncwarp();
 }
 
-__device__ __forceinline__ void put4(uint32_t at, const float *g) {
-  st_shared_v4(at, make_uint4(pack_bf16(g[0], g[1]), pack_bf16(g[2], g[3]),
-                              pack_bf16(g[4], g[5]), pack_bf16(g[6], g[7])));
+// 32 x 32 values as bf16 into one of the warp's two boxes of 2 KB (rows of 64
+// bytes, 64-byte swizzle), in turn: at most one store is still reading the other
+__device__ __forceinline__ uint32_t put_32x32(const HalfTile &t, int b, const float (&g)[32]) {
+  const uint32_t box = t.box + (b & 1) * (H_OUT_BOX / 2);
+  if (t.lane == 0) bulk_wait_read<1>();
+  __syncwarp();
+#pragma unroll
+  for (int c = 0; c < 4; ++c)
+    st_shared_v4(box + t.lane * 64 + ((c ^ ((t.lane >> 1) & 3)) << 4),
+                 make_uint4(pack_bf16(g[8 * c], g[8 * c + 1]), pack_bf16(g[8 * c + 2], g[8 * c + 3]),
+                            pack_bf16(g[8 * c + 4], g[8 * c + 5]),
+                            pack_bf16(g[8 * c + 6], g[8 * c + 7])));
+  fence_proxy_async_smem();
+  __syncwarp();
+  return box;
 }
 
 // LSE: lanes are vocabulary entries, columns rows of A.  A 32 x 32 block is
@@ -507,14 +529,14 @@ struct LseRows {
   int target[4];
 };
 
-__device__ __forceinline__ LseRows lse_rows(const HeadParams &p, const float2 *slot, int n,
-                                            int cols, int part, int lane) {
+__device__ __forceinline__ LseRows lse_rows(const HeadParams &p, const float2 *slot, bool first,
+                                            int n, int cols, int part, int lane) {
   LseRows r;
 #pragma unroll
   for (int b = 0; b < 4; ++b) {
     const int c = part * 32 + b * 64;
     if (c < cols) {
-      r.run[b] = slot[n + c + lane];
+      r.run[b] = first ? make_float2(-INFINITY, 0.0f) : slot[n + c + lane];
       r.target[b] = p.rows.target[n + c + lane];
     }
   }
@@ -525,7 +547,7 @@ __device__ __forceinline__ void lse_tile(const HeadParams &p, const HalfTile &t,
                                          const LseRows &rows, float2 *slot) {
   const int lane = t.lane;
   const bool beyond = v_first + lane >= p.vocab;
-  each_block<false>(t, [&](int b, int c0, uint32_t (&acc)[32]) {
+  each_block(t, [&](int b, int c0, uint32_t (&acc)[32]) {
     const int row = t.n + c0 + lane;
     if (beyond) {
 #pragma unroll
@@ -558,8 +580,7 @@ __device__ __forceinline__ void lse_tile(const HeadParams &p, const HalfTile &t,
 #pragma unroll
     for (int v = 3; v < 32; ++v) m[v & 3] = fmaxf(m[v & 3], z[v]);
     const float top = fmaxf(fmaxf(m[0], m[1]), fmaxf(m[2], m[3]));
-    // a row of -infinity keeps a finite reference: its sum is 0
-    const float ref = top == -INFINITY ? 0.0f : top * kLog2e;
+    const float ref = reference(top);
     float part[4] = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
     for (int v = 0; v < 32; ++v) part[v & 3] += ex2(fmaf(z[v], kLog2e, -ref));
@@ -574,7 +595,7 @@ __device__ __forceinline__ void prob_tile(const HeadParams &p, const CUtensorMap
                                           const HalfTile &t, int row0) {
   const int lane = t.lane, v_first = p.v0 + row0;
   const bool beyond = v_first + lane >= p.vocab;
-  each_block<false>(t, [&](int b, int c0, uint32_t (&acc)[32]) {
+  each_block(t, [&](int b, int c0, uint32_t (&acc)[32]) {
     const float4 *lse2 = reinterpret_cast<const float4 *>(p.rows.lse2 + t.n + c0);
     const float4 *weight = reinterpret_cast<const float4 *>(p.rows.weight + t.n + c0);
     const int at = p.rows.target[t.n + c0 + lane] - v_first;
@@ -601,16 +622,7 @@ __device__ __forceinline__ void prob_tile(const HeadParams &p, const CUtensorMap
 #pragma unroll
       for (int e = 0; e < 32; ++e) g[e] = 0.0f;
     }
-    // two boxes of 2 KB in turn: the one before the last store's is free
-    const uint32_t box = t.box + (b & 1) * (H_OUT_BOX / 2);
-    if (lane == 0) bulk_wait_read<1>();
-    __syncwarp();
-    // rows of 64 bytes, 64-byte swizzle
-#pragma unroll
-    for (int c = 0; c < 4; ++c)
-      put4(box + lane * 64 + ((c ^ ((lane >> 1) & 3)) << 4), g + 8 * c);
-    fence_proxy_async_smem();
-    __syncwarp();
+    const uint32_t box = put_32x32(t, b, g);
     if (lane == 0) {
       tma_store_2d(&g_out, box, t.n + c0, row0);
       bulk_commit();
@@ -622,7 +634,7 @@ __device__ __forceinline__ void prob_tile(const HeadParams &p, const CUtensorMap
 __device__ __forceinline__ void sum_tile(const HeadParams &p, const CUtensorMap &acc_map,
                                          const HalfTile &t, int split, int row0) {
   const int lane = t.lane;
-  each_block<false>(t, [&](int, int c0, uint32_t (&acc)[32]) {
+  each_block(t, [&](int, int c0, uint32_t (&acc)[32]) {
     if (row0 >= p.cols_pad) return;
     box_is_free(lane);
 #pragma unroll
@@ -642,31 +654,26 @@ __device__ __forceinline__ void sum_tile(const HeadParams &p, const CUtensorMap 
   });
 }
 
-// dB: lanes are vocabulary entries, columns those of [W, V].
+// dB: lanes are vocabulary entries, columns those of [W, V].  Two boxes of 2 KB
+// in turn, as for PROB.
 __device__ __forceinline__ void weight_tile(const HeadParams &p, const HeadMaps &maps,
                                             const HalfTile &t, int row0) {
   const int lane = t.lane;
   const float scale = *p.rows.scale;
-  each_block<true>(t, [&](int b, int c0, uint32_t (&acc)[32]) {
-    const int half = (b & 1) * 32, col = t.n + c0 - half;
+  each_block(t, [&](int b, int c0, uint32_t (&acc)[32]) {
+    const int col = t.n + c0;
     const bool in_d = col < p.kd * HK;
     const int left = in_d ? p.d - col : p.rank - (col - p.kd * HK);
     if (left <= 0 || p.v0 + row0 >= p.vocab) return;
-    if (half == 0) box_is_free(lane);
     float g[32];
 #pragma unroll
     for (int e = 0; e < 32; ++e) g[e] = __uint_as_float(acc[e]) * scale;
-#pragma unroll
-    for (int c = 0; c < 4; ++c)
-      put4(t.box + lane * 128 + (((half / 8 + c) ^ (lane & 7)) << 4), g + 8 * c);
-    if (half == 0) return;
-    fence_proxy_async_smem();
-    __syncwarp();
+    const uint32_t box = put_32x32(t, b, g);
     if (lane == 0) {
       if (in_d)
-        tma_store_2d(&maps.dw, t.box, col, p.v0 + row0);
+        tma_store_2d(&maps.dw, box, col, p.v0 + row0);
       else
-        tma_store_2d(&maps.dv, t.box, col - p.kd * HK, p.v0 + row0);
+        tma_store_2d(&maps.dv, box, col - p.kd * HK, p.v0 + row0);
       bulk_commit();
     }
   });
@@ -675,6 +682,7 @@ __device__ __forceinline__ void weight_tile(const HeadParams &p, const HeadMaps 
 template <int KIND>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(H_THREADS, 1)
     head_gemm_kernel(const __grid_constant__ HeadMaps maps, const HeadParams p) {
+  constexpr int HALVES = KIND == kGrad ? 2 : 1;
   extern __shared__ uint8_t smem_raw[];
   const uint32_t raw_addr = smem_u32(smem_raw);
   uint8_t *smem = smem_raw + ((1024u - (raw_addr & 1023u)) & 1023u);
@@ -717,10 +725,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(H_THREADS, 1)
   const uint32_t tmem_base = *tmem_slot;
   const int n_valid = __shfl_sync(0xFFFFFFFFu, *p.rows.n_valid, 0);
   const HeadWork work = head_work<KIND>(p, n_valid, pair, pairs);
-  // a stage holds 128 rows and up to 128 columns of one half or of two
+  // a stage holds 128 rows and up to 128 columns of one half or of two, or 64
   const bool wide = work.width == HW || (KIND == kGrad && weight_width(n_valid) == HW);
-  const int stages = wide ? 4 : 6;
-  const int stage_bytes = wide ? 3 * H_OPERAND : 2 * H_OPERAND;
+  const bool few = KIND != kGrad && n_valid <= 128;
+  const int stages = wide ? 4 : few ? 8 : 6;
+  const int stage_bytes = H_RING / stages;
   HeadTile x;
 
   if (warp == 0) {
@@ -750,7 +759,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(H_THREADS, 1)
           // few and large copies, also of fewer rows: exact ones of 64, 32 and
           // 16 rows instead took up to 1.3 times as long
 #pragma unroll
-          for (int h = 0; h < 2; ++h)
+          for (int h = 0; h < HALVES; ++h)
             if (blocks[h])
               tma_load_2d_pair(one, sb + h * H_OPERAND, blocks[h] == 2 ? &maps.a_rows : &maps.a,
                                bar, kb * HK, col0[h]);
@@ -770,7 +779,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(H_THREADS, 1)
           }
           // G^T's columns: any 16 of them begin a block
 #pragma unroll
-          for (int h = 0; h < 2; ++h)
+          for (int h = 0; h < HALVES; ++h)
 #pragma unroll
             for (int j = 0; j < 2; ++j)
               if (j < blocks[h])
@@ -779,7 +788,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(H_THREADS, 1)
         } else {
           tma_load_2d_pair(one, sa, &maps.g_rows, bar, kb * HK, x.m + cta * 128);
 #pragma unroll
-          for (int h = 0; h < 2; ++h) {
+          for (int h = 0; h < HALVES; ++h) {
             if (mine[h] == 128) {
               tma_load_3d_pair(one, sb + h * H_OPERAND, &maps.a_wide, bar, 0, kb * HK,
                                col0[h] / 64);
@@ -854,7 +863,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(H_THREADS, 1)
             phase ^= 1u;
           }
         };
-        const bool two = x.cols[1] > 0;
+        const bool two = HALVES == 2 && x.cols[1] > 0;
         if (!acc_free(ig)) break;
         int kb = 0;
         if (two) {
@@ -899,26 +908,31 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(H_THREADS, 1)
     int ig = 0;
     bool ok = true;
     float2 *slot = nullptr;
+    int period = 0;  // the pair's tiles after which the same rows come again
     if (KIND == kLse) {
+      int g = pairs, r = work.nt;
+      while (r) {
+        const int m = g % r;
+        g = r;
+        r = m;
+      }
+      period = work.nt / g;
       // the running pairs of these 32 lanes' entries, one for a row of A; each
       // of the two warps has the rows that it will meet
       slot = p.partial + static_cast<int64_t>(blockIdx.x * 4 + q) * p.rows_pad;
       for (int i = 0; i < work.nt; ++i) {
         row_tile(n_valid, work.width, i, x);
-        for (int h = 0; h < 2; ++h)
+        for (int h = 0; h < HALVES; ++h)
           for (int c0 = part * 32; c0 < x.cols[h]; c0 += 64)
             slot[x.n + h * x.cols[0] + c0 + lane] = make_float2(-INFINITY, 0.0f);
       }
     }
     for (int i = 0; ok && head_tile<KIND>(p, work, n_valid, pair, pairs, i, x); ++i) {
       const int row0 = x.m + cta * 128 + q * 32;  // the warp's first output row
-      LseRows rows[2];
-      if (KIND == kLse) {
-        rows[0] = lse_rows(p, slot, x.n, x.cols[0], part, lane);
-        rows[1] = lse_rows(p, slot, x.n + x.cols[0], x.cols[1], part, lane);
-      }
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
+      LseRows rows;
+      if (KIND == kLse) rows = lse_rows(p, slot, i < period, x.n, x.cols[0], part, lane);
+#pragma unroll 1
+      for (int h = 0; h < HALVES; ++h) {
         if (x.cols[h] == 0) break;
         const int buf = ig & 1;
         if (x.nk > 0) {
@@ -938,7 +952,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(H_THREADS, 1)
         t.acc_empty = acc_empty0 + buf * 8;
         t.lane = lane;
         if (KIND == kLse)
-          lse_tile(p, t, p.v0 + row0, rows[h], slot);
+          lse_tile(p, t, p.v0 + row0, rows, slot);
         else if (KIND == kProb)
           prob_tile(p, maps.g_out, t, row0);
         else if (x.da)
@@ -962,55 +976,57 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(H_THREADS, 1)
 }
 
 // --------------------------------------------------------------- joining
-// Joins the (max, sum) pairs of a row: a warp reads 32 neighbouring rows of
-// one slot, 32 warps share the slots.
-constexpr int JOIN_WARPS = 32;
+// Joins the (max, sum) pairs of a row.  A CTA takes eight neighbouring rows (64
+// bytes of a slot), 128 slots at a time, in a fixed order.
+constexpr int JOIN_ROWS = 8;
+constexpr int JOIN_THREADS = 1024;
 
-__global__ void __launch_bounds__(JOIN_WARPS * 32)
+__device__ __forceinline__ float2 join_pairs(float2 a, float2 b) {
+  const float top = fmaxf(a.x, b.x);
+  const float ref = reference(top);
+  return make_float2(top, a.y * ex2(fmaf(a.x, kLog2e, -ref)) + b.y * ex2(fmaf(b.x, kLog2e, -ref)));
+}
+__device__ __forceinline__ float2 join_across(float2 a, int lanes) {
+  return join_pairs(a, make_float2(__shfl_xor_sync(0xFFFFFFFFu, a.x, lanes),
+                                   __shfl_xor_sync(0xFFFFFFFFu, a.y, lanes)));
+}
+
+__global__ void __launch_bounds__(JOIN_THREADS)
     head_join_kernel(const float2 *partial, int slots, int rows_pad, RowInfo rows,
                      float *loss, float *lse) {
+  __shared__ float2 part[JOIN_THREADS / 32][JOIN_ROWS];
   allow_next_kernel();
   wait_for_earlier_kernel();
-  __shared__ float2 part[JOIN_WARPS][33];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int row = blockIdx.x * 32 + lane;
+  const int row = blockIdx.x * JOIN_ROWS + (lane & 7);
   const int n_valid = *rows.n_valid;
-  if (blockIdx.x * 32 >= n_valid) return;
-  float m = -INFINITY, s = 0.0f;
-  constexpr int U = 8;
-  for (int v = warp; v < slots; v += JOIN_WARPS * U) {
+  if (blockIdx.x * JOIN_ROWS >= n_valid) return;
+  constexpr int U = 5;  // 608 slots at once
+  float2 run = make_float2(-INFINITY, 0.0f);
+  for (int v = warp * 4 + (lane >> 3); v < slots; v += 128 * U) {
     float2 x[U];
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-      const int at = v + u * JOIN_WARPS;
-      x[u] = at < slots && row < n_valid
-                 ? partial[static_cast<int64_t>(at) * rows_pad + row]
-                 : make_float2(-INFINITY, 0.0f);
+      const int at = v + u * 128;
+      x[u] = at < slots && row < n_valid ? partial[static_cast<int64_t>(at) * rows_pad + row]
+                                         : make_float2(-INFINITY, 0.0f);
     }
-    float top = m;
 #pragma unroll
-    for (int u = 0; u < U; ++u) top = fmaxf(top, x[u].x);
-    const float ref = top == -INFINITY ? 0.0f : top * kLog2e;
-    s *= ex2(fmaf(m, kLog2e, -ref));
-#pragma unroll
-    for (int u = 0; u < U; ++u) s += x[u].y * ex2(fmaf(x[u].x, kLog2e, -ref));
-    m = top;
+    for (int u = 0; u < U; ++u) run = join_pairs(run, x[u]);
   }
-  part[warp][lane] = make_float2(m, s);
+  run = join_across(join_across(run, 8), 16);
+  if (lane < JOIN_ROWS) part[warp][lane] = run;
   __syncthreads();
-  if (warp == 0) {
-    float top = -INFINITY;
-    for (int w = 0; w < JOIN_WARPS; ++w) top = fmaxf(top, part[w][lane].x);
-    const float ref = top == -INFINITY ? 0.0f : top * kLog2e;
-    float sum = 0.0f;
-    for (int w = 0; w < JOIN_WARPS; ++w)
-      sum += part[w][lane].y * ex2(fmaf(part[w][lane].x, kLog2e, -ref));
-    if (row < n_valid) {
-      const int i = rows.index[row];
-      const float l = fmaf(log2f(sum), kLn2, top);
-      lse[i] = l;
-      loss[i] = l - rows.z_target[row];
-    }
+  if (warp > 0) return;
+  run = part[(lane >> 3) * 8][lane & 7];
+#pragma unroll
+  for (int w = 1; w < 8; ++w) run = join_pairs(run, part[(lane >> 3) * 8 + w][lane & 7]);
+  run = join_across(join_across(run, 8), 16);
+  if (lane < JOIN_ROWS && row < n_valid) {
+    const int i = rows.index[row];
+    const float l = fmaf(log2f(run.y), kLn2, run.x);
+    lse[i] = l;
+    loss[i] = l - rows.z_target[row];
   }
 }
 
@@ -1031,12 +1047,15 @@ __global__ void __launch_bounds__(256)
   if (r0 >= n_valid) return;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const float scale = *rows.scale;
+  {
+    const float *x = acc + static_cast<int64_t>(c0 + warp) * rows_pad + r0 + lane;
+    float s[TURN_COLS / 8] = {};
+    for (int k = 0; k < splits; ++k, x += static_cast<int64_t>(cols_pad) * rows_pad) {
 #pragma unroll
-  for (int c = warp; c < TURN_COLS; c += 8) {
-    const float *x = acc + static_cast<int64_t>(c0 + c) * rows_pad + r0 + lane;
-    float s = 0.0f;
-    for (int k = 0; k < splits; ++k) s += x[static_cast<int64_t>(k) * cols_pad * rows_pad];
-    block[lane][c] = s * scale;
+      for (int j = 0; j < TURN_COLS / 8; ++j) s[j] += x[static_cast<int64_t>(j) * 8 * rows_pad];
+    }
+#pragma unroll
+    for (int j = 0; j < TURN_COLS / 8; ++j) block[lane][warp + j * 8] = s[j] * scale;
   }
   __syncthreads();
   const int r = threadIdx.x >> 3, c = (threadIdx.x & 7) * 8;
@@ -1174,6 +1193,7 @@ dspark_status head_plan(const HeadArgs &a, bool grad, HeadPlan &o) {
   }
   const HeadLayout &l = o.lay = head_layout(a.M, a.vocab, a.d, a.rank, grad);
   uint8_t *ws = a.workspace;
+  const auto bf16 = CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
   const int64_t vr = a.rank ? a.rank : a.d;
   const void *V = a.rank ? a.V : a.W;
   const void *A = ws + l.a, *G = ws + l.g;
@@ -1191,10 +1211,10 @@ dspark_status head_plan(const HeadArgs &a, bool grad, HeadPlan &o) {
          (!o.p.v_whole || encode_wide(&m.v_wide, V, vr, a.vocab)) &&
          encode_bf16(&m.g, G, l.rows_pad, l.piece, 64) &&
          encode_bf16(&m.g_rows, G, l.rows_pad, l.piece, 128) &&
-         encode_2d(&m.g_out, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, G, l.rows_pad, l.piece,
+         encode_2d(&m.g_out, bf16, 2, G, l.rows_pad, l.piece,
                    l.rows_pad, 32, 32) &&
-         encode_bf16(&m.dw, a.dW, a.d, a.vocab, 32) &&
-         encode_bf16(&m.dv, a.rank ? a.dV : a.dW, vr, a.vocab, 32) &&
+         encode_2d(&m.dw, bf16, 2, a.dW, a.d, a.vocab, a.d, 32, 32) &&
+         encode_2d(&m.dv, bf16, 2, a.rank ? a.dV : a.dW, vr, a.vocab, vr, 32, 32) &&
          encode_2d(&m.acc, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 4, ws + l.acc, l.rows_pad,
                    l.cols_pad * l.splits, l.rows_pad, 32, 32);
   }
@@ -1283,10 +1303,16 @@ HeadLayout head_layout(int32_t M, int32_t vocab, int32_t d, int32_t rank, bool g
     const int64_t most = std::max<int64_t>(4096, kPieceBytes / (2 * l.rows_pad) / HT * HT);
     const int64_t pieces = (v_pad + most - 1) / most;
     l.piece = up((v_pad + pieces - 1) / pieces, HT);
-    const int64_t tiles = (l.rows_pad + HW - 1) / HW * ((l.cols_pad + HT - 1) / HT);
-    const int64_t deep = l.piece / HK;  // 64-entry blocks of the reduction
+    // dA's reduction over the piece is split where a tile of it would take longer
+    // than a pair's share of all tiles (as in head_work, in 64-entry blocks of 256
+    // columns)
+    const int64_t nt = (l.rows_pad + HW - 1) / HW, dt = (l.cols_pad + HT - 1) / HT;
+    const double deep = static_cast<double>(l.piece) / HK;
+    const double t_da = deep * M / (static_cast<double>(HT) * nt);
+    const double t_db = (static_cast<double>(M) / HK + 3.0) * l.cols_pad / HT * l.piece / HT;
+    const double share = (static_cast<double>(nt * dt) * t_da + t_db) / kPairs;
     l.splits = static_cast<int32_t>(
-        std::max<int64_t>(1, std::min<int64_t>({kPairs / tiles, deep / 8, 16})));
+        std::max(1.0, std::min({std::ceil(t_da / (0.9 * share)), deep / 8.0, 16.0})));
     l.g = take(static_cast<size_t>(l.rows_pad) * l.piece * 2);
     l.acc = take(static_cast<size_t>(l.splits) * l.rows_pad * l.cols_pad * 4);
     l.de = take(static_cast<size_t>(l.rows_pad) * rank * 4);
@@ -1303,7 +1329,7 @@ dspark_status head_loss_launch(const HeadArgs &a, cudaStream_t stream) {
       launch_overlapped(head_pack_kernel<false>, o.pack_grid, PACK_THREADS, 0, stream, o.pack);
   if (e == cudaSuccess) e = head_gemm<kLse>(o, o.p, stream);
   if (e == cudaSuccess)
-    e = launch_overlapped(head_join_kernel, (a.M + 31) / 32, JOIN_WARPS * 32, 0, stream,
+    e = launch_overlapped(head_join_kernel, (a.M + JOIN_ROWS - 1) / JOIN_ROWS, JOIN_THREADS, 0, stream,
                           static_cast<const float2 *>(o.p.partial), head_pairs<kLse>(o, o.p) * 8,
                           o.p.rows_pad, o.p.rows, a.loss, a.lse);
   return e == cudaSuccess ? DSPARK_OK : DSPARK_ERR_CUDA;

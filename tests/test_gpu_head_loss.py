@@ -168,3 +168,202 @@ def _reference_cuda(c):
     for k, m in mags.items():
         tol[k] = 2.0 ** -8 * ref[k].abs() + rel * m
     return {k: v.cpu() for k, v in ref.items()}, {k: v.cpu() for k, v in tol.items()}
+
+
+# ------------------------------------------------- what goes wrong at edges
+def _mixed(seed=11):
+    x = make(300, 700, 72, 24, 0.3, seed=seed)
+    return x
+
+
+def test_ignored_rows_may_hold_anything():
+    """NaN, infinities and tokens out of range in rows without a target reach
+    no output."""
+    import torch
+    x = _mixed()
+    ref, tol = reference(x)
+    bad = (x["target"] < 0).nonzero()[:, 0]
+    x["h"][bad[0::3]] = float("nan")
+    x["h"][bad[1::3]] = float("inf")
+    x["prev"][bad[0::2]] = 1 << 30
+    x["target"][bad[0::2]] = -(1 << 31)
+    x["dloss"][bad] = float("nan")
+    got = run(x)
+    assert got["status"] == 0
+    check(got, ref, tol)
+    for k in ("loss", "lse", "dh"):
+        assert torch.all(got[k][bad] == 0)
+
+
+@pytest.mark.parametrize("M", [1, 300])
+def test_no_row_has_a_target(M):
+    import torch
+    x = make(M, 333, 64, 16, seed=5)
+    x["target"][:] = -1
+    x["h"][:] = float("nan")
+    got = run(x)
+    for k in ("loss", "lse", "dh", "dW", "dU", "dV"):
+        assert torch.all(got[k] == 0), k
+
+
+def test_tokens_out_of_range_are_flagged():
+    from speculative_decoding_draft_dspark_gb300 import dspark as D
+    x = _mixed(12)
+    ok = (x["target"] >= 0).nonzero()[:, 0]
+    x["prev"][ok[0]] = -5
+    x["prev"][ok[1]] = 700
+    ref, tol = reference(x)
+    got = run(x)
+    assert got["status"] == D.DEV_TOKEN_OOR
+    check(got, ref, tol)
+    x["prev"][ok[:2]] = 3
+    x["target"][ok[2]] = 700
+    x["dloss"][ok[2]] = 0.0
+    ref, tol = reference(x)
+    got = run(x)
+    assert got["status"] == D.DEV_TOKEN_OOR
+    check(got, ref, tol)
+    assert got["loss"][ok[2]] == 0
+
+
+def test_rows_apart_and_another_stream():
+    import torch
+    x = _mixed(13)
+    h = torch.full((300, 104), 5.0, dtype=torch.bfloat16, device="cuda")
+    dh = torch.full((300, 80), 3.0, dtype=torch.bfloat16, device="cuda")
+    h[:, 16:88] = x["h"].cuda()
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(s):
+        got = run(x, h=h[:, 16:88], dh=dh[:, :72])
+    ref, tol = reference(x)
+    check(got, ref, tol)
+    assert torch.all(dh[:, 72:] == 3.0)
+
+
+def test_rows_weigh_differently():
+    import torch
+    x = _mixed(14)
+    g = torch.Generator().manual_seed(1)
+    x["dloss"] = torch.randn(300, generator=g) * torch.exp2(torch.randint(-20, 4, (300,), generator=g).float())
+    x["dloss"][::7] = 0.0
+    ref, tol = reference(x)
+    check(run(x), ref, tol)
+    x["dloss"][:] = 0.0
+    got = run(x)
+    for k in ("dh", "dW", "dU", "dV"):
+        assert torch.all(got[k] == 0), k
+
+
+@pytest.mark.parametrize("tokens", [1, 3])
+def test_rows_share_a_token_and_runs_agree(tokens):
+    """dU sums the rows of a token; the same inputs give the same bits."""
+    import torch
+    x = make(900, 500, 64, 256, 0.1, seed=15)
+    x["prev"] = x["prev"] % tokens * 7
+    ref, tol = reference(x)
+    a, b = run(x), run(x)
+    check(a, ref, tol)
+    for k in ref:
+        assert torch.equal(a[k], b[k]), k
+
+
+def test_large_and_infinite_scores():
+    """Scores of thousands neither overflow nor lose the loss; an infinite or
+    NaN score stays in its own row."""
+    import torch
+    x = make(40, 600, 64, 0, seed=16, sd=600.0)
+    ref, tol = reference(x)
+    assert ref["lse"].abs().max() > 2000
+    got = run(x)
+    check(got, ref, tol, ["loss", "lse"])
+    x["h"][3, 0] = 1e38
+    x["W"][:, 0] = x["W"][:, 0].abs() + 10.0     # row 3: every score +infinity
+    x["h"][5, 1] = float("nan")
+    x["target"][7] = -1
+    x["h"][7] = float("nan")
+    ref, tol = reference(x)
+    got = run(x)
+    assert torch.isinf(got["lse"][3]) and got["lse"][3] > 0 and torch.isnan(got["loss"][3])
+    assert torch.isnan(got["lse"][5]) and torch.isnan(got["loss"][5])
+    rest = torch.ones(40, dtype=torch.bool)
+    rest[[3, 5]] = False
+    for k in ("loss", "lse"):
+        assert torch.all((got[k].double() - ref[k])[rest].abs() <= tol[k][rest])
+    for k in ("dh",):
+        keep = rest.clone()
+        assert torch.isfinite(got[k][keep]).all() and torch.isnan(got[k][5]).all()
+
+
+def test_gradient_against_differences():
+    """Central differences of the kernel's own loss along random sign patterns
+    of step 2^-6.  The factors are multiples of 2^-5 below 2, so that both sides
+    are exact in bf16.  Error: the third derivative (bounded by twice the cube
+    of the change of a score, |dz| <= step sum |other factor|) times step^2 / 6,
+    the loss's own error over the step, and the gradient's bound."""
+    import torch
+    from speculative_decoding_draft_dspark_gb300 import head as H
+    M, vocab, d, rank, step = 6, 90, 32, 16, 2.0 ** -6
+    g = torch.Generator().manual_seed(21)
+    grid = lambda *s: (torch.randint(-8, 9, s, generator=g).float() / 32).bfloat16()  # noqa: E731
+    x = {"h": grid(M, d), "W": grid(vocab, d), "U": grid(vocab, rank), "V": grid(vocab, rank),
+         "prev": torch.randint(0, vocab, (M,), generator=g, dtype=torch.int32),
+         "target": torch.randint(0, vocab, (M,), generator=g, dtype=torch.int32)}
+    x["target"][2] = -1
+    x["dloss"] = torch.randn(M, generator=g)
+    got = run(x)
+    ref, tol = reference(x)
+    weight = x["dloss"].double()
+
+    def objective(y):
+        o = run(y, grad=False)
+        return (o["loss"].double() * weight).sum().item()
+
+    for name, grad in (("h", "dh"), ("W", "dW"), ("U", "dU"), ("V", "dV")):
+        for _ in range(3):
+            sign = torch.randint(0, 2, x[name].shape, generator=g).float() * 2 - 1
+            hi, lo = dict(x), dict(x)
+            hi[name] = (x[name].float() + step * sign).bfloat16()
+            lo[name] = (x[name].float() - step * sign).bfloat16()
+            assert torch.equal(hi[name].float() - lo[name].float(), 2 * step * sign)
+            slope = (objective(hi) - objective(lo)) / (2 * step)
+            other = {"h": "W", "W": "h", "U": "V", "V": "U"}[name]
+            dz = x[other].double().abs().sum(1).max().item()       # change of a score by a unit step
+            err = (2 * (2 * dz) ** 3 * step ** 2 / 6 + tol["loss"].max().item() / step) * weight.abs().sum().item()
+            err += (tol[grad].double()).sum().item()
+            have = (got[grad].double() * sign.double()).sum().item()
+            assert abs(slope - have) <= err, (name, slope, have, err)
+            assert err < 0.5 * abs(ref[grad]).sum().item()          # the bound says something
+
+
+def test_captured_in_a_graph():
+    """Loss and gradient replayed from a CUDA graph follow the inputs."""
+    import torch
+    from speculative_decoding_draft_dspark_gb300 import head as H
+    a, b = _mixed(17), _mixed(18)
+    c = {k: v.cuda() for k, v in a.items()}
+    M, vocab, d, rank = 300, 700, 72, 24
+    new = lambda t: torch.empty_like(t)  # noqa: E731
+    o = {"loss": torch.empty(M, device="cuda"), "lse": torch.empty(M, device="cuda"), "dh": new(c["h"]),
+         "dW": new(c["W"]), "dU": new(c["U"]), "dV": new(c["V"])}
+    ws = H.new_workspace(H.dspark_head_workspace_size(M, vocab, d, rank, True))
+
+    def step():
+        H.dspark_head_loss(c["h"], c["W"], c["U"], c["V"], c["prev"], c["target"], o["loss"], o["lse"], ws)
+        H.dspark_head_loss_grad(c["h"], c["W"], c["U"], c["V"], c["prev"], c["target"], o["lse"], c["dloss"],
+                                o["dh"], o["dW"], o["dU"], o["dV"], ws)
+
+    s = torch.cuda.Stream()
+    with torch.cuda.stream(s):
+        step()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        step()
+    for x in (b, a):
+        for k in c:
+            c[k].copy_(x[k])
+        graph.replay()
+        torch.cuda.synchronize()
+        ref, tol = reference(x)
+        check({k: v.cpu() for k, v in o.items()}, ref, tol)

@@ -187,3 +187,195 @@ def test_dropout(M, d, name, p, pad, res):
     b = f8(residual) if res else np.zeros((M, d))
     dx = np.where(m, f8(x) * s, 0.0)
     assert np.all(np.abs(f8(y) - (b + dx)) <= 2 * U * (np.abs(b) + np.abs(dx)) + ub * np.abs(b + dx))
+
+
+# ------------------------------------------------- what goes wrong at edges
+@pytest.mark.parametrize("d", [264, 1003, 9000])
+def test_in_place(d):
+    """r may be the residual or x, dx dy and dresidual dr."""
+    import torch
+    from speculative_decoding_draft_dspark_gb300 import head as H
+    M = 9
+    x, res, r, y, dy, dr = tensors(M, d, torch.bfloat16, 6, d)
+    gain = torch.ones(d, dtype=torch.bfloat16, device="cuda")
+    kw = dict(p=0.3, seed=3, offset=4)
+    rstd = torch.zeros(M, device="cuda")
+    H.dspark_residual_norm(x, res, gain, r, y, None, rstd, eps=1e-5, **kw)
+    for which in ("residual", "x"):
+        x2, res2, y2 = x.clone(), res.clone(), torch.empty_like(y)
+        r2 = res2 if which == "residual" else x2
+        H.dspark_residual_norm(x2, res2, gain, r2, y2, None, None, eps=1e-5, **kw)
+        assert torch.equal(r2, r) and torch.equal(y2, y)
+    ws = H.new_workspace(H.dspark_norm_workspace_size(M, d))
+    dx, ds, dg = torch.empty_like(x), torch.empty_like(x), torch.empty_like(gain)
+    H.dspark_residual_norm_grad(dy, dr, r, gain, rstd, dx, ds, dg, ws, **kw)
+    a, b, g = dy.clone(), dr.clone(), torch.empty_like(gain)
+    H.dspark_residual_norm_grad(a, b, r, gain, rstd, a, b, g, ws, **kw)
+    assert torch.equal(a, dx) and torch.equal(b, ds) and torch.equal(g, dg)
+    z = x.clone()
+    H.dspark_dropout(x, res, y, **kw)
+    H.dspark_dropout(z, res, z, **kw)
+    assert torch.equal(z, y)
+
+
+@pytest.mark.parametrize("d", [256, 1003, 8200])
+@pytest.mark.parametrize("name", ["bf16", "f32"])
+def test_nan_and_infinity_stay_where_they_are(name, d):
+    """In its own row; nowhere where it is dropped."""
+    import torch
+    from speculative_decoding_draft_dspark_gb300 import head as H
+    dtype, _ = dtypes(name)
+    M, p, seed, offset = 6, 0.5, 77, 1
+    m, _ = kept(M, d, p, seed, offset)
+    x, res, r, y = tensors(M, d, dtype, 4, d)
+    gain = torch.ones(d, dtype=dtype, device="cuda")
+    lost, held = int(np.argmin(m[1])), int(np.argmax(m[4]))
+    x[1, lost] = float("nan")
+    x[2, int(np.argmin(m[2]))] = float("inf")
+    x[4, held] = float("nan")
+    for out in ("same", "row8", "group8"):
+        q = y if out == "same" else torch.empty(M, d, dtype=torch.float8_e4m3fn, device="cuda")
+        n = 1 if out == "row8" else -(-d // 128)
+        scale = torch.zeros(M, n, device="cuda")
+        H.dspark_residual_norm(x, res, gain, r, q, scale, None, eps=1e-5, group=128 if out == "group8" else 0,
+                               p=p, seed=seed, offset=offset)
+        bad = torch.isnan(q.float()).any(1).cpu().tolist()
+        assert bad == [False, False, False, False, True, False], out
+        assert torch.isnan(r.float()).sum() == 1 and torch.isinf(r.float()).sum() == 0
+    H.dspark_dropout(x, None, y, p=p, seed=seed, offset=offset)
+    f = y.float().cpu()
+    assert torch.isnan(f).sum() == 1 and torch.isnan(f[4, held])
+    assert torch.all(f[torch.from_numpy(~m)] == 0)
+
+
+@pytest.mark.parametrize("out", ["same", "row8", "group8"])
+def test_zero_rows_and_tiny_rows(out):
+    """A row of zeros gives zeros and scales of 1; a row whose largest value is
+    near fp32's smallest normals still uses the whole 8-bit range."""
+    import torch
+    from speculative_decoding_draft_dspark_gb300 import head as H
+    M, d = 3, 300
+    x = torch.zeros(M, d, device="cuda")
+    x[1] = torch.linspace(-1, 1, d, device="cuda")
+    gain = torch.full((d,), 1e-37, device="cuda")
+    gain[:128] = 1.0 if out == "same" else 1e-37
+    y = torch.empty(M, d, device="cuda") if out == "same" else \
+        torch.empty(M, d, dtype=torch.float8_e4m3fn, device="cuda")
+    n = 3 if out == "group8" else 1
+    scale = torch.zeros(M, n, device="cuda")
+    H.dspark_residual_norm(x, None, gain, None, y, scale, None, eps=1e-6, group=128 if out == "group8" else 0)
+    assert torch.all(y.float()[[0, 2]] == 0) and torch.isfinite(y.float()).all()
+    if out != "same":
+        assert torch.all(scale[[0, 2]] == 1.0)
+        assert y.float()[1].abs().max() == 448.0
+
+
+def test_optional_outputs_and_streams():
+    import torch
+    from speculative_decoding_draft_dspark_gb300 import head as H
+    M, d = 50, 520
+    x, res, r, y, dy = tensors(M, d, torch.float32, 5, 9)
+    gain = torch.rand(d, device="cuda") + 0.5
+    rstd = torch.zeros(M, device="cuda")
+    H.dspark_residual_norm(x, res, gain, r, y, None, rstd, eps=1e-5)
+    y2 = torch.empty_like(y)
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(s):
+        H.dspark_residual_norm(x, res, gain, None, y2, None, None, eps=1e-5)
+    s.synchronize()
+    assert torch.equal(y, y2)
+    ws = H.new_workspace(H.dspark_norm_workspace_size(M, d))
+    full = [torch.empty_like(x), torch.empty_like(x), torch.empty_like(gain)]
+    H.dspark_residual_norm_grad(dy, None, r, gain, rstd, *full, ws)
+    for i in range(3):
+        one = [None, None, None]
+        one[i] = torch.empty_like(full[i])
+        H.dspark_residual_norm_grad(dy, None, r, gain, rstd, *one, ws, stream=s)
+        s.synchronize()
+        assert torch.equal(one[i], full[i])
+
+
+def test_norm_gradient_against_differences():
+    """Central differences in 32 bits of sum(w y + v r) along random directions.
+    Step 2^-7 of values of order 1: truncation step^2 times a third derivative
+    of at most 30 sum |w gain| / d^(1/2), rounding 2^-20 of the sum's magnitude
+    over the step."""
+    import torch
+    from speculative_decoding_draft_dspark_gb300 import head as H
+    M, d, step = 4, 200, 2.0 ** -7
+    g = torch.Generator().manual_seed(2)
+    n = lambda *s: torch.randn(*s, generator=g).cuda()  # noqa: E731
+    x, res, gain, w, v = n(M, d), n(M, d), n(d), n(M, d), n(M, d)
+    kw = dict(p=0.2, seed=8, offset=2)
+    rstd, r, y = torch.zeros(M, device="cuda"), torch.empty_like(x), torch.empty_like(x)
+
+    def objective(x, res, gain):
+        H.dspark_residual_norm(x, res, gain, r, y, None, rstd, eps=1e-5, **kw)
+        return ((w.double() * y.double()).sum() + (v.double() * r.double()).sum()).item()
+
+    size = objective(x, res, gain)
+    size = ((w * y).abs().sum() + (v * r).abs().sum()).item()
+    dx, ds, dg = torch.empty_like(x), torch.empty_like(x), torch.empty_like(gain)
+    ws = H.new_workspace(H.dspark_norm_workspace_size(M, d))
+    H.dspark_residual_norm_grad(w, v, r, gain, rstd, dx, ds, dg, ws, **kw)
+    tol = 30 * step ** 2 * (w * gain).abs().sum().item() / d ** 0.5 + 2.0 ** -20 * size / step
+    for name, grad in (("x", dx), ("residual", ds), ("gain", dg)):
+        for _ in range(3):
+            u = n(*grad.shape)
+            u = u / u.norm()
+            at = {"x": x, "residual": res, "gain": gain}
+            hi, lo = dict(at), dict(at)
+            hi[name], lo[name] = at[name] + step * u, at[name] - step * u
+            slope = (objective(*hi.values()) - objective(*lo.values())) / (2 * step)
+            have = (grad.double() * u.double()).sum().item()
+            assert abs(slope - have) <= tol, (name, slope, have, tol)
+
+
+def test_rows_are_summed_in_a_fixed_order():
+    import torch
+    from speculative_decoding_draft_dspark_gb300 import head as H
+    for M, d in ((4000, 1000), (500, 2048), (300, 1001), (40, 20000)):
+        dy, dr, r = tensors(M, d, torch.bfloat16, 3, M)
+        gain = torch.ones(d, dtype=torch.bfloat16, device="cuda")
+        rstd = torch.rsqrt(r.float().square().mean(1) + 1e-6)
+        ws = H.new_workspace(H.dspark_norm_workspace_size(M, d))
+        out = []
+        for _ in range(3):
+            o = [torch.empty_like(r), torch.empty_like(r), torch.empty_like(gain)]
+            H.dspark_residual_norm_grad(dy, dr, r, gain, rstd, *o, ws)
+            out.append(o)
+        for o in out[1:]:
+            assert all(torch.equal(a, b) for a, b in zip(o, out[0]))
+
+
+def test_captured_in_a_graph():
+    import torch
+    from speculative_decoding_draft_dspark_gb300 import head as H
+    M, d = 30, 264
+    x, res, r, y = tensors(M, d, torch.bfloat16, 4, 1)
+    gain = torch.ones(d, dtype=torch.bfloat16, device="cuda")
+    rstd, dg = torch.zeros(M, device="cuda"), torch.empty_like(gain)
+    dx, ds = torch.empty_like(x), torch.empty_like(x)
+    ws = H.new_workspace(H.dspark_norm_workspace_size(M, d))
+    kw = dict(p=0.1, seed=5, offset=6)
+
+    def step():
+        H.dspark_residual_norm(x, res, gain, r, y, None, rstd, eps=1e-5, **kw)
+        H.dspark_residual_norm_grad(y, res, r, gain, rstd, dx, ds, dg, ws, **kw)
+        H.dspark_dropout(dx, ds, r, **kw)
+
+    s = torch.cuda.Stream()
+    with torch.cuda.stream(s):
+        step()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        step()
+    x.copy_(res * 0.5 + 1)
+    graph.replay()
+    torch.cuda.synchronize()
+    got = [t.clone() for t in (r, y, rstd, dx, ds, dg)]
+    step()
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(got, (r, y, rstd, dx, ds, dg)))
