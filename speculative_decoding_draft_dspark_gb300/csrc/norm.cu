@@ -275,14 +275,16 @@ __device__ __forceinline__ uint32_t e4m3x2(float lo, float hi) {
 constexpr float kE4m3Max = 448.0f;
 
 __device__ __forceinline__ float scale_of(float top) {
-  return top == 0.0f ? 1.0f : top / kE4m3Max;
+  return top == 0.0f ? 1.0f : top * (1.0f / kE4m3Max);
 }
 
-// q = y / scale.  The product with the reciprocal is within an ulp of it, and
-// e4m3 keeps 4 bits; where the reciprocal would overflow it divides.
+// y / scale, where e4m3 will keep 4 bits: a product with the reciprocal (an ulp
+// off, half the instructions of a division); where that would overflow, it
+// divides.
 __device__ __forceinline__ void over_scale(V8 &y, float scale) {
   if (scale > 1e-35f || scale != scale) {
-    const float inv = 1.0f / scale;
+    float inv;
+    asm("rcp.approx.f32 %0, %1;" : "=f"(inv) : "f"(scale));
     const uint64_t i2 = pair(inv, inv);
 #pragma unroll
     for (int i = 0; i < 4; ++i) y.p[i] = mul2(y.p[i], i2);
