@@ -49,12 +49,22 @@ __device__ __forceinline__ Philox4 drop_words(const DropArgs &d, int group, int 
 }
 
 // ----------------------------------------------------- eight columns a lane
-// A warp holds 256 columns of a row.  Aligned rows (VEC): lane l has columns
-// 8l .. 8l+7, one or two 16-byte accesses.  Other rows: lane l has columns l,
-// 32 + l, ..., 224 + l, so that every access of the warp is contiguous.
-template <bool VEC>
+// A warp holds 256 columns of a row, in one of three layouts for all tensors of
+// a call:
+//   kWide   rows at 16 bytes, d a multiple of 8: lane l has columns 8l .. 8l+7,
+//           one or two 16-byte accesses
+//   kPairs  bf16 rows at 4 bytes: columns 2l, 64 + 2l, 128 + 2l, 192 + 2l and
+//           their neighbours, four accesses (at 15360 x 2044 the norm takes 51 us,
+//           107 by single columns)
+//   kSingle anything: columns l, 32 + l, ..., 224 + l, eight accesses
+// Every access of the warp is to neighbouring words.
+enum Layout { kWide = 0, kPairs = 1, kSingle = 2 };
+
+template <int L>
 __device__ __forceinline__ int column(int base, int lane, int e) {
-  return VEC ? base + lane * 8 + e : base + e * 32 + lane;
+  return L == kWide    ? base + lane * 8 + e
+         : L == kPairs ? base + (e >> 1) * 64 + lane * 2 + (e & 1)
+                       : base + e * 32 + lane;
 }
 
 __device__ __forceinline__ float bf16_lo(uint32_t v) { return __uint_as_float(v << 16); }
@@ -116,9 +126,9 @@ struct Raw {
   uint32_t w[F32 ? 8 : 4];
 };
 
-template <bool F32, bool VEC>
+template <bool F32, int L>
 __device__ __forceinline__ void load8(const void *row, int base, int lane, int d, Raw<F32> &r) {
-  if (VEC) {
+  if (L == kWide) {
     const int c = base + lane * 8;
     if (c < d) {
       const uint4 *p = reinterpret_cast<const uint4 *>(static_cast<const uint8_t *>(row) +
@@ -135,12 +145,18 @@ __device__ __forceinline__ void load8(const void *row, int base, int lane, int d
 #pragma unroll
       for (int j = 0; j < (F32 ? 8 : 4); ++j) r.w[j] = 0u;
     }
+  } else if (L == kPairs) {  // d is even
+#pragma unroll
+    for (int e = 0; e < 8; e += 2) {
+      const int c = column<L>(base, lane, e);
+      r.w[e / 2] = c < d ? static_cast<const uint32_t *>(row)[c / 2] : 0u;
+    }
   } else {
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
-      const int c = base + e * 32 + lane;
+      const int c = column<L>(base, lane, e);
       if (F32) {
-        r.w[e] = c < d ? static_cast<const uint32_t *>(row)[c] : 0u;
+        r.w[F32 ? e : 0] = c < d ? static_cast<const uint32_t *>(row)[c] : 0u;
       } else {
         const uint32_t v = c < d ? static_cast<const uint16_t *>(row)[c] : 0u;
         if (e & 1)
@@ -162,11 +178,11 @@ __device__ __forceinline__ V8 unpack8(const Raw<F32> &r) {
   return v;
 }
 
-template <bool F32, bool VEC>
+template <bool F32, int L>
 __device__ __forceinline__ void store8(void *row, int base, int lane, int d, const V8 &x) {
   float v[8];
   split8(x, v);
-  if (VEC) {
+  if (L == kWide) {
     const int c = base + lane * 8;
     if (c >= d) return;
     uint4 *p = reinterpret_cast<uint4 *>(static_cast<uint8_t *>(row) +
@@ -180,10 +196,16 @@ __device__ __forceinline__ void store8(void *row, int base, int lane, int d, con
       p[0] = make_uint4(pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]), pack_bf16(v[4], v[5]),
                         pack_bf16(v[6], v[7]));
     }
+  } else if (L == kPairs) {
+#pragma unroll
+    for (int e = 0; e < 8; e += 2) {
+      const int c = column<L>(base, lane, e);
+      if (c < d) static_cast<uint32_t *>(row)[c / 2] = pack_bf16(v[e], v[e + 1]);
+    }
   } else {
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
-      const int c = base + e * 32 + lane;
+      const int c = column<L>(base, lane, e);
       if (c < d) {
         if (F32)
           static_cast<float *>(row)[c] = v[e];
@@ -194,29 +216,50 @@ __device__ __forceinline__ void store8(void *row, int base, int lane, int d, con
   }
 }
 
+__device__ __forceinline__ uint32_t pick(bool c, uint32_t a, uint32_t b) { return c ? a : b; }
+
 // The Philox words of a lane's eight columns, two 16-bit lanes each.
-template <bool VEC>
+template <int L>
 __device__ __forceinline__ Philox4 drop8_words(const DropArgs &dr, int base, int lane, int row) {
-  Philox4 p = drop_words(dr, base / 8 + lane, row);
-  if (!VEC) {
-    // lane l drew the words of columns 8l .. 8l+7; column 32e + l is lane
-    // (l % 8) of group 4e + l / 8
-    Philox4 q = {};
+  const Philox4 p = drop_words(dr, base / 8 + lane, row);
+  if (L == kWide) return p;
+  // Lane g drew the four words of columns 8g .. 8g+7.
+  const int t = lane >> 3;
+  uint32_t a[4], b[4], q[4];
+  if (L == kPairs) {
+    // Pair i of lane l wants word l % 4 of lane 8i + l / 4.  In step s, lane l
+    // asks for its pair (s + l) % 4, so that lane g is asked for one word only,
+    // (g / 8 - s) % 4: four shuffles between a rotation before and one after.
 #pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      const int src = 4 * e + (lane >> 3);
-      const uint32_t a = __shfl_sync(0xFFFFFFFFu, p.w[0], src);
-      const uint32_t b = __shfl_sync(0xFFFFFFFFu, p.w[1], src);
-      const uint32_t c = __shfl_sync(0xFFFFFFFFu, p.w[2], src);
-      const uint32_t f = __shfl_sync(0xFFFFFFFFu, p.w[3], src);
-      const uint32_t lo = lane & 2 ? b : a, hi = lane & 2 ? f : c;
-      const uint32_t w = lane & 4 ? hi : lo;
-      const uint32_t half = lane & 1 ? w >> 16 : w & 0xFFFFu;
-      q.w[e >> 1] |= half << (16 * (e & 1));
-    }
-    p = q;
+    for (int j = 0; j < 4; ++j) a[j] = pick(t & 2, p.w[(j + 2) & 3], p.w[j]);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) b[j] = pick(t & 1, a[(j + 1) & 3], a[j]);  // word (j + t) % 4
+#pragma unroll
+    for (int s = 0; s < 4; ++s)
+      a[s] = __shfl_sync(0xFFFFFFFFu, b[(4 - s) & 3], ((s + lane) & 3) * 8 + (lane >> 2));
+    // a[s] is pair (s + lane) % 4
+#pragma unroll
+    for (int j = 0; j < 4; ++j) b[j] = pick(lane & 2, a[(j + 2) & 3], a[j]);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) q[j] = pick(lane & 1, b[(j + 3) & 3], b[j]);
+    return {{q[0], q[1], q[2], q[3]}};
   }
-  return p;
+  // column e of lane l wants the 16 bits l % 8 of lane 4e + l / 8
+#pragma unroll
+  for (int e = 0; e < 8; ++e) {
+    const int src = 4 * e + (lane >> 3);
+    const uint32_t w0 = __shfl_sync(0xFFFFFFFFu, p.w[0], src);
+    const uint32_t w1 = __shfl_sync(0xFFFFFFFFu, p.w[1], src);
+    const uint32_t w2 = __shfl_sync(0xFFFFFFFFu, p.w[2], src);
+    const uint32_t w3 = __shfl_sync(0xFFFFFFFFu, p.w[3], src);
+    const uint32_t w = pick(lane & 4, pick(lane & 2, w3, w2), pick(lane & 2, w1, w0));
+    const uint32_t half = lane & 1 ? w >> 16 : w & 0xFFFFu;
+    if (e & 1)
+      q[e / 2] |= half << 16;
+    else
+      q[e / 2] = half;
+  }
+  return {{q[0], q[1], q[2], q[3]}};
 }
 
 // dropout(x); a select, so that what a dropped element holds (NaN, infinity)
@@ -297,20 +340,27 @@ __device__ __forceinline__ void over_scale(V8 &y, float scale) {
   }
 }
 
-template <bool VEC>
+template <int L>
 __device__ __forceinline__ void store8_e4m3(uint8_t *row, int base, int lane, int d,
                                             const V8 &x) {
   float q[8];
   split8(x, q);
-  if (VEC) {
+  if (L == kWide) {
     const int c = base + lane * 8;
     if (c >= d) return;
     *reinterpret_cast<uint2 *>(row + c) = make_uint2(e4m3x2(q[0], q[1]) | e4m3x2(q[2], q[3]) << 16,
                                                      e4m3x2(q[4], q[5]) | e4m3x2(q[6], q[7]) << 16);
+  } else if (L == kPairs) {
+#pragma unroll
+    for (int e = 0; e < 8; e += 2) {
+      const int c = column<L>(base, lane, e);
+      if (c < d)
+        *reinterpret_cast<uint16_t *>(row + c) = static_cast<uint16_t>(e4m3x2(q[e], q[e + 1]));
+    }
   } else {
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
-      const int c = base + e * 32 + lane;
+      const int c = column<L>(base, lane, e);
       if (c < d) row[c] = static_cast<uint8_t>(e4m3x2(q[e], 0.0f) & 0xFFu);
     }
   }
@@ -318,7 +368,7 @@ __device__ __forceinline__ void store8_e4m3(uint8_t *row, int base, int lane, in
 
 // y -> y / scale with a scale for 128 columns: 16 lanes if a lane's columns are
 // neighbours, else the warp's first or last four
-template <bool VEC>
+template <int L>
 __device__ __forceinline__ void by_groups(const NormArgs &a, int64_t row, int base, int lane,
                                           V8 &y) {
   float v[8];
@@ -328,7 +378,7 @@ __device__ __forceinline__ void by_groups(const NormArgs &a, int64_t row, int ba
   for (int e = 0; e < 4; ++e) t0 = fmax_nan(t0, fabsf(v[e]));
 #pragma unroll
   for (int e = 4; e < 8; ++e) t1 = fmax_nan(t1, fabsf(v[e]));
-  if (VEC) {
+  if (L == kWide) {
     t0 = fmax_nan(t0, t1);
 #pragma unroll
     for (int o = 8; o; o >>= 1) t0 = fmax_nan(t0, __shfl_xor_sync(0xFFFFFFFFu, t0, o));
@@ -363,11 +413,11 @@ __device__ __forceinline__ void squares8(const V8 &r, uint64_t &sum) {
 }
 
 // r rstd gain
-template <bool F32, bool VEC>
+template <bool F32, int L>
 __device__ __forceinline__ V8 times_gain(const void *gain, float rstd, int base, int lane, int d,
                                          const V8 &r) {
   Raw<F32> raw;
-  load8<F32, VEC>(gain, base, lane, d, raw);
+  load8<F32, L>(gain, base, lane, d, raw);
   const V8 g = unpack8<F32>(raw);
   const uint64_t s = pair(rstd, rstd);
   V8 y;
@@ -379,7 +429,7 @@ __device__ __forceinline__ V8 times_gain(const void *gain, float rstd, int base,
 // ---------------------------------------------------------------- forward
 // `warps` warps hold a row, NV x 256 columns each (chunk i of a warp starts at
 // column 256 (i warps + w)); a CTA has as many rows as fit.
-template <bool F32, bool VEC, int NV>
+template <bool F32, int L, int NV>
 __global__ void __launch_bounds__(256) norm_kernel(const NormArgs a, int warps) {
   allow_next_kernel();
   wait_for_earlier_kernel();
@@ -398,17 +448,17 @@ __global__ void __launch_bounds__(256) norm_kernel(const NormArgs a, int warps) 
   if (live) {
     Raw<F32> rx[NV], rr[NV];
 #pragma unroll
-    for (int i = 0; i < NV; ++i) load8<F32, VEC>(x, (i * warps + w) * 256, lane, a.d, rx[i]);
+    for (int i = 0; i < NV; ++i) load8<F32, L>(x, (i * warps + w) * 256, lane, a.d, rx[i]);
     if (a.residual) {
 #pragma unroll
-      for (int i = 0; i < NV; ++i) load8<F32, VEC>(res, (i * warps + w) * 256, lane, a.d, rr[i]);
+      for (int i = 0; i < NV; ++i) load8<F32, L>(res, (i * warps + w) * 256, lane, a.d, rr[i]);
     }
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
       r[i] = unpack8<F32>(rx[i]);
       if (a.drop.on)
         r[i] = drop8(a.drop,
-                     drop8_words<VEC>(a.drop, (i * warps + w) * 256, lane, static_cast<int>(row)), r[i]);
+                     drop8_words<L>(a.drop, (i * warps + w) * 256, lane, static_cast<int>(row)), r[i]);
       if (a.residual) {
         const V8 t = unpack8<F32>(rr[i]);
 #pragma unroll
@@ -429,15 +479,15 @@ __global__ void __launch_bounds__(256) norm_kernel(const NormArgs a, int warps) 
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
       const int base = (i * warps + w) * 256;
-      if (a.r) store8<F32, VEC>(ro, base, lane, a.d, r[i]);
-      r[i] = times_gain<F32, VEC>(a.gain, rstd, base, lane, a.d, r[i]);
+      if (a.r) store8<F32, L>(ro, base, lane, a.d, r[i]);
+      r[i] = times_gain<F32, L>(a.gain, rstd, base, lane, a.d, r[i]);
       if (!a.e4m3) {
-        store8<F32, VEC>(yo, base, lane, a.d, r[i]);
+        store8<F32, L>(yo, base, lane, a.d, r[i]);
       } else if (a.group == 0) {
         top = top8(top, r[i]);
       } else {
-        by_groups<VEC>(a, row, base, lane, r[i]);
-        store8_e4m3<VEC>(yo, base, lane, a.d, r[i]);
+        by_groups<L>(a, row, base, lane, r[i]);
+        store8_e4m3<L>(yo, base, lane, a.d, r[i]);
       }
     }
   }
@@ -449,7 +499,7 @@ __global__ void __launch_bounds__(256) norm_kernel(const NormArgs a, int warps) 
 #pragma unroll
       for (int i = 0; i < NV; ++i) {
         over_scale(r[i], s);
-        store8_e4m3<VEC>(yo, (i * warps + w) * 256, lane, a.d, r[i]);
+        store8_e4m3<L>(yo, (i * warps + w) * 256, lane, a.d, r[i]);
       }
     }
   }
@@ -459,14 +509,14 @@ __global__ void __launch_bounds__(256) norm_kernel(const NormArgs a, int warps) 
 // every use of it.
 constexpr int WIDE_WARPS = 16;
 
-template <bool F32, bool VEC>
+template <bool F32, int L>
 __device__ __forceinline__ V8 stream8(const NormArgs &a, const uint8_t *x, const uint8_t *res,
                                       int64_t row, int base, int lane) {
   Raw<F32> rx, rr;
-  load8<F32, VEC>(x, base, lane, a.d, rx);
-  if (a.residual) load8<F32, VEC>(res, base, lane, a.d, rr);
+  load8<F32, L>(x, base, lane, a.d, rx);
+  if (a.residual) load8<F32, L>(res, base, lane, a.d, rr);
   V8 r = unpack8<F32>(rx);
-  if (a.drop.on) r = drop8(a.drop, drop8_words<VEC>(a.drop, base, lane, static_cast<int>(row)), r);
+  if (a.drop.on) r = drop8(a.drop, drop8_words<L>(a.drop, base, lane, static_cast<int>(row)), r);
   if (a.residual) {
     const V8 t = unpack8<F32>(rr);
 #pragma unroll
@@ -475,7 +525,7 @@ __device__ __forceinline__ V8 stream8(const NormArgs &a, const uint8_t *x, const
   return r;
 }
 
-template <bool F32, bool VEC>
+template <bool F32, int L>
 __global__ void __launch_bounds__(WIDE_WARPS * 32) norm_wide_kernel(const NormArgs a) {
   allow_next_kernel();
   wait_for_earlier_kernel();
@@ -487,7 +537,7 @@ __global__ void __launch_bounds__(WIDE_WARPS * 32) norm_wide_kernel(const NormAr
   const uint8_t *res = static_cast<const uint8_t *>(a.residual) + row * a.residual_stride * E;
   uint64_t sum2 = 0;
   for (int base = w * 256; base < a.d; base += WIDE_WARPS * 256)
-    squares8(stream8<F32, VEC>(a, x, res, row, base, lane), sum2);
+    squares8(stream8<F32, L>(a, x, res, row, base, lane), sum2);
   float lo, hi;
   halves(sum2, lo, hi);
   const float sum = row_sum(lo + hi, slots[0], w, WIDE_WARPS, lane);
@@ -497,8 +547,8 @@ __global__ void __launch_bounds__(WIDE_WARPS * 32) norm_wide_kernel(const NormAr
   if (a.e4m3 && a.group == 0) {
     float top = 0.0f;
     for (int base = w * 256; base < a.d; base += WIDE_WARPS * 256) {
-      const V8 r = stream8<F32, VEC>(a, x, res, row, base, lane);
-      top = top8(top, times_gain<F32, VEC>(a.gain, rstd, base, lane, a.d, r));
+      const V8 r = stream8<F32, L>(a, x, res, row, base, lane);
+      top = top8(top, times_gain<F32, L>(a.gain, rstd, base, lane, a.d, r));
     }
     s = scale_of(row_max_nan(top, slots[1], w, WIDE_WARPS, lane));
     if (threadIdx.x == 0) a.scale[row] = s;
@@ -506,18 +556,18 @@ __global__ void __launch_bounds__(WIDE_WARPS * 32) norm_wide_kernel(const NormAr
   uint8_t *ro = static_cast<uint8_t *>(a.r) + row * a.r_stride * E;
   uint8_t *yo = static_cast<uint8_t *>(a.y) + row * a.y_stride * (a.e4m3 ? 1 : E);
   for (int base = w * 256; base < a.d; base += WIDE_WARPS * 256) {
-    const V8 r = stream8<F32, VEC>(a, x, res, row, base, lane);
-    if (a.r) store8<F32, VEC>(ro, base, lane, a.d, r);
-    V8 y = times_gain<F32, VEC>(a.gain, rstd, base, lane, a.d, r);
+    const V8 r = stream8<F32, L>(a, x, res, row, base, lane);
+    if (a.r) store8<F32, L>(ro, base, lane, a.d, r);
+    V8 y = times_gain<F32, L>(a.gain, rstd, base, lane, a.d, r);
     if (!a.e4m3) {
-      store8<F32, VEC>(yo, base, lane, a.d, y);
+      store8<F32, L>(yo, base, lane, a.d, y);
       continue;
     }
     if (a.group == 0)
       over_scale(y, s);
     else
-      by_groups<VEC>(a, row, base, lane, y);
-    store8_e4m3<VEC>(yo, base, lane, a.d, y);
+      by_groups<L>(a, row, base, lane, y);
+    store8_e4m3<L>(yo, base, lane, a.d, y);
   }
 }
 
@@ -532,14 +582,14 @@ struct GradRow {
   float rstd;
 };
 
-template <bool F32, bool VEC>
+template <bool F32, int L>
 __device__ __forceinline__ void load_row(const NormGradArgs &a, int64_t row, int base, int lane,
                                          GradRow<F32> &x) {
   constexpr int E = F32 ? 4 : 2;
-  load8<F32, VEC>(static_cast<const uint8_t *>(a.dy) + row * a.dy_stride * E, base, lane, a.d, x.dy);
-  load8<F32, VEC>(static_cast<const uint8_t *>(a.r) + row * a.r_stride * E, base, lane, a.d, x.r);
+  load8<F32, L>(static_cast<const uint8_t *>(a.dy) + row * a.dy_stride * E, base, lane, a.d, x.dy);
+  load8<F32, L>(static_cast<const uint8_t *>(a.r) + row * a.r_stride * E, base, lane, a.d, x.r);
   if (a.dr)
-    load8<F32, VEC>(static_cast<const uint8_t *>(a.dr) + row * a.dr_stride * E, base, lane, a.d,
+    load8<F32, L>(static_cast<const uint8_t *>(a.dr) + row * a.dr_stride * E, base, lane, a.d,
                     x.dr);
   x.rstd = a.rstd[row];
 }
@@ -593,23 +643,23 @@ __device__ __forceinline__ V8 grad_sum(const Raw<F32> *dr, const GradHalf &h, fl
   return o;
 }
 
-template <bool F32, bool VEC>
+template <bool F32, int L>
 __device__ __forceinline__ void grad_out(const NormGradArgs &a, int64_t row, int base, int lane,
                                          const GradRow<F32> &x, const GradHalf &h, float mean,
                                          const Philox4 &words) {
   constexpr int E = F32 ? 4 : 2;
   V8 o = grad_sum<F32>(a.dr ? &x.dr : nullptr, h, x.rstd, mean);
   if (a.dresidual)
-    store8<F32, VEC>(static_cast<uint8_t *>(a.dresidual) + row * a.dresidual_stride * E, base, lane,
+    store8<F32, L>(static_cast<uint8_t *>(a.dresidual) + row * a.dresidual_stride * E, base, lane,
                      a.d, o);
   if (a.dx) {
     if (a.drop.on) o = drop8(a.drop, words, o);
-    store8<F32, VEC>(static_cast<uint8_t *>(a.dx) + row * a.dx_stride * E, base, lane, a.d, o);
+    store8<F32, L>(static_cast<uint8_t *>(a.dx) + row * a.dx_stride * E, base, lane, a.d, o);
   }
 }
 
 // a CTA's line of dgain: the row groups' sums, joined in order
-template <bool VEC>
+template <int L>
 __device__ __forceinline__ void write_line(const NormGradArgs &a, float *lines, int group,
                                            int groups, int base, int lane, const V8 &dg) {
   float *line = a.partial + static_cast<int64_t>(blockIdx.x) * a.d;
@@ -619,7 +669,7 @@ __device__ __forceinline__ void write_line(const NormGradArgs &a, float *lines, 
     if (group == k) {
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
-        const int c = column<VEC>(base, lane, e);
+        const int c = column<L>(base, lane, e);
         if (c < a.d) {
           if (groups == 1)
             line[c] = sums[e];
@@ -636,15 +686,18 @@ __device__ __forceinline__ void write_line(const NormGradArgs &a, float *lines, 
   }
 }
 
-// Aligned rows, NV chunks a warp.  Every thread copies its own columns of the
-// next rows into shared memory, `ahead` rows before it reads them, and no other
+// Aligned bf16 rows, NV chunks a warp.  Every thread copies its own columns of the
+// next rows into shared memory, two rows before it reads them, and no other
 // thread's: the copies need no barrier and hold no registers.
-template <bool F32, int NV>
+constexpr int kAhead = 2;
+
+template <int NV>
 __global__ void __launch_bounds__(NV == 1 ? 1024 : 512)
-    norm_grad_kernel(const NormGradArgs a, int warps, int ahead) {
+    norm_grad_kernel(const NormGradArgs a, int warps) {
   __shared__ float slots[2][32];
   extern __shared__ __align__(16) uint8_t dyn[];
-  constexpr int E = F32 ? 4 : 2, PARTS = F32 ? 2 : 1;  // 16-byte parts of eight columns
+  constexpr bool F32 = false;
+  constexpr int E = 2;
   wait_for_earlier_kernel();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int group = warp / warps, w = warp - group * warps;
@@ -665,37 +718,31 @@ __global__ void __launch_bounds__(NV == 1 ? 1024 : 512)
           *ds = const_cast<uint8_t *>(at(a.dresidual, a.dresidual_stride));
   const int64_t dx_step = step * a.dx_stride * E, ds_step = step * a.dresidual_stride * E;
 
-  // a stage: dy, r and dr, each NV x PARTS parts of 16 bytes a thread, and rstd
-  const uint32_t part = blockDim.x * 16, tensor = NV * PARTS * part;
+  // a stage: dy, r and dr, each NV parts of 16 bytes a thread, and rstd
+  const uint32_t part = blockDim.x * 16, tensor = NV * part;
   const uint32_t stage = 3 * tensor + part / 4;
   const uint32_t mine = smem_u32(dyn) + threadIdx.x * 16;
   const uint32_t rstd_at = 3 * tensor - threadIdx.x * 12;
   uint32_t fill = mine, use = mine;
-  const uint32_t end = mine + (ahead + 1) * stage;
+  const uint32_t end = mine + (kAhead + 1) * stage;
   int fill_row = row;
   // the gain's columns, behind the stages
 #pragma unroll
   for (int i = 0; i < NV; ++i) {
-    if (c + i * chunk < a.d) {
-#pragma unroll
-      for (int j = 0; j < PARTS; ++j)
-        cp_async_16(end + (i * PARTS + j) * part, static_cast<const uint8_t *>(a.gain) +
-                                                      static_cast<size_t>(c + i * chunk) * E + j * 16);
-    }
+    if (c + i * chunk < a.d)
+      cp_async_16(end + i * part,
+                  static_cast<const uint8_t *>(a.gain) + static_cast<size_t>(c + i * chunk) * E);
   }
   auto copy_row = [&] {
     if (fill_row < a.M) {
 #pragma unroll
       for (int i = 0; i < NV; ++i) {
         if (c + i * chunk < a.d) {
-#pragma unroll
-          for (int j = 0; j < PARTS; ++j) {
-            const uint32_t to = fill + (i * PARTS + j) * part;
-            const int from = i * chunk * E + j * 16;
-            cp_async_16(to, dy + from);
-            cp_async_16(to + tensor, r + from);
-            if (a.dr) cp_async_16(to + 2 * tensor, dr + from);
-          }
+          const uint32_t to = fill + i * part;
+          const int from = i * chunk * E;
+          cp_async_16(to, dy + from);
+          cp_async_16(to + tensor, r + from);
+          if (a.dr) cp_async_16(to + 2 * tensor, dr + from);
         }
       }
       cp_async_4(fill + rstd_at, a.rstd + fill_row);
@@ -709,23 +756,17 @@ __global__ void __launch_bounds__(NV == 1 ? 1024 : 512)
     if (fill == end) fill = mine;
   };
   auto get = [&](uint32_t from, Raw<F32> &x) {
-#pragma unroll
-    for (int j = 0; j < PARTS; ++j) {
-      const uint4 v = ld_shared_v4(from + j * part);
-      x.w[4 * j] = v.x;
-      x.w[4 * j + 1] = v.y;
-      x.w[4 * j + 2] = v.z;
-      x.w[4 * j + 3] = v.w;
-    }
+    const uint4 v = ld_shared_v4(from);
+    x.w[0] = v.x;
+    x.w[1] = v.y;
+    x.w[2] = v.z;
+    x.w[3] = v.w;
   };
-  for (int i = 0; i < ahead; ++i) copy_row();
+  for (int i = 0; i < kAhead; ++i) copy_row();
 
   for (int k = 0; k < rounds; ++k, row += step) {
     copy_row();
-    if (ahead == 2)
-      cp_async_wait<2>();
-    else
-      cp_async_wait<1>();
+    cp_async_wait<kAhead>();
     const bool live = row < a.M;
     uint64_t dot2 = 0;
     float rstd = 0.0f;
@@ -738,9 +779,9 @@ __global__ void __launch_bounds__(NV == 1 ? 1024 : 512)
           GradRow<F32> x;
           Raw<F32> g;
           x.rstd = rstd;
-          get(use + i * PARTS * part, x.dy);
-          get(use + tensor + i * PARTS * part, x.r);
-          get(end + i * PARTS * part, g);
+          get(use + i * part, x.dy);
+          get(use + tensor + i * part, x.r);
+          get(end + i * part, g);
           h[i] = grad_dot<F32>(x, g, dg[i], dot2);
         }
       }
@@ -760,13 +801,13 @@ __global__ void __launch_bounds__(NV == 1 ? 1024 : 512)
       for (int i = 0; i < NV; ++i) {
         if (c + i * chunk < a.d) {
           Raw<F32> t;
-          if (a.dr) get(use + 2 * tensor + i * PARTS * part, t);
+          if (a.dr) get(use + 2 * tensor + i * part, t);
           V8 o = grad_sum<F32>(a.dr ? &t : nullptr, h[i], rstd, mean);
           // (column 0 of a row that begins at these columns)
-          if (a.dresidual) store8<F32, true>(ds + i * chunk * E, -lane * 8, lane, 1, o);
+          if (a.dresidual) store8<F32, kWide>(ds + i * chunk * E, -lane * 8, lane, 1, o);
           if (a.dx) {
             if (a.drop.on) o = drop8(a.drop, words[i], o);
-            store8<F32, true>(dx + i * chunk * E, -lane * 8, lane, 1, o);
+            store8<F32, kWide>(dx + i * chunk * E, -lane * 8, lane, 1, o);
           }
         }
       }
@@ -783,13 +824,14 @@ __global__ void __launch_bounds__(NV == 1 ? 1024 : 512)
   __syncthreads();
 #pragma unroll
   for (int i = 0; i < NV; ++i)
-    write_line<true>(a, reinterpret_cast<float *>(dyn), group, groups, w * 256 + i * chunk, lane,
+    write_line<kWide>(a, reinterpret_cast<float *>(dyn), group, groups, w * 256 + i * chunk, lane,
                      dg[i]);
 }
 
-// Rows of any alignment: the next row's lines are sent to L2 instead.
-template <bool F32>
-__global__ void __launch_bounds__(1024) norm_grad_odd_kernel(const NormGradArgs a, int warps) {
+// Other rows: the next row's lines are sent to L2 instead.  (fp32 rows too: copied
+// ahead, with two chunks a warp, 7680 x 2048 of them took 102 us instead of 57.)
+template <bool F32, int L>
+__global__ void __launch_bounds__(1024) norm_grad_direct_kernel(const NormGradArgs a, int warps) {
   __shared__ float slots[2][32];
   extern __shared__ __align__(16) uint8_t dyn[];
   allow_next_kernel();
@@ -800,7 +842,7 @@ __global__ void __launch_bounds__(1024) norm_grad_odd_kernel(const NormGradArgs 
   const int base = w * 256;
   V8 dg = {};
   Raw<F32> g;
-  load8<F32, false>(a.gain, base, lane, a.d, g);
+  load8<F32, L>(a.gain, base, lane, a.d, g);
   const int64_t step = static_cast<int64_t>(gridDim.x) * groups;
   int turn = 0;
   for (int64_t r0 = static_cast<int64_t>(blockIdx.x) * groups; r0 < a.M; r0 += step, turn ^= 1) {
@@ -810,24 +852,24 @@ __global__ void __launch_bounds__(1024) norm_grad_odd_kernel(const NormGradArgs 
     GradHalf h;
     GradRow<F32> x;
     if (live) {
-      load_row<F32, false>(a, row, base, lane, x);
+      load_row<F32, L>(a, row, base, lane, x);
       row_to_l2<F32>(a, row + step, base, lane);
       h = grad_dot<F32>(x, g, dg, dot2);
     }
     float lo, hi;
     halves(dot2, lo, hi);
     Philox4 words = {};
-    if (a.drop.on && a.dx) words = drop8_words<false>(a.drop, base, lane, static_cast<int>(row));
+    if (a.drop.on && a.dx) words = drop8_words<L>(a.drop, base, lane, static_cast<int>(row));
     const float mean = row_sum(lo + hi, slots[turn] + group * warps, w, warps, lane) * a.inv_d;
-    if (live) grad_out<F32, false>(a, row, base, lane, x, h, mean, words);
+    if (live) grad_out<F32, L>(a, row, base, lane, x, h, mean, words);
   }
   if (!a.dgain) return;
-  write_line<false>(a, reinterpret_cast<float *>(dyn), group, groups, base, lane, dg);
+  write_line<L>(a, reinterpret_cast<float *>(dyn), group, groups, base, lane, dg);
 }
 
 // Rows too wide to hold: a CTA to a row, read twice; dgain's sums stay in
 // shared memory, every column with one thread.
-template <bool F32, bool VEC>
+template <bool F32, int L>
 __global__ void __launch_bounds__(WIDE_WARPS * 32) norm_grad_wide_kernel(const NormGradArgs a) {
   __shared__ float slots[2][32];
   extern __shared__ float line[];
@@ -838,7 +880,7 @@ __global__ void __launch_bounds__(WIDE_WARPS * 32) norm_grad_wide_kernel(const N
     for (int base = w * 256; base < a.d; base += WIDE_WARPS * 256)
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
-        const int c = column<VEC>(base, lane, e);
+        const int c = column<L>(base, lane, e);
         if (c < a.d) line[c] = 0.0f;
       }
   int turn = 0;
@@ -847,15 +889,15 @@ __global__ void __launch_bounds__(WIDE_WARPS * 32) norm_grad_wide_kernel(const N
     for (int base = w * 256; base < a.d; base += WIDE_WARPS * 256) {
       GradRow<F32> x;
       Raw<F32> g;
-      load8<F32, VEC>(a.gain, base, lane, a.d, g);
-      load_row<F32, VEC>(a, row, base, lane, x);
+      load8<F32, L>(a.gain, base, lane, a.d, g);
+      load_row<F32, L>(a, row, base, lane, x);
       V8 dg = {};
       grad_dot<F32>(x, g, dg, dot2);
       float s[8];
       split8(dg, s);
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
-        const int c = column<VEC>(base, lane, e);
+        const int c = column<L>(base, lane, e);
         if (a.dgain && c < a.d) line[c] += s[e];
       }
     }
@@ -865,13 +907,13 @@ __global__ void __launch_bounds__(WIDE_WARPS * 32) norm_grad_wide_kernel(const N
     for (int base = w * 256; base < a.d; base += WIDE_WARPS * 256) {
       GradRow<F32> x;
       Raw<F32> g;
-      load8<F32, VEC>(a.gain, base, lane, a.d, g);
-      load_row<F32, VEC>(a, row, base, lane, x);
+      load8<F32, L>(a.gain, base, lane, a.d, g);
+      load_row<F32, L>(a, row, base, lane, x);
       V8 dg = {};
       const GradHalf h = grad_dot<F32>(x, g, dg, dot2);
       Philox4 words = {};
-      if (a.drop.on && a.dx) words = drop8_words<VEC>(a.drop, base, lane, static_cast<int>(row));
-      grad_out<F32, VEC>(a, row, base, lane, x, h, mean, words);
+      if (a.drop.on && a.dx) words = drop8_words<L>(a.drop, base, lane, static_cast<int>(row));
+      grad_out<F32, L>(a, row, base, lane, x, h, mean, words);
     }
   }
   if (!a.dgain) return;
@@ -879,7 +921,7 @@ __global__ void __launch_bounds__(WIDE_WARPS * 32) norm_grad_wide_kernel(const N
   for (int base = w * 256; base < a.d; base += WIDE_WARPS * 256)
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
-      const int c = column<VEC>(base, lane, e);
+      const int c = column<L>(base, lane, e);
       if (c < a.d) out[c] = line[c];
     }
 }
@@ -922,7 +964,7 @@ __global__ void __launch_bounds__(1024)
 // ------------------------------------------------- dropout by itself
 // A CTA takes `rows_per_cta` rows of `chunks` 256-column chunks; warps go over
 // them in order.
-template <bool F32, bool VEC>
+template <bool F32, int L>
 __global__ void __launch_bounds__(256) dropout_kernel(const DropoutArgs a, int rows_per_cta,
                                                       int chunks) {
   allow_next_kernel();
@@ -935,23 +977,24 @@ __global__ void __launch_bounds__(256) dropout_kernel(const DropoutArgs a, int r
     const int rr = i / chunks, base = (i - rr * chunks) * 256;
     const int64_t row = r0 + rr;
     Raw<F32> rx, rs;
-    load8<F32, VEC>(static_cast<const uint8_t *>(a.x) + row * a.x_stride * E, base, lane, a.d, rx);
+    load8<F32, L>(static_cast<const uint8_t *>(a.x) + row * a.x_stride * E, base, lane, a.d, rx);
     if (a.residual)
-      load8<F32, VEC>(static_cast<const uint8_t *>(a.residual) + row * a.residual_stride * E, base,
+      load8<F32, L>(static_cast<const uint8_t *>(a.residual) + row * a.residual_stride * E, base,
                       lane, a.d, rs);
     V8 v = unpack8<F32>(rx);
-    if (a.drop.on) v = drop8(a.drop, drop8_words<VEC>(a.drop, base, lane, static_cast<int>(row)), v);
+    if (a.drop.on) v = drop8(a.drop, drop8_words<L>(a.drop, base, lane, static_cast<int>(row)), v);
     if (a.residual) {
       const V8 t = unpack8<F32>(rs);
 #pragma unroll
       for (int e = 0; e < 4; ++e) v.p[e] = add2(v.p[e], t.p[e]);
     }
-    store8<F32, VEC>(static_cast<uint8_t *>(a.y) + row * a.y_stride * E, base, lane, a.d, v);
+    store8<F32, L>(static_cast<uint8_t *>(a.y) + row * a.y_stride * E, base, lane, a.d, v);
   }
 }
 
 // ------------------------------------------------------------------ host
-bool wide(const void *p, int64_t stride, int esz, int bytes) {
+// Whether every row of a tensor (or none: NULL) begins at a multiple of `bytes`.
+bool rows_at(const void *p, int64_t stride, int esz, int bytes) {
   return p == nullptr || ((reinterpret_cast<uintptr_t>(p) & (bytes - 1)) == 0 &&
                           (stride * esz) % bytes == 0);
 }
@@ -980,14 +1023,8 @@ RowPlan norm_plan(int d) { return row_plan(d, 4); }
 
 // Gradient.  Aligned bf16 rows: two chunks a warp, as what a warp does once for
 // a row (its sum, pointers, branches) costs a third of what it does for a chunk.
-// Rows of other alignments and fp32: one, so that 64 registers hold it.  Aligned
-// fp32 rows are held while two of them (dy, r, dr) and the gain fit shared memory.
-constexpr int kHeldGradF32 = 7168;
-
-RowPlan norm_grad_plan(int d, bool f32, bool vec) {
-  if (!vec) return row_plan(d, 1);
-  return row_plan(f32 && d > kHeldGradF32 ? kHeldColumns + 1 : d, f32 ? 1 : 2);
-}
+// Others: one, so that 64 registers hold it.
+RowPlan norm_grad_plan(int d, bool copied) { return row_plan(d, copied ? 2 : 1); }
 
 // CTAs go over the rows: as many as a GB300 holds at 64 registers a thread (112
 // with two chunks a warp).
@@ -997,55 +1034,54 @@ int grad_grid(int32_t M, const RowPlan &p) {
       std::min<int64_t>((static_cast<int64_t>(M) + p.rows_per_cta - 1) / p.rows_per_cta, most));
 }
 
-template <bool F32, bool VEC>
+template <bool F32, int L>
 cudaError_t norm_launch_t(const NormArgs &a, cudaStream_t st) {
   const RowPlan p = norm_plan(a.d);
   const unsigned grid = (static_cast<int64_t>(a.M) + p.rows_per_cta - 1) / p.rows_per_cta;
   switch (p.nv) {
-    case 0: return launch_overlapped(norm_wide_kernel<F32, VEC>, grid, p.threads, 0, st, a);
-    case 1: return launch_overlapped(norm_kernel<F32, VEC, 1>, grid, p.threads, 0, st, a, p.warps);
-    case 2: return launch_overlapped(norm_kernel<F32, VEC, 2>, grid, p.threads, 0, st, a, p.warps);
-    default: return launch_overlapped(norm_kernel<F32, VEC, 4>, grid, p.threads, 0, st, a, p.warps);
+    case 0: return launch_overlapped(norm_wide_kernel<F32, L>, grid, p.threads, 0, st, a);
+    case 1: return launch_overlapped(norm_kernel<F32, L, 1>, grid, p.threads, 0, st, a, p.warps);
+    case 2: return launch_overlapped(norm_kernel<F32, L, 2>, grid, p.threads, 0, st, a, p.warps);
+    default: return launch_overlapped(norm_kernel<F32, L, 4>, grid, p.threads, 0, st, a, p.warps);
   }
 }
 
-template <bool F32, bool VEC>
+template <bool F32, int L>
 cudaError_t norm_grad_launch_t(const NormGradArgs &a, cudaStream_t st) {
-  const RowPlan p = norm_grad_plan(a.d, F32, VEC);
+  constexpr bool COPIED = !F32 && L == kWide;
+  const RowPlan p = norm_grad_plan(a.d, COPIED);
   const int grid = grad_grid(a.M, p);
   const size_t line = static_cast<size_t>(a.d) * 4;
   const size_t sm = p.rows_per_cta > 1 ? line : 0;
+  const auto most = cudaFuncAttributeMaxDynamicSharedMemorySize;
   cudaError_t e;
   if (p.nv == 0) {
-    const auto kernel = norm_grad_wide_kernel<F32, VEC>;
-    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             kMaxNormColumns * 4);
+    const auto kernel = norm_grad_wide_kernel<F32, L>;
+    e = cudaFuncSetAttribute(kernel, most, kMaxNormColumns * 4);
     if (e == cudaSuccess)
       e = launch_overlapped(kernel, grid, p.threads, a.dgain ? line : 0, st, a);
-  } else if (VEC) {
-    // two rows ahead where three stages fit (they do but for the widest fp32)
-    const size_t part = static_cast<size_t>(p.threads) * 16 * p.nv * (F32 ? 2 : 1);
+  } else if (COPIED) {
+    const size_t part = static_cast<size_t>(p.threads) * 16 * p.nv;
     const size_t stage = 3 * part + static_cast<size_t>(p.threads) * 4;
-    const int ahead = 3 * stage + part <= kGradShared ? 2 : 1;
-    const size_t bytes = std::max((ahead + 1) * stage + part, sm);
-    const auto kernel = p.nv == 1 ? norm_grad_kernel<F32, 1> : norm_grad_kernel<F32, 2>;
-    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kGradShared);
+    const auto kernel = p.nv == 1 ? norm_grad_kernel<1> : norm_grad_kernel<2>;
+    e = cudaFuncSetAttribute(kernel, most, kGradShared);
     if (e == cudaSuccess)
-      e = launch_overlapped(kernel, grid, p.threads, bytes, st, a, p.warps, ahead);
+      e = launch_overlapped(kernel, grid, p.threads, std::max((kAhead + 1) * stage + part, sm), st,
+                            a, p.warps);
   } else {
-    e = launch_overlapped(norm_grad_odd_kernel<F32>, grid, p.threads, sm, st, a, p.warps);
+    e = launch_overlapped(norm_grad_direct_kernel<F32, L>, grid, p.threads, sm, st, a, p.warps);
   }
   if (e != cudaSuccess || !a.dgain) return e;
   return launch_overlapped(dgain_kernel<F32>, (a.d + DGAIN_COLS - 1) / DGAIN_COLS, 1024, 0, st,
                            static_cast<const float *>(a.partial), grid, a.d, a.dgain);
 }
 
-template <bool F32, bool VEC>
+template <bool F32, int L>
 cudaError_t dropout_launch_t(const DropoutArgs &a, cudaStream_t st) {
   const int chunks = (a.d + 255) / 256;
   const int rows = std::max(1, 16 / chunks);
   const unsigned grid = (static_cast<int64_t>(a.M) + rows - 1) / rows;
-  return launch_overlapped(dropout_kernel<F32, VEC>, grid, 256, 0, st, a, rows, chunks);
+  return launch_overlapped(dropout_kernel<F32, L>, grid, 256, 0, st, a, rows, chunks);
 }
 
 dspark_status result(cudaError_t e) { return e == cudaSuccess ? DSPARK_OK : DSPARK_ERR_CUDA; }
@@ -1053,41 +1089,60 @@ dspark_status result(cudaError_t e) { return e == cudaSuccess ? DSPARK_OK : DSPA
 }  // namespace
 
 size_t norm_workspace_bytes(int32_t M, int32_t d) {
-  // any type's and alignment's lines
-  const int lines = std::max({grad_grid(M, norm_grad_plan(d, false, true)),
-                              grad_grid(M, norm_grad_plan(d, true, true)),
-                              grad_grid(M, norm_grad_plan(d, false, false))});
+  // either kernel's lines
+  const int lines =
+      std::max(grad_grid(M, norm_grad_plan(d, true)), grad_grid(M, norm_grad_plan(d, false)));
   return kNormPartialOffset + static_cast<size_t>(lines) * d * 4;
+}
+
+template <class F>
+Layout layout(int f32, int d, F rows_at_all) {
+  if (d % 8 == 0 && rows_at_all(16)) return kWide;
+  return !f32 && d % 2 == 0 && rows_at_all(4) ? kPairs : kSingle;
 }
 
 dspark_status norm_launch(const NormArgs &a, cudaStream_t st) {
   const int e = a.f32 ? 4 : 2;
-  const bool vec = a.d % 8 == 0 && wide(a.x, a.x_stride, e, 16) &&
-                   wide(a.residual, a.residual_stride, e, 16) && wide(a.r, a.r_stride, e, 16) &&
-                   wide(a.gain, 0, e, 16) &&
-                   wide(a.y, a.y_stride, a.e4m3 ? 1 : e, a.e4m3 ? 8 : 16);
-  if (a.f32) return result(vec ? norm_launch_t<true, true>(a, st) : norm_launch_t<true, false>(a, st));
-  return result(vec ? norm_launch_t<false, true>(a, st) : norm_launch_t<false, false>(a, st));
+  const Layout l = layout(a.f32, a.d, [&](int n) {
+    return rows_at(a.x, a.x_stride, e, n) && rows_at(a.residual, a.residual_stride, e, n) &&
+           rows_at(a.r, a.r_stride, e, n) && rows_at(a.gain, 0, e, n) &&
+           (a.e4m3 ? rows_at(a.y, a.y_stride, 1, n / 2) : rows_at(a.y, a.y_stride, e, n));
+  });
+  if (a.f32)
+    return result(l == kWide ? norm_launch_t<true, kWide>(a, st)
+                             : norm_launch_t<true, kSingle>(a, st));
+  return result(l == kWide    ? norm_launch_t<false, kWide>(a, st)
+                : l == kPairs ? norm_launch_t<false, kPairs>(a, st)
+                              : norm_launch_t<false, kSingle>(a, st));
 }
 
 dspark_status norm_grad_launch(const NormGradArgs &a, cudaStream_t st) {
   const int e = a.f32 ? 4 : 2;
-  const bool vec = a.d % 8 == 0 && wide(a.dy, a.dy_stride, e, 16) &&
-                   wide(a.dr, a.dr_stride, e, 16) && wide(a.r, a.r_stride, e, 16) &&
-                   wide(a.gain, 0, e, 16) && wide(a.dx, a.dx_stride, e, 16) &&
-                   wide(a.dresidual, a.dresidual_stride, e, 16);
+  const Layout l = layout(a.f32, a.d, [&](int n) {
+    return rows_at(a.dy, a.dy_stride, e, n) && rows_at(a.dr, a.dr_stride, e, n) &&
+           rows_at(a.r, a.r_stride, e, n) && rows_at(a.gain, 0, e, n) &&
+           rows_at(a.dx, a.dx_stride, e, n) && rows_at(a.dresidual, a.dresidual_stride, e, n);
+  });
   if (a.f32)
-    return result(vec ? norm_grad_launch_t<true, true>(a, st) : norm_grad_launch_t<true, false>(a, st));
-  return result(vec ? norm_grad_launch_t<false, true>(a, st) : norm_grad_launch_t<false, false>(a, st));
+    return result(l == kWide ? norm_grad_launch_t<true, kWide>(a, st)
+                             : norm_grad_launch_t<true, kSingle>(a, st));
+  return result(l == kWide    ? norm_grad_launch_t<false, kWide>(a, st)
+                : l == kPairs ? norm_grad_launch_t<false, kPairs>(a, st)
+                              : norm_grad_launch_t<false, kSingle>(a, st));
 }
 
 dspark_status dropout_launch(const DropoutArgs &a, cudaStream_t st) {
   const int e = a.f32 ? 4 : 2;
-  const bool vec = a.d % 8 == 0 && wide(a.x, a.x_stride, e, 16) &&
-                   wide(a.residual, a.residual_stride, e, 16) && wide(a.y, a.y_stride, e, 16);
+  const Layout l = layout(a.f32, a.d, [&](int n) {
+    return rows_at(a.x, a.x_stride, e, n) && rows_at(a.residual, a.residual_stride, e, n) &&
+           rows_at(a.y, a.y_stride, e, n);
+  });
   if (a.f32)
-    return result(vec ? dropout_launch_t<true, true>(a, st) : dropout_launch_t<true, false>(a, st));
-  return result(vec ? dropout_launch_t<false, true>(a, st) : dropout_launch_t<false, false>(a, st));
+    return result(l == kWide ? dropout_launch_t<true, kWide>(a, st)
+                             : dropout_launch_t<true, kSingle>(a, st));
+  return result(l == kWide    ? dropout_launch_t<false, kWide>(a, st)
+                : l == kPairs ? dropout_launch_t<false, kPairs>(a, st)
+                              : dropout_launch_t<false, kSingle>(a, st));
 }
 
 }  // namespace dspark
