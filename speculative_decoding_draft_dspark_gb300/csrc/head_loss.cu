@@ -460,6 +460,7 @@ struct HalfTile {
   uint32_t acc, box;  // tensor memory, shared memory
   uint32_t acc_empty; // barrier, in the cluster's window
   int lane;
+  int *stores;        // the warp's stores so far: which half of its box is next
 };
 
 __device__ __forceinline__ void give_back(const HalfTile &t) {
@@ -504,9 +505,12 @@ __device__ __forceinline__ void box_is_free(int lane) {
 }
 
 // 32 x 32 values as bf16 into one of the warp's two boxes of 2 KB (rows of 64
-// bytes, 64-byte swizzle), in turn: at most one store is still reading the other
-__device__ __forceinline__ uint32_t put_32x32(const HalfTile &t, int b, const float (&g)[32]) {
-  const uint32_t box = t.box + (b & 1) * (H_OUT_BOX / 2);
+// bytes, 64-byte swizzle).  They take turns store by store, over tiles too
+// (which may have an odd number of blocks, or skip some): the only store that
+// may still be reading is then the other box's.
+__device__ __forceinline__ uint32_t put_32x32(const HalfTile &t, const float (&g)[32]) {
+  const uint32_t box = t.box + (*t.stores & 1) * (H_OUT_BOX / 2);
+  ++*t.stores;
   if (t.lane == 0) bulk_wait_read<1>();
   __syncwarp();
 #pragma unroll
@@ -595,7 +599,7 @@ __device__ __forceinline__ void prob_tile(const HeadParams &p, const CUtensorMap
                                           const HalfTile &t, int row0) {
   const int lane = t.lane, v_first = p.v0 + row0;
   const bool beyond = v_first + lane >= p.vocab;
-  each_block(t, [&](int b, int c0, uint32_t (&acc)[32]) {
+  each_block(t, [&](int, int c0, uint32_t (&acc)[32]) {
     const float4 *lse2 = reinterpret_cast<const float4 *>(p.rows.lse2 + t.n + c0);
     const float4 *weight = reinterpret_cast<const float4 *>(p.rows.weight + t.n + c0);
     const int at = p.rows.target[t.n + c0 + lane] - v_first;
@@ -622,7 +626,7 @@ __device__ __forceinline__ void prob_tile(const HeadParams &p, const CUtensorMap
 #pragma unroll
       for (int e = 0; e < 32; ++e) g[e] = 0.0f;
     }
-    const uint32_t box = put_32x32(t, b, g);
+    const uint32_t box = put_32x32(t, g);
     if (lane == 0) {
       tma_store_2d(&g_out, box, t.n + c0, row0);
       bulk_commit();
@@ -651,7 +655,7 @@ __device__ __forceinline__ void sum_tile(const HeadParams &p, const CUtensorMap 
         tma_reduce_add_2d(&acc_map, t.box, t.n + c0, y);
       bulk_commit();
     }
-  });
+  });  box_is_free(lane);  // the whole box: a dB tile's stores use halves of it
 }
 
 // dB: lanes are vocabulary entries, columns those of [W, V].  Two boxes of 2 KB
@@ -660,7 +664,7 @@ __device__ __forceinline__ void weight_tile(const HeadParams &p, const HeadMaps 
                                             const HalfTile &t, int row0) {
   const int lane = t.lane;
   const float scale = *p.rows.scale;
-  each_block(t, [&](int b, int c0, uint32_t (&acc)[32]) {
+  each_block(t, [&](int, int c0, uint32_t (&acc)[32]) {
     const int col = t.n + c0;
     const bool in_d = col < p.kd * HK;
     const int left = in_d ? p.d - col : p.rank - (col - p.kd * HK);
@@ -668,7 +672,7 @@ __device__ __forceinline__ void weight_tile(const HeadParams &p, const HeadMaps 
     float g[32];
 #pragma unroll
     for (int e = 0; e < 32; ++e) g[e] = __uint_as_float(acc[e]) * scale;
-    const uint32_t box = put_32x32(t, b, g);
+    const uint32_t box = put_32x32(t, g);
     if (lane == 0) {
       if (in_d)
         tma_store_2d(&maps.dw, box, col, p.v0 + row0);
@@ -905,7 +909,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(H_THREADS, 1)
     const uint32_t acc_empty0 = mapa_u32(smem_u32(acc_empty), 0);
     const uint32_t lane_base = tmem_base + (static_cast<uint32_t>(q * 32) << 16);
     const uint32_t box = smem_u32(smem + H_RING + (warp - 4) * H_OUT_BOX);
-    int ig = 0;
+    int ig = 0, stores = 0;
     bool ok = true;
     float2 *slot = nullptr;
     int period = 0;  // the pair's tiles after which the same rows come again
@@ -951,6 +955,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(H_THREADS, 1)
         t.box = box;
         t.acc_empty = acc_empty0 + buf * 8;
         t.lane = lane;
+        t.stores = &stores;
         if (KIND == kLse)
           lse_tile(p, t, p.v0 + row0, rows, slot);
         else if (KIND == kProb)
