@@ -44,8 +44,8 @@ extern "C" {
  * loss, lse   out [M] fp32.
  * workspace   >= dspark_head_workspace_size(M, vocab, d, rank, 0) bytes (a
  *             workspace for the gradient is large enough), 256-byte aligned.
- * Limits: 1 <= M <= 2^20, 1 <= vocab < 2^30, d a multiple of 8 in [8, 65536],
- * rank a multiple of 8 in [0, 256].
+ * Limits: 1 <= M <= 2^20, 1 <= vocab < 2^30, ceil(M / 256) ceil(vocab / 256) <=
+ * 2^30, d a multiple of 8 in [8, 65536], rank a multiple of 8 in [0, 256].
  * ------------------------------------------------------------------------ */
 DSPARK_API size_t dspark_head_workspace_size(int32_t M, int32_t vocab, int32_t d, int32_t rank,
                                              int32_t grad);

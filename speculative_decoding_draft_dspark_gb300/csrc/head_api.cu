@@ -18,6 +18,10 @@ dspark_status check_head_dims(int32_t M, int32_t vocab, int32_t d, int32_t rank)
   if (M > (1 << 20) || vocab >= (1 << 30)) return DSPARK_ERR_UNSUPPORTED;
   if (d % 8 != 0 || d > 65536) return DSPARK_ERR_UNSUPPORTED;
   if (rank % 8 != 0 || rank > 256) return DSPARK_ERR_UNSUPPORTED;
+  // tiles of 256 x 256 are counted in 32 bits
+  const int64_t tiles = ((static_cast<int64_t>(M) + 255) / 256) *
+                        ((static_cast<int64_t>(vocab) + 255) / 256);
+  if (tiles > (1ll << 30)) return DSPARK_ERR_UNSUPPORTED;
   return DSPARK_OK;
 }
 

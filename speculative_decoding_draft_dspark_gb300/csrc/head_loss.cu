@@ -256,6 +256,15 @@ __global__ void __launch_bounds__(PACK_THREADS) head_pack_kernel(const PackParam
 // multiplied, and at a tile's start the first half gets ahead as far as the ring
 // holds.  With 256 columns the accumulators are two tiles' in turn.
 //
+// What bounds them.  Many rows: the tensor cores and, after a tenth of a second
+// of them, the 1400 W limit.  1632 columns x 262144 x 2304 (LSE) take 1.17 to
+// 1.22 ms, 1.62 to 1.68 PFLOP/s, 0.85 to 0.88 of cuBLAS's measured burst and as
+// much as its 1.71 PFLOP/s of seconds allows for the added weight stream; by
+// themselves, cool, LSE reaches 1.97, PROB 1.87 and GRAD 1.79 PFLOP/s at 6464
+// columns.  Few rows: HBM; 64 columns take 179 us, 6.75 TB/s of W and V.  In
+// between a tile's operands: each SM takes in at most some 50 bytes a cycle,
+// which a 256 x 256 tile needs for 0.8 of the tensor cores' rate.
+//
 // The rows of A are always the tile's columns or the reduction: those come in
 // steps of 32 and 16, where a tile's rows are always 256, so that 403 rows cost
 // 416 and not 512.  Both operands of z^T and G^T in dB have the reduction index
@@ -336,13 +345,14 @@ __device__ __forceinline__ int row_width(int n_valid) {
 // behind the next tile (512: 835 us instead of 790 for 403 rows).
 __device__ __forceinline__ int weight_width(int n_valid) { return n_valid > 1024 ? HW : HT; }
 
-// What a pair does: tiles t = first, first + step, ... < end of its list.  dA
-// tiles go round over the pairs, and each pair gets a run of dB tiles, shorter
-// where it has one dA tile more, so that all have the same to do.
+// What a pair does.  z^T tiles, and dA tiles before dB tiles, go round over the
+// pairs; each pair then gets a run of dB tiles, shorter where it has one dA tile
+// more, so that all have the same to do.
 struct HeadWork {
   int width;             // of tiles whose columns are rows of A
   int nt;                // and how many there are side by side
-  int da_tiles, db_lo, db_hi;
+  int round;             // z^T or dA tiles
+  int db_lo, db_hi;      // the pair's dB tiles
 };
 
 template <int KIND>
@@ -352,12 +362,12 @@ __device__ __forceinline__ HeadWork head_work(const HeadParams &p, int n_valid, 
   w.width = row_width<KIND>(n_valid);
   const int nt = w.nt = row_tiles(n_valid, w.width);
   if (KIND != kGrad) {
-    w.da_tiles = nt * p.v_tiles;
+    w.round = nt * p.v_tiles;
     w.db_lo = w.db_hi = 0;
     return w;
   }
   const int d_tiles = (p.cols_pad + HT - 1) / HT;
-  w.da_tiles = nt * d_tiles * p.splits;
+  w.round = nt * d_tiles * p.splits;
   const int width = weight_width(n_valid);
   const int n_db = p.v_tiles * ((p.cols_pad + width - 1) / width);
   // times in 64-entry blocks of 256 columns; a dB tile's stores take about as
@@ -366,7 +376,7 @@ __device__ __forceinline__ HeadWork head_work(const HeadParams &p, int n_valid, 
                      (static_cast<float>(n_valid) / (HT * (nt > 0 ? nt : 1)));
   const float t_db = ((n_valid + HK - 1) / HK + 3) * static_cast<float>(p.cols_pad) * p.v_tiles /
                      (static_cast<float>(HT) * n_db);
-  const int more = w.da_tiles % pairs;  // pairs with one dA tile more
+  const int more = w.round % pairs;  // pairs with one dA tile more
   const float gap = t_da / t_db;
   float x = (n_db - (pairs - more) * gap) / pairs, y = x + gap;
   if (x < 0.0f) {
@@ -394,7 +404,7 @@ __device__ __forceinline__ bool head_tile(const HeadParams &p, const HeadWork &w
   int t = pair + i * pairs;
   x.da = 0;
   x.split = 0;
-  if (t < w.da_tiles) {
+  if (t < w.round) {
     if (KIND != kGrad) {
       x.m = (t / nt) * HT;
       row_tile(n_valid, w.width, t % nt, x);
@@ -414,7 +424,7 @@ __device__ __forceinline__ bool head_tile(const HeadParams &p, const HeadWork &w
     return true;
   }
   if (KIND != kGrad) return false;
-  const int da = w.da_tiles > pair ? (w.da_tiles - pair + pairs - 1) / pairs : 0;
+  const int da = w.round > pair ? (w.round - pair + pairs - 1) / pairs : 0;
   t = w.db_lo + i - da;
   if (t >= w.db_hi) return false;
   const int width = weight_width(n_valid), tiles = (p.cols_pad + width - 1) / width;
@@ -655,7 +665,8 @@ __device__ __forceinline__ void sum_tile(const HeadParams &p, const CUtensorMap 
         tma_reduce_add_2d(&acc_map, t.box, t.n + c0, y);
       bulk_commit();
     }
-  });  box_is_free(lane);  // the whole box: a dB tile's stores use halves of it
+  });
+  box_is_free(lane);  // the whole box: a dB tile's stores use halves of it
 }
 
 // dB: lanes are vocabulary entries, columns those of [W, V].  Two boxes of 2 KB
@@ -1271,9 +1282,9 @@ dspark_status head_plan(const HeadArgs &a, bool grad, HeadPlan &o) {
 // no more pairs than there can be tiles
 template <int KIND>
 int head_pairs(const HeadPlan &o, const HeadParams &p) {
-  const int64_t nt = (o.lay.rows_pad + HW - 1) / HW, dt = (o.lay.cols_pad + HT - 1) / HT;
-  const int64_t tiles =
-      KIND == kGrad ? dt * (nt * p.splits + p.v_tiles) : nt * int64_t(p.v_tiles);
+  const int64_t rows = o.lay.rows_pad, dt = (o.lay.cols_pad + HT - 1) / HT;
+  const int64_t tiles = KIND == kGrad ? dt * ((rows + HW - 1) / HW * p.splits + p.v_tiles)
+                                      : rows / HT * p.v_tiles;
   return static_cast<int>(std::min<int64_t>(std::min(o.sms / 2, kPairs), tiles));
 }
 
@@ -1301,7 +1312,7 @@ HeadLayout head_layout(int32_t M, int32_t vocab, int32_t d, int32_t rank, bool g
   const int64_t v_pad = up(vocab, HT);
   l.splits = 1;
   if (!grad) {
-    const int64_t pairs = std::min<int64_t>(kPairs, (l.rows_pad + HW - 1) / HW * (v_pad / HT));
+    const int64_t pairs = std::min<int64_t>(kPairs, l.rows_pad / HT * (v_pad / HT));
     l.partial = take(static_cast<size_t>(pairs) * 8 * l.rows_pad * 8);
   } else {
     constexpr int64_t kPieceBytes = 192ll << 20;

@@ -31,7 +31,8 @@ def test_head_workspace_size(lib):
     assert f(7168, 262144, 2048, 256, False) > f(1792, 262144, 2048, 256, False)
     assert f(1, 1, 8, 0, True) > 0
     for bad in ((0, 10, 8, 0), (1, 0, 8, 0), (1, 10, 12, 0), (1, 10, 8, 12), (1, 10, 8, 264),
-                (1, 10, 8, -8), (1, 10, 65544, 0), ((1 << 20) + 1, 10, 8, 0), (1, 1 << 30, 8, 0)):
+                (1, 10, 8, -8), (1, 10, 65544, 0), ((1 << 20) + 1, 10, 8, 0), (1, 1 << 30, 8, 0),
+                (1 << 20, (1 << 30) - 1, 8, 0)):
         assert f(*bad, True) == 0, bad
 
 
