@@ -86,7 +86,7 @@ __device__ __forceinline__ float reference(float top) {
 
 // ------------------------------------------------------------------ pack
 // Gathers the rows with a target into A = [h, U[prev]], zero-padded to whole
-// 64-column blocks and 256-row tiles, and their row data.  A row that is
+// 64-column blocks and to a multiple of 32 rows, and their row data.  A row that is
 // ignored is never read, so what it holds (NaN, infinities) reaches nothing.
 // Every CTA counts the targets before its rows itself: the target array is a
 // few KB from L2, and a scan across CTAs would cost a second launch.
@@ -223,8 +223,9 @@ __global__ void __launch_bounds__(PACK_THREADS) head_pack_kernel(const PackParam
       *reinterpret_cast<uint4 *>(ar + col) = v;
     }
   }
-  // the rows that fill up the last tile
-  const int end = (total + HT - 1) / HT * HT;
+  // the rows that fill up the last tile's columns; what its boxes read beyond
+  // them is not multiplied
+  const int end = (total + HU - 1) / HU * HU;
   for (int j = total + blockIdx.x * PACK_WARPS + warp; j < end; j += gridDim.x * PACK_WARPS) {
     uint16_t *ar = p.a + static_cast<int64_t>(j) * p.cols_pad;
     for (int c = lane; c < chunks; c += 32)
@@ -1066,9 +1067,11 @@ __global__ void __launch_bounds__(256)
   {
     const float *x = acc + static_cast<int64_t>(c0 + warp) * rows_pad + r0 + lane;
     float s[TURN_COLS / 8] = {};
-    for (int k = 0; k < splits; ++k, x += static_cast<int64_t>(cols_pad) * rows_pad) {
+#pragma unroll 4
+    for (int k = 0; k < splits; ++k) {
 #pragma unroll
-      for (int j = 0; j < TURN_COLS / 8; ++j) s[j] += x[static_cast<int64_t>(j) * 8 * rows_pad];
+      for (int j = 0; j < TURN_COLS / 8; ++j)
+        s[j] += x[(static_cast<int64_t>(k) * cols_pad + j * 8) * rows_pad];
     }
 #pragma unroll
     for (int j = 0; j < TURN_COLS / 8; ++j) block[lane][warp + j * 8] = s[j] * scale;
@@ -1275,7 +1278,8 @@ dspark_status head_plan(const HeadArgs &a, bool grad, HeadPlan &o) {
   k.a = reinterpret_cast<uint16_t *>(ws + l.a);
   k.rows = p.rows;
   k.status = p.status;
-  o.pack_grid = (a.M + k.rows_per_cta - 1) / k.rows_per_cta;
+  // some CTAs also for the rows that fill up
+  o.pack_grid = std::max(4, (a.M + k.rows_per_cta - 1) / k.rows_per_cta);
   return DSPARK_OK;
 }
 
