@@ -291,21 +291,33 @@ __device__ __forceinline__ float warp_max_nan(float v) {
   return v;
 }
 
-// A row's warps share values through `slots` (warps per row of them); all of
-// the CTA's threads call this together.
-__device__ __forceinline__ float row_sum(float v, float *slots, int w, int warps, int lane) {
+// A row's warps share values through `slots` (as many as warps).  They meet at
+// the CTA's barrier, or (OWN) at one of the row's own, so that the CTA's rows do
+// not wait for one another; that takes all 16 barriers of a CTA, and few CTAs
+// then fit an SM.
+template <bool OWN = false>
+__device__ __forceinline__ void row_barrier(int group, int warps) {
+  if (OWN)
+    asm volatile("bar.sync %0, %1;" ::"r"(group + 1), "r"(warps * 32) : "memory");
+  else
+    __syncthreads();
+}
+template <bool OWN = false>
+__device__ __forceinline__ float row_sum(float v, float *slots, int group, int w, int warps,
+                                         int lane) {
   v = warp_sum(v);
   if (warps == 1) return v;
-  if (lane == 0) slots[w] = v;
-  __syncthreads();
-  return warp_sum(lane < warps ? slots[lane] : 0.0f);
+  if (lane == 0) slots[group * warps + w] = v;
+  row_barrier<OWN>(group, warps);
+  return warp_sum(lane < warps ? slots[group * warps + lane] : 0.0f);
 }
-__device__ __forceinline__ float row_max_nan(float v, float *slots, int w, int warps, int lane) {
+__device__ __forceinline__ float row_max_nan(float v, float *slots, int group, int w, int warps,
+                                             int lane) {
   v = warp_max_nan(v);
   if (warps == 1) return v;
-  if (lane == 0) slots[w] = v;
-  __syncthreads();
-  return warp_max_nan(lane < warps ? slots[lane] : 0.0f);
+  if (lane == 0) slots[group * warps + w] = v;
+  row_barrier(group, warps);
+  return warp_max_nan(lane < warps ? slots[group * warps + lane] : 0.0f);
 }
 
 // eight e4m3 numbers of y / scale
@@ -469,7 +481,7 @@ __global__ void __launch_bounds__(256) norm_kernel(const NormArgs a, int warps) 
   }
   float lo, hi;
   halves(sum2, lo, hi);
-  const float sum = row_sum(lo + hi, slots[0] + group * warps, w, warps, lane);
+  const float sum = row_sum(lo + hi, slots[0], group, w, warps, lane);
   const float rstd = rsqrtf(fmaf(sum, a.inv_d, a.eps));
   float top = 0.0f;
   if (live) {
@@ -492,7 +504,7 @@ __global__ void __launch_bounds__(256) norm_kernel(const NormArgs a, int warps) 
     }
   }
   if (a.e4m3 && a.group == 0) {
-    const float s = scale_of(row_max_nan(top, slots[1] + group * warps, w, warps, lane));
+    const float s = scale_of(row_max_nan(top, slots[1], group, w, warps, lane));
     if (live) {
       if (w == 0 && lane == 0) a.scale[row] = s;
       uint8_t *yo = static_cast<uint8_t *>(a.y) + row * a.y_stride;
@@ -540,7 +552,7 @@ __global__ void __launch_bounds__(WIDE_WARPS * 32) norm_wide_kernel(const NormAr
     squares8(stream8<F32, L>(a, x, res, row, base, lane), sum2);
   float lo, hi;
   halves(sum2, lo, hi);
-  const float sum = row_sum(lo + hi, slots[0], w, WIDE_WARPS, lane);
+  const float sum = row_sum(lo + hi, slots[0], 0, w, WIDE_WARPS, lane);
   const float rstd = rsqrtf(fmaf(sum, a.inv_d, a.eps));
   if (a.rstd && threadIdx.x == 0) a.rstd[row] = rstd;
   float s = 1.0f;
@@ -550,7 +562,7 @@ __global__ void __launch_bounds__(WIDE_WARPS * 32) norm_wide_kernel(const NormAr
       const V8 r = stream8<F32, L>(a, x, res, row, base, lane);
       top = top8(top, times_gain<F32, L>(a.gain, rstd, base, lane, a.d, r));
     }
-    s = scale_of(row_max_nan(top, slots[1], w, WIDE_WARPS, lane));
+    s = scale_of(row_max_nan(top, slots[1], 0, w, WIDE_WARPS, lane));
     if (threadIdx.x == 0) a.scale[row] = s;
   }
   uint8_t *ro = static_cast<uint8_t *>(a.r) + row * a.r_stride * E;
@@ -692,7 +704,7 @@ __device__ __forceinline__ void write_line(const NormGradArgs &a, float *lines, 
 constexpr int kAhead = 2;
 
 template <int NV>
-__global__ void __launch_bounds__(NV == 1 ? 1024 : 512)
+__global__ void __launch_bounds__(512)
     norm_grad_kernel(const NormGradArgs a, int warps) {
   __shared__ float slots[2][32];
   extern __shared__ __align__(16) uint8_t dyn[];
@@ -795,7 +807,7 @@ __global__ void __launch_bounds__(NV == 1 ? 1024 : 512)
       for (int i = 0; i < NV; ++i) words[i] = drop_words(a.drop, (c + i * chunk) / 8, row);
     }
     // two sets of slots: a row's sums are read while the next row's are written
-    const float mean = row_sum(lo + hi, slots[k & 1] + group * warps, w, warps, lane) * a.inv_d;
+    const float mean = row_sum<true>(lo + hi, slots[k & 1], group, w, warps, lane) * a.inv_d;
     if (live) {
 #pragma unroll
       for (int i = 0; i < NV; ++i) {
@@ -860,7 +872,7 @@ __global__ void __launch_bounds__(1024) norm_grad_direct_kernel(const NormGradAr
     halves(dot2, lo, hi);
     Philox4 words = {};
     if (a.drop.on && a.dx) words = drop8_words<L>(a.drop, base, lane, static_cast<int>(row));
-    const float mean = row_sum(lo + hi, slots[turn] + group * warps, w, warps, lane) * a.inv_d;
+    const float mean = row_sum(lo + hi, slots[turn], group, w, warps, lane) * a.inv_d;
     if (live) grad_out<F32, L>(a, row, base, lane, x, h, mean, words);
   }
   if (!a.dgain) return;
@@ -903,7 +915,7 @@ __global__ void __launch_bounds__(WIDE_WARPS * 32) norm_grad_wide_kernel(const N
     }
     float lo, hi;
     halves(dot2, lo, hi);
-    const float mean = row_sum(lo + hi, slots[turn], w, WIDE_WARPS, lane) * a.inv_d;
+    const float mean = row_sum(lo + hi, slots[turn], 0, w, WIDE_WARPS, lane) * a.inv_d;
     for (int base = w * 256; base < a.d; base += WIDE_WARPS * 256) {
       GradRow<F32> x;
       Raw<F32> g;
@@ -1006,30 +1018,41 @@ struct RowPlan {
 };
 
 constexpr int kHeldColumns = 8192;
+constexpr int kSms = 152;  // a GB300's
 constexpr int kGradShared = 226 * 1024;
 
-RowPlan row_plan(int d, int nv) {
+RowPlan row_plan(int d, int nv, int warps) {
   if (d > kHeldColumns) return {0, WIDE_WARPS, 1, WIDE_WARPS * 32};
   RowPlan p;
   const int chunks = (d + 255) / 256;
   p.nv = std::min(nv, chunks >= 4 ? 4 : chunks >= 2 ? 2 : 1);
   p.warps = (chunks + p.nv - 1) / p.nv;
-  p.rows_per_cta = std::max(1, 4 / p.warps);
+  p.rows_per_cta = std::max(1, warps / p.warps);
   p.threads = p.rows_per_cta * p.warps * 32;
   return p;
 }
 
-RowPlan norm_plan(int d) { return row_plan(d, 4); }
+RowPlan norm_plan(int d) { return row_plan(d, 4, 4); }
 
 // Gradient.  Aligned bf16 rows: two chunks a warp, as what a warp does once for
-// a row (its sum, pointers, branches) costs a third of what it does for a chunk.
-// Others: one, so that 64 registers hold it.
-RowPlan norm_grad_plan(int d, bool copied) { return row_plan(d, copied ? 2 : 1); }
+// a row (its sum, pointers, branches) costs a third of what it does for a chunk,
+// and one CTA of 16 warps an SM, as each CTA writes a line of dgain's sums (608
+// lines of four smaller CTAs an SM: 59.1 us instead of 57.6 at 15360 x 2048); few
+// rows are spread over the SMs first.  Others: one chunk, so that 64 registers
+// hold it.
+RowPlan norm_grad_plan(int32_t M, int d, bool copied) {
+  if (!copied) return row_plan(d, 1, 4);
+  RowPlan p = row_plan(d, 2, 16);
+  if (p.nv) {
+    p.rows_per_cta = std::min({p.rows_per_cta, (M + kSms - 1) / kSms, 15});
+    p.threads = p.rows_per_cta * p.warps * 32;
+  }
+  return p;
+}
 
-// CTAs go over the rows: as many as a GB300 holds at 64 registers a thread (112
-// with two chunks a warp).
-int grad_grid(int32_t M, const RowPlan &p) {
-  const int64_t most = 152 * std::max(1, (p.nv == 2 ? 512 : 1024) / p.threads);
+// CTAs go over the rows: as many as a GB300 holds.
+int grad_grid(int32_t M, const RowPlan &p, bool copied) {
+  const int64_t most = kSms * (p.nv == 0 ? 2 : copied ? 1 : std::max(1, 1024 / p.threads));
   return static_cast<int>(
       std::min<int64_t>((static_cast<int64_t>(M) + p.rows_per_cta - 1) / p.rows_per_cta, most));
 }
@@ -1049,8 +1072,8 @@ cudaError_t norm_launch_t(const NormArgs &a, cudaStream_t st) {
 template <bool F32, int L>
 cudaError_t norm_grad_launch_t(const NormGradArgs &a, cudaStream_t st) {
   constexpr bool COPIED = !F32 && L == kWide;
-  const RowPlan p = norm_grad_plan(a.d, COPIED);
-  const int grid = grad_grid(a.M, p);
+  const RowPlan p = norm_grad_plan(a.M, a.d, COPIED);
+  const int grid = grad_grid(a.M, p, COPIED);
   const size_t line = static_cast<size_t>(a.d) * 4;
   const size_t sm = p.rows_per_cta > 1 ? line : 0;
   const auto most = cudaFuncAttributeMaxDynamicSharedMemorySize;
@@ -1091,7 +1114,8 @@ dspark_status result(cudaError_t e) { return e == cudaSuccess ? DSPARK_OK : DSPA
 size_t norm_workspace_bytes(int32_t M, int32_t d) {
   // either kernel's lines
   const int lines =
-      std::max(grad_grid(M, norm_grad_plan(d, true)), grad_grid(M, norm_grad_plan(d, false)));
+      std::max(grad_grid(M, norm_grad_plan(M, d, true), true),
+               grad_grid(M, norm_grad_plan(M, d, false), false));
   return kNormPartialOffset + static_cast<size_t>(lines) * d * 4;
 }
 
