@@ -371,10 +371,11 @@ __device__ __forceinline__ HeadWork head_work(const HeadParams &p, int n_valid, 
   w.round = nt * d_tiles * p.splits;
   const int width = weight_width(n_valid);
   const int n_db = p.v_tiles * ((p.cols_pad + width - 1) / width);
-  // times in 64-entry blocks of 256 columns; a dB tile's stores take about as
-  // long as three of them
+  // times in 64-entry blocks of 256 columns; with fewer columns a block of dA
+  // takes as long, for W streams through it (2 rows x 89769 x 1152: 0.28 us a
+  // block); a dB tile's stores take about as long as three
   const float t_da = static_cast<float>(p.v_tiles) * (HT / HK) / p.splits *
-                     (static_cast<float>(n_valid) / (HT * (nt > 0 ? nt : 1)));
+                     fmaxf(1.0f, static_cast<float>(n_valid) / (HT * (nt > 0 ? nt : 1)));
   const float t_db = ((n_valid + HK - 1) / HK + 3) * static_cast<float>(p.cols_pad) * p.v_tiles /
                      (static_cast<float>(HT) * n_db);
   const int more = w.round % pairs;  // pairs with one dA tile more
@@ -1067,11 +1068,20 @@ __global__ void __launch_bounds__(256)
   {
     const float *x = acc + static_cast<int64_t>(c0 + warp) * rows_pad + r0 + lane;
     float s[TURN_COLS / 8] = {};
-#pragma unroll 4
-    for (int k = 0; k < splits; ++k) {
+    // eight splits' values in flight at a time; added in the splits' order
+    for (int k = 0; k < splits; k += 8) {
+      float v[8][TURN_COLS / 8];
 #pragma unroll
-      for (int j = 0; j < TURN_COLS / 8; ++j)
-        s[j] += x[(static_cast<int64_t>(k) * cols_pad + j * 8) * rows_pad];
+      for (int u = 0; u < 8; ++u)
+#pragma unroll
+        for (int j = 0; j < TURN_COLS / 8; ++j)
+          v[u][j] = k + u < splits
+                        ? x[(static_cast<int64_t>(k + u) * cols_pad + j * 8) * rows_pad]
+                        : 0.0f;
+#pragma unroll
+      for (int u = 0; u < 8; ++u)
+#pragma unroll
+        for (int j = 0; j < TURN_COLS / 8; ++j) s[j] += v[u][j];
     }
 #pragma unroll
     for (int j = 0; j < TURN_COLS / 8; ++j) block[lane][warp + j * 8] = s[j] * scale;
@@ -1325,14 +1335,15 @@ HeadLayout head_layout(int32_t M, int32_t vocab, int32_t d, int32_t rank, bool g
     l.piece = up((v_pad + pieces - 1) / pieces, HT);
     // dA's reduction over the piece is split where a tile of it would take longer
     // than a pair's share of all tiles (as in head_work, in 64-entry blocks of 256
-    // columns)
+    // columns).  2 rows x 89769 x 1152 take 127 us in 10 splits, and 387 in one,
+    // whose five pairs alone read all of W.
     const int64_t nt = (l.rows_pad + HW - 1) / HW, dt = (l.cols_pad + HT - 1) / HT;
     const double deep = static_cast<double>(l.piece) / HK;
-    const double t_da = deep * M / (static_cast<double>(HT) * nt);
+    const double t_da = deep * std::max(1.0, M / (static_cast<double>(HT) * nt));
     const double t_db = (static_cast<double>(M) / HK + 3.0) * l.cols_pad / HT * l.piece / HT;
     const double share = (static_cast<double>(nt * dt) * t_da + t_db) / kPairs;
     l.splits = static_cast<int32_t>(
-        std::max(1.0, std::min({std::ceil(t_da / (0.9 * share)), deep / 8.0, 16.0})));
+        std::max(1.0, std::min({std::ceil(t_da / (0.9 * share)), deep / 8.0, 32.0})));
     l.g = take(static_cast<size_t>(l.rows_pad) * l.piece * 2);
     l.acc = take(static_cast<size_t>(l.splits) * l.rows_pad * l.cols_pad * 4);
     l.de = take(static_cast<size_t>(l.rows_pad) * rank * 4);
