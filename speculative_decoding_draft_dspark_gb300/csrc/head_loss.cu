@@ -285,7 +285,7 @@ struct HeadMaps {
   CUtensorMap g;             // G^T
   CUtensorMap g_rows;        // 128 rows
   CUtensorMap g_out;         // 32 x 32
-  CUtensorMap dw, dv;        // dW and dV, 32 x 32
+  CUtensorMap dw, dv;        // dW and dV, 64 x 32
   CUtensorMap acc;           // fp32 sums of dA^T, 32 x 32
 };
 
@@ -482,10 +482,13 @@ __device__ __forceinline__ void give_back(const HalfTile &t) {
   if (t.lane == 0) mbar_arrive_cluster(t.acc_empty);
 }
 
-// use(b, column, values) for each block b of 32 columns
-template <class F>
+// use(b, column, values) for each block b of 32 columns; the two warps take every
+// second one, or with BY64 every second two
+template <bool BY64 = false, class F>
 __device__ __forceinline__ void each_block(const HalfTile &t, F use) {
-  auto column = [&](int b) { return t.part * 32 + b * 64; };
+  auto column = [&](int b) {
+    return BY64 ? t.part * 64 + (b >> 1) * 128 + (b & 1) * 32 : t.part * 32 + b * 64;
+  };
   uint32_t v[2][32];
   if (t.empty) {
 #pragma unroll
@@ -668,29 +671,39 @@ __device__ __forceinline__ void sum_tile(const HeadParams &p, const CUtensorMap 
       bulk_commit();
     }
   });
-  box_is_free(lane);  // the whole box: a dB tile's stores use halves of it
 }
 
-// dB: lanes are vocabulary entries, columns those of [W, V].  Two boxes of 2 KB
-// in turn, as for PROB.
+// dB: lanes are vocabulary entries, columns those of [W, V].  Stored 64 columns
+// at a time, whole lines of 128 bytes.
 __device__ __forceinline__ void weight_tile(const HeadParams &p, const HeadMaps &maps,
                                             const HalfTile &t, int row0) {
   const int lane = t.lane;
   const float scale = *p.rows.scale;
-  each_block(t, [&](int, int c0, uint32_t (&acc)[32]) {
-    const int col = t.n + c0;
-    const bool in_d = col < p.kd * HK;
-    const int left = in_d ? p.d - col : p.rank - (col - p.kd * HK);
-    if (left <= 0 || p.v0 + row0 >= p.vocab) return;
-    float g[32];
+  if (p.v0 + row0 >= p.vocab) {
+    give_back(t);
+    return;
+  }
+  each_block<true>(t, [&](int b, int c0, uint32_t (&acc)[32]) {
+    const int odd = b & 1;
+    if (!odd) box_is_free(lane);
 #pragma unroll
-    for (int e = 0; e < 32; ++e) g[e] = __uint_as_float(acc[e]) * scale;
-    const uint32_t box = put_32x32(t, g);
+    for (int c = 0; c < 4; ++c) {
+      float g[8];
+#pragma unroll
+      for (int e = 0; e < 8; ++e) g[e] = __uint_as_float(acc[8 * c + e]) * scale;
+      st_shared_v4(t.box + lane * 128 + (((odd * 4 + c) ^ (lane & 7)) << 4),
+                   make_uint4(pack_bf16(g[0], g[1]), pack_bf16(g[2], g[3]),
+                              pack_bf16(g[4], g[5]), pack_bf16(g[6], g[7])));
+    }
+    if (!odd) return;
+    fence_proxy_async_smem();
+    __syncwarp();
     if (lane == 0) {
-      if (in_d)
-        tma_store_2d(&maps.dw, box, col, p.v0 + row0);
+      const int col = t.n + c0 - 32;
+      if (col < p.kd * HK)
+        tma_store_2d(&maps.dw, t.box, col, p.v0 + row0);
       else
-        tma_store_2d(&maps.dv, box, col - p.kd * HK, p.v0 + row0);
+        tma_store_2d(&maps.dv, t.box, col - p.kd * HK, p.v0 + row0);
       bulk_commit();
     }
   });
@@ -1242,8 +1255,8 @@ dspark_status head_plan(const HeadArgs &a, bool grad, HeadPlan &o) {
          encode_bf16(&m.g_rows, G, l.rows_pad, l.piece, 128) &&
          encode_2d(&m.g_out, bf16, 2, G, l.rows_pad, l.piece,
                    l.rows_pad, 32, 32) &&
-         encode_2d(&m.dw, bf16, 2, a.dW, a.d, a.vocab, a.d, 32, 32) &&
-         encode_2d(&m.dv, bf16, 2, a.rank ? a.dV : a.dW, vr, a.vocab, vr, 32, 32) &&
+         encode_2d(&m.dw, bf16, 2, a.dW, a.d, a.vocab, a.d, 64, 32) &&
+         encode_2d(&m.dv, bf16, 2, a.rank ? a.dV : a.dW, vr, a.vocab, vr, 64, 32) &&
          encode_2d(&m.acc, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 4, ws + l.acc, l.rows_pad,
                    l.cols_pad * l.splits, l.rows_pad, 32, 32);
   }
