@@ -315,8 +315,10 @@ struct HeadTile {
 // as hold them: tile i of them, the first half as wide as it can be.
 __device__ __forceinline__ void spread(int units, int unit, int width, int tiles, int i,
                                        HeadTile &x) {
-  const int lo = static_cast<int>(static_cast<int64_t>(units) * i / tiles);
-  const int n = static_cast<int>(static_cast<int64_t>(units) * (i + 1) / tiles) - lo;
+  // below 2^28: no more than 2^15 units and 2^12 tiles
+  const int lo = static_cast<int>(static_cast<uint32_t>(units * i) / static_cast<uint32_t>(tiles));
+  const int n = static_cast<int>(static_cast<uint32_t>(units * (i + 1)) /
+                                 static_cast<uint32_t>(tiles)) - lo;
   x.n = lo * unit;
   x.cols[0] = min(n * unit, HT);
   x.cols[1] = n * unit - x.cols[0];
@@ -421,8 +423,8 @@ __device__ __forceinline__ bool head_tile(const HeadParams &p, const HeadWork &w
     row_tile(n_valid, w.width, u % nt, x);
     x.split = u / nt;
     const int kb = p.v_tiles * (HT / HK);
-    x.k0 = static_cast<int>(static_cast<int64_t>(kb) * x.split / p.splits);
-    x.nk = static_cast<int>(static_cast<int64_t>(kb) * (x.split + 1) / p.splits) - x.k0;
+    x.k0 = kb * x.split / p.splits;
+    x.nk = kb * (x.split + 1) / p.splits - x.k0;
     return true;
   }
   if (KIND != kGrad) return false;
@@ -676,9 +678,8 @@ __device__ __forceinline__ void sum_tile(const HeadParams &p, const CUtensorMap 
 // dB: lanes are vocabulary entries, columns those of [W, V].  Stored 64 columns
 // at a time, whole lines of 128 bytes.
 __device__ __forceinline__ void weight_tile(const HeadParams &p, const HeadMaps &maps,
-                                            const HalfTile &t, int row0) {
+                                            const HalfTile &t, int row0, float scale) {
   const int lane = t.lane;
-  const float scale = *p.rows.scale;
   if (p.v0 + row0 >= p.vocab) {
     give_back(t);
     return;
@@ -935,6 +936,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(H_THREADS, 1)
     const uint32_t acc_empty0 = mapa_u32(smem_u32(acc_empty), 0);
     const uint32_t lane_base = tmem_base + (static_cast<uint32_t>(q * 32) << 16);
     const uint32_t box = smem_u32(smem + H_RING + (warp - 4) * H_OUT_BOX);
+    const float scale = KIND == kGrad ? *p.rows.scale : 0.0f;
     int ig = 0, stores = 0;
     bool ok = true;
     float2 *slot = nullptr;
@@ -989,7 +991,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(H_THREADS, 1)
         else if (x.da)
           sum_tile(p, maps.acc, t, x.split, row0);
         else
-          weight_tile(p, maps, t, row0);
+          weight_tile(p, maps, t, row0, scale);
       }
     }
     if (lane == 0) bulk_wait_all();
