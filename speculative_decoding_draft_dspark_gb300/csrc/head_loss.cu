@@ -375,11 +375,13 @@ __device__ __forceinline__ HeadWork head_work(const HeadParams &p, int n_valid, 
   const int n_db = p.v_tiles * ((p.cols_pad + width - 1) / width);
   // times in 64-entry blocks of 256 columns; with fewer columns a block of dA
   // takes as long, for W streams through it (2 rows x 89769 x 1152: 0.28 us a
-  // block); a dB tile's stores take about as long as three
+  // block); a dB tile takes as long as its reduction and about three more for
+  // the stores, but no less than seven (four: 1062 us instead of 965 for 16 rows
+  // x 262144 x 2560, loss and gradient)
   const float t_da = static_cast<float>(p.v_tiles) * (HT / HK) / p.splits *
                      fmaxf(1.0f, static_cast<float>(n_valid) / (HT * (nt > 0 ? nt : 1)));
-  const float t_db = ((n_valid + HK - 1) / HK + 3) * static_cast<float>(p.cols_pad) * p.v_tiles /
-                     (static_cast<float>(HT) * n_db);
+  const float t_db = max((n_valid + HK - 1) / HK + 3, 7) * static_cast<float>(p.cols_pad) *
+                     p.v_tiles / (static_cast<float>(HT) * n_db);
   const int more = w.round % pairs;  // pairs with one dA tile more
   const float gap = t_da / t_db;
   float x = (n_db - (pairs - more) * gap) / pairs, y = x + gap;
@@ -1355,7 +1357,8 @@ HeadLayout head_layout(int32_t M, int32_t vocab, int32_t d, int32_t rank, bool g
     const int64_t nt = (l.rows_pad + HW - 1) / HW, dt = (l.cols_pad + HT - 1) / HT;
     const double deep = static_cast<double>(l.piece) / HK;
     const double t_da = deep * std::max(1.0, M / (static_cast<double>(HT) * nt));
-    const double t_db = (static_cast<double>(M) / HK + 3.0) * l.cols_pad / HT * l.piece / HT;
+    const double t_db = std::max(static_cast<double>(M) / HK + 3.0, 7.0) * l.cols_pad / HT *
+                        l.piece / HT;
     const double share = (static_cast<double>(nt * dt) * t_da + t_db) / kPairs;
     l.splits = static_cast<int32_t>(
         std::max(1.0, std::min({std::ceil(t_da / (0.9 * share)), deep / 8.0, 32.0})));
