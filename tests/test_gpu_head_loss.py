@@ -378,3 +378,36 @@ def test_captured_in_a_graph():
         torch.cuda.synchronize()
         ref, tol = reference(x)
         check({k: v.cpu() for k, v in o.items()}, ref, tol)
+
+
+@pytest.mark.parametrize("M,vocab,d,rank", [(2, 33000, 72, 24), (97, 21003, 136, 0), (7, 9000, 1032, 56)])
+def test_few_rows_in_many_splits(M, vocab, d, rank):
+    """Few rows: the reduction over the vocabulary is split up to 32 times, and a
+    block of 64 columns of dW and dV may lie on either side of d's end."""
+    x = make(M, vocab, d, rank, seed=M)
+    got = run(x)
+    ref, tol = reference(x)
+    assert got["status"] == 0
+    check(got, ref, tol)
+
+
+@pytest.mark.parametrize("d,scale", [(256, 16.0), (2304, 4.0), (2304, -16.0), (4096, 16.0)])
+def test_scores_are_not_too_small(d, scale):
+    """One vocabulary entry: lse is the score itself and the loss 0.  An adder
+    that truncates takes about 2^-26 of a score with each 16 products; a quarter
+    of that is allowed of the mean of 4096 rows' scores (a score's own share means
+    nothing where it is near 0).  The loss: six roundings of
+    2^-24 of the score (its product with log2 e and back, the two constants, the
+    scaling, lse) and 2^-21 for the exponential and the logarithm."""
+    import torch
+    g = torch.Generator().manual_seed(d)
+    W = (torch.randn(1, d, generator=g) * 2.0 / d ** 0.5).bfloat16()
+    w = W.float()
+    h = (torch.randn(4096, d, generator=g) + scale * w / w.square().sum()).bfloat16()
+    x = {"h": h, "W": W, "U": None, "V": None, "prev": None,
+         "target": torch.zeros(4096, dtype=torch.int32), "dloss": torch.ones(4096)}
+    got = run(x, grad=False)
+    z = h.double() @ W.double()[0]
+    lost = ((z - got["lse"].double()).sum() / z.sum()).item()
+    assert abs(lost) <= 0.25 * d / 16 * 2.0 ** -26, lost
+    assert (got["loss"].double().abs() <= 6 * 2.0 ** -24 * z.abs() + 2.0 ** -21).all()
