@@ -226,7 +226,7 @@ __device__ __forceinline__ Philox4 drop8_words(const DropArgs &dr, int base, int
   // Lane g drew the four words of columns 8g .. 8g+7.
   const int t = lane >> 3;
   uint32_t a[4], b[4], q[4];
-  if (L == kPairs) {
+  if constexpr (L == kPairs) {
     // Pair i of lane l wants word l % 4 of lane 8i + l / 4.  In step s, lane l
     // asks for its pair (s + l) % 4, so that lane g is asked for one word only,
     // (g / 8 - s) % 4: four shuffles between a rotation before and one after.
@@ -242,22 +242,22 @@ __device__ __forceinline__ Philox4 drop8_words(const DropArgs &dr, int base, int
     for (int j = 0; j < 4; ++j) b[j] = pick(lane & 2, a[(j + 2) & 3], a[j]);
 #pragma unroll
     for (int j = 0; j < 4; ++j) q[j] = pick(lane & 1, b[(j + 3) & 3], b[j]);
-    return {{q[0], q[1], q[2], q[3]}};
-  }
-  // column e of lane l wants the 16 bits l % 8 of lane 4e + l / 8
+  } else {
+    // column e of lane l wants the 16 bits l % 8 of lane 4e + l / 8
 #pragma unroll
-  for (int e = 0; e < 8; ++e) {
-    const int src = 4 * e + (lane >> 3);
-    const uint32_t w0 = __shfl_sync(0xFFFFFFFFu, p.w[0], src);
-    const uint32_t w1 = __shfl_sync(0xFFFFFFFFu, p.w[1], src);
-    const uint32_t w2 = __shfl_sync(0xFFFFFFFFu, p.w[2], src);
-    const uint32_t w3 = __shfl_sync(0xFFFFFFFFu, p.w[3], src);
-    const uint32_t w = pick(lane & 4, pick(lane & 2, w3, w2), pick(lane & 2, w1, w0));
-    const uint32_t half = lane & 1 ? w >> 16 : w & 0xFFFFu;
-    if (e & 1)
-      q[e / 2] |= half << 16;
-    else
-      q[e / 2] = half;
+    for (int e = 0; e < 8; ++e) {
+      const int src = 4 * e + (lane >> 3);
+      const uint32_t w0 = __shfl_sync(0xFFFFFFFFu, p.w[0], src);
+      const uint32_t w1 = __shfl_sync(0xFFFFFFFFu, p.w[1], src);
+      const uint32_t w2 = __shfl_sync(0xFFFFFFFFu, p.w[2], src);
+      const uint32_t w3 = __shfl_sync(0xFFFFFFFFu, p.w[3], src);
+      const uint32_t w = pick(lane & 4, pick(lane & 2, w3, w2), pick(lane & 2, w1, w0));
+      const uint32_t half = lane & 1 ? w >> 16 : w & 0xFFFFu;
+      if (e & 1)
+        q[e / 2] |= half << 16;
+      else
+        q[e / 2] = half;
+    }
   }
   return {{q[0], q[1], q[2], q[3]}};
 }
@@ -1083,7 +1083,7 @@ cudaError_t norm_grad_launch_t(const NormGradArgs &a, cudaStream_t st) {
     e = cudaFuncSetAttribute(kernel, most, kMaxNormColumns * 4);
     if (e == cudaSuccess)
       e = launch_overlapped(kernel, grid, p.threads, a.dgain ? line : 0, st, a);
-  } else if (COPIED) {
+  } else if constexpr (COPIED) {
     const size_t part = static_cast<size_t>(p.threads) * 16 * p.nv;
     const size_t stage = 3 * part + static_cast<size_t>(p.threads) * 4;
     const auto kernel = p.nv == 1 ? norm_grad_kernel<1> : norm_grad_kernel<2>;
