@@ -49,22 +49,27 @@ __device__ __forceinline__ Philox4 drop_words(const DropArgs &d, int group, int 
 }
 
 // ----------------------------------------------------- eight columns a lane
-// A warp holds 256 columns of a row, in one of three layouts for all tensors of
-// a call:
+// A warp holds 256 columns of a row, in one of four layouts for all tensors of a
+// call:
 //   kWide   rows at 16 bytes, d a multiple of 8: lane l has columns 8l .. 8l+7,
 //           one or two 16-byte accesses
 //   kPairs  bf16 rows at 4 bytes: columns 2l, 64 + 2l, 128 + 2l, 192 + 2l and
 //           their neighbours, four accesses (at 15360 x 2044 the norm takes 42 us,
 //           107 by single columns)
+//   kShifted other bf16 rows: the same columns; where a row begins in the middle
+//           of a word its words are columns 2l - 1 and 2l, and the lanes hand
+//           halves on (at 15360 x 2047 the norm takes 70 us and dropout 48, by
+//           single columns 111 and 57; not for the gradient, 86 us by single
+//           columns and 111 so: its 64 registers do not hold it)
 //   kSingle anything: columns l, 32 + l, ..., 224 + l, eight accesses
 // Every access of the warp is to neighbouring words.
-enum Layout { kWide = 0, kPairs = 1, kSingle = 2 };
+enum Layout { kWide = 0, kPairs = 1, kShifted = 2, kSingle = 3 };
 
 template <int L>
 __device__ __forceinline__ int column(int base, int lane, int e) {
-  return L == kWide    ? base + lane * 8 + e
-         : L == kPairs ? base + (e >> 1) * 64 + lane * 2 + (e & 1)
-                       : base + e * 32 + lane;
+  return L == kWide     ? base + lane * 8 + e
+         : L != kSingle ? base + (e >> 1) * 64 + lane * 2 + (e & 1)
+                        : base + e * 32 + lane;
 }
 
 __device__ __forceinline__ float bf16_lo(uint32_t v) { return __uint_as_float(v << 16); }
@@ -120,11 +125,91 @@ __device__ __forceinline__ V8 join8(const float (&f)[8]) {
   return v;
 }
 
-// eight values as they lie in memory
+// eight values as they lie in memory; kShifted rows that begin in the middle of a
+// word are still a half off, until settle()
 template <bool F32>
 struct Raw {
-  uint32_t w[F32 ? 8 : 4];
+  uint32_t w[F32 ? 8 : 5];
+  bool off;
 };
+
+// A row at 2 bytes: no half word of another row is touched.  Where the row is a half
+// off, a lane's words are columns c - 1 and c, and lane 0 has the last word's next
+// column as well.
+__device__ __forceinline__ void load_shifted(const uint16_t *row, int base, int lane, int d,
+                                             Raw<false> &r) {
+  const int off = static_cast<int>(reinterpret_cast<uintptr_t>(row) >> 1) & 1;
+  const int c = base + lane * 2 - off;
+  const uint16_t *p = row + c;
+  r.off = off;
+  r.w[4] = 0u;
+  if (base + 256 <= d && base >= off) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) r.w[i] = *reinterpret_cast<const uint32_t *>(p + i * 64);
+    if (lane == 0) r.w[4] = row[base + 255];
+    return;
+  }
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const bool lo = c + i * 64 >= 0 && c + i * 64 < d, hi = c + i * 64 + 1 < d;
+    r.w[i] = 0u;
+    if (lo && hi)
+      r.w[i] = *reinterpret_cast<const uint32_t *>(p + i * 64);
+    else if (hi)
+      r.w[i] = static_cast<uint32_t>(p[i * 64 + 1]) << 16;
+    else if (lo)
+      r.w[i] = p[i * 64];
+  }
+  if (lane == 0 && base + 255 < d) r.w[4] = row[base + 255];
+}
+
+// After the loads, by all lanes: the halves to where they belong.
+template <int L>
+__device__ __forceinline__ void settle(Raw<false> &r, int lane) {
+  if (L != kShifted || !r.off) return;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const uint32_t next =
+        __shfl_sync(0xFFFFFFFFu, lane == 0 ? r.w[i + 1] : r.w[i], (lane + 1) & 31);
+    r.w[i] = __byte_perm(r.w[i], next, 0x5432);
+  }
+}
+template <int L>
+__device__ __forceinline__ void settle(Raw<true> &, int) {}
+
+// Pairs of columns, a word W of two halves H each, likewise.
+template <class H, class W>
+__device__ __forceinline__ void store_shifted(H *row, int base, int lane, int d,
+                                              const uint32_t (&w)[4]) {
+  constexpr int B = sizeof(H) * 8;
+  const int c = base + lane * 2;
+  if (!(reinterpret_cast<uintptr_t>(row) & sizeof(H))) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      H *p = row + c + i * 64;
+      if (c + i * 64 + 1 < d)
+        *reinterpret_cast<W *>(p) = static_cast<W>(w[i]);
+      else if (c + i * 64 < d)
+        *p = static_cast<H>(w[i]);
+    }
+    return;
+  }
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const uint32_t before = __shfl_sync(
+        0xFFFFFFFFu, lane == 31 ? w[i > 0 ? i - 1 : 0] : w[i], (lane + 31) & 31);
+    H *p = row + c + i * 64;
+    if (c + i * 64 < d) {
+      if (i == 0 && lane == 0)
+        *p = static_cast<H>(w[i]);
+      else
+        *reinterpret_cast<W *>(p - 1) = static_cast<W>((before >> B) | (w[i] << B));
+    } else if (c + i * 64 == d && (i > 0 || lane > 0)) {
+      p[-1] = static_cast<H>(before >> B);
+    }
+  }
+  if (lane == 31 && base + 255 < d) row[base + 255] = static_cast<H>(w[3] >> B);
+}
 
 template <bool F32, int L>
 __device__ __forceinline__ void load8(const void *row, int base, int lane, int d, Raw<F32> &r) {
@@ -151,6 +236,8 @@ __device__ __forceinline__ void load8(const void *row, int base, int lane, int d
       const int c = column<L>(base, lane, e);
       r.w[e / 2] = c < d ? static_cast<const uint32_t *>(row)[c / 2] : 0u;
     }
+  } else if (L == kShifted) {
+    if constexpr (!F32) load_shifted(static_cast<const uint16_t *>(row), base, lane, d, r);
   } else {
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
@@ -202,6 +289,10 @@ __device__ __forceinline__ void store8(void *row, int base, int lane, int d, con
       const int c = column<L>(base, lane, e);
       if (c < d) static_cast<uint32_t *>(row)[c / 2] = pack_bf16(v[e], v[e + 1]);
     }
+  } else if (L == kShifted) {
+    const uint32_t w[4] = {pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]), pack_bf16(v[4], v[5]),
+                           pack_bf16(v[6], v[7])};
+    store_shifted<uint16_t, uint32_t>(static_cast<uint16_t *>(row), base, lane, d, w);
   } else {
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
@@ -226,7 +317,7 @@ __device__ __forceinline__ Philox4 drop8_words(const DropArgs &dr, int base, int
   // Lane g drew the four words of columns 8g .. 8g+7.
   const int t = lane >> 3;
   uint32_t a[4], b[4], q[4];
-  if constexpr (L == kPairs) {
+  if constexpr (L != kSingle) {
     // Pair i of lane l wants word l % 4 of lane 8i + l / 4.  In step s, lane l
     // asks for its pair (s + l) % 4, so that lane g is asked for one word only,
     // (g / 8 - s) % 4: four shuffles between a rotation before and one after.
@@ -369,6 +460,10 @@ __device__ __forceinline__ void store8_e4m3(uint8_t *row, int base, int lane, in
       if (c < d)
         *reinterpret_cast<uint16_t *>(row + c) = static_cast<uint16_t>(e4m3x2(q[e], q[e + 1]));
     }
+  } else if (L == kShifted) {
+    const uint32_t w[4] = {e4m3x2(q[0], q[1]), e4m3x2(q[2], q[3]), e4m3x2(q[4], q[5]),
+                           e4m3x2(q[6], q[7])};
+    store_shifted<uint8_t, uint16_t>(row, base, lane, d, w);
   } else {
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
@@ -430,6 +525,7 @@ __device__ __forceinline__ V8 times_gain(const void *gain, float rstd, int base,
                                          const V8 &r) {
   Raw<F32> raw;
   load8<F32, L>(gain, base, lane, d, raw);
+  settle<L>(raw, lane);
   const V8 g = unpack8<F32>(raw);
   const uint64_t s = pair(rstd, rstd);
   V8 y;
@@ -473,11 +569,13 @@ __global__ void __launch_bounds__(256) norm_kernel(const NormArgs a, int warps) 
     }
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
+      settle<L>(rx[i], lane);
       r[i] = unpack8<F32>(rx[i]);
       if (a.drop.on)
         r[i] = drop8(a.drop,
                      drop8_words<L>(a.drop, (i * warps + w) * 256, lane, static_cast<int>(row)), r[i]);
       if (a.residual) {
+        settle<L>(rr[i], lane);
         const V8 t = unpack8<F32>(rr[i]);
 #pragma unroll
         for (int e = 0; e < 4; ++e) r[i].p[e] = add2(r[i].p[e], t.p[e]);
@@ -533,9 +631,11 @@ __device__ __forceinline__ V8 stream8(const NormArgs &a, const uint8_t *x, const
   Raw<F32> rx, rr;
   load8<F32, L>(x, base, lane, a.d, rx);
   if (a.residual) load8<F32, L>(res, base, lane, a.d, rr);
+  settle<L>(rx, lane);
   V8 r = unpack8<F32>(rx);
   if (a.drop.on) r = drop8(a.drop, drop8_words<L>(a.drop, base, lane, static_cast<int>(row)), r);
   if (a.residual) {
+    settle<L>(rr, lane);
     const V8 t = unpack8<F32>(rr);
 #pragma unroll
     for (int e = 0; e < 4; ++e) r.p[e] = add2(r.p[e], t.p[e]);
@@ -1001,9 +1101,11 @@ __global__ void __launch_bounds__(256) dropout_kernel(const DropoutArgs a, int r
     if (a.residual)
       load8<F32, L>(static_cast<const uint8_t *>(a.residual) + row * a.residual_stride * E, base,
                       lane, a.d, rs);
+    settle<L>(rx, lane);
     V8 v = unpack8<F32>(rx);
     if (a.drop.on) v = drop8(a.drop, drop8_words<L>(a.drop, base, lane, static_cast<int>(row)), v);
     if (a.residual) {
+      settle<L>(rs, lane);
       const V8 t = unpack8<F32>(rs);
 #pragma unroll
       for (int e = 0; e < 4; ++e) v.p[e] = add2(v.p[e], t.p[e]);
@@ -1145,7 +1247,7 @@ dspark_status norm_launch(const NormArgs &a, cudaStream_t st) {
                              : norm_launch_t<true, kSingle>(a, st));
   return result(l == kWide    ? norm_launch_t<false, kWide>(a, st)
                 : l == kPairs ? norm_launch_t<false, kPairs>(a, st)
-                              : norm_launch_t<false, kSingle>(a, st));
+                              : norm_launch_t<false, kShifted>(a, st));
 }
 
 dspark_status norm_grad_launch(const NormGradArgs &a, cudaStream_t st) {
@@ -1174,7 +1276,7 @@ dspark_status dropout_launch(const DropoutArgs &a, cudaStream_t st) {
                              : dropout_launch_t<true, kSingle>(a, st));
   return result(l == kWide    ? dropout_launch_t<false, kWide>(a, st)
                 : l == kPairs ? dropout_launch_t<false, kPairs>(a, st)
-                              : dropout_launch_t<false, kSingle>(a, st));
+                              : dropout_launch_t<false, kShifted>(a, st));
 }
 
 }  // namespace dspark

@@ -379,3 +379,36 @@ def test_captured_in_a_graph():
     step()
     torch.cuda.synchronize()
     assert all(torch.equal(a, b) for a, b in zip(got, (r, y, rstd, dx, ds, dg)))
+
+
+@pytest.mark.parametrize("M,d,pad,first", [(3, 77, 0, 1), (4, 256, 1, 0), (3, 257, 2, 2), (2, 512, 0, 1),
+                                           (5, 1003, 3, 0), (2, 2049, 0, 3), (2, 8195, 1, 1)])
+def test_rows_at_any_address(M, d, pad, first, monkeypatch):
+    """bf16 rows that begin in the middle of a word, each tensor's elsewhere;
+    nothing beside a row is written."""
+    import sys
+    import torch
+    kept_flat = []
+
+    def placed(M, d, dtype, n, seed, pad=0):
+        g = torch.Generator().manual_seed(seed)
+        out = []
+        for k in range(n):
+            at, step = (first + k) % 4, d + pad
+            flat = torch.full((at + M * step + 8,), -7.0, dtype=dtype, device="cuda")
+            t = flat.as_strided((M, d), (step, 1), at)
+            t.copy_((torch.randn(M, d, generator=g) * (1.0 + k)).to(dtype))
+            kept_flat.append((flat, at, step, d))
+            out.append(t)
+        return out
+
+    monkeypatch.setattr(sys.modules[__name__], "tensors", placed)
+    run_norm(M, d, "bf16", "same", 0.3, pad, True)
+    run_norm(M, d, "bf16", "row8", 0.0, pad, True)
+    run_norm(M, d, "bf16", "group8", 0.3, pad, False)
+    test_norm_grad(M, d, "bf16", 0.3, pad, True, True)
+    test_dropout(M, d, "bf16", 0.3, pad, True)
+    for flat, at, step, d in kept_flat:
+        beside = torch.ones_like(flat, dtype=torch.bool)
+        beside.as_strided((M, d), (step, 1), at)[:] = False
+        assert (flat[beside] == -7.0).all()
