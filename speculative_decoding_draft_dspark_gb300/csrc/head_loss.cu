@@ -181,6 +181,7 @@ __global__ void __launch_bounds__(PACK_THREADS) head_pack_kernel(const PackParam
     total += s_total[w];
     top = fmaxf(top, s_max[w]);
   }
+  if (!(top < INFINITY)) top = 1.0f;  // an infinite one is its own row's alone in dh
   if (first() && blockIdx.x == 0 && tid == 0) {
     *p.rows.n_valid = total;
     if (GRAD) *p.rows.scale = top;

@@ -411,3 +411,16 @@ def test_scores_are_not_too_small(d, scale):
     lost = ((z - got["lse"].double()).sum() / z.sum()).item()
     assert abs(lost) <= 0.25 * d / 16 * 2.0 ** -26, lost
     assert (got["loss"].double().abs() <= 6 * 2.0 ** -24 * z.abs() + 2.0 ** -21).all()
+
+
+@pytest.mark.parametrize("weight", [float("inf"), float("nan")])
+def test_a_weight_that_is_not_finite_stays_in_its_row(weight):
+    import torch
+    x = make(45, 700, 72, 24, seed=11)
+    x["dloss"] = torch.rand(45, generator=torch.Generator().manual_seed(1)) - 0.3
+    ref, tol = reference({**x, "dloss": torch.where(torch.arange(45) == 7, 0.0, x["dloss"])})
+    x["dloss"][7] = weight
+    got = run(x)
+    rest = torch.arange(45) != 7
+    check({"dh": got["dh"][rest]}, {"dh": ref["dh"][rest]}, {"dh": tol["dh"][rest]})
+    assert not torch.isfinite(got["dh"][7]).any()
