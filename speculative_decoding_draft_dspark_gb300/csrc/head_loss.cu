@@ -551,7 +551,8 @@ __device__ __forceinline__ uint32_t put_32x32(const HalfTile &t, const float (&g
 #pragma unroll
   for (int c = 0; c < 4; ++c)
     st_shared_v4(box + t.lane * 64 + ((c ^ ((t.lane >> 1) & 3)) << 4),
-                 make_uint4(pack_bf16(g[8 * c], g[8 * c + 1]), pack_bf16(g[8 * c + 2], g[8 * c + 3]),
+                 make_uint4(pack_bf16(g[8 * c], g[8 * c + 1]),
+                            pack_bf16(g[8 * c + 2], g[8 * c + 3]),
                             pack_bf16(g[8 * c + 4], g[8 * c + 5]),
                             pack_bf16(g[8 * c + 6], g[8 * c + 7])));
   fence_proxy_async_smem();
@@ -1342,7 +1343,7 @@ dspark_status head_plan(const HeadArgs &a, bool grad, HeadPlan &o) {
   o.pack_grid = dim3(std::max(4, (a.M + k.rows_per_cta - 1) / k.rows_per_cta));
   const int64_t most = (l.cols_pad + 1023) / 1024;
   const int64_t parts =
-      std::max<int64_t>(1, std::min<int64_t>(most, 2 * o.sms / static_cast<int64_t>(o.pack_grid.x)));
+      std::max<int64_t>(1, std::min<int64_t>(most, 2 * o.sms / int64_t{o.pack_grid.x}));
   k.cols_per_cta = static_cast<int32_t>(up((l.cols_pad + parts - 1) / parts, HK));
   o.pack_grid.y = static_cast<unsigned>((l.cols_pad + k.cols_per_cta - 1) / k.cols_per_cta);
   return DSPARK_OK;
@@ -1416,9 +1417,10 @@ dspark_status head_loss_launch(const HeadArgs &a, cudaStream_t stream) {
       launch_overlapped(head_pack_kernel<false>, o.pack_grid, PACK_THREADS, 0, stream, o.pack);
   if (e == cudaSuccess) e = head_gemm<kLse>(o, o.p, stream);
   if (e == cudaSuccess)
-    e = launch_overlapped(head_join_kernel, (a.M + JOIN_ROWS - 1) / JOIN_ROWS, JOIN_THREADS, 0, stream,
-                          static_cast<const float2 *>(o.p.partial), head_pairs<kLse>(o, o.p) * 8,
-                          o.p.rows_pad, o.p.rows, o.p.z_more, a.loss, a.lse);
+    e = launch_overlapped(head_join_kernel, (a.M + JOIN_ROWS - 1) / JOIN_ROWS, JOIN_THREADS, 0,
+                          stream, static_cast<const float2 *>(o.p.partial),
+                          head_pairs<kLse>(o, o.p) * 8, o.p.rows_pad, o.p.rows, o.p.z_more, a.loss,
+                          a.lse);
   return e == cudaSuccess ? DSPARK_OK : DSPARK_ERR_CUDA;
 }
 

@@ -260,7 +260,8 @@ __device__ __forceinline__ V8 unpack8(const Raw<F32> &r) {
   V8 v;
 #pragma unroll
   for (int i = 0; i < 4; ++i)
-    v.p[i] = F32 ? pair(__uint_as_float(r.w[F32 ? 2 * i : 0]), __uint_as_float(r.w[F32 ? 2 * i + 1 : 0]))
+    v.p[i] = F32 ? pair(__uint_as_float(r.w[F32 ? 2 * i : 0]),
+                        __uint_as_float(r.w[F32 ? 2 * i + 1 : 0]))
                  : pair(bf16_lo(r.w[i]), bf16_hi(r.w[i]));
   return v;
 }
@@ -572,8 +573,9 @@ __global__ void __launch_bounds__(256) norm_kernel(const NormArgs a, int warps) 
       settle<L>(rx[i], lane);
       r[i] = unpack8<F32>(rx[i]);
       if (a.drop.on)
-        r[i] = drop8(a.drop,
-                     drop8_words<L>(a.drop, (i * warps + w) * 256, lane, static_cast<int>(row)), r[i]);
+        r[i] = drop8(
+            a.drop, drop8_words<L>(a.drop, (i * warps + w) * 256, lane, static_cast<int>(row)),
+            r[i]);
       if (a.residual) {
         settle<L>(rr[i], lane);
         const V8 t = unpack8<F32>(rr[i]);
