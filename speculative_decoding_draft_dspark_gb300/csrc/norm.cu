@@ -166,12 +166,14 @@ __device__ __forceinline__ void load_shifted(const uint16_t *row, int base, int 
 // After the loads, by all lanes: the halves to where they belong.
 template <int L>
 __device__ __forceinline__ void settle(Raw<false> &r, int lane) {
-  if (L != kShifted || !r.off) return;
+  if constexpr (L == kShifted) {
+    if (!r.off) return;
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const uint32_t next =
-        __shfl_sync(0xFFFFFFFFu, lane == 0 ? r.w[i + 1] : r.w[i], (lane + 1) & 31);
-    r.w[i] = __byte_perm(r.w[i], next, 0x5432);
+    for (int i = 0; i < 4; ++i) {
+      const uint32_t next =
+          __shfl_sync(0xFFFFFFFFu, lane == 0 ? r.w[i + 1] : r.w[i], (lane + 1) & 31);
+      r.w[i] = __byte_perm(r.w[i], next, 0x5432);
+    }
   }
 }
 template <int L>
