@@ -40,7 +40,7 @@ constexpr int H_SMEM = H_BAR_OFF + H_BARS * 8 + 16 + 1024;
 constexpr int H_THREADS = (4 + H_EPI_WARPS) * 32;
 constexpr int kPairs = 76;                  // CTA pairs of a GB300: the layout is planned for it
 constexpr uint32_t H_TMEM = 512;            // two accumulators of 256 columns
-static_assert(H_SMEM <= 232448, "shared memory budget");
+static_assert(H_SMEM <= 232448, "shared memory limit");
 
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
