@@ -52,7 +52,7 @@ struct RowInfo {
   int32_t *index;     // [rows_pad] the row's place in the caller's arrays
   int32_t *target;    // [rows_pad]
   int32_t *prev;      // [rows_pad]
-  float *lse2;        // [rows_pad] gradient: lse log2 e
+  float *lse;         // [rows_pad] gradient: as the caller gave it
   float *weight;      // [rows_pad] gradient: dloss / scale
   float *z_target;    // [rows_pad] loss: z at the target
 };
@@ -65,7 +65,7 @@ __host__ __device__ inline RowInfo row_info(uint8_t *at, int64_t rows_pad) {
   r.index = p;
   r.target = p + rows_pad;
   r.prev = p + 2 * rows_pad;
-  r.lse2 = reinterpret_cast<float *>(p + 3 * rows_pad);
+  r.lse = reinterpret_cast<float *>(p + 3 * rows_pad);
   r.weight = reinterpret_cast<float *>(p + 4 * rows_pad);
   r.z_target = reinterpret_cast<float *>(p + 5 * rows_pad);
   return r;
@@ -77,12 +77,12 @@ __device__ __forceinline__ float ex2(float x) {
   return y;
 }
 
-// Scores are held in base 2, and with their largest the sum of 2^(score -
-// base(largest)).  An infinite one is not subtracted from itself: scores of
-// -infinity alone sum to 0, one of +infinity makes the sum infinite.  The largest
-// is kept as it was rounded, so that rescaling a sum by 2^(old - new) is exact
-// where nothing changes (the unrounded one times log2 e each time, as an FMA, is
-// off by the rounding once a tile: 1.5e-5 for a score of 16 joined 20 times).
+// With the largest score goes the sum of e^(score - base(largest)).  An infinite
+// one is not subtracted from itself: scores of -infinity alone sum to 0, one of
+// +infinity makes the sum infinite.  The difference is taken first and then
+// multiplied by log2 e: where nothing changes a sum's rescaling by e^(old - new)
+// is exactly 1, and scores as large as fp32's largest (bf16's lowest value as a
+// mask) do not overflow.
 __device__ __forceinline__ float base(float top) {
   return fabsf(top) == INFINITY ? 0.0f : top;
 }
@@ -218,7 +218,7 @@ __global__ void __launch_bounds__(PACK_THREADS) head_pack_kernel(const PackParam
       p.rows.target[at] = p.target[row];
       p.rows.prev[at] = pv;
       if (GRAD) {
-        p.rows.lse2[at] = p.lse[row] * kLog2e;
+        p.rows.lse[at] = p.lse[row];
         // equal weights (a mean) become exactly 1
         p.rows.weight[at] = top > 0.0f ? p.dloss[row] / top : p.dloss[row];
       }
@@ -246,7 +246,7 @@ __global__ void __launch_bounds__(PACK_THREADS) head_pack_kernel(const PackParam
       *reinterpret_cast<uint4 *>(ar + c) = make_uint4(0u, 0u, 0u, 0u);
     if (first() && lane == 0) {
       p.rows.target[j] = -1;
-      p.rows.lse2[j] = 0.0f;
+      p.rows.lse[j] = 0.0f;
       p.rows.weight[j] = 0.0f;
     }
   }
@@ -621,13 +621,13 @@ __device__ __forceinline__ void lse_tile(const HeadParams &p, const HalfTile &t,
     float m[4] = {z[0], z[1], z[2], z[3]};
 #pragma unroll
     for (int v = 4; v < 32; ++v) m[v & 3] = fmaxf(m[v & 3], z[v]);
-    const float top = fmaxf(old.x, fmaxf(fmaxf(m[0], m[1]), fmaxf(m[2], m[3])) * p.z_log2e);
+    const float top = fmaxf(old.x, fmaxf(fmaxf(m[0], m[1]), fmaxf(m[2], m[3])));
     const float ref = base(top);
     float part[4] = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
-    for (int v = 0; v < 32; ++v) part[v & 3] += ex2(fmaf(z[v], p.z_log2e, -ref));
+    for (int v = 0; v < 32; ++v) part[v & 3] += ex2((z[v] - ref) * p.z_log2e);
     const float sum =
-        fmaf(old.y, ex2(old.x - ref), (part[0] + part[1]) + (part[2] + part[3]));
+        fmaf(old.y, ex2((old.x - ref) * p.z_log2e), (part[0] + part[1]) + (part[2] + part[3]));
     slot[row] = make_float2(top, sum);
   });
 }
@@ -636,23 +636,27 @@ __device__ __forceinline__ void lse_tile(const HeadParams &p, const HalfTile &t,
 // as an operand it has to be, for bf16 products; at most 2^-8 of an entry, and
 // the entries' roundings are independent in the sums.  dloss enters as a share of
 // the largest one, so that a mean's small weights lose nothing.
+__device__ __forceinline__ float prob(const HeadParams &p, uint32_t acc, float lse) {
+  const float z = __uint_as_float(acc);
+  return ex2((fmaf(z, p.z_more, z) - lse) * kLog2e);
+}
 __device__ __forceinline__ void prob_tile(const HeadParams &p, const CUtensorMap &g_out,
                                           const HalfTile &t, int row0) {
   const int lane = t.lane, v_first = p.v0 + row0;
   const bool beyond = v_first + lane >= p.vocab;
   each_block(t, [&](int, int c0, uint32_t (&acc)[32]) {
-    const float4 *lse2 = reinterpret_cast<const float4 *>(p.rows.lse2 + t.n + c0);
+    const float4 *lse = reinterpret_cast<const float4 *>(p.rows.lse + t.n + c0);
     const float4 *weight = reinterpret_cast<const float4 *>(p.rows.weight + t.n + c0);
     const int at = p.rows.target[t.n + c0 + lane] - v_first;
     const uint32_t hits = __ballot_sync(0xFFFFFFFFu, static_cast<uint32_t>(at) < 32u);
     float g[32];
 #pragma unroll
     for (int e = 0; e < 32; e += 4) {
-      const float4 l = lse2[e / 4], w = weight[e / 4];
-      g[e] = ex2(fmaf(__uint_as_float(acc[e]), p.z_log2e, -l.x)) * w.x;
-      g[e + 1] = ex2(fmaf(__uint_as_float(acc[e + 1]), p.z_log2e, -l.y)) * w.y;
-      g[e + 2] = ex2(fmaf(__uint_as_float(acc[e + 2]), p.z_log2e, -l.z)) * w.z;
-      g[e + 3] = ex2(fmaf(__uint_as_float(acc[e + 3]), p.z_log2e, -l.w)) * w.w;
+      const float4 l = lse[e / 4], w = weight[e / 4];
+      g[e] = prob(p, acc[e], l.x) * w.x;
+      g[e + 1] = prob(p, acc[e + 1], l.y) * w.y;
+      g[e + 2] = prob(p, acc[e + 2], l.z) * w.z;
+      g[e + 3] = prob(p, acc[e + 3], l.w) * w.w;
     }
     if (hits) {
       const float own = p.rows.weight[t.n + c0 + lane];
@@ -1050,19 +1054,19 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(H_THREADS, 1)
 constexpr int JOIN_ROWS = 8;
 constexpr int JOIN_THREADS = 1024;
 
-__device__ __forceinline__ float2 join_pairs(float2 a, float2 b) {
+__device__ __forceinline__ float2 join_pairs(float2 a, float2 b, float z_log2e) {
   const float top = fmaxf(a.x, b.x);
   const float ref = base(top);
-  return make_float2(top, a.y * ex2(a.x - ref) + b.y * ex2(b.x - ref));
+  return make_float2(top, a.y * ex2((a.x - ref) * z_log2e) + b.y * ex2((b.x - ref) * z_log2e));
 }
-__device__ __forceinline__ float2 join_across(float2 a, int lanes) {
+__device__ __forceinline__ float2 join_across(float2 a, int lanes, float z_log2e) {
   return join_pairs(a, make_float2(__shfl_xor_sync(0xFFFFFFFFu, a.x, lanes),
-                                   __shfl_xor_sync(0xFFFFFFFFu, a.y, lanes)));
+                                   __shfl_xor_sync(0xFFFFFFFFu, a.y, lanes)), z_log2e);
 }
 
 __global__ void __launch_bounds__(JOIN_THREADS)
     head_join_kernel(const float2 *partial, int slots, int rows_pad, RowInfo rows,
-                     float z_more, float *loss, float *lse) {
+                     float z_more, float z_log2e, float *loss, float *lse) {
   __shared__ float2 part[JOIN_THREADS / 32][JOIN_ROWS];
   allow_next_kernel();
   wait_for_earlier_kernel();
@@ -1081,21 +1085,23 @@ __global__ void __launch_bounds__(JOIN_THREADS)
                                          : make_float2(-INFINITY, 0.0f);
     }
 #pragma unroll
-    for (int u = 0; u < U; ++u) run = join_pairs(run, x[u]);
+    for (int u = 0; u < U; ++u) run = join_pairs(run, x[u], z_log2e);
   }
-  run = join_across(join_across(run, 8), 16);
+  run = join_across(join_across(run, 8, z_log2e), 16, z_log2e);
   if (lane < JOIN_ROWS) part[warp][lane] = run;
   __syncthreads();
   if (warp > 0) return;
   run = part[(lane >> 3) * 8][lane & 7];
 #pragma unroll
-  for (int w = 1; w < 8; ++w) run = join_pairs(run, part[(lane >> 3) * 8 + w][lane & 7]);
-  run = join_across(join_across(run, 8), 16);
+  for (int w = 1; w < 8; ++w) run = join_pairs(run, part[(lane >> 3) * 8 + w][lane & 7], z_log2e);
+  run = join_across(join_across(run, 8, z_log2e), 16, z_log2e);
   if (lane < JOIN_ROWS && row < n_valid) {
     const int i = rows.index[row];
-    const float l = fmaf(log2f(run.y), kLn2, run.x * kLn2), z = rows.z_target[row];
-    lse[i] = l;
-    loss[i] = l - fmaf(z, z_more, z);
+    // the loss by the distance to the largest score, which keeps what the largest
+    // one's own rounding would take from lse
+    const float log_sum = log2f(run.y) * kLn2, d = run.x - rows.z_target[row];
+    lse[i] = fmaf(run.x, z_more, run.x) + log_sum;
+    loss[i] = fmaf(d, z_more, d) + log_sum;
   }
 }
 
@@ -1432,8 +1438,8 @@ dspark_status head_loss_launch(const HeadArgs &a, cudaStream_t stream) {
   if (e == cudaSuccess)
     e = launch_overlapped(head_join_kernel, (a.M + JOIN_ROWS - 1) / JOIN_ROWS, JOIN_THREADS, 0,
                           stream, static_cast<const float2 *>(o.p.partial),
-                          head_pairs<kLse>(o, o.p) * 8, o.p.rows_pad, o.p.rows, o.p.z_more, a.loss,
-                          a.lse);
+                          head_pairs<kLse>(o, o.p) * 8, o.p.rows_pad, o.p.rows, o.p.z_more,
+                          o.p.z_log2e, a.loss, a.lse);
   return e == cudaSuccess ? DSPARK_OK : DSPARK_ERR_CUDA;
 }
 

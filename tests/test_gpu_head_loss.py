@@ -424,3 +424,35 @@ def test_a_weight_that_is_not_finite_stays_in_its_row(weight):
     rest = torch.arange(45) != 7
     check({"dh": got["dh"][rest]}, {"dh": ref["dh"][rest]}, {"dh": tol["dh"][rest]})
     assert not torch.isfinite(got["dh"][7]).any()
+
+
+def test_masks_of_the_lowest_value():
+    """bf16's lowest value as a mask, through a column of V: entries that it masks
+    weigh nothing, and where it masks every entry their scores are equal and
+    finite, so the loss is log vocab.  (A row's score is the mask's value alone
+    there, h being 0.)  The mask adds nothing to what remains, so the bounds are
+    those of the problem without it."""
+    import math
+    import torch
+    lowest = torch.finfo(torch.bfloat16).min
+    M, vocab, d, rank = 40, 600, 64, 16
+    x = make(M, vocab, d, rank, seed=19)
+    x["U"][:], x["V"][:] = 0.0, 0.0
+    x["U"][1, 0] = x["U"][2, 1] = 1.0
+    x["V"][:, 0], x["V"][::2, 1] = lowest, lowest
+    everything, half, nothing = slice(0, 10), slice(10, 30), slice(30, 40)
+    x["prev"][everything], x["prev"][half], x["prev"][nothing] = 1, 2, 3
+    x["h"][everything] = 0.0
+    x["target"][half] |= 1
+    x["dloss"][everything] = 0.0
+    got = run(x)
+    assert got["status"] == 0
+    assert ((got["loss"][everything] - math.log(vocab)).abs() <= 2.0 ** -20 * math.log(vocab)).all()
+    assert ((got["lse"][everything] / lowest - 1).abs() <= 2.0 ** -22).all()
+    for rows, entries in ((half, slice(1, None, 2)), (nothing, slice(None))):
+        part = {k: x[k][rows] for k in ("h", "target", "dloss")}
+        part["target"] = part["target"] // (2 if rows is half else 1)
+        ref, tol = reference({**part, "W": x["W"][entries], "U": None, "V": None, "prev": None})
+        check({k: got[k][rows] for k in ("loss", "lse", "dh")}, ref, tol, ["loss", "lse", "dh"])
+    for k in ("dW", "dU", "dV"):
+        assert torch.isfinite(got[k]).all(), k
