@@ -26,7 +26,9 @@ extern "C" {
 
 /* ------------------------------------------------------------------------
  * Loss.  For each of M rows (request x position, any order):
- *     z_v  = h_i . W_v + U[prev_i] . V_v      (bf16 products, fp32 sums)
+ *     z_v  = h_i . W_v + U[prev_i] . V_v      (bf16 products, fp32 sums: the
+ *            tensor cores', truncated, over up to 64 x 16 products at a time, and
+ *            the chunks' rounded to nearest)
  *     lse  = log sum_v exp z_v
  *     loss = lse - z[target_i]
  * The scores are computed a 256-entry tile at a time and never stored.  A row

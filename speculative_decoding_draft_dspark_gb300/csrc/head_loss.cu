@@ -39,6 +39,12 @@ constexpr int H_BARS = 2 * H_MAX_STAGES + 2 + 2 + 1;
 constexpr int H_SMEM = H_BAR_OFF + H_BARS * 8 + 16 + 1024;
 constexpr int H_THREADS = (4 + H_EPI_WARPS) * 32;
 constexpr int kPairs = 76;                  // CTA pairs of a GB300: the layout is planned for it
+// LSE and PROB: registers of an epilogue thread and of the others.  What the ones
+// gain the others have given up: no more in all than the launch's 168 a thread, which
+// the host checks before the first launch.
+constexpr int H_REGS = 168, H_Z_EPI_REGS = 216, H_Z_OTHER_REGS = 72;
+static_assert(H_EPI_WARPS * H_Z_EPI_REGS + 4 * H_Z_OTHER_REGS <= (4 + H_EPI_WARPS) * H_REGS,
+              "registers of a launch");
 constexpr uint32_t H_TMEM = 512;            // two accumulators of 256 columns
 static_assert(H_SMEM <= 232448, "shared memory limit");
 
@@ -269,7 +275,8 @@ __global__ void __launch_bounds__(PACK_THREADS) head_pack_kernel(const PackParam
 // 512 columns are two halves, both accumulators, for one read of the rows'
 // operand.  The epilogue of a half runs while the other one is still
 // multiplied, and at a tile's start the first half gets ahead as far as the ring
-// holds.  With 256 columns the accumulators are two tiles' in turn.
+// holds.  z^T tiles have up to 256 columns, and the accumulators take turns: a chunk of
+// the reduction each, of one tile after the other.
 //
 // What bounds them.  Many rows: the tensor cores and, after a tenth of a second
 // of them, the 1400 W limit.  1632 columns x 262144 x 2304 (LSE) take 1.17 to
@@ -314,7 +321,7 @@ struct HeadParams {
   int32_t first_piece;
   int32_t d, rank;
   int32_t w_whole, v_whole;  // d and rank are multiples of 64: the wide maps hold
-  float z_more, z_log2e;     // a score is its accumulator times 1 + z_more
+  int32_t chunk;        // z^T: steps of 16 products that an accumulator adds up, even
   float2 *partial;
   uint4 *zeroed;             // GRAD: what it sets to zero (dU), and how many
   int64_t n_zeroed;
@@ -350,9 +357,8 @@ __device__ __forceinline__ void row_tile(int n_valid, int width, int i, HeadTile
   spread((n_valid + HU - 1) / HU, HU, width, row_tiles(n_valid, width), i, x);
 }
 
-// Width of the tiles whose columns are rows of A.  z^T tiles have both
-// accumulators in turn, one half each: their epilogues (an exponential for each
-// entry) take a fifth of a tile's time and hide only behind another tile (512
+// Width of the tiles whose columns are rows of A.  z^T tiles leave an accumulator
+// to the chunk that follows: their epilogues (an exponential for each entry) take a fifth of a tile's time and hide only behind another tile (512
 // columns: 1280 us instead of 1190 at 1613 rows x 262144 x 2304).  dA^T tiles
 // have a long reduction and a short epilogue (256 columns: 19.8 ms instead of
 // 18.9 for 6452 rows, loss and gradient).
@@ -536,6 +542,53 @@ __device__ __forceinline__ void each_block(const HalfTile &t, F use) {
   }
 }
 
+// z^T: the warp's columns of a tile, 32 of each block.  The tensor cores truncate
+// their running sum each time they add 16 products to it, which takes up to an ulp
+// of that sum towards zero; over a whole reduction of 2304 scores that grow evenly
+// come out 2.1e-6 of themselves too small, others not at all.  So an accumulator
+// adds up a chunk of the reduction only (HeadParams::chunk), and the chunks are added
+// here, rounded to nearest, while the next ones are multiplied.  In five chunks
+// 1613 rows x 262144 x 2304 take 2 to 3 % longer than in one, 601 x 50003 x 1000 a
+// tenth; short reductions, whose epilogues are as long as their products, a quarter
+// to two fifths (256 and 576 entries).
+struct Scores {
+  float z[4][32];
+};
+
+// two blocks are on their way at once
+__device__ __forceinline__ void add_chunk(const HalfTile &t, Scores &s) {
+  auto column = [&](int b) { return t.part * 32 + b * 64; };
+#pragma unroll
+  for (int b = 0; b < 4; b += 2) {
+    if (column(b) >= t.cols) break;
+    uint32_t v[2][32];
+    const bool two = column(b + 1) < t.cols;
+    tmem_ld_32x32b_x32(t.acc + column(b), v[0]);
+    if (two) tmem_ld_32x32b_x32(t.acc + column(b + 1), v[1]);
+    tmem_ld_wait(v[0]);
+    if (b == 2 || column(2) >= t.cols) give_back(t);
+#pragma unroll
+    for (int e = 0; e < 32; ++e) s.z[b][e] += __uint_as_float(v[0][e]);
+    if (two) {
+      tmem_ld_wait(v[1]);
+#pragma unroll
+      for (int e = 0; e < 32; ++e) s.z[b + 1][e] += __uint_as_float(v[1][e]);
+    }
+  }
+  if (column(0) >= t.cols) give_back(t);
+}
+
+// use(b, column, scores) for each block of 32 columns
+template <class F>
+__device__ __forceinline__ void each_scores(const HalfTile &t, Scores &s, F use) {
+#pragma unroll
+  for (int b = 0; b < 4; ++b) {
+    const int c = t.part * 32 + b * 64;
+    if (c >= t.cols) break;
+    use(b, c, s.z[b]);
+  }
+}
+
 __device__ __forceinline__ void box_is_free(int lane) {
   if (lane == 0) bulk_wait_read<0>();  // the last store has read it
   __syncwarp();
@@ -585,21 +638,22 @@ __device__ __forceinline__ LseRows lse_rows(const HeadParams &p, const float2 *s
   return r;
 }
 
-__device__ __forceinline__ void lse_tile(const HeadParams &p, const HalfTile &t, int v_first,
-                                         const LseRows &rows, float2 *slot) {
+__device__ __forceinline__ void lse_tile(const HeadParams &p, const HalfTile &t, Scores &scores,
+                                         int v_first, const LseRows &rows, float2 *slot) {
   const int lane = t.lane;
   const bool beyond = v_first + lane >= p.vocab;
-  each_block(t, [&](int b, int c0, uint32_t (&acc)[32]) {
+  each_scores(t, scores, [&](int b, int c0, float (&own)[32]) {
     const int row = t.n + c0 + lane;
     if (beyond) {
 #pragma unroll
-      for (int e = 0; e < 32; ++e) acc[e] = 0xFF800000u;  // -infinity
+      for (int e = 0; e < 32; ++e) own[e] = -INFINITY;
     }
     __syncwarp();  // the block before has been read
 #pragma unroll
     for (int c = 0; c < 8; ++c)
       st_shared_v4(t.box + lane * 128 + ((c ^ (lane & 7)) << 4),
-                   make_uint4(acc[4 * c], acc[4 * c + 1], acc[4 * c + 2], acc[4 * c + 3]));
+                   make_uint4(__float_as_uint(own[4 * c]), __float_as_uint(own[4 * c + 1]),
+                              __float_as_uint(own[4 * c + 2]), __float_as_uint(own[4 * c + 3])));
     __syncwarp();
     float z[32];
 #pragma unroll
@@ -625,9 +679,9 @@ __device__ __forceinline__ void lse_tile(const HeadParams &p, const HalfTile &t,
     const float ref = base(top);
     float part[4] = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
-    for (int v = 0; v < 32; ++v) part[v & 3] += ex2((z[v] - ref) * p.z_log2e);
+    for (int v = 0; v < 32; ++v) part[v & 3] += ex2((z[v] - ref) * kLog2e);
     const float sum =
-        fmaf(old.y, ex2((old.x - ref) * p.z_log2e), (part[0] + part[1]) + (part[2] + part[3]));
+        fmaf(old.y, ex2((old.x - ref) * kLog2e), (part[0] + part[1]) + (part[2] + part[3]));
     slot[row] = make_float2(top, sum);
   });
 }
@@ -636,15 +690,12 @@ __device__ __forceinline__ void lse_tile(const HeadParams &p, const HalfTile &t,
 // as an operand it has to be, for bf16 products; at most 2^-8 of an entry, and
 // the entries' roundings are independent in the sums.  dloss enters as a share of
 // the largest one, so that a mean's small weights lose nothing.
-__device__ __forceinline__ float prob(const HeadParams &p, uint32_t acc, float lse) {
-  const float z = __uint_as_float(acc);
-  return ex2((fmaf(z, p.z_more, z) - lse) * kLog2e);
-}
+__device__ __forceinline__ float prob(float z, float lse) { return ex2((z - lse) * kLog2e); }
 __device__ __forceinline__ void prob_tile(const HeadParams &p, const CUtensorMap &g_out,
-                                          const HalfTile &t, int row0) {
+                                          const HalfTile &t, Scores &scores, int row0) {
   const int lane = t.lane, v_first = p.v0 + row0;
   const bool beyond = v_first + lane >= p.vocab;
-  each_block(t, [&](int, int c0, uint32_t (&acc)[32]) {
+  each_scores(t, scores, [&](int, int c0, float (&z)[32]) {
     const float4 *lse = reinterpret_cast<const float4 *>(p.rows.lse + t.n + c0);
     const float4 *weight = reinterpret_cast<const float4 *>(p.rows.weight + t.n + c0);
     const int at = p.rows.target[t.n + c0 + lane] - v_first;
@@ -653,10 +704,10 @@ __device__ __forceinline__ void prob_tile(const HeadParams &p, const CUtensorMap
 #pragma unroll
     for (int e = 0; e < 32; e += 4) {
       const float4 l = lse[e / 4], w = weight[e / 4];
-      g[e] = prob(p, acc[e], l.x) * w.x;
-      g[e + 1] = prob(p, acc[e + 1], l.y) * w.y;
-      g[e + 2] = prob(p, acc[e + 2], l.z) * w.z;
-      g[e + 3] = prob(p, acc[e + 3], l.w) * w.w;
+      g[e] = prob(z[e], l.x) * w.x;
+      g[e + 1] = prob(z[e + 1], l.y) * w.y;
+      g[e + 2] = prob(z[e + 2], l.z) * w.z;
+      g[e + 3] = prob(z[e + 3], l.w) * w.w;
     }
     if (hits) {
       const float own = p.rows.weight[t.n + c0 + lane];
@@ -793,175 +844,214 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(H_THREADS, 1)
   const int stage_bytes = H_RING / stages;
   HeadTile x;
 
-  if (warp == 0) {
-    // ---------------------------------------------------------- loads
-    const uint32_t one = elect_one();
-    const uint32_t full0 = mapa_u32(smem_u32(full), 0), ring = smem_u32(smem);
-    bool ok = true;
-    int s = 0;
-    uint32_t phase = 1u;
-    for (int i = 0; ok && head_tile<KIND>(p, work, n_valid, pair, pairs, i, x); ++i) {
-      // this CTA's half of each half's columns, in whole blocks of 64
-      const int mine[2] = {x.cols[0] / 2, x.cols[1] / 2};
-      const int col0[2] = {x.n + cta * mine[0], x.n + x.cols[0] + cta * mine[1]};
-      const int blocks[2] = {(mine[0] + 63) / 64, (mine[1] + 63) / 64};
-      const uint32_t bytes = 2 * (H_OPERAND + (blocks[0] + blocks[1]) * H_BOX);
-      for (int kb = x.k0; kb < x.k0 + x.nk; ++kb) {
-        ok = __all_sync(0xFFFFFFFFu, wait_bounded(&empty[s], phase, abort_flag, p.status));
-        if (!ok) break;
-        if (cta == 0 && one) mbar_arrive_expect_tx(&full[s], bytes);
-        __syncwarp();
-        const uint32_t bar = full0 + s * 8;
-        const uint32_t sa = ring + s * stage_bytes, sb = sa + H_OPERAND;
-        if (KIND != kGrad) {
-          const bool in_d = kb < p.kd;
-          tma_load_2d_pair(one, sa, in_d ? &maps.w_rows : &maps.v_rows, bar,
-                           (in_d ? kb : kb - p.kd) * HK, p.v0 + x.m + cta * 128);
-          // few and large copies, also of fewer rows: exact ones of 64, 32 and
-          // 16 rows instead took up to 1.3 times as long
+  if (warp < 4) {
+    if (KIND != kGrad) registers_down<H_Z_OTHER_REGS>();
+    if (warp == 0) {
+      // ---------------------------------------------------------- loads
+      const uint32_t one = elect_one();
+      const uint32_t full0 = mapa_u32(smem_u32(full), 0), ring = smem_u32(smem);
+      bool ok = true;
+      int s = 0;
+      uint32_t phase = 1u;
+      for (int i = 0; ok && head_tile<KIND>(p, work, n_valid, pair, pairs, i, x); ++i) {
+        // this CTA's half of each half's columns, in whole blocks of 64
+        const int mine[2] = {x.cols[0] / 2, x.cols[1] / 2};
+        const int col0[2] = {x.n + cta * mine[0], x.n + x.cols[0] + cta * mine[1]};
+        const int blocks[2] = {(mine[0] + 63) / 64, (mine[1] + 63) / 64};
+        const uint32_t bytes = 2 * (H_OPERAND + (blocks[0] + blocks[1]) * H_BOX);
+        for (int kb = x.k0; kb < x.k0 + x.nk; ++kb) {
+          ok = __all_sync(0xFFFFFFFFu, wait_bounded(&empty[s], phase, abort_flag, p.status));
+          if (!ok) break;
+          if (cta == 0 && one) mbar_arrive_expect_tx(&full[s], bytes);
+          __syncwarp();
+          const uint32_t bar = full0 + s * 8;
+          const uint32_t sa = ring + s * stage_bytes, sb = sa + H_OPERAND;
+          if (KIND != kGrad) {
+            const bool in_d = kb < p.kd;
+            tma_load_2d_pair(one, sa, in_d ? &maps.w_rows : &maps.v_rows, bar,
+                             (in_d ? kb : kb - p.kd) * HK, p.v0 + x.m + cta * 128);
+            // few and large copies, also of fewer rows: exact ones of 64, 32 and
+            // 16 rows instead took up to 1.3 times as long
 #pragma unroll
-          for (int h = 0; h < HALVES; ++h)
-            if (blocks[h])
-              tma_load_2d_pair(one, sb + h * H_OPERAND, blocks[h] == 2 ? &maps.a_rows : &maps.a,
-                               bar, kb * HK, col0[h]);
-        } else if (x.da) {
-          const int cb = (x.m + cta * 128) / HK;
-          const bool in_d = cb < p.kd || p.kr == 0, both = in_d == (cb + 1 < p.kd || p.kr == 0);
-          if (both && (in_d ? p.w_whole : p.v_whole)) {
-            tma_load_3d_pair(one, sa, in_d ? &maps.w_wide : &maps.v_wide, bar, 0, p.v0 + kb * HK,
-                             in_d ? cb : cb - p.kd);
-          } else {
-#pragma unroll
-            for (int j = 0; j < 2; ++j) {
-              const bool d = cb + j < p.kd || p.kr == 0;
-              tma_load_2d_pair(one, sa + j * H_BOX, d ? &maps.w : &maps.v, bar,
-                               (d ? cb + j : cb + j - p.kd) * HK, p.v0 + kb * HK);
-            }
-          }
-          // G^T's columns: any 16 of them begin a block
-#pragma unroll
-          for (int h = 0; h < HALVES; ++h)
-#pragma unroll
-            for (int j = 0; j < 2; ++j)
-              if (j < blocks[h])
-                tma_load_2d_pair(one, sb + h * H_OPERAND + j * H_BOX, &maps.g, bar,
-                                 col0[h] + j * 64, kb * HK);
-        } else {
-          tma_load_2d_pair(one, sa, &maps.g_rows, bar, kb * HK, x.m + cta * 128);
-#pragma unroll
-          for (int h = 0; h < HALVES; ++h) {
-            if (mine[h] == 128) {
-              tma_load_3d_pair(one, sb + h * H_OPERAND, &maps.a_wide, bar, 0, kb * HK,
-                               col0[h] / 64);
+            for (int h = 0; h < HALVES; ++h)
+              if (blocks[h])
+                tma_load_2d_pair(one, sb + h * H_OPERAND, blocks[h] == 2 ? &maps.a_rows : &maps.a,
+                                 bar, kb * HK, col0[h]);
+          } else if (x.da) {
+            const int cb = (x.m + cta * 128) / HK;
+            const bool in_d = cb < p.kd || p.kr == 0, both = in_d == (cb + 1 < p.kd || p.kr == 0);
+            if (both && (in_d ? p.w_whole : p.v_whole)) {
+              tma_load_3d_pair(one, sa, in_d ? &maps.w_wide : &maps.v_wide, bar, 0, p.v0 + kb * HK,
+                               in_d ? cb : cb - p.kd);
             } else {
+#pragma unroll
+              for (int j = 0; j < 2; ++j) {
+                const bool d = cb + j < p.kd || p.kr == 0;
+                tma_load_2d_pair(one, sa + j * H_BOX, d ? &maps.w : &maps.v, bar,
+                                 (d ? cb + j : cb + j - p.kd) * HK, p.v0 + kb * HK);
+              }
+            }
+            // G^T's columns: any 16 of them begin a block
+#pragma unroll
+            for (int h = 0; h < HALVES; ++h)
 #pragma unroll
               for (int j = 0; j < 2; ++j)
                 if (j < blocks[h])
-                  tma_load_2d_pair(one, sb + h * H_OPERAND + j * H_BOX, &maps.a, bar,
+                  tma_load_2d_pair(one, sb + h * H_OPERAND + j * H_BOX, &maps.g, bar,
                                    col0[h] + j * 64, kb * HK);
+          } else {
+            tma_load_2d_pair(one, sa, &maps.g_rows, bar, kb * HK, x.m + cta * 128);
+#pragma unroll
+            for (int h = 0; h < HALVES; ++h) {
+              if (mine[h] == 128) {
+                tma_load_3d_pair(one, sb + h * H_OPERAND, &maps.a_wide, bar, 0, kb * HK,
+                                 col0[h] / 64);
+              } else {
+#pragma unroll
+                for (int j = 0; j < 2; ++j)
+                  if (j < blocks[h])
+                    tma_load_2d_pair(one, sb + h * H_OPERAND + j * H_BOX, &maps.a, bar,
+                                     col0[h] + j * 64, kb * HK);
+              }
             }
           }
-        }
-        if (++s == stages) {
-          s = 0;
-          phase ^= 1u;
-        }
-      }
-    }
-    if (!ok) {
-      // copies in flight land before the shared memory is given back
-      const uint64_t t0 = global_timer_ns();
-      while (global_timer_ns() - t0 < 20000000ull) __nanosleep(1000);
-    }
-    __syncwarp();
-  } else if (warp == 1) {
-    // ------------------------------------------------------------ MMA
-    if (cta == 0) {
-      const uint32_t one = elect_one();
-      const uint32_t base = smem_u32(smem);
-      const uint32_t empty0 = smem_u32(empty), acc_full0 = smem_u32(acc_full);
-      bool ok = true;
-      int s = 0, ig = 0;
-      uint32_t phase = 0u;
-      for (int i = 0; ok && head_tile<KIND>(p, work, n_valid, pair, pairs, i, x); ++i) {
-        if (x.nk == 0) continue;
-        const bool a_mn = KIND == kGrad && x.da, b_mn = KIND == kGrad;
-        const uint32_t a_step = desc_step(a_mn), b_step = desc_step(b_mn);
-        const uint32_t a_lo = desc_lo(base, a_mn);
-        const uint32_t majors = (a_mn ? 1u << 15 : 0u) | (b_mn ? 1u << 16 : 0u);
-        const uint32_t idesc[2] = {
-            umma_idesc_bf16_f32(HT, static_cast<uint32_t>(x.cols[0])) | majors,
-            umma_idesc_bf16_f32(HT, static_cast<uint32_t>(x.cols[1])) | majors};
-        const uint32_t d_tmem[2] = {tmem_base + static_cast<uint32_t>((ig & 1) * HT),
-                                    tmem_base + static_cast<uint32_t>((~ig & 1) * HT)};
-        const uint32_t b_lo[2] = {desc_lo(base + H_OPERAND, b_mn),
-                                  desc_lo(base + 2 * H_OPERAND, b_mn)};
-        auto multiply = [&](int half, int stage, int kb) {
-          const uint32_t at = static_cast<uint32_t>(stage * stage_bytes) >> 4;
-          const uint32_t a = a_lo + at, b = b_lo[half] + at;
-          // dB's reduction ends with the rows: no 16 of them are multiplied
-          // that hold none (nor were written)
-          const int left = KIND == kGrad && !x.da ? n_valid - kb * HK : HK;
-#pragma unroll
-          for (int kk = 0; kk < HK / 16; ++kk)
-            umma_bf16_pair(left > kk * 16 ? one : 0u, d_tmem[half], a + kk * a_step,
-                           b + kk * b_step, kDescHi, idesc[half], kb | kk);
-        };
-        auto acc_free = [&](int g) {
-          ok = __all_sync(0xFFFFFFFFu, wait_bounded(&acc_empty[g & 1], ((g >> 1) & 1) ^ 1u,
-                                                    abort_flag, p.status));
-          tc_fence_after();
-          return ok;
-        };
-        auto arrived = [&] {
-          ok = __all_sync(0xFFFFFFFFu, wait_bounded(&full[s], phase, abort_flag, p.status));
-          tc_fence_after();
-          return ok;
-        };
-        auto advance = [&] {
           if (++s == stages) {
             s = 0;
             phase ^= 1u;
           }
-        };
-        const bool two = HALVES == 2 && x.cols[1] > 0;
-        if (!acc_free(ig)) break;
-        int kb = 0;
-        if (two) {
-          // the first half alone, until the second one's accumulator is free
-          const int s0 = s;
-          const int ahead = min(stages - 1, x.nk);
-          for (; kb < ahead; ++kb) {
+        }
+      }
+      if (!ok) {
+        // copies in flight land before the shared memory is given back
+        const uint64_t t0 = global_timer_ns();
+        while (global_timer_ns() - t0 < 20000000ull) __nanosleep(1000);
+      }
+      __syncwarp();
+    } else if (warp == 1) {
+      // ------------------------------------------------------------ MMA
+      if (cta == 0) {
+        const uint32_t one = elect_one();
+        const uint32_t base = smem_u32(smem);
+        const uint32_t empty0 = smem_u32(empty), acc_full0 = smem_u32(acc_full);
+        bool ok = true;
+        int s = 0, ig = 0;
+        uint32_t phase = 0u;
+        for (int i = 0; ok && head_tile<KIND>(p, work, n_valid, pair, pairs, i, x); ++i) {
+          if (x.nk == 0) continue;
+          const bool a_mn = KIND == kGrad && x.da, b_mn = KIND == kGrad;
+          const uint32_t a_step = desc_step(a_mn), b_step = desc_step(b_mn);
+          const uint32_t a_lo = desc_lo(base, a_mn);
+          const uint32_t majors = (a_mn ? 1u << 15 : 0u) | (b_mn ? 1u << 16 : 0u);
+          const uint32_t idesc[2] = {
+              umma_idesc_bf16_f32(HT, static_cast<uint32_t>(x.cols[0])) | majors,
+              umma_idesc_bf16_f32(HT, static_cast<uint32_t>(x.cols[1])) | majors};
+          const uint32_t d_tmem[2] = {tmem_base + static_cast<uint32_t>((ig & 1) * HT),
+                                      tmem_base + static_cast<uint32_t>((~ig & 1) * HT)};
+          const uint32_t b_lo[2] = {desc_lo(base + H_OPERAND, b_mn),
+                                    desc_lo(base + 2 * H_OPERAND, b_mn)};
+          auto multiply = [&](int half, int stage, int kb) {
+            const uint32_t at = static_cast<uint32_t>(stage * stage_bytes) >> 4;
+            const uint32_t a = a_lo + at, b = b_lo[half] + at;
+            // dB's reduction ends with the rows: no 16 of them are multiplied
+            // that hold none (nor were written)
+            const int left = KIND == kGrad && !x.da ? n_valid - kb * HK : HK;
+#pragma unroll
+            for (int kk = 0; kk < HK / 16; ++kk)
+              umma_bf16_pair(left > kk * 16 ? one : 0u, d_tmem[half], a + kk * a_step,
+                             b + kk * b_step, kDescHi, idesc[half], kb | kk);
+          };
+          auto acc_free = [&](int g) {
+            ok = __all_sync(0xFFFFFFFFu, wait_bounded(&acc_empty[g & 1], ((g >> 1) & 1) ^ 1u,
+                                                      abort_flag, p.status));
+            tc_fence_after();
+            return ok;
+          };
+          auto arrived = [&] {
+            ok = __all_sync(0xFFFFFFFFu, wait_bounded(&full[s], phase, abort_flag, p.status));
+            tc_fence_after();
+            return ok;
+          };
+          auto advance = [&] {
+            if (++s == stages) {
+              s = 0;
+              phase ^= 1u;
+            }
+          };
+          if (KIND != kGrad) {
+            // an accumulator for each chunk of the reduction, in turn
+            int step = 0;
+            for (int kb = 0; kb < x.nk; ++kb) {
+              if (!arrived()) break;
+              const uint32_t at = static_cast<uint32_t>(s * stage_bytes) >> 4;
+#pragma unroll
+              for (int kk = 0; kk < HK / 16; ++kk) {
+                if (step == 0 && !acc_free(ig)) break;
+                umma_bf16_pair(one, tmem_base + static_cast<uint32_t>((ig & 1) * HT),
+                               a_lo + at + kk * a_step, b_lo[0] + at + kk * b_step, kDescHi,
+                               idesc[0], step);
+                if (++step == p.chunk || (kb == x.nk - 1 && kk == HK / 16 - 1)) {
+                  umma_commit_pair(one, acc_full0 + (ig & 1) * 8);
+                  ++ig;
+                  step = 0;
+                }
+              }
+              if (!ok) break;
+              umma_commit_pair(one, empty0 + s * 8);
+              advance();
+            }
+            if (!ok) break;
+            continue;
+          }
+          const bool two = HALVES == 2 && x.cols[1] > 0;
+          if (!acc_free(ig)) break;
+          int kb = 0;
+          if (two) {
+            // the first half alone, until the second one's accumulator is free
+            const int s0 = s;
+            const int ahead = min(stages - 1, x.nk);
+            for (; kb < ahead; ++kb) {
+              if (!arrived()) break;
+              multiply(0, s, kb);
+              advance();
+            }
+            if (!ok) break;
+            if (ahead == x.nk) umma_commit_pair(one, acc_full0 + (ig & 1) * 8);
+            if (!acc_free(ig + 1)) break;
+            for (int k = 0, t = s0; k < ahead; ++k) {
+              multiply(1, t, k);
+              umma_commit_pair(one, empty0 + t * 8);
+              t = t + 1 == stages ? 0 : t + 1;
+            }
+          }
+          for (; kb < x.nk; ++kb) {
             if (!arrived()) break;
             multiply(0, s, kb);
+            if (kb == x.nk - 1) umma_commit_pair(one, acc_full0 + (ig & 1) * 8);
+            if (two) multiply(1, s, kb);
+            umma_commit_pair(one, empty0 + s * 8);
             advance();
           }
           if (!ok) break;
-          if (ahead == x.nk) umma_commit_pair(one, acc_full0 + (ig & 1) * 8);
-          if (!acc_free(ig + 1)) break;
-          for (int k = 0, t = s0; k < ahead; ++k) {
-            multiply(1, t, k);
-            umma_commit_pair(one, empty0 + t * 8);
-            t = t + 1 == stages ? 0 : t + 1;
-          }
+          if (two) umma_commit_pair(one, acc_full0 + ((ig + 1) & 1) * 8);
+          ig += two ? 2 : 1;
         }
-        for (; kb < x.nk; ++kb) {
-          if (!arrived()) break;
-          multiply(0, s, kb);
-          if (kb == x.nk - 1) umma_commit_pair(one, acc_full0 + (ig & 1) * 8);
-          if (two) multiply(1, s, kb);
-          umma_commit_pair(one, empty0 + s * 8);
-          advance();
-        }
-        if (!ok) break;
-        if (two) umma_commit_pair(one, acc_full0 + ((ig + 1) & 1) * 8);
-        ig += two ? 2 : 1;
+        umma_commit_pair(one, smem_u32(mma_done));
       }
-      umma_commit_pair(one, smem_u32(mma_done));
+      __syncwarp();
+    } else if (KIND == kGrad) {
+      // dU, of which the last kernel writes the rows with a token.  Beside the
+      // products and without a launch of its own: loss and gradient of 64 rows x
+      // 32000 x (1024 + 256) 100 us instead of 106, 250 x 262144 x (2048 + 256) 964
+      // instead of 972; by PROB's warps the z tiles took longer.
+      const int64_t step = static_cast<int64_t>(gridDim.x) * 64;
+      for (int64_t i = static_cast<int64_t>(blockIdx.x) * 64 + threadIdx.x - 64; i < p.n_zeroed;
+           i += step)
+        p.zeroed[i] = make_uint4(0u, 0u, 0u, 0u);
     }
-    __syncwarp();
-  } else if (warp >= 4) {
+  } else {
     // ------------------------------------------------------- epilogue
+    // the scores of a z^T tile take 128 registers of a thread
+    if (KIND != kGrad) registers_up<H_Z_EPI_REGS>();
     const int q = warp & 3, part = (warp - 4) >> 2;
     const uint32_t acc_empty0 = mapa_u32(smem_u32(acc_empty), 0);
     const uint32_t lane_base = tmem_base + (static_cast<uint32_t>(q * 32) << 16);
@@ -991,50 +1081,76 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(H_THREADS, 1)
     }
     for (int i = 0; ok && head_tile<KIND>(p, work, n_valid, pair, pairs, i, x); ++i) {
       const int row0 = x.m + cta * 128 + q * 32;  // the warp's first output row
-      LseRows rows;
-      if (KIND == kLse) rows = lse_rows(p, slot, i < period, x.n, x.cols[0], part, lane);
-#pragma unroll 1
-      for (int h = 0; h < HALVES; ++h) {
-        if (x.cols[h] == 0) break;
-        const int buf = ig & 1;
-        if (x.nk > 0) {
-          ok = __all_sync(0xFFFFFFFFu,
-                          wait_bounded(&acc_full[buf], (ig >> 1) & 1, abort_flag, p.status));
-          if (!ok) break;
-          tc_fence_after();
-          ++ig;
-        }
+      if constexpr (KIND != kGrad) {
+        LseRows rows;
+        if (KIND == kLse) rows = lse_rows(p, slot, i < period, x.n, x.cols[0], part, lane);
         HalfTile t;
-        t.n = x.n + h * x.cols[0];
-        t.cols = x.cols[h];
+        t.n = x.n;
+        t.cols = x.cols[0];
         t.part = part;
-        t.empty = x.nk == 0;
-        t.acc = lane_base + static_cast<uint32_t>(buf * HT);
+        t.empty = false;
         t.box = box;
-        t.acc_empty = acc_empty0 + buf * 8;
         t.lane = lane;
         t.stores = &stores;
+        Scores scores;
+        auto arrived = [&] {
+          const int buf = ig & 1;
+          ok = __all_sync(0xFFFFFFFFu,
+                          wait_bounded(&acc_full[buf], (ig >> 1) & 1, abort_flag, p.status));
+          tc_fence_after();
+          t.acc = lane_base + static_cast<uint32_t>(buf * HT);
+          t.acc_empty = acc_empty0 + buf * 8;
+          ++ig;
+          return ok;
+        };
+        const int chunks = (x.nk * (HK / 16) + p.chunk - 1) / p.chunk;
+        scores = {};
+#pragma unroll 1
+        for (int c = 0; c < chunks && arrived(); ++c) add_chunk(t, scores);
+        if (!ok) break;
         if (KIND == kLse)
-          lse_tile(p, t, p.v0 + row0, rows, slot);
-        else if (KIND == kProb)
-          prob_tile(p, maps.g_out, t, row0);
-        else if (x.da)
-          sum_tile(p, maps.acc, t, x.split, row0);
+          lse_tile(p, t, scores, p.v0 + row0, rows, slot);
         else
-          weight_tile(p, maps, t, row0, scale);
+          prob_tile(p, maps.g_out, t, scores, row0);
+      } else {
+#pragma unroll 1
+        for (int h = 0; h < HALVES; ++h) {
+          if (x.cols[h] == 0) break;
+          const int buf = ig & 1;
+          if (x.nk > 0) {
+            ok = __all_sync(0xFFFFFFFFu,
+                            wait_bounded(&acc_full[buf], (ig >> 1) & 1, abort_flag, p.status));
+            if (!ok) break;
+            tc_fence_after();
+            ++ig;
+          }
+          HalfTile t;
+          t.n = x.n + h * x.cols[0];
+          t.cols = x.cols[h];
+          t.part = part;
+          t.empty = x.nk == 0;
+          t.acc = lane_base + static_cast<uint32_t>(buf * HT);
+          t.box = box;
+          t.acc_empty = acc_empty0 + buf * 8;
+          t.lane = lane;
+          t.stores = &stores;
+          if (x.da)
+            sum_tile(p, maps.acc, t, x.split, row0);
+          else
+            weight_tile(p, maps, t, row0, scale);
+        }
       }
     }
     if (lane == 0) bulk_wait_all();
     __syncwarp();
-  } else if (KIND == kGrad) {
-    // dU, of which the last kernel writes the rows with a token.  Beside the
-    // products and without a launch of its own: loss and gradient of 64 rows x
-    // 32000 x (1024 + 256) 100 us instead of 106, 250 x 262144 x (2048 + 256) 964
-    // instead of 972; by PROB's warps the z tiles took longer.
-    const int64_t step = static_cast<int64_t>(gridDim.x) * 64;
-    for (int64_t i = static_cast<int64_t>(blockIdx.x) * 64 + threadIdx.x - 64; i < p.n_zeroed;
-         i += step)
-      p.zeroed[i] = make_uint4(0u, 0u, 0u, 0u);
+    if (KIND != kGrad) {
+      // all alike again; the warpgroup meets between two changes
+      if (part == 0)
+        warpgroup_sync<1>();
+      else
+        warpgroup_sync<2>();
+      registers_down<H_Z_OTHER_REGS>();
+    }
   }
 
   tc_fence_before();
@@ -1054,19 +1170,19 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(H_THREADS, 1)
 constexpr int JOIN_ROWS = 8;
 constexpr int JOIN_THREADS = 1024;
 
-__device__ __forceinline__ float2 join_pairs(float2 a, float2 b, float z_log2e) {
+__device__ __forceinline__ float2 join_pairs(float2 a, float2 b) {
   const float top = fmaxf(a.x, b.x);
   const float ref = base(top);
-  return make_float2(top, a.y * ex2((a.x - ref) * z_log2e) + b.y * ex2((b.x - ref) * z_log2e));
+  return make_float2(top, a.y * ex2((a.x - ref) * kLog2e) + b.y * ex2((b.x - ref) * kLog2e));
 }
-__device__ __forceinline__ float2 join_across(float2 a, int lanes, float z_log2e) {
+__device__ __forceinline__ float2 join_across(float2 a, int lanes) {
   return join_pairs(a, make_float2(__shfl_xor_sync(0xFFFFFFFFu, a.x, lanes),
-                                   __shfl_xor_sync(0xFFFFFFFFu, a.y, lanes)), z_log2e);
+                                   __shfl_xor_sync(0xFFFFFFFFu, a.y, lanes)));
 }
 
 __global__ void __launch_bounds__(JOIN_THREADS)
     head_join_kernel(const float2 *partial, int slots, int rows_pad, RowInfo rows,
-                     float z_more, float z_log2e, float *loss, float *lse) {
+                     float *loss, float *lse) {
   __shared__ float2 part[JOIN_THREADS / 32][JOIN_ROWS];
   allow_next_kernel();
   wait_for_earlier_kernel();
@@ -1085,23 +1201,23 @@ __global__ void __launch_bounds__(JOIN_THREADS)
                                          : make_float2(-INFINITY, 0.0f);
     }
 #pragma unroll
-    for (int u = 0; u < U; ++u) run = join_pairs(run, x[u], z_log2e);
+    for (int u = 0; u < U; ++u) run = join_pairs(run, x[u]);
   }
-  run = join_across(join_across(run, 8, z_log2e), 16, z_log2e);
+  run = join_across(join_across(run, 8), 16);
   if (lane < JOIN_ROWS) part[warp][lane] = run;
   __syncthreads();
   if (warp > 0) return;
   run = part[(lane >> 3) * 8][lane & 7];
 #pragma unroll
-  for (int w = 1; w < 8; ++w) run = join_pairs(run, part[(lane >> 3) * 8 + w][lane & 7], z_log2e);
-  run = join_across(join_across(run, 8, z_log2e), 16, z_log2e);
+  for (int w = 1; w < 8; ++w) run = join_pairs(run, part[(lane >> 3) * 8 + w][lane & 7]);
+  run = join_across(join_across(run, 8), 16);
   if (lane < JOIN_ROWS && row < n_valid) {
     const int i = rows.index[row];
     // the loss by the distance to the largest score, which keeps what the largest
     // one's own rounding would take from lse
-    const float log_sum = log2f(run.y) * kLn2, d = run.x - rows.z_target[row];
-    lse[i] = fmaf(run.x, z_more, run.x) + log_sum;
-    loss[i] = fmaf(d, z_more, d) + log_sum;
+    const float log_sum = log2f(run.y) * kLn2;
+    lse[i] = run.x + log_sum;
+    loss[i] = (run.x - rows.z_target[row]) + log_sum;
   }
 }
 
@@ -1277,6 +1393,12 @@ dspark_status head_plan(const HeadArgs &a, bool grad, HeadPlan &o) {
           cudaFuncSetAttribute(head_gemm_kernel<kProb>, at, H_SMEM) != cudaSuccess ||
           cudaFuncSetAttribute(head_gemm_kernel<kGrad>, at, H_SMEM) != cudaSuccess)
         return DSPARK_ERR_CUDA;
+      // an increase of registers beyond the launch's own would wait for ever
+      cudaFuncAttributes lse = {}, prob = {};
+      if (cudaFuncGetAttributes(&lse, head_gemm_kernel<kLse>) != cudaSuccess ||
+          cudaFuncGetAttributes(&prob, head_gemm_kernel<kProb>) != cudaSuccess ||
+          lse.numRegs < H_REGS || prob.numRegs < H_REGS)
+        return DSPARK_ERR_CUDA;
       g_head_attr[dev] = true;
     }
   }
@@ -1322,14 +1444,12 @@ dspark_status head_plan(const HeadArgs &a, bool grad, HeadPlan &o) {
   p.first_piece = 0;
   p.zeroed = nullptr;
   p.n_zeroed = 0;
-  // The tensor cores truncate their running sum each time they add to it, 16
-  // products at a time, so scores come out too small, on the mean by 2^-26 of
-  // themselves for each 16 (measured 1.46e-8 to 1.56e-8 for 256 to 4096 of them
-  // and scores of 1 to 16 of either sign).  Scaled back, the error of the loss is
-  // 1.8e-7 at 262144 entries x 2304 instead of 7.6e-7.
   const int adds = (a.d + 15) / 16 + (a.rank + 15) / 16;
-  p.z_more = static_cast<float>(adds) * (1.0f / (1 << 26));
-  p.z_log2e = static_cast<float>(1.4426950408889634 * (1.0 + static_cast<double>(p.z_more)));
+  // A chunk is a bit more than a fifth of the reduction, and at most 64 additions: a
+  // score that grows evenly loses n + 1 of 2^-26 of itself for n additions to a
+  // chunk (measured for 16 to 256 of them), a quarter or less of what one accumulator
+  // would take, and one whose sums are exact loses nothing.
+  p.chunk = std::max(2, std::min(64, adds * 2 / 9 / 2 * 2));
   p.d = a.d;
   p.rank = a.rank;
   p.partial = reinterpret_cast<float2 *>(ws + l.partial);
@@ -1438,8 +1558,7 @@ dspark_status head_loss_launch(const HeadArgs &a, cudaStream_t stream) {
   if (e == cudaSuccess)
     e = launch_overlapped(head_join_kernel, (a.M + JOIN_ROWS - 1) / JOIN_ROWS, JOIN_THREADS, 0,
                           stream, static_cast<const float2 *>(o.p.partial),
-                          head_pairs<kLse>(o, o.p) * 8, o.p.rows_pad, o.p.rows, o.p.z_more,
-                          o.p.z_log2e, a.loss, a.lse);
+                          head_pairs<kLse>(o, o.p) * 8, o.p.rows_pad, o.p.rows, a.loss, a.lse);
   return e == cudaSuccess ? DSPARK_OK : DSPARK_ERR_CUDA;
 }
 

@@ -26,8 +26,11 @@ __device__ __forceinline__ uint32_t mapa_u32(uint32_t addr, uint32_t rank) {
   return d;
 }
 
+// Without a release: it orders tensor memory only, by the fence before it, and a
+// release at the cluster's scope would wait for the thread's earlier stores (some 1000
+// cycles, once for every accumulator).
 __device__ __forceinline__ void mbar_arrive_cluster(uint32_t cluster_addr) {
-  asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(
+  asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(
                    cluster_addr)
                : "memory");
 }
@@ -146,6 +149,23 @@ __device__ __forceinline__ void umma_commit_pair(uint32_t one, uint32_t bar) {
       "b64 [%0], %1;\n\t}" ::"r"(bar),
       "h"(static_cast<uint16_t>(3)), "r"(one)
       : "memory");
+}
+
+// ------------------------------------------------------------- registers
+// The warps of a warpgroup (four, from a multiple of four) give registers back, or
+// wait for as many as they then have; by all threads of all four, which meet at a
+// barrier between two such changes.
+template <int BARRIER>
+__device__ __forceinline__ void warpgroup_sync() {
+  asm volatile("bar.sync %0, 128;" ::"n"(BARRIER) : "memory");
+}
+template <int N>
+__device__ __forceinline__ void registers_down() {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
+}
+template <int N>
+__device__ __forceinline__ void registers_up() {
+  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
 }
 
 }  // namespace dspark

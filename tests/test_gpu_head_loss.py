@@ -456,3 +456,43 @@ def test_masks_of_the_lowest_value():
         check({k: got[k][rows] for k in ("loss", "lse", "dh")}, ref, tol, ["loss", "lse", "dh"])
     for k in ("dW", "dU", "dV"):
         assert torch.isfinite(got[k]).all(), k
+
+
+@pytest.mark.parametrize("d,rank", [(256, 0), (2048, 256), (4096, 256), (65536, 0), (65536, 256)])
+@pytest.mark.parametrize("where", ["one", "first", "last", "all"])
+def test_exact_scores_stay_exact(d, rank, where):
+    """One vocabulary entry, so that lse is the score and the loss and its gradient
+    are 0.  The factors are integers, and every product and sum of a row's is an
+    integer below 2^24, which fp32 and an adder that truncates both hold: the
+    score has no error at all, in one column of h, at the reduction's beginning,
+    at its end (the factors' part) or all over it."""
+    import torch
+    M, g = 300, torch.Generator().manual_seed(d + rank)
+    n = lambda *s: torch.randint(-8, 9, s, generator=g).float()  # noqa: E731
+    h, W, U, V = n(M, d), n(1, d), n(1, rank), n(1, rank)
+    if where == "one":
+        keep = torch.zeros(d)
+        keep[d // 3] = 1.0
+        W[0, d // 3] = 5.0
+        h[:, d // 3] += 16.0
+    else:
+        keep = torch.zeros(d)
+        keep[:40] = where in ("first", "all")
+        keep[-40:] = where in ("last", "all") and rank == 0 or where == "all"
+        keep[40:-40] = where == "all"
+    h *= keep
+    if where in ("one", "first"):
+        U[:] = 0.0
+    x = {k: v.bfloat16() for k, v in (("h", h), ("W", W), ("U", U), ("V", V))}
+    if rank == 0:
+        x["U"] = x["V"] = None
+    x.update(prev=torch.zeros(M, dtype=torch.int32) if rank else None,
+             target=torch.zeros(M, dtype=torch.int32), dloss=torch.ones(M))
+    got = run(x)
+    z = (h.double() @ W.double().T)[:, 0]
+    if rank:
+        z += (U.double() @ V.double().T)[0, 0]
+    assert 0 < z.abs().max() < 2 ** 24
+    assert torch.equal(got["lse"].double(), z)
+    for k in ("loss", "dh", "dW") + (("dU", "dV") if rank else ()):
+        assert torch.all(got[k] == 0), k
