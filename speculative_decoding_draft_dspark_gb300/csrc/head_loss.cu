@@ -358,10 +358,11 @@ __device__ __forceinline__ void row_tile(int n_valid, int width, int i, HeadTile
 }
 
 // Width of the tiles whose columns are rows of A.  z^T tiles leave an accumulator
-// to the chunk that follows: their epilogues (an exponential for each entry) take a fifth of a tile's time and hide only behind another tile (512
-// columns: 1280 us instead of 1190 at 1613 rows x 262144 x 2304).  dA^T tiles
-// have a long reduction and a short epilogue (256 columns: 19.8 ms instead of
-// 18.9 for 6452 rows, loss and gradient).
+// to the chunk that follows: their epilogues (an exponential for each entry) take a
+// fifth of a tile's time and hide only behind other products (512 columns: 1280 us
+// instead of 1190 at 1613 rows x 262144 x 2304).  dA^T tiles have a long reduction
+// and a short epilogue (256 columns: 19.8 ms instead of 18.9 for 6452 rows, loss and
+// gradient).
 template <int KIND>
 __device__ __forceinline__ int row_width(int n_valid) {
   return KIND == kGrad && n_valid > HT ? HW : HT;

@@ -414,7 +414,7 @@ __device__ __forceinline__ float row_max_nan(float v, float *slots, int group, i
   return warp_max_nan(lane < warps ? slots[group * warps + lane] : 0.0f);
 }
 
-// eight e4m3 numbers of y / scale
+// two e4m3 numbers
 __device__ __forceinline__ uint32_t e4m3x2(float lo, float hi) {
   uint16_t r;
   asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(hi), "f"(lo));
@@ -424,63 +424,84 @@ __device__ __forceinline__ uint32_t e4m3x2(float lo, float hi) {
 constexpr float kE4m3Max = 448.0f;
 
 __device__ __forceinline__ float scale_of(float top) {
-  return top == 0.0f ? 1.0f : top * (1.0f / kE4m3Max);
+  return top == 0.0f ? 1.0f : top / kE4m3Max;
 }
 
-// y / scale, where e4m3 will keep 4 bits: a product with the reciprocal (an ulp
-// off, half the instructions of a division); where that would overflow, it
-// divides.
-__device__ __forceinline__ void over_scale(V8 &y, float scale) {
-  if (scale > 1e-35f || scale != scale) {
-    float inv;
-    asm("rcp.approx.f32 %0, %1;" : "=f"(inv) : "f"(scale));
-    const uint64_t i2 = pair(inv, inv);
+// The bytes of y / scale, the quotient that fp32 division gives.  Rounding is
+// monotone: where products with a little less and a little more than 1 / scale give
+// the same byte, the quotient between them has it too (each is off by three
+// roundings of 2^-24, the quotient by one; 2^-21 is put between).  Where they differ,
+// next to a tie, or where the reciprocal would overflow, it is divided.  15360 x 2048
+// with a scale for 128 columns take 39.0 us, 45.2 if all is divided, and 37.5 with
+// the reciprocal alone, whose bytes next to a tie are a step off.
+struct Quotients {
+  float scale;
+  uint64_t less, more;
+  bool divide;
+};
+
+__device__ __forceinline__ Quotients by_scale(float scale) {
+  Quotients q;
+  const float inv = 1.0f / scale;
+  const float less = inv * (1.0f - 0x1p-21f), more = inv * (1.0f + 0x1p-21f);
+  q.scale = scale;
+  q.less = pair(less, less);
+  q.more = pair(more, more);
+  q.divide = scale <= 1e-35f;
+  return q;
+}
+
+// pairs FIRST .. FIRST + N - 1 of the eight
+template <int FIRST, int N>
+__device__ __forceinline__ void e4m3_of(const V8 &y, const Quotients &q, uint32_t (&w)[4]) {
+  uint32_t differ = q.divide;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) y.p[i] = mul2(y.p[i], i2);
-  } else {
-    float v[8];
-    split8(y, v);
+  for (int i = FIRST; i < FIRST + N; ++i) {
+    float a, b;
+    halves(mul2(y.p[i], q.less), a, b);
+    w[i] = e4m3x2(a, b);
+    halves(mul2(y.p[i], q.more), a, b);
+    differ |= w[i] ^ e4m3x2(a, b);
+  }
+  if (differ) {
 #pragma unroll
-    for (int e = 0; e < 8; ++e) v[e] /= scale;
-    y = join8(v);
+    for (int i = FIRST; i < FIRST + N; ++i) {
+      float a, b;
+      halves(y.p[i], a, b);
+      w[i] = e4m3x2(a / q.scale, b / q.scale);
+    }
   }
 }
 
 template <int L>
 __device__ __forceinline__ void store8_e4m3(uint8_t *row, int base, int lane, int d,
-                                            const V8 &x) {
-  float q[8];
-  split8(x, q);
+                                            const uint32_t (&w)[4]) {
   if (L == kWide) {
     const int c = base + lane * 8;
     if (c >= d) return;
-    *reinterpret_cast<uint2 *>(row + c) = make_uint2(e4m3x2(q[0], q[1]) | e4m3x2(q[2], q[3]) << 16,
-                                                     e4m3x2(q[4], q[5]) | e4m3x2(q[6], q[7]) << 16);
+    *reinterpret_cast<uint2 *>(row + c) = make_uint2(w[0] | w[1] << 16, w[2] | w[3] << 16);
   } else if (L == kPairs) {
 #pragma unroll
     for (int e = 0; e < 8; e += 2) {
       const int c = column<L>(base, lane, e);
-      if (c < d)
-        *reinterpret_cast<uint16_t *>(row + c) = static_cast<uint16_t>(e4m3x2(q[e], q[e + 1]));
+      if (c < d) *reinterpret_cast<uint16_t *>(row + c) = static_cast<uint16_t>(w[e / 2]);
     }
   } else if (L == kShifted) {
-    const uint32_t w[4] = {e4m3x2(q[0], q[1]), e4m3x2(q[2], q[3]), e4m3x2(q[4], q[5]),
-                           e4m3x2(q[6], q[7])};
     store_shifted<uint8_t, uint16_t>(row, base, lane, d, w);
   } else {
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
       const int c = column<L>(base, lane, e);
-      if (c < d) row[c] = static_cast<uint8_t>(e4m3x2(q[e], 0.0f) & 0xFFu);
+      if (c < d) row[c] = static_cast<uint8_t>(w[e / 2] >> (8 * (e & 1)));
     }
   }
 }
 
-// y -> y / scale with a scale for 128 columns: 16 lanes if a lane's columns are
+// The bytes with a scale for 128 columns: 16 lanes if a lane's columns are
 // neighbours, else the warp's first or last four
 template <int L>
 __device__ __forceinline__ void by_groups(const NormArgs &a, int64_t row, int base, int lane,
-                                          V8 &y) {
+                                          const V8 &y, uint32_t (&w)[4]) {
   float v[8];
   split8(y, v);
   float t0 = 0.0f, t1 = 0.0f;
@@ -495,16 +516,13 @@ __device__ __forceinline__ void by_groups(const NormArgs &a, int64_t row, int ba
     const float s = scale_of(t0);
     if ((lane & 15) == 0 && base + lane * 8 < a.d)
       a.scale[row * a.groups + (base + lane * 8) / 128] = s;
-    over_scale(y, s);
+    e4m3_of<0, 4>(y, by_scale(s), w);
   } else {
     const float s0 = scale_of(warp_max_nan(t0)), s1 = scale_of(warp_max_nan(t1));
     if (lane == 0 && base < a.d) a.scale[row * a.groups + base / 128] = s0;
     if (lane == 0 && base + 128 < a.d) a.scale[row * a.groups + base / 128 + 1] = s1;
-    V8 q = y;
-    over_scale(q, s0);
-    over_scale(y, s1);
-    y.p[0] = q.p[0];
-    y.p[1] = q.p[1];
+    e4m3_of<0, 2>(y, by_scale(s0), w);
+    e4m3_of<2, 2>(y, by_scale(s1), w);
   }
 }
 
@@ -542,7 +560,7 @@ __device__ __forceinline__ V8 times_gain(const void *gain, float rstd, int base,
 // column 256 (i warps + w)); a CTA has as many rows as fit.  Up to four chunks a
 // warp: one row's loads are all in flight before its sum, and most rows need one
 // or two warps and a barrier of few.  At 15360 x 2048 bf16 39 us in 16 bits (95%
-// of measured HBM), 37.5 in 8 bits with a scale for 128 columns (87%: the scales'
+// of measured HBM), 39 in 8 bits with a scale for 128 columns (84%: the scales'
 // maxima and conversions), 45 with dropout as well (72%: the ten rounds of each
 // Philox block, for which the integer multipliers are the limit).  Few rows: the
 // latency of a load, a sum and a store, 3.7 us for 56 rows.
@@ -606,8 +624,9 @@ __global__ void __launch_bounds__(256) norm_kernel(const NormArgs a, int warps) 
       } else if (a.group == 0) {
         top = top8(top, r[i]);
       } else {
-        by_groups<L>(a, row, base, lane, r[i]);
-        store8_e4m3<L>(yo, base, lane, a.d, r[i]);
+        uint32_t bytes[4];
+        by_groups<L>(a, row, base, lane, r[i], bytes);
+        store8_e4m3<L>(yo, base, lane, a.d, bytes);
       }
     }
   }
@@ -616,10 +635,12 @@ __global__ void __launch_bounds__(256) norm_kernel(const NormArgs a, int warps) 
     if (live) {
       if (w == 0 && lane == 0) a.scale[row] = s;
       uint8_t *yo = static_cast<uint8_t *>(a.y) + row * a.y_stride;
+      const Quotients q = by_scale(s);
 #pragma unroll
       for (int i = 0; i < NV; ++i) {
-        over_scale(r[i], s);
-        store8_e4m3<L>(yo, (i * warps + w) * 256, lane, a.d, r[i]);
+        uint32_t bytes[4];
+        e4m3_of<0, 4>(r[i], q, bytes);
+        store8_e4m3<L>(yo, (i * warps + w) * 256, lane, a.d, bytes);
       }
     }
   }
@@ -680,16 +701,17 @@ __global__ void __launch_bounds__(WIDE_WARPS * 32) norm_wide_kernel(const NormAr
   for (int base = w * 256; base < a.d; base += WIDE_WARPS * 256) {
     const V8 r = stream8<F32, L>(a, x, res, row, base, lane);
     if (a.r) store8<F32, L>(ro, base, lane, a.d, r);
-    V8 y = times_gain<F32, L>(a.gain, rstd, base, lane, a.d, r);
+    const V8 y = times_gain<F32, L>(a.gain, rstd, base, lane, a.d, r);
     if (!a.e4m3) {
       store8<F32, L>(yo, base, lane, a.d, y);
       continue;
     }
+    uint32_t bytes[4];
     if (a.group == 0)
-      over_scale(y, s);
+      e4m3_of<0, 4>(y, by_scale(s), bytes);
     else
-      by_groups<L>(a, row, base, lane, y);
-    store8_e4m3<L>(yo, base, lane, a.d, y);
+      by_groups<L>(a, row, base, lane, y, bytes);
+    store8_e4m3<L>(yo, base, lane, a.d, bytes);
   }
 }
 

@@ -412,3 +412,27 @@ def test_rows_at_any_address(M, d, pad, first, monkeypatch):
         beside = torch.ones_like(flat, dtype=torch.bool)
         beside.as_strided((M, d), (step, 1), at)[:] = False
         assert (flat[beside] == -7.0).all()
+
+
+@pytest.mark.parametrize("d", [1024, 1003])
+@pytest.mark.parametrize("out", ["row8", "group8"])
+def test_bytes_are_the_quotients_rounded_to_nearest(out, d):
+    """The same call with y in 32 bits gives the kernel's own y: scale is max |y| /
+    448 and the bytes y / scale, both as fp32 divides, and rounded to nearest even.
+    Enough elements that some lie within an ulp of a tie."""
+    import torch
+    from speculative_decoding_draft_dspark_gb300 import head as H
+    M, group = 4096, 128 if out == "group8" else 0
+    x, res, y = tensors(M, d, torch.float32, 3, 77)
+    gain = torch.rand(d, generator=torch.Generator().manual_seed(d)).cuda() + 0.5
+    H.dspark_residual_norm(x, res, gain, None, y, None, None, eps=1e-6)
+    n = -(-d // 128) if group else 1
+    scale = torch.zeros(M, n, device="cuda")
+    q = torch.empty(M, d, dtype=torch.float8_e4m3fn, device="cuda")
+    H.dspark_residual_norm(x, res, gain, None, q, scale, None, eps=1e-6, group=group)
+    width = group or d
+    parts = torch.nn.functional.pad(y.cpu(), (0, n * width - d)).reshape(M, n, width)
+    want = parts.abs().amax(2) / 448.0
+    assert torch.equal(scale.cpu(), want)
+    byte = (parts / want[:, :, None]).reshape(M, n * width)[:, :d].to(torch.float8_e4m3fn)
+    assert torch.equal(q.cpu().view(torch.uint8), byte.contiguous().view(torch.uint8))
