@@ -95,8 +95,9 @@ DSPARK_API dspark_status dspark_head_loss_grad(
  * y              out [M, d]: of dtype, or DSPARK_E4M3 (one byte each, y_dtype)
  *                with scales: group 0 = one scale for a row, group 128 = one
  *                for each 128 columns (the last may be narrower).  scale =
- *                max |y| / 448 over its columns (1 where that is 0), and the
- *                byte is y / scale rounded to nearest even; scale is fp32
+ *                max |y| / 448 over its columns (1 where that fp32 quotient is
+ *                0), and the byte is y / scale, divided in fp32 too, rounded to
+ *                nearest even; scale is fp32
  *                [M, ceil(d / 128)] or [M], contiguous.  group and scale are
  *                not used when y is of dtype.
  * rstd           out [M] fp32: 1 / sqrt(mean r^2 + eps), or NULL.

@@ -424,7 +424,8 @@ __device__ __forceinline__ uint32_t e4m3x2(float lo, float hi) {
 constexpr float kE4m3Max = 448.0f;
 
 __device__ __forceinline__ float scale_of(float top) {
-  return top == 0.0f ? 1.0f : top / kE4m3Max;
+  const float s = top / kE4m3Max;
+  return s == 0.0f ? 1.0f : s;  // also where it underflows
 }
 
 // The bytes of y / scale, the quotient that fp32 division gives.  Rounding is

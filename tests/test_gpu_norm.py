@@ -436,3 +436,20 @@ def test_bytes_are_the_quotients_rounded_to_nearest(out, d):
     assert torch.equal(scale.cpu(), want)
     byte = (parts / want[:, :, None]).reshape(M, n * width)[:, :d].to(torch.float8_e4m3fn)
     assert torch.equal(q.cpu().view(torch.uint8), byte.contiguous().view(torch.uint8))
+
+
+@pytest.mark.parametrize("out", ["row8", "group8"])
+@pytest.mark.parametrize("d", [256, 300])
+def test_scale_that_underflows_is_one(out, d):
+    """Values below 448 x 2^-150: max |y| / 448 is 0 in fp32, the scale 1 and every
+    byte 0, of the zeros among them too."""
+    import torch
+    from speculative_decoding_draft_dspark_gb300 import head as H
+    M = 4
+    x = torch.ones(M, d, device="cuda")
+    x[:, ::3] = 0.0
+    gain = torch.full((d,), 2.0 ** -143, device="cuda")       # y below 2^-142
+    scale = torch.zeros(M, -(-d // 128) if out == "group8" else 1, device="cuda")
+    q = torch.ones(M, d, device="cuda").to(torch.float8_e4m3fn)
+    H.dspark_residual_norm(x, None, gain, None, q, scale, None, eps=1e-6, group=128 if out == "group8" else 0)
+    assert torch.all(scale == 1.0) and torch.all(q.float() == 0.0)
