@@ -693,7 +693,8 @@ __device__ __forceinline__ void lse_tile(const HeadParams &p, const HalfTile &t,
 // the largest one, so that a mean's small weights lose nothing.
 __device__ __forceinline__ float prob(float z, float lse) { return ex2((z - lse) * kLog2e); }
 __device__ __forceinline__ void prob_tile(const HeadParams &p, const CUtensorMap &g_out,
-                                          const HalfTile &t, Scores &scores, int row0) {
+                                          const HalfTile &t, Scores &scores, int row0,
+                                          int n_valid) {
   const int lane = t.lane, v_first = p.v0 + row0;
   const bool beyond = v_first + lane >= p.vocab;
   each_scores(t, scores, [&](int, int c0, float (&z)[32]) {
@@ -719,9 +720,13 @@ __device__ __forceinline__ void prob_tile(const HeadParams &p, const CUtensorMap
         if (v == lane) g[e] -= w;
       }
     }
-    if (beyond) {
+    // Zero by choice, not by a product with 0, for entries and rows that there are
+    // not: the rows that fill up a 16 of dB's reduction score NaN at an entry that
+    // holds an infinity (a mask in V, say).
+    const int live = beyond ? 0 : n_valid - (t.n + c0);
+    if (live < 32) {
 #pragma unroll
-      for (int e = 0; e < 32; ++e) g[e] = 0.0f;
+      for (int e = 0; e < 32; ++e) g[e] = e < live ? g[e] : 0.0f;
     }
     const uint32_t box = put_32x32(t, g);
     if (lane == 0) {
@@ -1112,7 +1117,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(H_THREADS, 1)
         if (KIND == kLse)
           lse_tile(p, t, scores, p.v0 + row0, rows, slot);
         else
-          prob_tile(p, maps.g_out, t, scores, row0);
+          prob_tile(p, maps.g_out, t, scores, row0, n_valid);
       } else {
 #pragma unroll 1
         for (int h = 0; h < HALVES; ++h) {

@@ -496,3 +496,32 @@ def test_exact_scores_stay_exact(d, rank, where):
     assert torch.equal(got["lse"].double(), z)
     for k in ("loss", "dh", "dW") + (("dU", "dV") if rank else ()):
         assert torch.all(got[k] == 0), k
+
+
+@pytest.mark.parametrize("counted", [15, 16, 17, 33, 300])
+def test_an_infinite_mask_stays_in_its_entries(counted):
+    """V holds -infinity where U[prev] holds 1: masked entries score -infinity and
+    weigh nothing, so their dW and dV are 0, also where the counted rows do not fill
+    up a 16.  (dU is not defined there: the formula multiplies 0 by infinity.)"""
+    import torch
+    vocab, d, rank = 500, 64, 16
+    x = make(counted, vocab, d, rank, seed=23)
+    masked = torch.arange(vocab) % 3 == 1
+    x["U"][:, 0] = 1.0
+    x["V"][:, 0] = torch.where(masked, -float("inf"), 0.0)
+    x["target"] = x["target"] // 3 * 3 % vocab
+    assert not masked[x["target"].long()].any()
+    got = run(x)
+    keep = (~masked).nonzero()[:, 0]
+    place = torch.full((vocab,), -1)
+    place[keep] = torch.arange(len(keep))
+    A = torch.cat([x["h"], x["U"][x["prev"].long()]], 1)
+    B = torch.cat([x["W"], x["V"]], 1)[keep]
+    ref, tol = reference({"h": A, "W": B, "U": None, "V": None, "prev": None, "dloss": x["dloss"],
+                          "target": place[x["target"].long()].int()})
+    check(got, ref, tol, ["loss", "lse"])
+    check({"dh": got["dh"]}, {"dh": ref["dh"][:, :d]}, {"dh": tol["dh"][:, :d]})
+    check({"dW": got["dW"][keep]}, {"dW": ref["dW"][:, :d]}, {"dW": tol["dW"][:, :d]})
+    check({"dV": got["dV"][keep]}, {"dV": ref["dW"][:, d:]}, {"dV": tol["dW"][:, d:]})
+    for k in ("dW", "dV"):
+        assert torch.all(got[k][masked] == 0), k
