@@ -94,7 +94,7 @@ def _rows(name, t, shape, dtype):
     if one != 1 and shape[1] > 1:
         _refuse(name, t, shape, dtype)
     # the stride of a dimension with one entry means nothing
-    return t.data_ptr(), s if shape[0] > 1 else max(s, shape[1])
+    return t.data_ptr(), s if shape[0] > 1 else shape[1]
 
 
 def _matrix(name, t):

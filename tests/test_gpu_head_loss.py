@@ -525,3 +525,16 @@ def test_an_infinite_mask_stays_in_its_entries(counted):
     check({"dV": got["dV"][keep]}, {"dV": ref["dW"][:, d:]}, {"dV": tol["dW"][:, d:]})
     for k in ("dW", "dV"):
         assert torch.all(got[k][masked] == 0), k
+
+
+def test_one_row_of_a_wider_buffer():
+    """One row, of h and of dh, in a buffer whose pitch is not a multiple of 8."""
+    import torch
+    x = make(1, 300, 64, 16, seed=29)
+    h = torch.full((1, 1003), 5.0, dtype=torch.bfloat16, device="cuda")
+    dh = torch.full((1, 1003), 3.0, dtype=torch.bfloat16, device="cuda")
+    h[:, :64] = x["h"].cuda()
+    got = run(x, h=h[:, :64], dh=dh[:, :64])
+    ref, tol = reference(x)
+    check(got, ref, tol)
+    assert torch.all(dh[:, 64:] == 3.0)

@@ -162,3 +162,15 @@ def test_scales_have_a_column_for_each_group(lib, group, shape, right):
 def test_rows_apart_are_passed_on(lib):
     H.dspark_head_loss(**{**loss_arguments(), "h": Tensor(4, 64, strides=(1003, 1))})
     assert lib.calls[0][1][1] == 1003
+
+
+@pytest.mark.parametrize("pitch", [1003, 64, 1, 0])
+def test_one_row_has_no_stride(lib, pitch):
+    """A slice of one row has its buffer's pitch as the stride, or any other (an
+    expanded one 0): the row's width is passed on instead."""
+    row = dict(strides=(pitch, 1))
+    H.dspark_head_loss_grad(**{**grad_arguments(M=1), "h": Tensor(1, 64, **row), "dh": Tensor(1, 64, **row)})
+    H.dspark_residual_norm(**{**norm_arguments(M=1), "x": Tensor(1, 64, **row), "y": Tensor(1, 64, **row)})
+    (_, grad), (_, norm) = lib.calls
+    assert grad[1] == grad[14] == 64
+    assert norm[1] == norm[15] == 64
