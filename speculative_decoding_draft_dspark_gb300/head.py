@@ -135,6 +135,8 @@ def dspark_head_workspace_size(M: int, vocab: int, d: int, rank: int, grad: bool
 def _head_inputs(h, W, U, V, prev, target):
     M, d = _matrix("h", h)
     vocab, dw = _matrix("W", W)
+    if (U is None) != (V is None):
+        raise ValueError("U and V are required together (or neither)")
     rank = 0 if V is None else _matrix("V", V)[1]
     bf16, i32 = torch.bfloat16, torch.int32
     ph, sh = _rows("h", h, (M, dw), bf16)

@@ -174,3 +174,14 @@ def test_one_row_has_no_stride(lib, pitch):
     (_, grad), (_, norm) = lib.calls
     assert grad[1] == grad[14] == 64
     assert norm[1] == norm[15] == 64
+
+
+@pytest.mark.parametrize("call", ["loss", "grad"])
+@pytest.mark.parametrize("missing", ["U", "V"])
+def test_one_factor_alone_is_refused(lib, call, missing):
+    refused(lib, call, "U and V are required together", **{missing: None})
+
+
+def test_no_factors_are_rank_0(lib):
+    H.dspark_head_loss(**{**loss_arguments(), "U": None, "V": None, "prev": None})
+    assert lib.calls[0][1][3:6] == (None, None, None) and lib.calls[0][1][10] == 0
