@@ -100,7 +100,21 @@ def _rows(name, t, shape, dtype):
 def _matrix(name, t):
     if t is None or t.dim() != 2:
         raise ValueError(f"{name} must be 2-D")
-    return t.shape
+    rows, columns = shape = t.shape
+    _whole(f"{name}'s rows", rows, 31)
+    _whole(f"{name}'s columns", columns, 31)
+    return shape
+
+
+def _whole(name, value, bits):
+    """A whole number of so many bits; more would be cut off on the way to C."""
+    if not 0 <= value < 1 << bits:
+        raise ValueError(f"{name} must be in [0, 2^{bits}), got {value}")
+    return value
+
+
+def _mask(seed, offset):
+    return _whole("seed", seed, 64), _whole("offset", offset, 32)
 
 
 _TYPES = {torch.bfloat16: BF16, torch.float32: F32}
@@ -129,6 +143,8 @@ def _done(name, code, raise_on_error):
 
 # ------------------------------------------------------------------- loss
 def dspark_head_workspace_size(M: int, vocab: int, d: int, rank: int, grad: bool) -> int:
+    if max(M, vocab, d, rank) >= 1 << 31:
+        return 0                                   # as for all that is not supported
     return int(load().dspark_head_workspace_size(M, vocab, d, rank, int(bool(grad))))
 
 
@@ -200,6 +216,7 @@ def dspark_residual_norm(x, residual, gain, r, y, scale=None, rstd=None, *, eps,
     ps, ss = _rows("residual", residual, shape, t)
     pr, sr = _rows("r", r, shape, t)
     pscale = prstd = None
+    _whole("group", group, 31)
     if y is not None and y.dtype is torch.float8_e4m3fn:
         ydt, ty = E4M3, y.dtype
         n = -(-d // group) if group > 0 else 1
@@ -208,12 +225,14 @@ def dspark_residual_norm(x, residual, gain, r, y, scale=None, rstd=None, *, eps,
     if rstd is not None:
         prstd = _flat("rstd", rstd, (M,), torch.float32)
     code = (_lib or load()).dspark_residual_norm(
-        px, sx, ps, ss, _flat("gain", gain, (d,), t), dt, M, d, eps, p, seed, offset,
+        px, sx, ps, ss, _flat("gain", gain, (d,), t), dt, M, d, eps, p, *_mask(seed, offset),
         pr, sr, py, sy, ydt, group, pscale, prstd, _stream(stream))
     return _done("dspark_residual_norm", code, raise_on_error)
 
 
 def dspark_norm_workspace_size(M: int, d: int) -> int:
+    if max(M, d) >= 1 << 31:
+        return 0
     return int(load().dspark_norm_workspace_size(M, d))
 
 
@@ -230,7 +249,7 @@ def dspark_residual_norm_grad(dy, dr, r, gain, rstd, dx, dresidual, dgain, works
     code = (_lib or load()).dspark_residual_norm_grad(
         *_rows("dy", dy, shape, t), *_rows("dr", dr, shape, t), *_rows("r", r, shape, t),
         _flat("gain", gain, (d,), t), _flat("rstd", rstd, (M,), torch.float32),
-        dt, M, d, p, seed, offset, *_rows("dx", dx, shape, t),
+        dt, M, d, p, *_mask(seed, offset), *_rows("dx", dx, shape, t),
         *_rows("dresidual", dresidual, shape, t), pg, workspace.data_ptr(),
         _nbytes(workspace), _stream(stream))
     return _done("dspark_residual_norm_grad", code, raise_on_error)
@@ -244,6 +263,6 @@ def dspark_dropout(x, residual, y, *, p, seed, offset, stream=None,
     t = x.dtype
     code = (_lib or load()).dspark_dropout(
         *_rows("x", x, shape, t), *_rows("residual", residual, shape, t),
-        _dtype("x", x), M, d, p, seed, offset, *_rows("y", y, shape, t),
+        _dtype("x", x), M, d, p, *_mask(seed, offset), *_rows("y", y, shape, t),
         _stream(stream))
     return _done("dspark_dropout", code, raise_on_error)

@@ -185,3 +185,29 @@ def test_one_factor_alone_is_refused(lib, call, missing):
 def test_no_factors_are_rank_0(lib):
     H.dspark_head_loss(**{**loss_arguments(), "U": None, "V": None, "prev": None})
     assert lib.calls[0][1][3:6] == (None, None, None) and lib.calls[0][1][10] == 0
+
+
+@pytest.mark.parametrize("call", ["norm", "norm_grad", "dropout"])
+@pytest.mark.parametrize("name,value", [("offset", 1 << 32), ("offset", -1), ("seed", 1 << 64), ("seed", -1)])
+def test_a_mask_that_would_wrap_is_refused(lib, call, name, value):
+    """C takes the low bits: (seed, offset + 2^32) would draw (seed, offset)'s mask."""
+    refused(lib, call, f"{name} must be in", **{name: value})
+
+
+def test_the_last_mask_is_passed_on(lib):
+    H.dspark_dropout(**{**dropout_arguments(), "seed": (1 << 64) - 1, "offset": (1 << 32) - 1})
+    assert lib.calls[0][1][8:10] == ((1 << 64) - 1, (1 << 32) - 1)
+
+
+def test_dimensions_that_would_wrap_are_refused(lib):
+    """2^32 + 4 rows would be computed as 4, and a group of 2^32 + 128 as 128 with
+    scales for one."""
+    many = (1 << 32) + 4
+    refused(lib, "dropout", "x's rows", x=Tensor(many, 64), residual=None, y=Tensor(many, 64))
+    refused(lib, "loss", "W's rows", W=Tensor(many, 64), U=None, V=None)
+    refused(lib, "norm", "group must be in", y=Tensor(4, 64, dtype=F8), group=(1 << 32) + 128,
+            scale=Tensor(4, 1, dtype=F32))
+    assert H.dspark_head_workspace_size(many, 100, 64, 0, True) == 0
+    assert H.dspark_head_workspace_size(4, many, 64, 0, True) == 0
+    assert H.dspark_norm_workspace_size(many, 64) == 0
+    assert not lib.calls
