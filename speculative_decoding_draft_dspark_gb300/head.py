@@ -44,6 +44,7 @@ E4M3 = 2
 __all__ = sorted(_SIGS) + ["new_workspace"]
 
 _lib = None
+_device_now = torch._C._cuda_getDevice
 
 
 def header_functions() -> list[str]:
@@ -65,44 +66,66 @@ def load() -> ctypes.CDLL:
     return _lib
 
 
-def _refuse(name, t, shape, dtype):
+def _place(name, t):
+    """The GPU of a call's first tensor: the current one, whose stream it takes."""
+    dev = t.get_device()
+    if dev < 0:
+        raise ValueError(f"{name} must be on the GPU")
+    if dev != _device_now():
+        raise ValueError(f"{name} must be on the current GPU ({_device_now()}), not GPU {dev}")
+    return dev
+
+
+def _refuse(name, t, shape, dtype, dev):
     if t is None:
         raise ValueError(f"{name} is required")
-    if not t.is_cuda:
+    if t.get_device() < 0:
         raise ValueError(f"{name} must be on the GPU")
+    if t.get_device() != dev:
+        raise ValueError(f"{name} must be on GPU {dev} as the others, not GPU {t.get_device()}")
     if t.shape != shape or t.dtype is not dtype:
         raise ValueError(f"{name} must be {tuple(shape)} {dtype}, got {tuple(t.shape)} {t.dtype}")
     raise ValueError(f"{name} must be contiguous (a matrix: along its rows)")
 
 
-def _flat(name, t, shape, dtype):
+def _flat(name, t, shape, dtype, dev):
     """Pointer of a contiguous tensor of this shape and type."""
     if (t is None or t.dtype is not dtype or t.shape != shape or not t.is_contiguous()
-            or not t.is_cuda):
-        _refuse(name, t, shape, dtype)
+            or t.get_device() != dev):
+        _refuse(name, t, shape, dtype, dev)
     return t.data_ptr()
 
 
-def _rows(name, t, shape, dtype):
+def _rows(name, t, shape, dtype, dev):
     """(pointer, row stride) of a matrix of this shape and type whose rows are
     contiguous; (None, 0) for None."""
     if t is None:
         return None, 0
-    if t.dtype is not dtype or t.shape != shape or not t.is_cuda:
-        _refuse(name, t, shape, dtype)
+    if t.dtype is not dtype or t.shape != shape or t.get_device() != dev:
+        _refuse(name, t, shape, dtype, dev)
     s, one = t.stride()
     if one != 1 and shape[1] > 1:
-        _refuse(name, t, shape, dtype)
+        _refuse(name, t, shape, dtype, dev)
     # the stride of a dimension with one entry means nothing
     return t.data_ptr(), s if shape[0] > 1 else shape[1]
+
+
+def _space(workspace, dev):
+    """(pointer, bytes) of a workspace."""
+    if workspace is None or workspace.get_device() != dev or not workspace.is_contiguous():
+        raise ValueError(f"workspace must be a contiguous tensor on GPU {dev}")
+    return workspace.data_ptr(), _nbytes(workspace)
+
+
+_I32_MAX = (1 << 31) - 1
 
 
 def _matrix(name, t):
     if t is None or t.dim() != 2:
         raise ValueError(f"{name} must be 2-D")
     rows, columns = shape = t.shape
-    _whole(f"{name}'s rows", rows, 31)
-    _whole(f"{name}'s columns", columns, 31)
+    if rows > _I32_MAX or columns > _I32_MAX:
+        raise ValueError(f"{name}'s rows and columns must be below 2^31, got {tuple(shape)}")
     return shape
 
 
@@ -131,7 +154,7 @@ def _stream(stream):
     # the current stream's handle without the Stream object around it: the
     # object costs as long as a small call's kernel
     if stream is None:
-        return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
+        return torch._C._cuda_getCurrentRawStream(_device_now())
     return stream if isinstance(stream, int) else stream.cuda_stream
 
 
@@ -155,15 +178,16 @@ def _head_inputs(h, W, U, V, prev, target):
         raise ValueError("U and V are required together (or neither)")
     rank = 0 if V is None else _matrix("V", V)[1]
     bf16, i32 = torch.bfloat16, torch.int32
-    ph, sh = _rows("h", h, (M, dw), bf16)
-    pw = _flat("W", W, (vocab, dw), bf16)
+    dev = _place("h", h)
+    ph, sh = _rows("h", h, (M, dw), bf16, dev)
+    pw = _flat("W", W, (vocab, dw), bf16, dev)
     pu = pv = pp = None
     if rank:
-        pu = _flat("U", U, (vocab, rank), bf16)
-        pv = _flat("V", V, (vocab, rank), bf16)
-        pp = _flat("prev", prev, (M,), i32)
-    pt = _flat("target", target, (M,), i32)
-    return (ph, sh, pw, pu, pv, pp, pt), (M, vocab, d, rank)
+        pu = _flat("U", U, (vocab, rank), bf16, dev)
+        pv = _flat("V", V, (vocab, rank), bf16, dev)
+        pp = _flat("prev", prev, (M,), i32, dev)
+    pt = _flat("target", target, (M,), i32, dev)
+    return (ph, sh, pw, pu, pv, pp, pt), (M, vocab, d, rank), dev
 
 
 def dspark_head_loss(h, W, U, V, prev, target, loss, lse, workspace, *,
@@ -171,12 +195,12 @@ def dspark_head_loss(h, W, U, V, prev, target, loss, lse, workspace, *,
     """h [M, d] bf16 (rows may be apart), W [vocab, d] bf16, U/V [vocab, rank]
     bf16 or None, prev/target [M] int32 (target < 0: ignored), loss/lse [M]
     fp32 (out), workspace of dspark_head_workspace_size bytes."""
-    x, dims = _head_inputs(h, W, U, V, prev, target)
+    x, dims, dev = _head_inputs(h, W, U, V, prev, target)
     rows = (dims[0],)
     code = (_lib or load()).dspark_head_loss(
-        *x, *dims, _flat("loss", loss, rows, torch.float32),
-        _flat("lse", lse, rows, torch.float32), workspace.data_ptr(),
-        _nbytes(workspace), _stream(stream))
+        *x, *dims, _flat("loss", loss, rows, torch.float32, dev),
+        _flat("lse", lse, rows, torch.float32, dev), *_space(workspace, dev),
+        _stream(stream))
     return _done("dspark_head_loss", code, raise_on_error)
 
 
@@ -185,19 +209,19 @@ def dspark_head_loss_grad(h, W, U, V, prev, target, lse, dloss, dh, dW, dU, dV,
     """Gradients of sum_i dloss_i loss_i: dh [M, d] (rows may be apart), dW
     [vocab, d], dU/dV [vocab, rank] or None, all bf16 and written in full; lse
     [M] as written by dspark_head_loss, dloss [M] fp32."""
-    x, dims = _head_inputs(h, W, U, V, prev, target)
+    x, dims, dev = _head_inputs(h, W, U, V, prev, target)
     M, vocab, d, rank = dims
     bf16 = torch.bfloat16
-    pdh, sdh = _rows("dh", dh, (M, d), bf16)
+    pdh, sdh = _rows("dh", dh, (M, d), bf16, dev)
     pdu = pdv = None
     if rank:
-        pdu = _flat("dU", dU, (vocab, rank), bf16)
-        pdv = _flat("dV", dV, (vocab, rank), bf16)
+        pdu = _flat("dU", dU, (vocab, rank), bf16, dev)
+        pdv = _flat("dV", dV, (vocab, rank), bf16, dev)
     code = (_lib or load()).dspark_head_loss_grad(
-        *x, _flat("lse", lse, (M,), torch.float32),
-        _flat("dloss", dloss, (M,), torch.float32), *dims, pdh, sdh,
-        _flat("dW", dW, (vocab, d), bf16), pdu, pdv, workspace.data_ptr(),
-        _nbytes(workspace), _stream(stream))
+        *x, _flat("lse", lse, (M,), torch.float32, dev),
+        _flat("dloss", dloss, (M,), torch.float32, dev), *dims, pdh, sdh,
+        _flat("dW", dW, (vocab, d), bf16, dev), pdu, pdv, *_space(workspace, dev),
+        _stream(stream))
     return _done("dspark_head_loss_grad", code, raise_on_error)
 
 
@@ -210,22 +234,23 @@ def dspark_residual_norm(x, residual, gain, r, y, scale=None, rstd=None, *, eps,
     same type, or float8_e4m3fn with scale [M, 1] (group 0) or [M, ceil(d /
     128)] (group 128) fp32; rstd [M] fp32 or None."""
     shape = M, d = _matrix("x", x)
+    dev = _place("x", x)
     ydt = dt = _dtype("x", x)
     ty = t = x.dtype
-    px, sx = _rows("x", x, shape, t)
-    ps, ss = _rows("residual", residual, shape, t)
-    pr, sr = _rows("r", r, shape, t)
+    px, sx = _rows("x", x, shape, t, dev)
+    ps, ss = _rows("residual", residual, shape, t, dev)
+    pr, sr = _rows("r", r, shape, t, dev)
     pscale = prstd = None
     _whole("group", group, 31)
     if y is not None and y.dtype is torch.float8_e4m3fn:
         ydt, ty = E4M3, y.dtype
         n = -(-d // group) if group > 0 else 1
-        pscale = _flat("scale", scale, (M, n), torch.float32)
-    py, sy = _rows("y", y, shape, ty)
+        pscale = _flat("scale", scale, (M, n), torch.float32, dev)
+    py, sy = _rows("y", y, shape, ty, dev)
     if rstd is not None:
-        prstd = _flat("rstd", rstd, (M,), torch.float32)
+        prstd = _flat("rstd", rstd, (M,), torch.float32, dev)
     code = (_lib or load()).dspark_residual_norm(
-        px, sx, ps, ss, _flat("gain", gain, (d,), t), dt, M, d, eps, p, *_mask(seed, offset),
+        px, sx, ps, ss, _flat("gain", gain, (d,), t, dev), dt, M, d, eps, p, *_mask(seed, offset),
         pr, sr, py, sy, ydt, group, pscale, prstd, _stream(stream))
     return _done("dspark_residual_norm", code, raise_on_error)
 
@@ -244,14 +269,16 @@ def dspark_residual_norm_grad(dy, dr, r, gain, rstd, dx, dresidual, dgain, works
     be None; everything of r's type but rstd [M] fp32 (as written by
     dspark_residual_norm)."""
     shape = M, d = _matrix("r", r)
+    dev = _place("r", r)
     dt, t = _dtype("r", r), r.dtype
-    pg = None if dgain is None else _flat("dgain", dgain, (d,), t)
+    pg = None if dgain is None else _flat("dgain", dgain, (d,), t, dev)
     code = (_lib or load()).dspark_residual_norm_grad(
-        *_rows("dy", dy, shape, t), *_rows("dr", dr, shape, t), *_rows("r", r, shape, t),
-        _flat("gain", gain, (d,), t), _flat("rstd", rstd, (M,), torch.float32),
-        dt, M, d, p, *_mask(seed, offset), *_rows("dx", dx, shape, t),
-        *_rows("dresidual", dresidual, shape, t), pg, workspace.data_ptr(),
-        _nbytes(workspace), _stream(stream))
+        *_rows("dy", dy, shape, t, dev), *_rows("dr", dr, shape, t, dev),
+        *_rows("r", r, shape, t, dev),
+        _flat("gain", gain, (d,), t, dev), _flat("rstd", rstd, (M,), torch.float32, dev),
+        dt, M, d, p, *_mask(seed, offset), *_rows("dx", dx, shape, t, dev),
+        *_rows("dresidual", dresidual, shape, t, dev), pg, *_space(workspace, dev),
+        _stream(stream))
     return _done("dspark_residual_norm_grad", code, raise_on_error)
 
 
@@ -260,9 +287,10 @@ def dspark_dropout(x, residual, y, *, p, seed, offset, stream=None,
     """y = residual + dropout(x) ([M, d] bf16 or fp32; residual may be None);
     seed (uint64) and offset (uint32) as in include/dspark_head.h."""
     shape = M, d = _matrix("x", x)
+    dev = _place("x", x)
     t = x.dtype
     code = (_lib or load()).dspark_dropout(
-        *_rows("x", x, shape, t), *_rows("residual", residual, shape, t),
-        _dtype("x", x), M, d, p, *_mask(seed, offset), *_rows("y", y, shape, t),
+        *_rows("x", x, shape, t, dev), *_rows("residual", residual, shape, t, dev),
+        _dtype("x", x), M, d, p, *_mask(seed, offset), *_rows("y", y, shape, t, dev),
         _stream(stream))
     return _done("dspark_dropout", code, raise_on_error)

@@ -64,6 +64,7 @@ class Library:
 def lib(monkeypatch):
     lib = Library()
     monkeypatch.setattr(H, "_lib", lib)
+    monkeypatch.setattr(H, "_device_now", lambda: 0)
     return lib
 
 
@@ -211,3 +212,28 @@ def test_dimensions_that_would_wrap_are_refused(lib):
     assert H.dspark_head_workspace_size(4, many, 64, 0, True) == 0
     assert H.dspark_norm_workspace_size(many, 64) == 0
     assert not lib.calls
+
+
+@pytest.mark.parametrize("call", list(CALLS))
+@pytest.mark.parametrize("device", [-1, 1])
+def test_every_tensor_is_on_the_current_gpu(lib, call, device):
+    """One tensor at a time on the CPU or on another GPU, the workspace too."""
+    fn, arguments = CALLS[call]
+    for name, t in arguments().items():
+        if isinstance(t, Tensor):
+            with pytest.raises(ValueError, match=f"^{name} must be .*GPU"):
+                fn(**{**arguments(), name: Tensor(*t.shape, dtype=t.dtype, device=device)})
+    assert not lib.calls
+
+
+def test_all_tensors_on_another_gpu_than_the_current(lib):
+    a = {k: Tensor(*t.shape, dtype=t.dtype, device=1) if isinstance(t, Tensor) else t
+         for k, t in dropout_arguments().items()}
+    with pytest.raises(ValueError, match="x must be on the current GPU"):
+        H.dspark_dropout(**a)
+
+
+@pytest.mark.parametrize("call", ["loss", "grad", "norm_grad"])
+def test_a_workspace_is_contiguous(lib, call):
+    refused(lib, call, "workspace must be", workspace=Tensor(64, 64, strides=(128, 1)))
+    refused(lib, call, "workspace must be", workspace=None)
