@@ -453,3 +453,126 @@ def test_scale_that_underflows_is_one(out, d):
     q = torch.ones(M, d, device="cuda").to(torch.float8_e4m3fn)
     H.dspark_residual_norm(x, None, gain, None, q, scale, None, eps=1e-6, group=128 if out == "group8" else 0)
     assert torch.all(scale == 1.0) and torch.all(q.float() == 0.0)
+
+
+# -------------------------------------------------- every layout of a row
+def kept_by_arrays(M, d, p, seed, offset):
+    """kept() with the words of all elements at once."""
+    if p == 0.0:
+        return np.ones((M, d), bool), 1.0
+    T = int(np.floor((1.0 - p) * 65536.0 + 0.5))
+    n = -(-d // 8)
+    low, half = np.uint64(MASK), np.uint64(32)
+    c = [np.broadcast_to(np.arange(n, dtype=np.uint64)[None, :], (M, n)),
+         np.broadcast_to(np.arange(M, dtype=np.uint64)[:, None], (M, n)),
+         np.full((M, n), 1 << 31, np.uint64), np.full((M, n), offset, np.uint64)]
+    k = [seed & MASK, seed >> 32]
+    for _ in range(10):
+        p0, p1 = c[0] * np.uint64(0xD2511F53), c[2] * np.uint64(0xCD9E8D57)
+        c = [(p1 >> half) ^ c[1] ^ np.uint64(k[0]), p1 & low, (p0 >> half) ^ c[3] ^ np.uint64(k[1]), p0 & low]
+        k = [(k[0] + 0x9E3779B9) & MASK, (k[1] + 0xBB67AE85) & MASK]
+    lanes = np.stack([h for w in c for h in (w & np.uint64(0xFFFF), w >> np.uint64(16))], -1)
+    return lanes.reshape(M, 8 * n)[:, :d] < T, 65536.0 / max(T, 1)
+
+
+def guarded(monkeypatch, first):
+    """Makes tensors() place each tensor `first` elements (0 or 2) into a buffer of
+    its own, and returns a check that nothing beside the rows was written."""
+    import sys
+    import torch
+    buffers = []
+
+    def placed(M, d, dtype, n, seed, pad=0):
+        g = torch.Generator().manual_seed(seed)
+        out = []
+        for k in range(n):
+            at, step = first, d + pad
+            flat = torch.full((at + M * step + 8,), -7.0, dtype=dtype, device="cuda")
+            t = flat.as_strided((M, d), (step, 1), at)
+            t.copy_((torch.randn(M, d, generator=g) * (1.0 + k)).to(dtype))
+            buffers.append((flat, at, step, M, d))
+            out.append(t)
+        return out
+
+    def untouched():
+        for flat, at, step, M, d in buffers:
+            beside = torch.ones_like(flat, dtype=torch.bool)
+            beside.as_strided((M, d), (step, 1), at)[:] = False
+            assert (flat[beside] == -7.0).all()
+
+    here = sys.modules[__name__]
+    monkeypatch.setattr(here, "tensors", placed)
+    monkeypatch.setattr(here, "kept", kept_by_arrays)
+    return untouched
+
+
+def test_both_ways_to_draw_the_words_agree():
+    a, b = kept(5, 77, 0.3, 0x123456789ABCDEF, 41), kept_by_arrays(5, 77, 0.3, 0x123456789ABCDEF, 41)
+    assert np.array_equal(a[0], b[0]) and a[1] == b[1]
+
+
+@pytest.mark.parametrize("M,d,pad,first", [
+    (1, 2, 0, 0), (5, 2, 2, 2), (3, 6, 0, 0), (7, 126, 0, 2), (4, 130, 2, 0), (9, 300, 0, 0),
+    (5, 1002, 2, 0), (3, 2044, 0, 2), (2, 8190, 0, 0), (2, 8194, 0, 0), (3, 20002, 2, 2),
+    (6, 64, 2, 0), (5, 264, 0, 2), (4, 2048, 2, 0), (2, 9000, 2, 0),
+])
+def test_bf16_rows_at_four_bytes(M, d, pad, first, monkeypatch):
+    """Even widths that are no multiple of 8, and rows that begin at 4 bytes but
+    not at 16: norm in 16 and 8 bits, its gradient and dropout, with and without a
+    mask, and nothing beside a row is written."""
+    untouched = guarded(monkeypatch, first)
+    for out in ("same", "row8", "group8"):
+        for p in (0.0, 0.3):
+            run_norm(M, d, "bf16", out, p, pad, out != "group8")
+    for p, dr in ((0.0, False), (0.3, True)):
+        test_norm_grad(M, d, "bf16", p, pad, dr, True)
+        test_dropout(M, d, "bf16", p, pad, dr)
+    untouched()
+
+
+@pytest.mark.parametrize("d,pad", [(300, 0), (264, 2), (9002, 0)])
+def test_bf16_rows_at_four_bytes_in_place(d, pad):
+    """As test_in_place; every other buffer is a clone at the same strides."""
+    import torch
+    from speculative_decoding_draft_dspark_gb300 import head as H
+    M, kw = 9, dict(p=0.3, seed=3, offset=4)
+
+    def clone(t):
+        c = torch.empty(M, d + pad, dtype=t.dtype, device="cuda")[:, :d]
+        return c.copy_(t)
+
+    x, res, r, y, dy, dr, dx, ds = tensors(M, d, torch.bfloat16, 8, d, pad)
+    gain = torch.ones(d, dtype=torch.bfloat16, device="cuda")
+    rstd = torch.zeros(M, device="cuda")
+    H.dspark_residual_norm(x, res, gain, r, y, None, rstd, eps=1e-5, **kw)
+    for which in ("residual", "x"):
+        x2, res2, y2 = clone(x), clone(res), clone(y)
+        r2 = res2 if which == "residual" else x2
+        H.dspark_residual_norm(x2, res2, gain, r2, y2, None, None, eps=1e-5, **kw)
+        assert torch.equal(r2, r) and torch.equal(y2, y)
+    ws = H.new_workspace(H.dspark_norm_workspace_size(M, d))
+    dg, g = torch.empty_like(gain), torch.empty_like(gain)
+    H.dspark_residual_norm_grad(dy, dr, r, gain, rstd, dx, ds, dg, ws, **kw)
+    a, b = clone(dy), clone(dr)
+    H.dspark_residual_norm_grad(a, b, r, gain, rstd, a, b, g, ws, **kw)
+    assert torch.equal(a, dx) and torch.equal(b, ds) and torch.equal(g, dg)
+    z = clone(x)
+    H.dspark_dropout(x, res, y, **kw)
+    H.dspark_dropout(z, res, z, **kw)
+    assert torch.equal(z, y)
+
+
+@pytest.mark.parametrize("M,d,name,p,pad", [
+    (9500, 256, "bf16", 0.0, 0), (9500, 264, "bf16", 0.2, 0),      # copied ahead: 15, 8, 4 and 1 rows a CTA
+    (5001, 1000, "bf16", 0.1, 8), (3000, 2048, "bf16", 0.0, 0), (701, 8192, "bf16", 0.1, 0),
+    (8001, 264, "f32", 0.1, 0), (8001, 265, "f32", 0.0, 0), (1000, 4104, "f32", 0.0, 0),
+    (8001, 300, "bf16", 0.1, 0), (8001, 301, "bf16", 0.1, 0), (4001, 1002, "bf16", 0.0, 2),
+    (1001, 9000, "f32", 0.0, 0), (1001, 9000, "bf16", 0.1, 0), (1001, 9002, "bf16", 0.0, 0),
+])
+def test_gradient_of_many_rounds(M, d, name, p, pad, monkeypatch):
+    """More rows than the CTAs take in three rounds, whichever kernel goes over
+    them: the ring of copies ahead (three stages) and the two sets of sums come
+    round again, and the last round is not full."""
+    untouched = guarded(monkeypatch, 0)
+    test_norm_grad(M, d, name, p, pad, True, True)
+    untouched()
