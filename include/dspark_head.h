@@ -33,8 +33,8 @@ extern "C" {
  *     loss = lse - z[target_i]
  * The scores are computed a 256-entry tile at a time and never stored.  A row
  * whose target is negative is ignored: its loss and lse are 0 and nothing else
- * of it is read (it costs no arithmetic either).  NaN or infinite scores give
- * the NaN or infinity of the formula in their own row.
+ * that it holds has an effect (it costs no arithmetic either).  NaN or infinite
+ * scores give the NaN or infinity of the formula in their own row.
  *
  * h           bf16 [M, d], row i at i*h_stride elements; h_stride >= d and a
  *             multiple of 8; 16-byte aligned.
@@ -48,6 +48,9 @@ extern "C" {
  *             workspace for the gradient is large enough), 256-byte aligned.
  * Limits: 1 <= M <= 2^20, 1 <= vocab < 2^30, ceil(M / 256) ceil(vocab / 256) <=
  * 2^30, d a multiple of 8 in [8, 65536], rank a multiple of 8 in [0, 256].
+ * The rows are gathered, and dU summed, by looking through all rows' tokens once
+ * for each block of rows, and for each row: for M = 131072 with as many different
+ * tokens that is some 6 ms, and four times as much for twice the rows.
  * ------------------------------------------------------------------------ */
 DSPARK_API size_t dspark_head_workspace_size(int32_t M, int32_t vocab, int32_t d, int32_t rank,
                                              int32_t grad);
@@ -66,6 +69,9 @@ DSPARK_API dspark_status dspark_head_loss(
  * for one piece (relative to the largest |dloss|, so a mean's equal weights
  * round nothing), sums in fp32, and the results are rounded once.  Nothing
  * depends on the order in which blocks run: the same inputs give the same bits.
+ * exp(z - lse) is as good as lse is in fp32: off by up to 2^-24 of |lse|, and 1
+ * for every entry of a row whose scores are all one mask's value (as large as
+ * bf16's lowest, lse does not hold log vocab beside it).
  *
  * h ... target   as above.
  * lse            [M] fp32, as written by dspark_head_loss.
@@ -99,7 +105,9 @@ DSPARK_API dspark_status dspark_head_loss_grad(
  *                0), and the byte is y / scale, divided in fp32 too, rounded to
  *                nearest even; scale is fp32
  *                [M, ceil(d / 128)] or [M], contiguous.  group and scale are
- *                not used when y is of dtype.
+ *                not used when y is of dtype.  (The 8-bit form is for a layer
+ *                outside this library: dspark_head_loss and dspark_chain_lmhead
+ *                read bf16.)
  * rstd           out [M] fp32: 1 / sqrt(mean r^2 + eps), or NULL.
  * p              probability of dropping an element of x, 0 <= p <= 1; 0 = none.
  *                Rounded so that T = round(65536 (1 - p)) of 65536 values are
@@ -134,7 +142,8 @@ DSPARK_API dspark_status dspark_residual_norm(
  * dgain          out [d], or NULL.
  * workspace      >= dspark_norm_workspace_size(M, d) bytes, 256-byte aligned.
  * All of dtype with strides as above; rstd fp32.  dgain is summed in an order
- * fixed by M, d and dtype. */
+ * fixed by M, d, dtype and whether the rows are aligned to 16 bytes, d being a
+ * multiple of 8. */
 DSPARK_API size_t dspark_norm_workspace_size(int32_t M, int32_t d);
 
 DSPARK_API dspark_status dspark_residual_norm_grad(

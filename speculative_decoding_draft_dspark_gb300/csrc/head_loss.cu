@@ -95,10 +95,12 @@ __device__ __forceinline__ float base(float top) {
 
 // ------------------------------------------------------------------ pack
 // Gathers the rows with a target into A = [h, U[prev]], zero-padded to whole
-// 64-column blocks and to a multiple of 32 rows, and their row data.  A row that is
-// ignored is never read, so what it holds (NaN, infinities) reaches nothing.
-// Every CTA counts the targets before its rows itself: the target array is a
-// few KB from L2, and a scan across CTAs would cost a second launch.  A warp takes
+// 64-column blocks and to a multiple of 32 rows, and their row data.  What an ignored
+// row holds (NaN, infinities, tokens out of range) reaches nothing: its first lines
+// may be prefetched, no more.  Every CTA counts the targets before its rows itself:
+// 4 bytes a row from L2 (8 for the gradient), where a scan across CTAs would cost a
+// second launch.  It is quadratic, but with blocks of 256 rows: the largest M, 2^20,
+// reads 34 GB, some milliseconds beside products of a second.  A warp takes
 // a row, eight a CTA; where that leaves SMs idle the columns are spread over CTAs
 // too, 1024 or more to each (300 rows of 8192: 6 us instead of 19; loss and
 // gradient with 4000 entries 143 us instead of 171).
@@ -279,14 +281,15 @@ __global__ void __launch_bounds__(PACK_THREADS) head_pack_kernel(const PackParam
 // the reduction each, of one tile after the other.
 //
 // What bounds them.  Many rows: the tensor cores and, after a tenth of a second
-// of them, the 1400 W limit.  1632 columns x 262144 x 2304 (LSE) take 1.17 to
-// 1.22 ms, 1.62 to 1.68 PFLOP/s, 0.85 to 0.88 of cuBLAS's measured burst and as
+// of them, the 1400 W limit.  1632 columns x 262144 x 2304 (LSE) take 1.20 to
+// 1.25 ms, 1.58 to 1.64 PFLOP/s, 0.83 to 0.86 of cuBLAS's measured burst and as
 // much as its 1.71 PFLOP/s of seconds allows for the added weight stream; by
-// themselves, cool, LSE reaches 1.97, PROB 1.87 and GRAD 1.79 PFLOP/s at 6464
-// columns.  Few rows: HBM; LSE for 64 columns takes 175 us, 6.9 TB/s of W and V,
-// GRAD for 16 rows x 65536 x 2560 128 us, 5.2 TB/s of them read and written.  In
-// between a tile's operands: each SM takes in at most some 50 bytes a cycle,
-// which a 256 x 256 tile needs for 0.8 of the tensor cores' rate.
+// themselves, cool, LSE reaches 2.04, PROB 1.89 and GRAD 1.85 PFLOP/s at 6464
+// columns.  Few rows: HBM; LSE for 64 columns takes 180 us, 6.7 TB/s of W and V,
+// GRAD for 16 rows x 65536 x 2560 138 us, 5.1 TB/s of them read and written and of
+// dU's zeros.  In between a tile's operands: each SM takes in at most some 50 bytes a
+// cycle, which a 256 x 256 tile needs for 0.8 of the tensor cores' rate.  Short
+// reductions (some 600 entries and below): the epilogues of z^T.
 //
 // The rows of A are always the tile's columns or the reduction: those come in
 // steps of 32 and 16, where a tile's rows are always 256, so that 403 rows cost
@@ -738,7 +741,8 @@ __device__ __forceinline__ void prob_tile(const HeadParams &p, const CUtensorMap
 
 // dA^T: lanes are columns of A, columns its rows; fp32, one addition a piece.
 // What its truncated additions lose (at most 393216 / 16 of them, 2^-26 of the
-// sum each) is below 2^-11 of it; the result's rounding to bf16 is up to 2^-8.
+// sum each) is below 2^-11 of it, and dB's (2^20 rows at most) below 2^-10; the
+// results' rounding to bf16 is up to 2^-8.
 __device__ __forceinline__ void sum_tile(const HeadParams &p, const CUtensorMap &acc_map,
                                          const HalfTile &t, int split, int row0) {
   const int lane = t.lane;
@@ -1287,7 +1291,8 @@ __global__ void __launch_bounds__(256)
 // rows in a fixed order (eight warps take consecutive eighths of the rows, and
 // their sums are joined in order), so the result does not depend on the order
 // in which CTAs run.  Tokens that no row names were zeroed by GRAD.  Each CTA looks
-// through all rows' tokens, from L2: 5 us for 403 rows, 23 for 7053.
+// through all rows' tokens, from L2: 5 us for 403 rows, 23 for 7053, and some 6 ms for
+// 131072 rows of different tokens (beside 53 ms of the narrowest products).
 constexpr int DU_WARPS = 8;
 
 __global__ void __launch_bounds__(DU_WARPS * 32)
@@ -1451,10 +1456,10 @@ dspark_status head_plan(const HeadArgs &a, bool grad, HeadPlan &o) {
   p.zeroed = nullptr;
   p.n_zeroed = 0;
   const int adds = (a.d + 15) / 16 + (a.rank + 15) / 16;
-  // A chunk is a bit more than a fifth of the reduction, and at most 64 additions: a
-  // score that grows evenly loses n + 1 of 2^-26 of itself for n additions to a
-  // chunk (measured for 16 to 256 of them), a quarter or less of what one accumulator
-  // would take, and one whose sums are exact loses nothing.
+  // A chunk is a bit more than a fifth of the reduction, 2 additions at least and 64
+  // at most: a score that grows evenly loses n + 1 of 2^-26 of itself for n additions
+  // to a chunk (measured for 16 to 256 of them), a quarter or so of what one
+  // accumulator would take, and one whose sums are exact loses nothing.
   p.chunk = std::max(2, std::min(64, adds * 2 / 9 / 2 * 2));
   p.d = a.d;
   p.rank = a.rank;

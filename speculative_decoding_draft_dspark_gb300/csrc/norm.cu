@@ -60,7 +60,8 @@ __device__ __forceinline__ Philox4 drop_words(const DropArgs &d, int group, int 
 //           of a word its words are columns 2l - 1 and 2l, and the lanes hand
 //           halves on (at 15360 x 2047 the norm takes 70 us and dropout 48, by
 //           single columns 111 and 57; not for the gradient, 86 us by single
-//           columns and 111 so: its 64 registers do not hold it)
+//           columns and 111 so: the 64 registers that its launch bound leaves do not
+//           hold it)
 //   kSingle anything: columns l, 32 + l, ..., 224 + l, eight accesses
 // Every access of the warp is to neighbouring words.
 enum Layout { kWide = 0, kPairs = 1, kShifted = 2, kSingle = 3 };
@@ -562,9 +563,10 @@ __device__ __forceinline__ V8 times_gain(const void *gain, float rstd, int base,
 // warp: one row's loads are all in flight before its sum, and most rows need one
 // or two warps and a barrier of few.  At 15360 x 2048 bf16 39 us in 16 bits (95%
 // of measured HBM), 39 in 8 bits with a scale for 128 columns (84%: the scales'
-// maxima and conversions), 45 with dropout as well (72%: the ten rounds of each
-// Philox block, for which the integer multipliers are the limit).  Few rows: the
-// latency of a load, a sum and a store, 3.7 us for 56 rows.
+// maxima and conversions), 45 with dropout as well (72%: a chunk's Philox words are
+// drawn after its load has been waited for, not under it; dropout_kernel draws as
+// many at 94%).  Few rows: the latency of a load, a sum and a store, 3.9 us for 56
+// rows.
 template <bool F32, int L, int NV>
 __global__ void __launch_bounds__(256) norm_kernel(const NormArgs a, int warps) {
   allow_next_kernel();
@@ -975,7 +977,9 @@ __global__ void __launch_bounds__(512)
 }
 
 // Other rows: the next row's lines are sent to L2 instead.  (fp32 rows too: copied
-// ahead, with two chunks a warp, 7680 x 2048 of them took 102 us instead of 57.)
+// ahead, with two chunks a warp, 7680 x 2048 of them took 102 us instead of 57.)  The
+// launch bound, 1024 threads for the widest rows, leaves 64 registers: aligned and
+// single-column fp32 rows spill 24 to 28 bytes, bf16 ones 8.
 template <bool F32, int L>
 __global__ void __launch_bounds__(1024) norm_grad_direct_kernel(const NormGradArgs a, int warps) {
   __shared__ float slots[2][32];
