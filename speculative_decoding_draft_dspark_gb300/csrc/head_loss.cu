@@ -690,11 +690,12 @@ __device__ __forceinline__ void lse_tile(const HeadParams &p, const HalfTile &t,
   });
 }
 
+__device__ __forceinline__ float prob(float z, float lse) { return ex2((z - lse) * kLog2e); }
+
 // PROB: lanes are vocabulary entries, columns rows of A.  G^T is rounded to bf16:
 // as an operand it has to be, for bf16 products; at most 2^-8 of an entry, and
 // the entries' roundings are independent in the sums.  dloss enters as a share of
 // the largest one, so that a mean's small weights lose nothing.
-__device__ __forceinline__ float prob(float z, float lse) { return ex2((z - lse) * kLog2e); }
 __device__ __forceinline__ void prob_tile(const HeadParams &p, const CUtensorMap &g_out,
                                           const HalfTile &t, Scores &scores, int row0,
                                           int n_valid) {
