@@ -18,7 +18,8 @@ CSRC = os.path.join(HERE, "csrc")
 BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "libdspark.so")
 SOURCES = ["chain.cu", "lmhead.cu", "select.cu", "verify.cu", "api.cu", "chain_noalloc.cu",
-           "head_loss.cu", "norm.cu", "head_api.cu"]
+           "head_loss.cu", "norm.cu", "head_api.cu", "rows.cu", "rotary.cu", "attention.cu",
+           "adjust.cu", "target_api.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC",
          "-Xcompiler", "-fvisibility=hidden", "--expt-relaxed-constexpr"]
@@ -44,7 +45,7 @@ def build(verbose: bool = False, force: bool = False) -> str:
     headers = [os.path.join(CSRC, f) for f in os.listdir(CSRC)
                if f.endswith((".cuh", ".h"))]
     headers += [os.path.join(os.path.dirname(HERE), "include", f)
-                for f in ("dspark.h", "dspark_head.h")]
+                for f in ("dspark.h", "dspark_head.h", "dspark_target.h")]
 
     def compile_one(src):
         s = os.path.join(CSRC, src)
