@@ -185,6 +185,7 @@ DSPARK_API dspark_status dspark_rotary_append(
  * lse        out fp32 [R, Hq], contiguous, or NULL.
  * workspace  >= dspark_attention_workspace_size(N, max_len, Hq, Hk, d) bytes,
  *            256-byte aligned.
+ * scale      positive (and a normal number).
  * All strides multiples of 8, all bases 16-byte aligned.
  * Limits: 1 <= N <= 16384, 1 <= R <= 2^22, Hq a multiple of Hk, Hq / Hk <= 128, Hq <=
  * 1024, d a multiple of 8 in [8, 256], num_pages * page_size < 2^31, max_pages *

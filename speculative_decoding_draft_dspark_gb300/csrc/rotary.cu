@@ -156,7 +156,7 @@ static dspark_status launch_type(const RotaryArgs &a, cudaStream_t stream) {
 }
 
 dspark_status rotary_launch(const RotaryArgs &a, cudaStream_t stream) {
-  if (a.R == 0 || a.Hq + a.Hk == 0) return DSPARK_OK;
+  if (a.Hq + a.Hk == 0) return DSPARK_OK;
   return a.f32 ? launch_type<float>(a, stream) : launch_type<__nv_bfloat16>(a, stream);
 }
 

@@ -70,8 +70,8 @@ bool heads_ok(const void *p, int64_t stride, int64_t head_stride, int32_t heads,
 // The same of one that is written.
 bool heads_out_ok(const HeadRows &t, int32_t rows, int32_t heads, int32_t d, uintptr_t align,
                   int64_t multiple) {
-  return heads_ok(t.p, t.stride, t.head_stride, heads, d, align, multiple) &&
-         distinct(d, rows, t.stride, heads, t.head_stride);
+  return heads == 0 || (heads_ok(t.p, t.stride, t.head_stride, heads, d, align, multiple) &&
+                        distinct(d, rows, t.stride, heads, t.head_stride));
 }
 
 // The strides of a cache: any order of pages, tokens and heads, one element a place.
@@ -89,6 +89,7 @@ dspark_status check_rotary(const RotaryArgs &a, int32_t dtype) {
     return DSPARK_ERR_INVALID_ARG;
   if (a.R > kMaxStepRows || a.Hq > 1024 || a.Hk > 1024 || a.d > 1024)
     return DSPARK_ERR_UNSUPPORTED;
+  if (a.R == 0) return DSPARK_OK;  // an empty tensor has no pointer
   const int e = dtype == DSPARK_F32 ? 4 : 2;
   if (!heads_ok(a.q.p, a.q.stride, a.q.head_stride, a.Hq, a.d, e, 1) ||
       !heads_out_ok(a.q_out, a.R, a.Hq, a.d, e, 1) ||
@@ -240,7 +241,7 @@ dspark_status dspark_rotary(const void *q, int64_t q_stride, int64_t q_head_stri
   a.inverse = inverse != 0;
   a.amplitude = amplitude;
   const dspark_status s = check_rotary(a, dtype);
-  if (s != DSPARK_OK) return s;
+  if (s != DSPARK_OK || R == 0) return s;
   if (!heads_out_ok(a.k_out, R, Hk, d, a.f32 ? 4 : 2, 1)) return DSPARK_ERR_INVALID_ARG;
   return rotary_launch(a, reinterpret_cast<cudaStream_t>(stream));
 }
@@ -278,7 +279,7 @@ dspark_status dspark_rotary_append(
   a.head_stride = head_stride;
   a.num_pages = num_pages;
   dspark_status s = check_rotary(a, dtype);
-  if (s != DSPARK_OK) return s;
+  if (s != DSPARK_OK || R == 0) return s;
   if ((s = check_pages(page_size, num_pages)) != DSPARK_OK) return s;
   const int e = a.f32 ? 4 : 2;
   if (Hk == 0 || !heads_ok(v, v_stride, v_head_stride, Hk, d, e, 1) || !given(slot, 4) ||
@@ -329,7 +330,8 @@ dspark_status dspark_tree_attention(
   if (page_stride >= (1ll << 38) || token_stride >= (1ll << 38) || head_stride >= (1ll << 38))
     return DSPARK_ERR_UNSUPPORTED;
   if (!given(block_table, 4) || table_stride < max_pages || !given(ctx_len, 4) ||
-      !given(cu_rows, 4) || !optional(lse, 4) || !std::isfinite(scale))
+      !given(cu_rows, 4) || !optional(lse, 4) || !(scale > 0.0f) ||
+      !std::isnormal(scale))
     return DSPARK_ERR_INVALID_ARG;
   if ((s = check_ws(workspace, workspace_bytes, attention_workspace_bytes(max_len, Hq, Hk, d))) !=
       DSPARK_OK)
