@@ -3,11 +3,12 @@
 // Few of a row's logits change: the tokens of the request's history and drafts, its
 // biases, and what a mask forbids.  A CTA takes one request and a slice of the
 // vocabulary that fits into shared memory: it counts the history's tokens there (a
-// word an entry, no hashing, whole numbers, so their order does not matter), lists
-// the entries that any row may change, and then goes through the request's rows.  In
-// place a row costs its listed entries and what its mask forbids, 16 bytes at a time
-// where eight (four) neighbours are; the masked logits are never read.  Elsewhere the
-// slice is copied first.
+// word an entry, no hashing, whole numbers, so their order does not matter) and lists
+// the entries that any row may change, then goes through the request's rows (a share
+// of them, where there are few CTAs): the listed entries one by one, and the slice 16
+// bytes at a time.  In place, vectors that the mask forbids whole are written unread
+// and those that it allows whole are left alone; elsewhere all are copied.
+#include <algorithm>
 #include <cuda_bf16.h>
 
 #include "common.cuh"
@@ -18,9 +19,11 @@ namespace dspark {
 
 constexpr int AJ_THREADS = 256;
 constexpr int AJ_SLICE = 8192;             // vocabulary entries of a CTA
-constexpr uint32_t kListed = 1u << 31;     // a draft or a bias: listed whatever its count
+constexpr int AJ_CTAS = 4 * 304;           // aimed at, by giving a CTA fewer rows
+constexpr uint32_t kListed = 1u << 31;
 constexpr uint32_t kInPrompt = 1u << 30;
-constexpr uint32_t kCount = kInPrompt - 1;
+constexpr uint32_t kBiased = 1u << 29;
+constexpr uint32_t kCount = kBiased - 1;
 
 template <typename T>
 __device__ __forceinline__ T minus_infinity();
@@ -39,28 +42,90 @@ __device__ __forceinline__ void logit_set(float v, __nv_bfloat16 *x) {
   *x = __float2bfloat16_rn(v);
 }
 
+// V bits of a row of mask words from entry i on, and beyond its end none.
+template <int V>
+__device__ __forceinline__ uint32_t mask_bits(const uint32_t *mask, int i, int words) {
+  const int w = i >> 5, shift = i & 31;
+  const uint32_t lo = mask[w];
+  const uint32_t hi = shift > 32 - V && w + 1 < words ? mask[w + 1] : 0u;
+  return __funnelshift_r(lo, hi, shift) & ((1u << V) - 1u);
+}
+
+// One row of the slice: what the mask forbids, and where `copies` the rest.
+template <typename T, bool COPIES>
+__device__ __forceinline__ void mask_row(const T *src, T *dst, int size, const uint32_t *mask,
+                                         int words, int thread, int threads) {
+  constexpr int V = 16 / sizeof(T);
+  auto one = [&](int i) {
+    if (mask != nullptr && (mask[i >> 5] >> (i & 31) & 1u) == 0u) dst[i] = minus_infinity<T>();
+    else if (COPIES) dst[i] = src[i];
+  };
+  // entries up to the first 16-byte boundary, vectors, and those left
+  const int lead =
+      min(size, static_cast<int>((16 - (reinterpret_cast<uintptr_t>(dst) & 15)) & 15) /
+                    static_cast<int>(sizeof(T)));
+  if (COPIES && ((reinterpret_cast<uintptr_t>(src) ^ reinterpret_cast<uintptr_t>(dst)) & 15) != 0) {
+    for (int i = thread; i < size; i += threads) one(i);
+    return;
+  }
+  const int vectors = (size - lead) / V, tail = lead + vectors * V;
+  if (thread < lead) one(thread);
+  if (thread < size - tail) one(tail + thread);
+  union Vec {
+    uint4 w;
+    T x[V];
+  };
+  constexpr int UNROLL = 4;
+  for (int v0 = thread; v0 < vectors; v0 += threads * UNROLL) {
+    Vec x[UNROLL];
+    uint32_t keep[UNROLL];
+#pragma unroll
+    for (int u = 0; u < UNROLL; ++u) {
+      const int v = v0 + u * threads;
+      keep[u] = v < vectors && mask != nullptr ? mask_bits<V>(mask, lead + v * V, words)
+                                               : (1u << V) - 1u;
+    }
+#pragma unroll
+    for (int u = 0; u < UNROLL; ++u) {
+      const int v = v0 + u * threads;
+      if (v < vectors && keep[u] != 0u && (COPIES || keep[u] != (1u << V) - 1u))
+        x[u].w = *reinterpret_cast<const uint4 *>(src + lead + v * V);
+    }
+#pragma unroll
+    for (int u = 0; u < UNROLL; ++u) {
+      const int v = v0 + u * threads;
+      if (v < vectors && (COPIES || keep[u] != (1u << V) - 1u)) {
+#pragma unroll
+        for (int e = 0; e < V; ++e)
+          if ((keep[u] >> e & 1u) == 0u) x[u].x[e] = minus_infinity<T>();
+        *reinterpret_cast<uint4 *>(dst + lead + v * V) = x[u].w;
+      }
+    }
+  }
+}
+
 template <typename T>
 __global__ void __launch_bounds__(AJ_THREADS) adjust_kernel(const AdjustArgs p) {
   extern __shared__ __align__(16) uint8_t aj_sm[];
   uint32_t *count = reinterpret_cast<uint32_t *>(aj_sm);           // [slice]
   uint16_t *list = reinterpret_cast<uint16_t *>(count + AJ_SLICE);  // [slice]
   float *bias = reinterpret_cast<float *>(list + AJ_SLICE);         // [slice], if there are any
-  __shared__ uint32_t listed;
-  const int tid = threadIdx.x, lane = tid & 31;
+  __shared__ int listed, drafts_here;
+  const int tid = threadIdx.x;
   wait_for_earlier_kernel();
   const int n = blockIdx.y;
   const RowSpan rows = row_span(p.cu_rows, n, p.R);
-  if (rows.count == 0) return;
+  // this CTA's share of them
+  const int share = (rows.count + gridDim.z - 1) / gridDim.z;
+  const int j0 = blockIdx.z * share, j1 = min(rows.count, j0 + share);
+  if (j0 >= j1) return;
   const int lo = blockIdx.x * AJ_SLICE, size = min(AJ_SLICE, p.vocab - lo);
-  const bool has_bias = p.bias_width > 0;
+  const int words = (size + 31) / 32;
   uint32_t flags = 0u;
 
-  // count
-  for (int i = tid; i < AJ_SLICE; i += AJ_THREADS) {
-    count[i] = 0u;
-    if (has_bias) bias[i] = 0.0f;
-  }
-  if (tid == 0) listed = 0u;
+  for (int i = tid; i < AJ_SLICE / 4; i += AJ_THREADS)
+    reinterpret_cast<uint4 *>(count)[i] = make_uint4(0u, 0u, 0u, 0u);
+  if (tid == 0) listed = drafts_here = 0;
   __syncthreads();
   int hist = p.hist_len[n];
   if (hist < 0 || hist > p.tokens_width) flags |= DSPARK_DEV_LEN_OOR;
@@ -70,20 +135,37 @@ __global__ void __launch_bounds__(AJ_THREADS) adjust_kernel(const AdjustArgs p) 
     if (t < 0 || t >= p.vocab) flags |= DSPARK_DEV_TOKEN_OOR;
     return t >= lo && t - lo < size;
   };
+  // the first to touch an entry lists it
+  auto first_touch = [&](int i) {
+    if ((atomicOr(&count[i], kListed) & kListed) == 0u)
+      list[atomicAdd(&listed, 1)] = static_cast<uint16_t>(i);
+  };
   const int32_t *text = p.tokens + n * p.tokens_stride;
-  for (int i = tid; i < hist; i += AJ_THREADS) {
-    const int t = text[i];
-    if (!in_slice(t)) continue;
-    if (i < prompt) atomicOr(&count[t - lo], kInPrompt);
-    else atomicAdd(&count[t - lo], 1u);
+  for (int i0 = tid; i0 < hist; i0 += 4 * AJ_THREADS) {
+    int t[4];
+#pragma unroll
+    for (int u = 0; u < 4; ++u)
+      t[u] = i0 + u * AJ_THREADS < hist ? text[i0 + u * AJ_THREADS] : lo + size;
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+      const int i = i0 + u * AJ_THREADS;
+      if (i >= hist || !in_slice(t[u])) continue;
+      const int e = t[u] - lo;
+      if (i < prompt) atomicOr(&count[e], kInPrompt);
+      else atomicAdd(&count[e], 1u);
+      first_touch(e);
+    }
   }
   const int drafts = min(p.K, rows.count - 1);
   const int32_t *draft = p.draft + static_cast<int64_t>(n) * p.K;
   if (tid < drafts) {
     const int t = draft[tid];
-    if (in_slice(t)) atomicOr(&count[t - lo], kListed);
+    if (in_slice(t)) {
+      first_touch(t - lo);
+      drafts_here = 1;
+    }
   }
-  if (has_bias) {
+  if (p.bias_width > 0) {
     const int biases = min(max(p.bias_count[n], 0), p.bias_width);
     const int32_t *token = p.bias_token + static_cast<int64_t>(n) * p.bias_width;
     const float *value = p.bias_value + static_cast<int64_t>(n) * p.bias_width;
@@ -98,66 +180,80 @@ __global__ void __launch_bounds__(AJ_THREADS) adjust_kernel(const AdjustArgs p) 
       for (int k = i + 1; k < biases; ++k)
         if (token[k] == t) sum = __fadd_rn(sum, value[k]);
       bias[t - lo] = sum;
-      atomicOr(&count[t - lo], kListed);
+      atomicOr(&count[t - lo], kBiased);
+      first_touch(t - lo);
     }
   }
   __syncthreads();
-  for (int i = tid; i < AJ_SLICE; i += AJ_THREADS) {
-    const bool on = count[i] != 0u;
-    const uint32_t votes = __ballot_sync(0xFFFFFFFFu, on);
-    uint32_t base = 0u;
-    if (lane == 0 && votes != 0u) base = atomicAdd(&listed, __popc(votes));
-    base = __shfl_sync(0xFFFFFFFFu, base, 0);
-    if (on) list[base + __popc(votes & ((1u << lane) - 1u))] = static_cast<uint16_t>(i);
-  }
-  __syncthreads();
-  const int entries = static_cast<int>(listed);
+  const int entries = listed;
+  const bool by_row = drafts_here != 0;  // counts that differ from row to row
 
   const float rep = p.repetition != nullptr ? p.repetition[n] : 1.0f;
   const float freq = p.frequency != nullptr ? p.frequency[n] : 0.0f;
   const float pres = p.presence != nullptr ? p.presence[n] : 0.0f;
-  const bool tree = is_tree(p.tree, p.tree_width, n, rows.count);
-  const bool copies = p.out != p.logits;
-  uint64_t path = 0ull;  // the rows whose drafts are counted
-  for (int j = 0; j < rows.count; ++j) {
+  auto source = [&](int j) {
+    return static_cast<const T *>(p.logits) + (rows.first + j) * p.stride + lo;
+  };
+  auto target = [&](int j) {
+    return static_cast<T *>(p.out) + (rows.first + j) * p.out_stride + lo;
+  };
+  auto mask_of = [&](int j) -> const uint32_t * {
+    if (p.mask == nullptr) return nullptr;
     const int64_t row = rows.first + j;
-    const T *src = static_cast<const T *>(p.logits) + row * p.stride + lo;
-    T *dst = static_cast<T *>(p.out) + row * p.out_stride + lo;
-    const uint32_t *mask = nullptr;
-    if (p.mask != nullptr) {
-      const int64_t m = p.mask_index != nullptr ? p.mask_index[row] : row;
-      if (m >= p.mask_rows) flags |= DSPARK_DEV_LEN_OOR;
-      else if (m >= 0) mask = p.mask + m * p.mask_stride + lo / 32;
+    const int64_t m = p.mask_index != nullptr ? p.mask_index[row] : row;
+    if (m >= p.mask_rows) flags |= DSPARK_DEV_LEN_OOR;
+    return m >= 0 && m < p.mask_rows ? p.mask + m * p.mask_stride + lo / 32 : nullptr;
+  };
+  auto adjust = [&](int j, int e) {
+    const int i = list[e];
+    const uint32_t *mask = mask_of(j);
+    if (mask != nullptr && (mask[i >> 5] >> (i & 31) & 1u) == 0u) return;
+    const uint32_t word = count[i], c = word & kCount;
+    float x = logit_f32(source(j)[i]);
+    if (c != 0u || (word & kInPrompt) != 0u) x = x > 0.0f ? __fdiv_rn(x, rep) : __fmul_rn(x, rep);
+    if (c != 0u) {
+      x = __fsub_rn(x, __fmul_rn(freq, static_cast<float>(c)));
+      x = __fsub_rn(x, pres);
     }
-    const uint64_t now =
-        (tree ? tree_bits(p.tree, p.tree_width, n, j, rows.count) : low_bits(j + 1)) & ~1ull;
-    if (tid >= 1 && tid <= drafts && ((now ^ path) >> tid & 1ull) != 0ull) {
-      const int t = draft[tid - 1] - lo;
-      if (t >= 0 && t < size && draft[tid - 1] >= 0)
-        atomicAdd(&count[t], (now >> tid & 1ull) != 0ull ? 1u : ~0u);
-    }
-    path = now;
-    // what the mask forbids, and a copy of the rest
-    for (int i = tid; i < size; i += AJ_THREADS) {
-      const bool forbidden = mask != nullptr && (mask[i >> 5] >> (i & 31) & 1u) == 0u;
-      if (forbidden) dst[i] = minus_infinity<T>();
-      else if (copies) dst[i] = src[i];
-    }
+    if ((word & kBiased) != 0u) x = __fadd_rn(x, bias[i]);
+    logit_set(x, target(j) + i);
+  };
+  const bool copies = p.out != p.logits;
+  if (copies) {
+    for (int j = j0; j < j1; ++j)
+      mask_row<T, true>(source(j), target(j), size, mask_of(j), words, tid, AJ_THREADS);
     __syncthreads();
-    for (int e = tid; e < entries; e += AJ_THREADS) {
-      const int i = list[e];
-      if (mask != nullptr && (mask[i >> 5] >> (i & 31) & 1u) == 0u) continue;
-      const uint32_t seen = count[i] & ~kListed, c = seen & kCount;
-      float x = logit_f32(src[i]);
-      if (seen != 0u) x = x > 0.0f ? __fdiv_rn(x, rep) : __fmul_rn(x, rep);
-      if (c != 0u) {
-        x = __fsub_rn(x, __fmul_rn(freq, static_cast<float>(c)));
-        x = __fsub_rn(x, pres);
+  }
+  if (!by_row) {
+    for (int x = tid; x < entries * (j1 - j0); x += AJ_THREADS) {
+      const int j = x / entries;
+      adjust(j0 + j, x - j * entries);
+    }
+  } else {
+    const bool tree = is_tree(p.tree, p.tree_width, n, rows.count);
+    uint64_t path = 0ull;  // the rows whose drafts are counted
+    for (int j = j0; j < j1; ++j) {
+      const uint64_t now =
+          (tree ? tree_bits(p.tree, p.tree_width, n, j, rows.count) : low_bits(j + 1)) & ~1ull;
+      if (tid >= 1 && tid <= drafts && ((now ^ path) >> tid & 1ull) != 0ull) {
+        const int t = draft[tid - 1];
+        if (t >= lo && t - lo < size)
+          atomicAdd(&count[t - lo], (now >> tid & 1ull) != 0ull ? 1u : ~0u);
       }
-      if (has_bias) x = __fadd_rn(x, bias[i]);
-      logit_set(x, dst + i);
+      path = now;
+      __syncthreads();
+      for (int e = tid; e < entries; e += AJ_THREADS) adjust(j, e);
+      __syncthreads();
     }
+  }
+  if (!copies && p.mask != nullptr) {
+    // vectors that are allowed in part are read again, with what was changed above
     __syncthreads();
+    for (int j = j0; j < j1; ++j) {
+      const uint32_t *mask = mask_of(j);
+      if (mask != nullptr)
+        mask_row<T, false>(target(j), target(j), size, mask, words, tid, AJ_THREADS);
+    }
   }
   if (flags != 0u) raise_status(p.status, flags);
 }
@@ -168,7 +264,13 @@ static dspark_status launch(const AdjustArgs &a, cudaStream_t stream) {
   if (cudaFuncSetAttribute(adjust_kernel<T>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                            AJ_SLICE * 10) != cudaSuccess)
     return DSPARK_ERR_CUDA;
-  const dim3 grid((a.vocab + AJ_SLICE - 1) / AJ_SLICE, a.N);
+  const int slices = (a.vocab + AJ_SLICE - 1) / AJ_SLICE;
+  // rows a request, as far as the host knows
+  const int64_t rows = (static_cast<int64_t>(a.R) + a.N - 1) / a.N;
+  const int64_t shares =
+      std::min(rows, (AJ_CTAS + static_cast<int64_t>(slices) * a.N - 1) /
+                         (static_cast<int64_t>(slices) * a.N));
+  const dim3 grid(slices, a.N, static_cast<unsigned>(std::max<int64_t>(1, shares)));
   return launch_overlapped(adjust_kernel<T>, grid, dim3(AJ_THREADS), smem, stream, a) ==
                  cudaSuccess
              ? DSPARK_OK
