@@ -10,6 +10,7 @@
 // and those that it allows whole are left alone; elsewhere all are copied.
 #include <algorithm>
 #include <cuda_bf16.h>
+#include <type_traits>
 
 #include "common.cuh"
 #include "launch.cuh"
@@ -17,9 +18,10 @@
 
 namespace dspark {
 
-constexpr int AJ_THREADS = 256;
+constexpr int AJ_THREADS = 512;
 constexpr int AJ_SLICE = 8192;             // vocabulary entries of a CTA
-constexpr int AJ_CTAS = 4 * 304;           // aimed at, by giving a CTA fewer rows
+constexpr int AJ_CTAS = 4 * 152;           // aimed at, by giving a CTA fewer rows
+constexpr int AJ_ROWS = 64;                // rows that are masked together
 constexpr uint32_t kListed = 1u << 31;
 constexpr uint32_t kInPrompt = 1u << 30;
 constexpr uint32_t kBiased = 1u << 29;
@@ -51,66 +53,90 @@ __device__ __forceinline__ uint32_t mask_bits(const uint32_t *mask, int i, int w
   return __funnelshift_r(lo, hi, shift) & ((1u << V) - 1u);
 }
 
-// One row of the slice: what the mask forbids, and where `copies` the rest.
-template <typename T, bool COPIES>
-__device__ __forceinline__ void mask_row(const T *src, T *dst, int size, const uint32_t *mask,
-                                         int words, int thread, int threads) {
-  constexpr int V = 16 / sizeof(T);
-  auto one = [&](int i) {
-    if (mask != nullptr && (mask[i >> 5] >> (i & 31) & 1u) == 0u) dst[i] = minus_infinity<T>();
-    else if (COPIES) dst[i] = src[i];
-  };
-  // entries up to the first 16-byte boundary, vectors, and those left
-  const int lead =
-      min(size, static_cast<int>((16 - (reinterpret_cast<uintptr_t>(dst) & 15)) & 15) /
-                    static_cast<int>(sizeof(T)));
-  if (COPIES && ((reinterpret_cast<uintptr_t>(src) ^ reinterpret_cast<uintptr_t>(dst)) & 15) != 0) {
-    for (int i = thread; i < size; i += threads) one(i);
-    return;
+// What the vectors of a row need, once for the CTA.
+template <typename T>
+struct MaskRow {
+  const T *src;
+  T *dst;
+  const uint32_t *mask;
+  int32_t lead, vectors;  // entries up to the first 16-byte boundary; then so many
+};
+
+// The entries of a vector whose bits are 0 become -inf.
+template <typename T>
+__device__ __forceinline__ void forbid(uint4 &w, uint32_t keep) {
+  uint32_t *x = &w.x;
+  if constexpr (sizeof(T) == 2) {
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      // two bits to two half words of ones
+      const uint32_t ones = ((keep >> (2 * e) & 3u) * 0x8001u & 0x10001u) * 0xFFFFu;
+      x[e] = (x[e] & ones) | (0xFF80FF80u & ~ones);
+    }
+  } else {
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+      if ((keep >> e & 1u) == 0u) x[e] = 0xFF800000u;
   }
-  const int vectors = (size - lead) / V, tail = lead + vectors * V;
-  if (thread < lead) one(thread);
-  if (thread < size - tail) one(tail + thread);
-  union Vec {
-    uint4 w;
-    T x[V];
-  };
-  constexpr int UNROLL = 4;
-  for (int v0 = thread; v0 < vectors; v0 += threads * UNROLL) {
-    Vec x[UNROLL];
+}
+
+// What the masks of `count` rows forbid in the slice, and where `copies` the rest.
+template <typename T, bool COPIES>
+__device__ __forceinline__ void mask_rows(const MaskRow<T> *row, int count, int size, int words) {
+  constexpr int V = 16 / sizeof(T), VECTORS = AJ_SLICE / V, UNROLL = 4;
+  constexpr uint32_t ALL = (1u << V) - 1u;
+  const int total = count * VECTORS;
+  for (int x0 = threadIdx.x; x0 < total; x0 += UNROLL * AJ_THREADS) {
+    uint4 x[UNROLL];
+    T *at[UNROLL];
     uint32_t keep[UNROLL];
 #pragma unroll
     for (int u = 0; u < UNROLL; ++u) {
-      const int v = v0 + u * threads;
-      keep[u] = v < vectors && mask != nullptr ? mask_bits<V>(mask, lead + v * V, words)
-                                               : (1u << V) - 1u;
+      const int i = x0 + u * AJ_THREADS;
+      at[u] = nullptr;
+      keep[u] = ALL;
+      if (i >= total) continue;
+      const MaskRow<T> &r = row[i / VECTORS];
+      const int v = i % VECTORS, e = r.lead + v * V;
+      if (v >= r.vectors) continue;
+      if (r.mask != nullptr) keep[u] = mask_bits<V>(r.mask, e, words);
+      if (!COPIES && keep[u] == ALL) continue;
+      at[u] = r.dst + e;
+      if (keep[u] != 0u) x[u] = *reinterpret_cast<const uint4 *>(r.src + e);
     }
 #pragma unroll
     for (int u = 0; u < UNROLL; ++u) {
-      const int v = v0 + u * threads;
-      if (v < vectors && keep[u] != 0u && (COPIES || keep[u] != (1u << V) - 1u))
-        x[u].w = *reinterpret_cast<const uint4 *>(src + lead + v * V);
+      if (at[u] == nullptr) continue;
+      forbid<T>(x[u], keep[u]);
+      *reinterpret_cast<uint4 *>(at[u]) = x[u];
     }
-#pragma unroll
-    for (int u = 0; u < UNROLL; ++u) {
-      const int v = v0 + u * threads;
-      if (v < vectors && (COPIES || keep[u] != (1u << V) - 1u)) {
-#pragma unroll
-        for (int e = 0; e < V; ++e)
-          if ((keep[u] >> e & 1u) == 0u) x[u].x[e] = minus_infinity<T>();
-        *reinterpret_cast<uint4 *>(dst + lead + v * V) = x[u].w;
-      }
+  }
+  // the entries that no vector held: a warp a row
+  for (int j = threadIdx.x >> 5; j < count; j += AJ_THREADS / 32) {
+    const MaskRow<T> r = row[j];
+    const int held = r.vectors * V;
+    for (int k = threadIdx.x & 31; k < size - held; k += 32) {
+      const int i = k < r.lead ? k : k + held;
+      if (r.mask != nullptr && (r.mask[i >> 5] >> (i & 31) & 1u) == 0u)
+        r.dst[i] = minus_infinity<T>();
+      else if (COPIES)
+        r.dst[i] = r.src[i];
     }
   }
 }
 
 template <typename T>
-__global__ void __launch_bounds__(AJ_THREADS) adjust_kernel(const AdjustArgs p) {
+__global__ void __launch_bounds__(AJ_THREADS, 3) adjust_kernel(const AdjustArgs p) {
   extern __shared__ __align__(16) uint8_t aj_sm[];
   uint32_t *count = reinterpret_cast<uint32_t *>(aj_sm);           // [slice]
   uint16_t *list = reinterpret_cast<uint16_t *>(count + AJ_SLICE);  // [slice]
-  float *bias = reinterpret_cast<float *>(list + AJ_SLICE);         // [slice], if there are any
-  __shared__ int listed, drafts_here;
+  // the slice's biases, in order, if there are any: each one's value, the sum of its
+  // token's, its entry
+  float *bias = reinterpret_cast<float *>(list + AJ_SLICE);
+  float *bias_sum = bias + p.bias_width;
+  uint16_t *bias_entry = reinterpret_cast<uint16_t *>(bias_sum + p.bias_width);
+  __shared__ int listed, drafts_here, masked_rows, warp_biases[AJ_THREADS / 32];
+  __shared__ MaskRow<T> mask_row[AJ_ROWS];
   const int tid = threadIdx.x;
   wait_for_earlier_kernel();
   const int n = blockIdx.y;
@@ -169,19 +195,38 @@ __global__ void __launch_bounds__(AJ_THREADS) adjust_kernel(const AdjustArgs p) 
     const int biases = min(max(p.bias_count[n], 0), p.bias_width);
     const int32_t *token = p.bias_token + static_cast<int64_t>(n) * p.bias_width;
     const float *value = p.bias_value + static_cast<int64_t>(n) * p.bias_width;
-    for (int i = tid; i < biases; i += AJ_THREADS) {
-      const int t = token[i];
-      if (!in_slice(t)) continue;
-      // a token's first place adds up all of its values, in order
-      bool first = true;
-      for (int k = 0; k < i && first; ++k) first = token[k] != t;
-      if (!first) continue;
-      float sum = value[i];
-      for (int k = i + 1; k < biases; ++k)
-        if (token[k] == t) sum = __fadd_rn(sum, value[k]);
-      bias[t - lo] = sum;
-      atomicOr(&count[t - lo], kBiased);
-      first_touch(t - lo);
+    int here = 0;  // in the slice, so far
+    for (int i0 = 0; i0 < biases; i0 += AJ_THREADS) {
+      const int i = i0 + tid;
+      const int t = i < biases ? token[i] : lo + size;
+      const bool in = i < biases && in_slice(t);
+      const uint32_t votes = __ballot_sync(0xFFFFFFFFu, in);
+      if ((tid & 31) == 0) warp_biases[tid >> 5] = __popc(votes);
+      __syncthreads();
+      int at = here;
+      for (int w = 0; w < AJ_THREADS / 32; ++w) {
+        if (w < tid >> 5) at += warp_biases[w];
+        here += warp_biases[w];
+      }
+      if (in) {
+        at += __popc(votes & ((1u << (tid & 31)) - 1u));
+        bias[at] = value[i];
+        bias_entry[at] = static_cast<uint16_t>(t - lo);
+        atomicOr(&count[t - lo], kBiased);
+        first_touch(t - lo);
+      }
+      __syncthreads();
+    }
+    // a token's first bias adds up all of them, in order
+    for (int i = tid; i < here; i += AJ_THREADS) {
+      const int e = bias_entry[i];
+      int k = 0;
+      while (bias_entry[k] != e) ++k;
+      if (k < i) continue;
+      float sum = bias[i];
+      for (k = i + 1; k < here; ++k)
+        if (bias_entry[k] == e) sum = __fadd_rn(sum, bias[k]);
+      bias_sum[i] = sum;
     }
   }
   __syncthreads();
@@ -215,13 +260,40 @@ __global__ void __launch_bounds__(AJ_THREADS) adjust_kernel(const AdjustArgs p) 
       x = __fsub_rn(x, __fmul_rn(freq, static_cast<float>(c)));
       x = __fsub_rn(x, pres);
     }
-    if ((word & kBiased) != 0u) x = __fadd_rn(x, bias[i]);
+    if ((word & kBiased) != 0u) {
+      int k = 0;
+      while (bias_entry[k] != i) ++k;
+      x = __fadd_rn(x, bias_sum[k]);
+    }
     logit_set(x, target(j) + i);
   };
   const bool copies = p.out != p.logits;
+  // rows that have something for mask_rows, AJ_ROWS at a time
+  auto mask_all = [&](auto copying) {
+    constexpr bool COPIES = decltype(copying)::value;
+    constexpr int V = 16 / sizeof(T);
+    for (int b0 = j0; b0 < j1; b0 += AJ_ROWS) {
+      __syncthreads();
+      if (tid == 0) masked_rows = 0;
+      __syncthreads();
+      const int j = b0 + tid;
+      if (tid < AJ_ROWS && j < j1) {
+        MaskRow<T> r;
+        r.src = source(j);
+        r.dst = target(j);
+        r.mask = mask_of(j);
+        const uintptr_t off = reinterpret_cast<uintptr_t>(r.dst) & 15;
+        r.lead = min(size, static_cast<int>((16 - off) & 15) / static_cast<int>(sizeof(T)));
+        // rows whose two sides are not aligned alike have no vectors
+        r.vectors = off == (reinterpret_cast<uintptr_t>(r.src) & 15) ? (size - r.lead) / V : 0;
+        if (COPIES || r.mask != nullptr) mask_row[atomicAdd(&masked_rows, 1)] = r;
+      }
+      __syncthreads();
+      mask_rows<T, COPIES>(mask_row, masked_rows, size, words);
+    }
+  };
   if (copies) {
-    for (int j = j0; j < j1; ++j)
-      mask_row<T, true>(source(j), target(j), size, mask_of(j), words, tid, AJ_THREADS);
+    mask_all(std::true_type());
     __syncthreads();
   }
   if (!by_row) {
@@ -246,23 +318,18 @@ __global__ void __launch_bounds__(AJ_THREADS) adjust_kernel(const AdjustArgs p) 
       __syncthreads();
     }
   }
-  if (!copies && p.mask != nullptr) {
-    // vectors that are allowed in part are read again, with what was changed above
-    __syncthreads();
-    for (int j = j0; j < j1; ++j) {
-      const uint32_t *mask = mask_of(j);
-      if (mask != nullptr)
-        mask_row<T, false>(target(j), target(j), size, mask, words, tid, AJ_THREADS);
-    }
-  }
+  // vectors that are allowed in part are read again, with what was changed above
+  if (!copies && p.mask != nullptr) mask_all(std::false_type());
   if (flags != 0u) raise_status(p.status, flags);
 }
 
 template <typename T>
 static dspark_status launch(const AdjustArgs &a, cudaStream_t stream) {
-  const size_t smem = AJ_SLICE * (a.bias_width > 0 ? 10 : 6);
+  const size_t smem = AJ_SLICE * 6 + static_cast<size_t>(a.bias_width) * 10;
   if (cudaFuncSetAttribute(adjust_kernel<T>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                           AJ_SLICE * 10) != cudaSuccess)
+                           AJ_SLICE * 6 + kMaxBias * 10) != cudaSuccess ||
+      cudaFuncSetAttribute(adjust_kernel<T>, cudaFuncAttributePreferredSharedMemoryCarveout,
+                           cudaSharedmemCarveoutMaxShared) != cudaSuccess)
     return DSPARK_ERR_CUDA;
   const int slices = (a.vocab + AJ_SLICE - 1) / AJ_SLICE;
   // rows a request, as far as the host knows
