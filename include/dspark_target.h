@@ -233,7 +233,8 @@ DSPARK_API dspark_status dspark_tree_attention(
  * mask_index   [R]: a row's row of mask, negative = none masked; or NULL: the row
  *              itself.  An index >= mask_rows masks nothing, DSPARK_DEV_LEN_OOR.
  * workspace    256 bytes (the status word).
- * Limits: 1 <= N <= 16384, 0 <= K <= 63, 1 <= vocab < 2^30, bias_width <= 1024.
+ * Limits: 1 <= N <= 16384, 0 <= K <= 63, 1 <= vocab < 2^30, bias_width <= 1024,
+ * tokens_width <= 2^26, 0 < R <= 2^22.
  * ------------------------------------------------------------------------ */
 DSPARK_API dspark_status dspark_adjust_logits(
     const void *logits, int64_t stride, int32_t dtype, int32_t R, int32_t vocab,

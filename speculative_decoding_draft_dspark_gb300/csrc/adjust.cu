@@ -1,16 +1,20 @@
-// Penalties, biases and masks on logits.
+// Penalties, biases and masks on logits, in two kernels.
 //
-// Few of a row's logits change: the tokens of the request's history and drafts, its
-// biases, and what a mask forbids.  A CTA takes one request and a slice of the
-// vocabulary that fits into shared memory: it counts the history's tokens there (a
-// word an entry, no hashing, whole numbers, so their order does not matter) and lists
-// the entries that any row may change, then goes through the request's rows (a share
-// of them, where there are few CTAs): the listed entries one by one, and the slice 16
-// bytes at a time.  In place, vectors that the mask forbids whole are written unread
-// and those that it allows whole are left alone; elsewhere all are copied.
+// mask_kernel streams what a mask forbids, 16 bytes at a time: in place, vectors that
+// are forbidden whole are written unread and those that are allowed whole are left
+// alone; elsewhere all are copied.
+//
+// adjust_kernel changes the few entries of a row that can change otherwise: the tokens
+// of the request's history and drafts, and its biases.  A CTA counts the tokens of one
+// request in shared memory, lists the distinct ones, and then takes a share of the
+// request's rows, entry by entry.  The counts are whole numbers, so their order does
+// not matter.  They are in a hash table where one holds every token that a request can
+// have; longer histories go through the vocabulary a slice at a time, a CTA each,
+// with a word for every entry.  (A slice costs the whole history again: at 262144
+// entries and 256 requests of up to 4096 tokens 32 slices took 490 us, in place and
+// with masks in the same kernel.)
 #include <algorithm>
 #include <cuda_bf16.h>
-#include <type_traits>
 
 #include "common.cuh"
 #include "launch.cuh"
@@ -18,14 +22,19 @@
 
 namespace dspark {
 
+constexpr int MK_THREADS = 256;
+constexpr int MK_CHUNK = 32768;            // entries of a CTA
 constexpr int AJ_THREADS = 512;
-constexpr int AJ_SLICE = 8192;             // vocabulary entries of a CTA
-constexpr int AJ_CTAS = 4 * 152;           // aimed at, by giving a CTA fewer rows
-constexpr int AJ_ROWS = 64;                // rows that are masked together
+constexpr int AJ_SLICE = 8192;             // vocabulary entries of a CTA without hashing
+constexpr int AJ_MOST_SLOTS = 16384;       // of a hash table
+constexpr int AJ_CTAS = 2 * 152;           // aimed at, by giving a CTA fewer rows
+constexpr uint32_t kEmpty = 0xFFFFFFFFu;
 constexpr uint32_t kListed = 1u << 31;
 constexpr uint32_t kInPrompt = 1u << 30;
 constexpr uint32_t kBiased = 1u << 29;
-constexpr uint32_t kCount = kBiased - 1;
+constexpr uint32_t kBiases = 1u << 28;     // more than one
+constexpr uint32_t kDraft = 1u << 27;
+constexpr uint32_t kCount = kDraft - 1;
 
 template <typename T>
 __device__ __forceinline__ T minus_infinity();
@@ -53,295 +62,276 @@ __device__ __forceinline__ uint32_t mask_bits(const uint32_t *mask, int i, int w
   return __funnelshift_r(lo, hi, shift) & ((1u << V) - 1u);
 }
 
-// What the vectors of a row need, once for the CTA.
+// ------------------------------------------------------------------- masks
 template <typename T>
-struct MaskRow {
-  const T *src;
-  T *dst;
-  const uint32_t *mask;
-  int32_t lead, vectors;  // entries up to the first 16-byte boundary; then so many
-};
-
-// The entries of a vector whose bits are 0 become -inf.
-template <typename T>
-__device__ __forceinline__ void forbid(uint4 &w, uint32_t keep) {
-  uint32_t *x = &w.x;
-  if constexpr (sizeof(T) == 2) {
-#pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      // two bits to two half words of ones
-      const uint32_t ones = ((keep >> (2 * e) & 3u) * 0x8001u & 0x10001u) * 0xFFFFu;
-      x[e] = (x[e] & ones) | (0xFF80FF80u & ~ones);
-    }
-  } else {
-#pragma unroll
-    for (int e = 0; e < 4; ++e)
-      if ((keep >> e & 1u) == 0u) x[e] = 0xFF800000u;
-  }
-}
-
-// What the masks of `count` rows forbid in the slice, and where `copies` the rest.
-template <typename T, bool COPIES>
-__device__ __forceinline__ void mask_rows(const MaskRow<T> *row, int count, int size, int words) {
-  constexpr int V = 16 / sizeof(T), VECTORS = AJ_SLICE / V, UNROLL = 4;
+__global__ void __launch_bounds__(MK_THREADS) mask_kernel(const AdjustArgs p) {
+  constexpr int V = 16 / sizeof(T), UNROLL = 4;
   constexpr uint32_t ALL = (1u << V) - 1u;
-  const int total = count * VECTORS;
-  for (int x0 = threadIdx.x; x0 < total; x0 += UNROLL * AJ_THREADS) {
+  constexpr uint32_t NONE = sizeof(T) == 2 ? 0xFF80FF80u : 0xFF800000u;
+  __shared__ uint4 ones[1 << V];  // a vector's bits, each as wide as an entry
+  const int tid = threadIdx.x;
+  if (tid < 1 << V) {
+    uint32_t m[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+      m[k] = V == 8 ? (tid >> (2 * k) & 1u) * 0xFFFFu | (tid >> (2 * k + 1) & 1u) * 0xFFFF0000u
+                    : (tid >> k & 1u) * 0xFFFFFFFFu;
+    ones[tid] = make_uint4(m[0], m[1], m[2], m[3]);
+  }
+  wait_for_earlier_kernel();
+  allow_next_kernel();
+  const int64_t row = blockIdx.x;
+  if (row < max(p.cu_rows[0], 0) || row >= p.cu_rows[p.N]) return;
+  const bool copies = p.out != p.logits;
+  const uint32_t *mask = nullptr;
+  if (p.mask != nullptr) {
+    const int64_t m = p.mask_index != nullptr ? p.mask_index[row] : row;
+    if (m >= p.mask_rows) raise_status(p.status, DSPARK_DEV_LEN_OOR);
+    else if (m >= 0) mask = p.mask + m * p.mask_stride;
+  }
+  if (!copies && mask == nullptr) return;
+  __syncthreads();
+  const int lo = blockIdx.y * MK_CHUNK, size = min(MK_CHUNK, p.vocab - lo);
+  const int words = (size + 31) / 32;
+  if (mask != nullptr) mask += lo / 32;
+  const T *src = static_cast<const T *>(p.logits) + row * p.stride + lo;
+  T *dst = static_cast<T *>(p.out) + row * p.out_stride + lo;
+  // entries up to the first 16-byte boundary, vectors, and those left; none of them
+  // vectors where the two sides are not aligned alike
+  const uintptr_t off = reinterpret_cast<uintptr_t>(dst) & 15;
+  const int lead = min(size, static_cast<int>((16 - off) & 15) / static_cast<int>(sizeof(T)));
+  const int vectors = off == (reinterpret_cast<uintptr_t>(src) & 15) ? (size - lead) / V : 0;
+  const uint8_t *bytes = reinterpret_cast<const uint8_t *>(mask);
+  for (int v0 = tid; v0 < vectors; v0 += UNROLL * MK_THREADS) {
     uint4 x[UNROLL];
-    T *at[UNROLL];
     uint32_t keep[UNROLL];
 #pragma unroll
     for (int u = 0; u < UNROLL; ++u) {
-      const int i = x0 + u * AJ_THREADS;
-      at[u] = nullptr;
+      const int v = v0 + u * MK_THREADS;
       keep[u] = ALL;
-      if (i >= total) continue;
-      const MaskRow<T> &r = row[i / VECTORS];
-      const int v = i % VECTORS, e = r.lead + v * V;
-      if (v >= r.vectors) continue;
-      if (r.mask != nullptr) keep[u] = mask_bits<V>(r.mask, e, words);
-      if (!COPIES && keep[u] == ALL) continue;
-      at[u] = r.dst + e;
-      if (keep[u] != 0u) x[u] = *reinterpret_cast<const uint4 *>(r.src + e);
+      if (mask != nullptr && v < vectors) {
+        if (lead == 0) keep[u] = V == 8 ? bytes[v] : bytes[v >> 1] >> (4 * (v & 1)) & ALL;
+        else keep[u] = mask_bits<V>(mask, lead + v * V, words);
+      }
     }
 #pragma unroll
     for (int u = 0; u < UNROLL; ++u) {
-      if (at[u] == nullptr) continue;
-      forbid<T>(x[u], keep[u]);
-      *reinterpret_cast<uint4 *>(at[u]) = x[u];
+      const int v = v0 + u * MK_THREADS;
+      if (v < vectors && keep[u] != 0u && (copies || keep[u] != ALL))
+        x[u] = *reinterpret_cast<const uint4 *>(src + lead + v * V);
+    }
+#pragma unroll
+    for (int u = 0; u < UNROLL; ++u) {
+      const int v = v0 + u * MK_THREADS;
+      if (v >= vectors || (!copies && keep[u] == ALL)) continue;
+      const uint4 m = ones[keep[u]];
+      x[u].x = (x[u].x & m.x) | (NONE & ~m.x);
+      x[u].y = (x[u].y & m.y) | (NONE & ~m.y);
+      x[u].z = (x[u].z & m.z) | (NONE & ~m.z);
+      x[u].w = (x[u].w & m.w) | (NONE & ~m.w);
+      *reinterpret_cast<uint4 *>(dst + lead + v * V) = x[u];
     }
   }
-  // the entries that no vector held: a warp a row
-  for (int j = threadIdx.x >> 5; j < count; j += AJ_THREADS / 32) {
-    const MaskRow<T> r = row[j];
-    const int held = r.vectors * V;
-    for (int k = threadIdx.x & 31; k < size - held; k += 32) {
-      const int i = k < r.lead ? k : k + held;
-      if (r.mask != nullptr && (r.mask[i >> 5] >> (i & 31) & 1u) == 0u)
-        r.dst[i] = minus_infinity<T>();
-      else if (COPIES)
-        r.dst[i] = r.src[i];
-    }
+  const int held = vectors * V;
+  for (int k = tid; k < size - held; k += MK_THREADS) {
+    const int i = k < lead ? k : k + held;
+    if (mask != nullptr && (mask[i >> 5] >> (i & 31) & 1u) == 0u) dst[i] = minus_infinity<T>();
+    else if (copies) dst[i] = src[i];
   }
 }
 
-template <typename T>
-__global__ void __launch_bounds__(AJ_THREADS, 3) adjust_kernel(const AdjustArgs p) {
+// ------------------------------------------------- penalties and biases
+// Shared memory of adjust_kernel: a word a slot for its count and flags; the token
+// (hashing); a bias's place; the list of slots in use.
+struct AdjustShape {
+  int slots;   // a power of two when hashing, AJ_SLICE otherwise
+  int slices;  // of the vocabulary: 1 when hashing
+  __host__ __device__ int bytes(bool hash, bool biases) const {
+    return slots * (4 + (hash ? 4 : 0) + 2 + (biases ? 2 : 0));
+  }
+};
+
+template <typename T, bool HASH>
+__global__ void __launch_bounds__(AJ_THREADS, 2)
+    adjust_kernel(const AdjustArgs p, const AdjustShape shape) {
   extern __shared__ __align__(16) uint8_t aj_sm[];
-  uint32_t *count = reinterpret_cast<uint32_t *>(aj_sm);           // [slice]
-  uint16_t *list = reinterpret_cast<uint16_t *>(count + AJ_SLICE);  // [slice]
-  // the slice's biases, in order, if there are any: each one's value, the sum of its
-  // token's, its entry
-  float *bias = reinterpret_cast<float *>(list + AJ_SLICE);
-  float *bias_sum = bias + p.bias_width;
-  uint16_t *bias_entry = reinterpret_cast<uint16_t *>(bias_sum + p.bias_width);
-  __shared__ int listed, drafts_here, masked_rows, warp_biases[AJ_THREADS / 32];
-  __shared__ MaskRow<T> mask_row[AJ_ROWS];
+  uint32_t *count = reinterpret_cast<uint32_t *>(aj_sm);
+  uint32_t *key = count + shape.slots;                                   // hashing
+  uint16_t *list = reinterpret_cast<uint16_t *>(HASH ? key + shape.slots : key);
+  uint16_t *bias_at = list + shape.slots;                                // with biases
+  __shared__ int listed;
+  __shared__ int32_t draft[kMaxStepDrafts + 1];  // [i]: the token of the request's row i
   const int tid = threadIdx.x;
-  wait_for_earlier_kernel();
+  // What is read up to the wait below was there before mask_kernel, whose CTAs had all
+  // waited for it when this kernel was let in; without mask_kernel this is the first.
+  const bool after_masks = p.out != p.logits || p.mask != nullptr;
+  if (!after_masks) wait_for_earlier_kernel();
   const int n = blockIdx.y;
+  for (int i = tid; i < shape.slots / 4; i += AJ_THREADS) {
+    reinterpret_cast<uint4 *>(count)[i] = make_uint4(0u, 0u, 0u, 0u);
+    if (HASH) reinterpret_cast<uint4 *>(key)[i] = make_uint4(kEmpty, kEmpty, kEmpty, kEmpty);
+  }
+  if (tid == 0) listed = 0;
   const RowSpan rows = row_span(p.cu_rows, n, p.R);
   // this CTA's share of them
   const int share = (rows.count + gridDim.z - 1) / gridDim.z;
   const int j0 = blockIdx.z * share, j1 = min(rows.count, j0 + share);
-  if (j0 >= j1) return;
-  const int lo = blockIdx.x * AJ_SLICE, size = min(AJ_SLICE, p.vocab - lo);
-  const int words = (size + 31) / 32;
-  uint32_t flags = 0u;
-
-  for (int i = tid; i < AJ_SLICE / 4; i += AJ_THREADS)
-    reinterpret_cast<uint4 *>(count)[i] = make_uint4(0u, 0u, 0u, 0u);
-  if (tid == 0) listed = drafts_here = 0;
-  __syncthreads();
+  if (j0 >= j1) {
+    if (after_masks) wait_for_earlier_kernel();
+    return;
+  }
   int hist = p.hist_len[n];
+  const int prompt = p.prompt_len != nullptr ? p.prompt_len[n] : 0;
+  const int biases = p.bias_width > 0 ? min(max(p.bias_count[n], 0), p.bias_width) : 0;
+  const int32_t *bias_token = p.bias_token + static_cast<int64_t>(n) * p.bias_width;
+  const float *bias_value = p.bias_value + static_cast<int64_t>(n) * p.bias_width;
+  const int drafts = min(p.K, rows.count - 1);
+  const int lo = HASH ? 0 : blockIdx.x * AJ_SLICE;
+  const int size = HASH ? p.vocab : min(AJ_SLICE, p.vocab - lo);
+  uint32_t flags = 0u;
   if (hist < 0 || hist > p.tokens_width) flags |= DSPARK_DEV_LEN_OOR;
   hist = min(max(hist, 0), p.tokens_width);
-  const int prompt = p.prompt_len != nullptr ? p.prompt_len[n] : 0;
-  auto in_slice = [&](int t) {
+  __syncthreads();
+
+  // the slot of a token that this CTA has, listed on first touch; -1 otherwise
+  auto slot_of = [&](int t) -> int {
     if (t < 0 || t >= p.vocab) flags |= DSPARK_DEV_TOKEN_OOR;
-    return t >= lo && t - lo < size;
+    if (t < lo || t - lo >= size) return -1;
+    int s = t - lo;
+    if constexpr (HASH) {
+      const uint32_t key_t = static_cast<uint32_t>(t);
+      s = static_cast<int>((key_t * 2654435769u) >> 16) & (shape.slots - 1);
+      while (true) {
+        const uint32_t old = atomicCAS(&key[s], kEmpty, key_t);
+        if (old == kEmpty || old == key_t) break;
+        s = (s + 1) & (shape.slots - 1);
+      }
+    }
+    return s;
   };
-  // the first to touch an entry lists it
-  auto first_touch = [&](int i) {
-    if ((atomicOr(&count[i], kListed) & kListed) == 0u)
-      list[atomicAdd(&listed, 1)] = static_cast<uint16_t>(i);
+  auto touch = [&](int s, uint32_t flag) -> uint32_t {
+    const uint32_t old = atomicOr(&count[s], flag | kListed);
+    if ((old & kListed) == 0u) list[atomicAdd(&listed, 1)] = static_cast<uint16_t>(s);
+    return old;
   };
   const int32_t *text = p.tokens + n * p.tokens_stride;
-  for (int i0 = tid; i0 < hist; i0 += 4 * AJ_THREADS) {
-    int t[4];
+  constexpr int UNROLL = 4;
+  for (int i0 = tid; i0 < hist; i0 += UNROLL * AJ_THREADS) {
+    int t[UNROLL];
 #pragma unroll
-    for (int u = 0; u < 4; ++u)
-      t[u] = i0 + u * AJ_THREADS < hist ? text[i0 + u * AJ_THREADS] : lo + size;
+    for (int u = 0; u < UNROLL; ++u)
+      if (i0 + u * AJ_THREADS < hist) t[u] = text[i0 + u * AJ_THREADS];
 #pragma unroll
-    for (int u = 0; u < 4; ++u) {
+    for (int u = 0; u < UNROLL; ++u) {
       const int i = i0 + u * AJ_THREADS;
-      if (i >= hist || !in_slice(t[u])) continue;
-      const int e = t[u] - lo;
-      if (i < prompt) atomicOr(&count[e], kInPrompt);
-      else atomicAdd(&count[e], 1u);
-      first_touch(e);
+      if (i >= hist) continue;
+      const int s = slot_of(t[u]);
+      if (s < 0) continue;
+      touch(s, i < prompt ? kInPrompt : 0u);
+      if (i >= prompt) atomicAdd(&count[s], 1u);
     }
   }
-  const int drafts = min(p.K, rows.count - 1);
-  const int32_t *draft = p.draft + static_cast<int64_t>(n) * p.K;
   if (tid < drafts) {
-    const int t = draft[tid];
-    if (in_slice(t)) {
-      first_touch(t - lo);
-      drafts_here = 1;
-    }
+    const int t = p.draft[static_cast<int64_t>(n) * p.K + tid];
+    draft[tid + 1] = t;
+    const int s = slot_of(t);
+    if (s >= 0) touch(s, kDraft);
   }
-  if (p.bias_width > 0) {
-    const int biases = min(max(p.bias_count[n], 0), p.bias_width);
-    const int32_t *token = p.bias_token + static_cast<int64_t>(n) * p.bias_width;
-    const float *value = p.bias_value + static_cast<int64_t>(n) * p.bias_width;
-    int here = 0;  // in the slice, so far
-    for (int i0 = 0; i0 < biases; i0 += AJ_THREADS) {
-      const int i = i0 + tid;
-      const int t = i < biases ? token[i] : lo + size;
-      const bool in = i < biases && in_slice(t);
-      const uint32_t votes = __ballot_sync(0xFFFFFFFFu, in);
-      if ((tid & 31) == 0) warp_biases[tid >> 5] = __popc(votes);
-      __syncthreads();
-      int at = here;
-      for (int w = 0; w < AJ_THREADS / 32; ++w) {
-        if (w < tid >> 5) at += warp_biases[w];
-        here += warp_biases[w];
-      }
-      if (in) {
-        at += __popc(votes & ((1u << (tid & 31)) - 1u));
-        bias[at] = value[i];
-        bias_entry[at] = static_cast<uint16_t>(t - lo);
-        atomicOr(&count[t - lo], kBiased);
-        first_touch(t - lo);
-      }
-      __syncthreads();
-    }
-    // a token's first bias adds up all of them, in order
-    for (int i = tid; i < here; i += AJ_THREADS) {
-      const int e = bias_entry[i];
-      int k = 0;
-      while (bias_entry[k] != e) ++k;
-      if (k < i) continue;
-      float sum = bias[i];
-      for (k = i + 1; k < here; ++k)
-        if (bias_entry[k] == e) sum = __fadd_rn(sum, bias[k]);
-      bias_sum[i] = sum;
-    }
+  for (int i = tid; i < biases; i += AJ_THREADS) {
+    const int s = slot_of(bias_token[i]);
+    if (s < 0) continue;
+    if ((touch(s, kBiased) & kBiased) != 0u) touch(s, kBiases);
+    bias_at[s] = static_cast<uint16_t>(i);
   }
   __syncthreads();
   const int entries = listed;
-  const bool by_row = drafts_here != 0;  // counts that differ from row to row
-
   const float rep = p.repetition != nullptr ? p.repetition[n] : 1.0f;
   const float freq = p.frequency != nullptr ? p.frequency[n] : 0.0f;
   const float pres = p.presence != nullptr ? p.presence[n] : 0.0f;
-  auto source = [&](int j) {
-    return static_cast<const T *>(p.logits) + (rows.first + j) * p.stride + lo;
-  };
-  auto target = [&](int j) {
-    return static_cast<T *>(p.out) + (rows.first + j) * p.out_stride + lo;
-  };
-  auto mask_of = [&](int j) -> const uint32_t * {
-    if (p.mask == nullptr) return nullptr;
+  const bool tree = is_tree(p.tree, p.tree_width, n, rows.count);
+  if (after_masks) wait_for_earlier_kernel();
+
+  // Entries that are allowed: in place their logits are as they were.
+  const int total = entries * (j1 - j0);
+  for (int x = tid; x < total; x += AJ_THREADS) {
+    const int r = x / entries, j = j0 + r, s = list[x - r * entries];
+    const int t = HASH ? static_cast<int>(key[s]) : lo + s;
     const int64_t row = rows.first + j;
-    const int64_t m = p.mask_index != nullptr ? p.mask_index[row] : row;
-    if (m >= p.mask_rows) flags |= DSPARK_DEV_LEN_OOR;
-    return m >= 0 && m < p.mask_rows ? p.mask + m * p.mask_stride + lo / 32 : nullptr;
-  };
-  auto adjust = [&](int j, int e) {
-    const int i = list[e];
-    const uint32_t *mask = mask_of(j);
-    if (mask != nullptr && (mask[i >> 5] >> (i & 31) & 1u) == 0u) return;
-    const uint32_t word = count[i], c = word & kCount;
-    float x = logit_f32(source(j)[i]);
-    if (c != 0u || (word & kInPrompt) != 0u) x = x > 0.0f ? __fdiv_rn(x, rep) : __fmul_rn(x, rep);
+    float v = logit_f32(static_cast<const T *>(p.logits)[row * p.stride + t]);
+    if (p.mask != nullptr) {
+      const int64_t m = p.mask_index != nullptr ? p.mask_index[row] : row;
+      if (m >= 0 && m < p.mask_rows &&
+          (p.mask[m * p.mask_stride + (t >> 5)] >> (t & 31) & 1u) == 0u)
+        continue;
+    }
+    const uint32_t word = count[s];
+    uint32_t c = word & kCount;
+    if ((word & kDraft) != 0u) {
+      // on row j's path: the rows that it attends, without row 0
+      const uint64_t path =
+          tree ? tree_bits(p.tree, p.tree_width, n, j, rows.count) : low_bits(j + 1);
+      for (int i = 1; i <= drafts; ++i)
+        if (draft[i] == t) c += static_cast<uint32_t>(path >> i) & 1u;
+    }
+    if (c != 0u || (word & kInPrompt) != 0u) v = v > 0.0f ? __fdiv_rn(v, rep) : __fmul_rn(v, rep);
     if (c != 0u) {
-      x = __fsub_rn(x, __fmul_rn(freq, static_cast<float>(c)));
-      x = __fsub_rn(x, pres);
+      v = __fsub_rn(v, __fmul_rn(freq, static_cast<float>(c)));
+      v = __fsub_rn(v, pres);
     }
-    if ((word & kBiased) != 0u) {
-      int k = 0;
-      while (bias_entry[k] != i) ++k;
-      x = __fadd_rn(x, bias_sum[k]);
-    }
-    logit_set(x, target(j) + i);
-  };
-  const bool copies = p.out != p.logits;
-  // rows that have something for mask_rows, AJ_ROWS at a time
-  auto mask_all = [&](auto copying) {
-    constexpr bool COPIES = decltype(copying)::value;
-    constexpr int V = 16 / sizeof(T);
-    for (int b0 = j0; b0 < j1; b0 += AJ_ROWS) {
-      __syncthreads();
-      if (tid == 0) masked_rows = 0;
-      __syncthreads();
-      const int j = b0 + tid;
-      if (tid < AJ_ROWS && j < j1) {
-        MaskRow<T> r;
-        r.src = source(j);
-        r.dst = target(j);
-        r.mask = mask_of(j);
-        const uintptr_t off = reinterpret_cast<uintptr_t>(r.dst) & 15;
-        r.lead = min(size, static_cast<int>((16 - off) & 15) / static_cast<int>(sizeof(T)));
-        // rows whose two sides are not aligned alike have no vectors
-        r.vectors = off == (reinterpret_cast<uintptr_t>(r.src) & 15) ? (size - r.lead) / V : 0;
-        if (COPIES || r.mask != nullptr) mask_row[atomicAdd(&masked_rows, 1)] = r;
+    if ((word & kBiases) != 0u) {
+      // several: their sum, in order
+      bool any = false;
+      float sum = 0.0f;
+      for (int i = 0; i < biases; ++i) {
+        if (bias_token[i] != t) continue;
+        sum = any ? __fadd_rn(sum, bias_value[i]) : bias_value[i];
+        any = true;
       }
-      __syncthreads();
-      mask_rows<T, COPIES>(mask_row, masked_rows, size, words);
+      v = __fadd_rn(v, sum);
+    } else if ((word & kBiased) != 0u) {
+      v = __fadd_rn(v, bias_value[bias_at[s]]);
     }
-  };
-  if (copies) {
-    mask_all(std::true_type());
-    __syncthreads();
+    logit_set(v, static_cast<T *>(p.out) + row * p.out_stride + t);
   }
-  if (!by_row) {
-    for (int x = tid; x < entries * (j1 - j0); x += AJ_THREADS) {
-      const int j = x / entries;
-      adjust(j0 + j, x - j * entries);
-    }
-  } else {
-    const bool tree = is_tree(p.tree, p.tree_width, n, rows.count);
-    uint64_t path = 0ull;  // the rows whose drafts are counted
-    for (int j = j0; j < j1; ++j) {
-      const uint64_t now =
-          (tree ? tree_bits(p.tree, p.tree_width, n, j, rows.count) : low_bits(j + 1)) & ~1ull;
-      if (tid >= 1 && tid <= drafts && ((now ^ path) >> tid & 1ull) != 0ull) {
-        const int t = draft[tid - 1];
-        if (t >= lo && t - lo < size)
-          atomicAdd(&count[t - lo], (now >> tid & 1ull) != 0ull ? 1u : ~0u);
-      }
-      path = now;
-      __syncthreads();
-      for (int e = tid; e < entries; e += AJ_THREADS) adjust(j, e);
-      __syncthreads();
-    }
-  }
-  // vectors that are allowed in part are read again, with what was changed above
-  if (!copies && p.mask != nullptr) mask_all(std::false_type());
   if (flags != 0u) raise_status(p.status, flags);
+}
+
+template <typename T, bool HASH>
+static dspark_status launch_adjust(const AdjustArgs &a, const AdjustShape &shape,
+                                   cudaStream_t stream) {
+  const bool biases = a.bias_width > 0;
+  const AdjustShape most = {HASH ? AJ_MOST_SLOTS : AJ_SLICE, 1};
+  if (cudaFuncSetAttribute(adjust_kernel<T, HASH>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                           most.bytes(HASH, true)) != cudaSuccess ||
+      cudaFuncSetAttribute(adjust_kernel<T, HASH>, cudaFuncAttributePreferredSharedMemoryCarveout,
+                           cudaSharedmemCarveoutMaxShared) != cudaSuccess)
+    return DSPARK_ERR_CUDA;
+  // rows a request, as far as the host knows
+  const int64_t rows = (static_cast<int64_t>(a.R) + a.N - 1) / a.N;
+  const int64_t each = static_cast<int64_t>(shape.slices) * a.N;
+  const int64_t shares = std::min(rows, (AJ_CTAS + each - 1) / each);
+  const dim3 grid(shape.slices, a.N, static_cast<unsigned>(shares));
+  return launch_overlapped(adjust_kernel<T, HASH>, grid, dim3(AJ_THREADS),
+                           shape.bytes(HASH, biases), stream, a, shape) == cudaSuccess
+             ? DSPARK_OK
+             : DSPARK_ERR_CUDA;
 }
 
 template <typename T>
 static dspark_status launch(const AdjustArgs &a, cudaStream_t stream) {
-  const size_t smem = AJ_SLICE * 6 + static_cast<size_t>(a.bias_width) * 10;
-  if (cudaFuncSetAttribute(adjust_kernel<T>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                           AJ_SLICE * 6 + kMaxBias * 10) != cudaSuccess ||
-      cudaFuncSetAttribute(adjust_kernel<T>, cudaFuncAttributePreferredSharedMemoryCarveout,
-                           cudaSharedmemCarveoutMaxShared) != cudaSuccess)
-    return DSPARK_ERR_CUDA;
-  const int slices = (a.vocab + AJ_SLICE - 1) / AJ_SLICE;
-  // rows a request, as far as the host knows
-  const int64_t rows = (static_cast<int64_t>(a.R) + a.N - 1) / a.N;
-  const int64_t shares =
-      std::min(rows, (AJ_CTAS + static_cast<int64_t>(slices) * a.N - 1) /
-                         (static_cast<int64_t>(slices) * a.N));
-  const dim3 grid(slices, a.N, static_cast<unsigned>(std::max<int64_t>(1, shares)));
-  return launch_overlapped(adjust_kernel<T>, grid, dim3(AJ_THREADS), smem, stream, a) ==
-                 cudaSuccess
-             ? DSPARK_OK
-             : DSPARK_ERR_CUDA;
+  if (a.out != a.logits || a.mask != nullptr) {
+    const dim3 grid(a.R, (a.vocab + MK_CHUNK - 1) / MK_CHUNK);
+    if (launch_overlapped(mask_kernel<T>, grid, dim3(MK_THREADS), 0, stream, a) != cudaSuccess)
+      return DSPARK_ERR_CUDA;
+  }
+  // every token that a request can have, in two thirds of a table
+  const int64_t most = std::min<int64_t>(
+      a.vocab, static_cast<int64_t>(a.tokens_width) + a.K + a.bias_width);
+  AdjustShape shape = {256, 1};
+  while (shape.slots < AJ_MOST_SLOTS && 2ll * shape.slots < 3 * most) shape.slots *= 2;
+  if (2ll * shape.slots >= 3 * most) return launch_adjust<T, true>(a, shape, stream);
+  shape = {AJ_SLICE, (a.vocab + AJ_SLICE - 1) / AJ_SLICE};
+  return launch_adjust<T, false>(a, shape, stream);
 }
 
 dspark_status adjust_launch(const AdjustArgs &a, cudaStream_t stream) {

@@ -379,7 +379,7 @@ dspark_status dspark_adjust_logits(
   if (R <= 0 || vocab <= 0 || N <= 0 || K < 0 || tokens_width <= 0 || bias_width < 0)
     return DSPARK_ERR_INVALID_ARG;
   if (R > kMaxStepRows || vocab >= (1 << 30) || N > kMaxRequests || K > kMaxStepDrafts ||
-      bias_width > kMaxBias)
+      bias_width > kMaxBias || tokens_width > kMaxHistory)
     return DSPARK_ERR_UNSUPPORTED;
   dspark_status s = check_tree(tree, tree_width);
   if (s != DSPARK_OK) return s;

@@ -16,6 +16,7 @@ constexpr int kMaxStepRows = 1 << 22;
 constexpr int kMaxTreeRows = 64;
 constexpr int kMaxStepDrafts = kMaxTreeRows - 1;
 constexpr int kMaxBias = 1024;
+constexpr int kMaxHistory = 1 << 26;
 constexpr int kMaxAttentionHead = 256;
 
 struct RowsArgs {

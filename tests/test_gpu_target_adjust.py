@@ -95,7 +95,8 @@ def test_sizes(vocab, pad, in_place, dtype):
 @pytest.mark.parametrize("kw", [
     dict(bias=0, masked=False), dict(bias=0), dict(masked=False), dict(penalties=False), dict(prompt=False),
     dict(K=0), dict(K=63, counts=[64, 1, 30], tree=True), dict(K=63, counts=[64, 1, 30]), dict(bias=300, few=40),
-    dict(width=5000, few=900, counts=[8]), dict(counts=[1] * 300, K=1), dict(counts=[40], K=5),
+    dict(width=5000, few=900, counts=[8]), dict(width=20000, few=2900, counts=[4, 1], bias=50),
+    dict(width=20000, few=2900, counts=[4, 9], tree=True), dict(bias=1024, few=900), dict(counts=[1] * 300, K=1), dict(counts=[40], K=5),
     dict(penalties=False, bias=0)])
 def test_parts(kw):
     kw = dict(kw)

@@ -132,6 +132,7 @@ I, U, W = D.ERR_INVALID_ARG, D.ERR_UNSUPPORTED, D.ERR_WORKSPACE
     ("dspark_adjust_logits", dict(os=1008), I),           # in place, rows elsewhere
     ("dspark_adjust_logits", dict(vocab=1 << 30, stride=1 << 30, os=1 << 30), U),
     ("dspark_adjust_logits", dict(K=64), U),
+    ("dspark_adjust_logits", dict(tokens_width=(1 << 26) + 1, tokens_stride=1 << 27), U),
     ("dspark_adjust_logits", dict(draft=None), I),
     ("dspark_adjust_logits", dict(tokens=None), I),
     ("dspark_adjust_logits", dict(hist=None), I),
