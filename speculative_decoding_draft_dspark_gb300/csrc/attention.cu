@@ -1,38 +1,46 @@
 // Attention of a step's rows over the paged cache, on sm_103a.
 //
-// For one request, key head and block of 128 packed rows (row m = j * G + g: token j,
-// query head g of the group of G that shares the key head) and the request's tokens,
-// 64 at a time:
-//     S = Q K^T                     tcgen05, 128 x 64, fp32 in tensor memory
+// For one request, key head and block of packed rows (row m = j * G + g: token j, query
+// head g of the group of G that shares the key head) and the request's tokens, a tile
+// at a time:
+//     S = Q K^T                     tcgen05, fp32 in tensor memory
 //     P = exp2((S - m) c)           m: running maximum, c = scale log2 e
 //     O = O + P V,  l = l + sum P   tcgen05, P in bf16 from tensor memory
 // and out = O / l at the end.  O is scaled only where the maximum grew by more than
 // 2^8 (P is then at most 2^8 in bf16, which has fp32's range; l is summed in fp32).
 //
 // Packing the group's heads into the tile's rows reads each key and value once for
-// all of them.  With few rows the time is the cache's bytes: K and V tiles come by TMA
-// through the block table into a ring, several tiles ahead, and two CTAs an SM hide
-// each other's chain of dependent steps.
+// all of them.  Two kernels:
+//
+//   narrow: 128 rows, 64 tokens.  With few rows the time is the cache's bytes: K and V
+//   tiles come by TMA through the block table into rings, several tiles ahead, the
+//   scores of the next tile are computed during the softmax of this one, and two CTAs
+//   an SM hide each other's chain of dependent steps.
+//
+//   wide: 2 x 128 rows, 128 tokens, for requests with more than 128 packed rows.  The
+//   time is the tensor cores' and the operands' way into the SM: two blocks of rows
+//   share each K and V tile, and one's softmax runs beside the other's products.
 //
 // Work is split by tiles of tokens, not by rows: all (request, head, block) items
 // laid end to end are cut into equal runs, one a CTA, so that one long context
 // occupies the whole GPU and short ones leave no tail.  A cut item leaves its O, m and
-// l in the workspace and a second kernel joins them, in order.
+// l in the workspace and a last kernel joins them, in order.
+#include <algorithm>
 #include <cuda_bf16.h>
 #include <mutex>
 
 #include "chain_common.cuh"
 #include "launch.cuh"
+#include "ptx_pair.cuh"
 #include "target_internal.h"
 
 namespace dspark {
 
-constexpr int AT_ROWS = 128;       // packed rows of a tile
-constexpr int AT_TOKENS = 64;      // tokens of a tile
-constexpr int AT_THREADS = 192;    // 4 softmax warps, TMA, MMA
-constexpr int AT_MAX_CTAS = 320;   // that leave partial results
+constexpr int AT_ROWS = 128;       // rows of a product
+constexpr int AT_MAX_NARROW = 320;  // CTAs that leave partial results
+constexpr int AT_MAX_WIDE = 160;
 constexpr int AT_SEGS = 4;         // segments told ahead
-constexpr int AT_INFOS = 8;        // tiles told ahead
+constexpr int AT_INFOS = 16;       // tiles told ahead: more than the K ring and the scores are
 constexpr float kRescale = 8.0f;   // log2 of what the maximum may grow by
 // Up to this a maximum is taken off as fma(s, c, -round(m c)): whatever m c was rounded
 // to is in lse too, so nothing is lost.  A larger m is taken off first, (s - m) c: at
@@ -42,21 +50,44 @@ constexpr float kLarge = 256.0f;
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr float kLog2e = 1.4426950408889634f;
 
-template <int HD>
+template <int HD, bool WIDE>
 struct AtShape {
-  static constexpr int kBoxes = HD / 64;                        // 64 columns each
-  static constexpr int kStages = HD == 64 ? 8 : 4;
-  static constexpr int kStage = kBoxes * AT_TOKENS * 128;        // bytes of a K or V tile
+  static constexpr int kGroups = WIDE ? 2 : 1;                   // blocks of rows, warpgroups
+  static constexpr int kRows = kGroups * AT_ROWS;
+  static constexpr int kTokens = WIDE ? 128 : 64;                // of a tile
+  static constexpr int kWords = kTokens / 64;                    // of a tile's mask
+  static constexpr int kBoxes = HD / 64;                         // 64 columns each
+  static constexpr int kBox = kTokens * 128;                     // bytes
+  static constexpr int kTile = kBoxes * kBox;                    // of K or V
   static constexpr int kQ = kBoxes * AT_ROWS * 128;
-  static constexpr int kCtas = HD == 256 ? 1 : 2;                // an SM
-  static constexpr int kTmem = HD == 256 ? 512 : 256;            // columns: S, S, O
-  static constexpr int kBytes = 1024 + kQ + kStages * kStage;    // aligned here to 1024
+  static constexpr int kK = HD == 64 ? 5 : HD == 128 ? 3 : 2;    // tiles of the rings
+  static constexpr int kV = HD == 64 ? 5 : 2;
+  static constexpr int kCtas = WIDE || HD == 256 ? 1 : 2;        // an SM
+  static constexpr int kTmem = kCtas == 1 ? 512 : 256;           // columns: S, S, O, (O)
+  static constexpr int kO = 2 * kTokens;                         // where O begins
+  static constexpr int kTiles = kGroups * kQ + (kK + kV) * kTile;
+  static constexpr int kThreads = kGroups * 128 + 128;           // softmax; K, V, products
+  // registers of the two kinds of warpgroups: together at most the launch's
+  static constexpr int kLaunchRegs = kCtas == 1 ? 168 : 128;
+  static constexpr int kSoftmaxRegs = WIDE ? 208 : 176;
+  static constexpr int kOtherRegs = 80;
+  static constexpr bool kSplitRegs = HD != 256;
+  static_assert(!kSplitRegs || kGroups * kSoftmaxRegs + kOtherRegs <= (kGroups + 1) * kLaunchRegs,
+                "registers of the launch");
 };
 
 // What the joining kernel needs about an item that begins in a CTA and is cut.
 struct AtMeta {
   int32_t last;    // CTA that holds its end; 0: nothing is cut here
   int32_t request, first, count, head, block;
+};
+
+// Partial results: slots 2 c (a run's beginning) and 2 c + 1 (an item's) of CTA c.
+struct AtParts {
+  AtMeta *meta;
+  float2 *ml;  // [slot][rows]: maximum, sum
+  float *o;    // [slot][rows][HD]
+  int32_t rows, ctas;
 };
 
 struct AtParams {
@@ -68,19 +99,18 @@ struct AtParams {
   const __nv_bfloat16 *v_cache;
   int64_t page_stride, token_stride, head_stride;
   int32_t tree_width, N, R, max_len, Hk, group, d;
-  int32_t page_shift, num_pages, max_pages, least_tiles, tile_rows;
+  int32_t page_shift, num_pages, max_pages, least_tiles;
+  int32_t both;  // both kernels run: each takes its requests
   float scale_log2;
   float *lse;
   uint32_t *status;
-  AtMeta *meta;
-  float2 *part_ml;  // [2 AT_MAX_CTAS][tile_rows]: maximum, sum
-  float *part_o;    // [2 AT_MAX_CTAS][tile_rows][HD]
+  AtParts parts;
 };
 
 // A run of an item's tiles that one CTA computes.
 struct AtSeg {
   int32_t request, first, count, ctx, head, block;  // request < 0: the end
-  int32_t t0, t1, tiles;                            // of the item's tiles
+  int32_t t0, t1;                                   // of the item's tiles
   int32_t tree, end;                                // tokens [0, end)
   int32_t part;                                     // slot of its partial result, or -1
 };
@@ -179,49 +209,75 @@ __device__ __forceinline__ float at_difference(float m, float above, float c) {
 }
 
 // Matrix descriptors with 128-byte swizzle, in halves (see common.cuh): K-major rows
-// of 64 columns; for V, whose rows run along the product's columns, boxes of 64 x 64.
+// of 64 columns; for V, whose rows run along the product's columns, boxes of 64
+// columns.
 constexpr uint32_t kAtDescHi = (1024u >> 4) | (1u << 14) | (2u << 29);
 __device__ __forceinline__ uint32_t at_desc_k(uint32_t addr) {
   return ((addr & 0x3FFFFu) >> 4) | 1u << 16;
 }
-__device__ __forceinline__ uint32_t at_desc_mn(uint32_t addr) {
-  return ((addr & 0x3FFFFu) >> 4) | static_cast<uint32_t>(AT_TOKENS * 128 >> 4) << 16;
+__device__ __forceinline__ uint32_t at_desc_mn(uint32_t addr, int box) {
+  return ((addr & 0x3FFFFu) >> 4) | static_cast<uint32_t>(box >> 4) << 16;
+}
+
+__device__ __forceinline__ uint64_t pair_f32(uint32_t lo, uint32_t hi) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "r"(lo), "r"(hi));
+  return r;
+}
+__device__ __forceinline__ void unpair_f32(uint64_t v, float &lo, float &hi) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(v));
+}
+__device__ __forceinline__ uint64_t pair_fma(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ uint64_t pair_add(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
 }
 
 // ----------------------------------------------------------------- planning
-__device__ __forceinline__ int at_blocks(const AtParams &p, int count) {
-  return (count * p.group + AT_ROWS - 1) / AT_ROWS;
-}
-// Tokens that some row of a block attends, as an end: those in the cache and the
-// step's, up to the block's last row where the request is a chain.
-__device__ __forceinline__ int at_end(const AtParams &p, int ctx, int count, bool tree, int b) {
-  const int last = tree ? count : min(count, ((b + 1) * AT_ROWS - 1) / p.group + 1);
-  const int64_t end = static_cast<int64_t>(ctx) + last;
-  return static_cast<int>(min(end, static_cast<int64_t>(p.max_pages) << p.page_shift));
-}
-__device__ __forceinline__ int at_tiles(int end) { return (end + AT_TOKENS - 1) / AT_TOKENS; }
-
 struct AtRequest {
-  int first, count, ctx;
+  int first, count, ctx, blocks;
   bool tree;
 };
-__device__ __forceinline__ AtRequest at_request(const AtParams &p, int n) {
-  AtRequest r;
-  const RowSpan rows = row_span(p.cu_rows, n, p.R);
-  r.first = rows.first;
-  r.count = min(rows.count, p.max_len);
-  r.ctx = max(p.ctx_len[n], 0);
-  r.tree = is_tree(p.tree, p.tree_width, n, rows.count);
-  return r;
-}
-__device__ __forceinline__ int64_t at_units(const AtParams &p, const AtRequest &r) {
-  int64_t sum = 0;
-  const int blocks = at_blocks(p, r.count);
-  for (int b = 0; b < blocks; ++b) sum += at_tiles(at_end(p, r.ctx, r.count, r.tree, b));
-  return sum * p.Hk;
-}
 
-// The CTAs' shares of U units: every CTA has at least `least_tiles` or the rest.
+template <int HD, bool WIDE>
+struct AtPlan {
+  using Sh = AtShape<HD, WIDE>;
+  // a request's rows; no blocks where they are the other kernel's
+  static __device__ __forceinline__ AtRequest request(const AtParams &p, int n) {
+    AtRequest r;
+    const RowSpan rows = row_span(p.cu_rows, n, p.R);
+    r.first = rows.first;
+    r.count = min(rows.count, p.max_len);
+    r.ctx = max(p.ctx_len[n], 0);
+    r.tree = is_tree(p.tree, p.tree_width, n, rows.count);
+    const int packed = r.count * p.group;
+    r.blocks = p.both && (packed > AT_ROWS) != WIDE ? 0 : (packed + Sh::kRows - 1) / Sh::kRows;
+    return r;
+  }
+  // Tokens that some row of a block attends, as an end: those in the cache and the
+  // step's, up to the block's last row where the request is a chain.
+  static __device__ __forceinline__ int end(const AtParams &p, const AtRequest &r, int b) {
+    const int last = r.tree ? r.count : min(r.count, ((b + 1) * Sh::kRows - 1) / p.group + 1);
+    const int64_t e = static_cast<int64_t>(r.ctx) + last;
+    return static_cast<int>(min(e, static_cast<int64_t>(p.max_pages) << p.page_shift));
+  }
+  static __device__ __forceinline__ int tiles(int end) {
+    return (end + Sh::kTokens - 1) / Sh::kTokens;
+  }
+  // the tiles of one head
+  static __device__ __forceinline__ int64_t head_tiles(const AtParams &p, const AtRequest &r) {
+    int64_t sum = 0;
+    for (int b = 0; b < r.blocks; ++b) sum += tiles(end(p, r, b));
+    return sum;
+  }
+};
+
+// The CTAs' equal shares of all tiles.
 struct AtShares {
   int64_t units;
   int ctas;
@@ -229,48 +285,69 @@ struct AtShares {
 };
 
 // Shared state besides the tiles
-template <int HD>
+template <int HD, bool WIDE>
 struct AtShared {
-  uint64_t full[AtShape<HD>::kStages], empty[AtShape<HD>::kStages];
-  uint64_t s_full[2], p_full[2], pv_done[2], q_full, scanned;  // pairs: by tile, in turn
+  using Sh = AtShape<HD, WIDE>;
+  uint64_t k_full[Sh::kK], k_empty[Sh::kK], v_full[Sh::kV], v_empty[Sh::kV];
+  // by block of rows (wide) or by tile, in turn (narrow)
+  uint64_t s_full[2], p_full[2], pv_done[2];
+  uint64_t q_full, scanned;
   uint64_t seg_full[AT_SEGS], seg_empty[AT_SEGS];
   uint64_t info_full[AT_INFOS];
-  uint64_t valid[AT_INFOS];        // a tile's tokens that are there
-  uint64_t poison[2][4][3];        // tokens whose values are not finite: warp, tile
+  uint64_t valid[AT_INFOS][Sh::kWords];  // a tile's tokens that are there
+  uint32_t poison[2][4][3];              // tokens whose values are not finite: warp, tile
   AtSeg seg[AT_SEGS];
-  int64_t scan[AT_THREADS / 32];
+  int64_t scan[Sh::kThreads / 32];
   int64_t start_rest;
   int32_t start_request;
   uint32_t tmem, abort;
 };
 
-template <int HD>
-__global__ void __launch_bounds__(AT_THREADS, AtShape<HD>::kCtas)
+// The tokens of a tile's word that a row attends: of the cache, and of the step's rows
+// (`bits` in a tree, the first `upto` tokens in a chain).
+__device__ __forceinline__ uint64_t at_seen(const AtSeg &s, uint64_t bits, int upto, int token) {
+  if (!s.tree) return low_bits(upto - token);
+  const int shift = s.ctx - token;
+  uint64_t seen = low_bits(shift);
+  if (shift >= 0 && shift < 64) seen |= bits << shift;
+  else if (shift < 0 && shift > -64) seen |= bits >> -shift;
+  return seen;
+}
+
+template <int HD, bool WIDE>
+__global__ void __launch_bounds__(AtShape<HD, WIDE>::kThreads, AtShape<HD, WIDE>::kCtas)
     attention_kernel(const __grid_constant__ CUtensorMap k_map,
                      const __grid_constant__ CUtensorMap v_map, const AtParams p) {
-  using Sh = AtShape<HD>;
-  extern __shared__ uint8_t at_raw[];
-  __shared__ AtShared<HD> sh;
-  uint8_t *smem = at_raw + ((1024u - (smem_u32(at_raw) & 1023u)) & 1023u);
-  uint8_t *ring = smem + Sh::kQ;
+  using Sh = AtShape<HD, WIDE>;
+  using Plan = AtPlan<HD, WIDE>;
+  constexpr int TOK = Sh::kTokens, WORDS = Sh::kWords, SOFTMAX = 4 * Sh::kGroups;
+  // Nothing else is in shared memory, so that it begins on a multiple of 1024 bytes:
+  // with room to align it, two narrow CTAs would not fit an SM.
+  extern __shared__ __align__(1024) uint8_t smem[];
+  AtShared<HD, WIDE> &sh = *reinterpret_cast<AtShared<HD, WIDE> *>(smem + Sh::kTiles);
+  uint8_t *k_ring = smem + Sh::kGroups * Sh::kQ, *v_ring = k_ring + Sh::kK * Sh::kTile;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   volatile uint32_t *abort_flag = &sh.abort;
 
   if (tid == 0) {
-    for (int i = 0; i < Sh::kStages; ++i) {
-      mbar_init(&sh.full[i], 1);
-      mbar_init(&sh.empty[i], 1);
+    for (int i = 0; i < Sh::kK; ++i) {
+      mbar_init(&sh.k_full[i], 1);
+      mbar_init(&sh.k_empty[i], 1);
+    }
+    for (int i = 0; i < Sh::kV; ++i) {
+      mbar_init(&sh.v_full[i], 1);
+      mbar_init(&sh.v_empty[i], 1);
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(&sh.s_full[i], 1);
       mbar_init(&sh.p_full[i], 4);
       mbar_init(&sh.pv_done[i], 1);
     }
-    mbar_init(&sh.q_full, 4);
+    mbar_init(&sh.q_full, SOFTMAX);
     mbar_init(&sh.scanned, 4);
     for (int i = 0; i < AT_SEGS; ++i) {
       mbar_init(&sh.seg_full[i], 1);
-      mbar_init(&sh.seg_empty[i], 5);
+      mbar_init(&sh.seg_empty[i], SOFTMAX + 2);
     }
     for (int i = 0; i < AT_INFOS; ++i) mbar_init(&sh.info_full[i], 1);
     sh.abort = 0u;
@@ -278,11 +355,11 @@ __global__ void __launch_bounds__(AT_THREADS, AtShape<HD>::kCtas)
     fence_mbarrier_init();
     fence_proxy_async_smem();
   }
-  if (warp == 5) {
+  if (warp == SOFTMAX + 2) {
     tmem_alloc(&sh.tmem, Sh::kTmem);
     tmem_relinquish();
   }
-  if (tid == 128) {
+  if (warp == SOFTMAX && lane == 0) {
     prefetch_tensormap(&k_map);
     prefetch_tensormap(&v_map);
   }
@@ -294,22 +371,22 @@ __global__ void __launch_bounds__(AT_THREADS, AtShape<HD>::kCtas)
   const uint32_t tmem = sh.tmem;
   const int cta = static_cast<int>(blockIdx.x);
 
-  // ---- plan: this CTA's run of units, and the request that it begins in
+  // ---- plan: this CTA's run of tiles, and the request that it begins in
   AtShares shares;
   {
-    const int C = (p.N + AT_THREADS - 1) / AT_THREADS;
+    const int C = (p.N + Sh::kThreads - 1) / Sh::kThreads;
     const int n0 = min(p.N, tid * C), n1 = min(p.N, n0 + C);
     int64_t mine = 0;
     for (int n = n0; n < n1; ++n) {
-      const AtRequest r = at_request(p, n);
-      if (cta == 0) {
+      const AtRequest r = Plan::request(p, n);
+      if (cta == 0 && !WIDE) {
         if (row_span(p.cu_rows, n, p.R).count > p.max_len)
           raise_status(p.status, DSPARK_DEV_LEN_OOR);
         if (r.count > 0 && static_cast<int64_t>(r.ctx) + r.count >
                                static_cast<int64_t>(p.max_pages) << p.page_shift)
           raise_status(p.status, DSPARK_DEV_PAGE_OOR);
       }
-      mine += at_units(p, r);
+      mine += p.Hk * Plan::head_tiles(p, r);
     }
     int64_t x = mine;
 #pragma unroll
@@ -320,7 +397,7 @@ __global__ void __launch_bounds__(AT_THREADS, AtShape<HD>::kCtas)
     if (lane == 31) sh.scan[warp] = x;
     __syncthreads();
     int64_t before = x - mine, total = 0;
-    for (int w = 0; w < AT_THREADS / 32; ++w) {
+    for (int w = 0; w < Sh::kThreads / 32; ++w) {
       if (w < warp) before += sh.scan[w];
       total += sh.scan[w];
     }
@@ -331,7 +408,7 @@ __global__ void __launch_bounds__(AT_THREADS, AtShape<HD>::kCtas)
       int64_t rest = shares.begin(cta) - before;
       if (rest >= 0 && rest < mine) {
         for (int n = n0; n < n1; ++n) {
-          const int64_t units = at_units(p, at_request(p, n));
+          const int64_t units = p.Hk * Plan::head_tiles(p, Plan::request(p, n));
           if (rest < units) {
             sh.start_request = n;
             sh.start_rest = rest;
@@ -344,215 +421,240 @@ __global__ void __launch_bounds__(AT_THREADS, AtShape<HD>::kCtas)
     __syncthreads();
   }
 
-  if (warp == 4) {
-    // ------------------------------------------------------------ K and V
+  if (warp >= SOFTMAX) {
+    if constexpr (Sh::kSplitRegs) registers_down<Sh::kOtherRegs>();
     const uint32_t one = at_elect();
-    const int rows_box = min(1 << p.page_shift, AT_TOKENS);
-    const int boxes = AT_TOKENS / rows_box;
     bool ok = true;
-    int it = 0, infos = 0, segs = 0;
-    AtMeta meta = {};
-    auto place = [&](const AtSeg &s) {
-      const int i = segs % AT_SEGS;
-      ok = __all_sync(0xFFFFFFFFu, wait_bounded(&sh.seg_empty[i], ((segs / AT_SEGS) & 1) ^ 1u,
-                                                abort_flag, p.status));
-      if (ok && one) {
-        sh.seg[i] = s;
-        mbar_arrive(&sh.seg_full[i]);
-      }
-      ++segs;
+    int g = 0, segs = 0;  // tiles and segments so far
+    auto wait = [&](uint64_t *bar, uint32_t parity) {
+      ok = ok && __all_sync(0xFFFFFFFFu, wait_bounded(bar, parity, abort_flag, p.status));
+      return ok;
     };
-    if (cta < shares.ctas) {
-      const int64_t end_unit = shares.begin(cta + 1);
-      int64_t unit = shares.begin(cta);
-      int n = sh.start_request;
-      int64_t rest = sh.start_rest;
-      while (ok && unit < end_unit && n < p.N) {
-        const AtRequest r = at_request(p, n);
-        const int blocks = at_blocks(p, r.count);
-        // the items before the first one of this run
-        int64_t a_head = 0;
-        for (int b = 0; b < blocks; ++b) a_head += at_tiles(at_end(p, r.ctx, r.count, r.tree, b));
-        int h = a_head > 0 ? static_cast<int>(rest / a_head) : p.Hk;
-        rest -= h * a_head;
-        int b = 0;
-        while (b < blocks && h < p.Hk) {
-          const int t = at_tiles(at_end(p, r.ctx, r.count, r.tree, b));
-          if (rest < t) break;
-          rest -= t;
-          ++b;
+    // A segment's K or V tiles, through its pages: a lane each, 32 at a time.
+    const int box_rows = min(1 << p.page_shift, TOK);
+    auto load_tiles = [&](const AtSeg &s, bool is_v) {
+      const int64_t table = static_cast<int64_t>(s.request) * p.table_stride;
+      const int stages = is_v ? Sh::kV : Sh::kK;
+      uint64_t *full = is_v ? sh.v_full : sh.k_full, *empty = is_v ? sh.v_empty : sh.k_empty;
+      const uint32_t ring = smem_u32(is_v ? v_ring : k_ring);
+      const CUtensorMap *map = is_v ? &v_map : &k_map;
+      int base = -1, ids = -1;
+      uint32_t good = 0u;  // of these pages, the ones that there are
+      for (int t = s.t0; t < s.t1; ++t, ++g) {
+        const int token = t * TOK, page0 = token >> p.page_shift;
+        if (base != (page0 & ~31)) {
+          base = page0 & ~31;
+          const int k = base + lane;
+          ids = k < p.max_pages ? p.block_table[table + k] : -1;
+          good = __ballot_sync(0xFFFFFFFFu, ids >= 0 && ids < p.num_pages);
         }
-        for (; ok && h < p.Hk && unit < end_unit; ++h, b = 0) {
-          for (; ok && b < blocks && unit < end_unit; ++b) {
-            AtSeg s;
-            s.request = n;
-            s.first = r.first;
-            s.count = r.count;
-            s.ctx = r.ctx;
-            s.head = h;
-            s.block = b;
-            s.tree = r.tree;
-            s.end = at_end(p, r.ctx, r.count, r.tree, b);
-            s.tiles = at_tiles(s.end);
-            s.t0 = static_cast<int>(rest);
-            s.t1 = static_cast<int>(min(static_cast<int64_t>(s.tiles), rest + (end_unit - unit)));
-            rest = 0;
-            unit += s.t1 - s.t0;
-            s.part = -1;
-            if (s.t0 > 0) {
-              s.part = 2 * cta;
-            } else if (s.t1 < s.tiles) {
-              s.part = 2 * cta + 1;
-              const int64_t last_unit = unit + (s.tiles - s.t1) - 1;
-              int c = static_cast<int>(last_unit * shares.ctas / shares.units);
-              while (c + 1 < shares.ctas && shares.begin(c + 1) <= last_unit) ++c;
-              while (shares.begin(c) > last_unit) --c;
-              meta = {c, n, s.first, s.count, h, b};
-            }
-            place(s);
-            if (!ok) break;
-            // its tiles: K 0, K 1, V 0, K 2, V 1, ... as the products take them
-            const int64_t table = static_cast<int64_t>(n) * p.table_stride;
-            int base[2] = {-1, -1}, ids[2];
-            const int T = s.t1 - s.t0;
-            for (int x = 0; ok && x < 2 * T; ++x) {
-              const bool is_v = x == 2 * T - 1 || (x > 1 && (x & 1) == 0);
-              const int tile = s.t0 + (is_v ? (x == 2 * T - 1 ? T - 1 : x / 2 - 1) : (x + 1) / 2);
-              const int token = tile * AT_TOKENS;
-              const int stage = it % Sh::kStages;
-              // pages of this and the following tiles, a lane each
-              const int page0 = token >> p.page_shift, want = page0 & ~31;
-              if (base[is_v] != want) {
-                base[is_v] = want;
-                const int k = want + lane;
-                ids[is_v] = k < p.max_pages ? p.block_table[table + k] : -1;
-              }
-              ok = __all_sync(0xFFFFFFFFu,
-                              wait_bounded(&sh.empty[stage], ((it / Sh::kStages) & 1) ^ 1u,
-                                           abort_flag, p.status));
-              if (!ok) break;
-              uint64_t there = 0ull;
-              int here[4], n_here = 0;
-              for (int k = 0; k < boxes; ++k) {
-                const int id = __shfl_sync(0xFFFFFFFFu, ids[is_v],
-                                           ((token + k * rows_box) >> p.page_shift) & 31);
-                const bool good = id >= 0 && id < p.num_pages && token + k * rows_box < s.end;
-                here[k] = good ? id : -1;
-                n_here += good;
-                if (good) there |= low_bits(rows_box) << (k * rows_box);
-                if (!good && token + k * rows_box < s.end && one)
-                  raise_status(p.status, DSPARK_DEV_PAGE_OOR);
-              }
-              if (!is_v) {
-                if (one) {
-                  sh.valid[infos % AT_INFOS] = there & low_bits(s.end - token);
-                  mbar_arrive(&sh.info_full[infos % AT_INFOS]);
-                }
-                ++infos;
-              }
-              if (one)
-                mbar_arrive_expect_tx(&sh.full[stage],
-                                      static_cast<uint32_t>(n_here * Sh::kBoxes * rows_box * 128));
-              __syncwarp();
-              const uint32_t dst = smem_u32(ring + stage * Sh::kStage);
-              for (int k = 0; k < boxes; ++k) {
-                if (here[k] < 0) continue;
+        const int stage = g % stages;
+        if (!wait(&empty[stage], ((g / stages) & 1) ^ 1u)) return;
+        const int boxes = (min(TOK, s.end - token) + box_rows - 1) / box_rows;
+        const uint32_t here = (good >> (page0 & 31)) & ((1u << boxes) - 1u);
+        if (!is_v) {
+          uint64_t valid[WORDS];
 #pragma unroll
-                for (int c = 0; c < Sh::kBoxes; ++c)
-                  tma_load_page(one, dst + c * (AT_TOKENS * 128) + k * rows_box * 128,
-                                is_v ? &v_map : &k_map, &sh.full[stage], c * 64, h,
-                                token & ((1 << p.page_shift) - 1), here[k]);
+          for (int w = 0; w < WORDS; ++w) {
+            valid[w] = low_bits(s.end - token - 64 * w);
+            if (here != (1u << boxes) - 1u)
+              for (int k = 0; k < boxes; ++k)
+                if ((here >> k & 1u) == 0u)
+                  valid[w] &= ~(low_bits((k + 1) * box_rows - 64 * w) & ~low_bits(k * box_rows - 64 * w));
+          }
+          if (one) {
+#pragma unroll
+            for (int w = 0; w < WORDS; ++w) sh.valid[g % AT_INFOS][w] = valid[w];
+            mbar_arrive(&sh.info_full[g % AT_INFOS]);
+            if (here != (1u << boxes) - 1u) raise_status(p.status, DSPARK_DEV_PAGE_OOR);
+          }
+        }
+        if (one)
+          mbar_arrive_expect_tx(&full[stage], __popc(here) * Sh::kBoxes * box_rows * 128);
+        __syncwarp();
+        uint32_t dst = ring + stage * Sh::kTile;
+        const int offset = token & ((1 << p.page_shift) - 1);
+#pragma unroll 1
+        for (int k = 0; k < boxes; ++k, dst += box_rows * 128) {
+          const int id = __shfl_sync(0xFFFFFFFFu, ids, (page0 + k) & 31);
+          const uint32_t go = here >> k & 1u ? one : 0u;
+#pragma unroll
+          for (int c = 0; c < Sh::kBoxes; ++c)
+            tma_load_page(go, dst + c * Sh::kBox, map, &full[stage], c * 64, s.head, offset, id);
+        }
+      }
+    };
+
+    if (warp == SOFTMAX) {
+      // ---------------------------------------------- segments, and their K
+      AtMeta meta = {};
+      auto place = [&](const AtSeg &s) {
+        const int i = segs % AT_SEGS;
+        if (!wait(&sh.seg_empty[i], ((segs / AT_SEGS) & 1) ^ 1u)) return;
+        if (one) {
+          sh.seg[i] = s;
+          mbar_arrive(&sh.seg_full[i]);
+        }
+        __syncwarp();
+        ++segs;
+      };
+      if (cta < shares.ctas) {
+        const int64_t end_unit = shares.begin(cta + 1);
+        int64_t unit = shares.begin(cta);
+        int n = sh.start_request;
+        int64_t rest = sh.start_rest;
+        for (; ok && unit < end_unit && n < p.N; ++n, rest = 0) {
+          const AtRequest r = Plan::request(p, n);
+          const int64_t a_head = Plan::head_tiles(p, r);
+          if (a_head == 0) continue;
+          // the items before the first one of this run
+          int h = static_cast<int>(rest / a_head), b = 0;
+          rest -= h * a_head;
+          for (; b < r.blocks; ++b) {
+            const int t = Plan::tiles(Plan::end(p, r, b));
+            if (rest < t) break;
+            rest -= t;
+          }
+          for (; ok && h < p.Hk && unit < end_unit; ++h, b = 0) {
+            for (; ok && b < r.blocks && unit < end_unit; ++b) {
+              AtSeg s;
+              s.request = n;
+              s.first = r.first;
+              s.count = r.count;
+              s.ctx = r.ctx;
+              s.head = h;
+              s.block = b;
+              s.tree = r.tree;
+              s.end = Plan::end(p, r, b);
+              const int tiles = Plan::tiles(s.end);
+              s.t0 = static_cast<int>(rest);
+              s.t1 = static_cast<int>(min(static_cast<int64_t>(tiles), rest + (end_unit - unit)));
+              rest = 0;
+              unit += s.t1 - s.t0;
+              s.part = -1;
+              if (s.t0 > 0) {
+                s.part = 2 * cta;
+              } else if (s.t1 < tiles) {
+                s.part = 2 * cta + 1;
+                const int64_t last_unit = unit + (tiles - s.t1) - 1;
+                int c = static_cast<int>(last_unit * shares.ctas / shares.units);
+                while (c + 1 < shares.ctas && shares.begin(c + 1) <= last_unit) ++c;
+                while (shares.begin(c) > last_unit) --c;
+                meta = {c, n, s.first, s.count, h, b};
               }
-              ++it;
+              place(s);
+              if (ok) load_tiles(s, false);
             }
           }
         }
-        ++n;
-        rest = 0;
       }
-    }
-    if (ok) {
-      AtSeg s = {};
-      s.request = -1;
-      place(s);
-    }
-    if (one) p.meta[cta] = meta;
-    if (!ok) {
-      // copies in flight land before the shared memory is given back
-      const uint64_t t0 = global_timer_ns();
-      while (global_timer_ns() - t0 < 20000000ull) __nanosleep(1000);
-    }
-    __syncwarp();
-  } else if (warp == 5) {
-    // ------------------------------------------------------------ products
-    const uint32_t one = at_elect();
-    const uint32_t q_lo = at_desc_k(smem_u32(smem)), ring0 = smem_u32(ring);
-    constexpr uint32_t idesc_s = umma_idesc_bf16_f32(AT_ROWS, AT_TOKENS);
-    constexpr uint32_t idesc_o = umma_idesc_bf16_f32(AT_ROWS, HD) | 1u << 16;
-    bool ok = true;
-    int it = 0, gi = 0, segs = 0;  // ring, tiles, segments so far
-    auto wait = [&](uint64_t *bar, uint32_t parity) {
-      ok = ok && __all_sync(0xFFFFFFFFu, wait_bounded(bar, parity, abort_flag, p.status));
-      tc_fence_after();
-      return ok;
-    };
-    while (ok) {
-      const int si = segs % AT_SEGS;
-      if (!wait(&sh.seg_full[si], (segs / AT_SEGS) & 1)) break;
-      const int request = sh.seg[si].request, T = sh.seg[si].t1 - sh.seg[si].t0;
-      __syncwarp();
-      if (one) mbar_arrive(&sh.seg_empty[si]);
-      if (request < 0) break;
-      if (!wait(&sh.q_full, segs & 1)) break;
-      ++segs;
-      auto score = [&](int i) {
-        // the buffer's last P has been multiplied
-        const int g = gi + i;
-        if (g >= 2 && !wait(&sh.pv_done[g & 1], ((g >> 1) - 1) & 1)) return;
-        const int stage = it % Sh::kStages;
-        if (!wait(&sh.full[stage], (it / Sh::kStages) & 1)) return;
-        const uint32_t k_lo = at_desc_k(ring0 + stage * Sh::kStage);
-        const uint32_t d = tmem + (g & 1) * AT_TOKENS;
-#pragma unroll
-        for (int kk = 0; kk < HD / 16; ++kk)
-          umma_ss(one, d, q_lo + (kk / 4) * (AT_ROWS * 128 >> 4) + (kk % 4) * 2,
-                  k_lo + (kk / 4) * (AT_TOKENS * 128 >> 4) + (kk % 4) * 2, kAtDescHi, idesc_s, kk);
-        umma_commit_one(one, &sh.empty[stage]);
-        umma_commit_one(one, &sh.s_full[g & 1]);
-        ++it;
+      if (ok) {
+        AtSeg s = {};
+        s.request = -1;
+        place(s);
+      }
+      if (one) p.parts.meta[cta] = meta;
+    } else if (warp == SOFTMAX + 1) {
+      // ------------------------------------------------------------------ V
+      while (ok) {
+        const int si = segs % AT_SEGS;
+        if (!wait(&sh.seg_full[si], (segs / AT_SEGS) & 1)) break;
+        const AtSeg s = sh.seg[si];
+        __syncwarp();
+        if (one) mbar_arrive(&sh.seg_empty[si]);
+        if (s.request < 0) break;
+        ++segs;
+        load_tiles(s, true);
+      }
+    } else if (warp == SOFTMAX + 2) {
+      // ----------------------------------------------------------- products
+      const uint32_t q_lo = at_desc_k(smem_u32(smem));
+      const uint32_t k0 = smem_u32(k_ring), v0 = smem_u32(v_ring);
+      constexpr uint32_t idesc_s = umma_idesc_bf16_f32(AT_ROWS, TOK);
+      constexpr uint32_t idesc_o = umma_idesc_bf16_f32(AT_ROWS, HD) | 1u << 16;
+      int turns[2] = {0, 0};  // wide: tiles of each block of rows so far
+      auto arrived = [&](uint64_t *bar, uint32_t parity) {
+        wait(bar, parity);
+        tc_fence_after();
+        return ok;
       };
-      score(0);
-      for (int i = 0; ok && i < T; ++i) {
-        if (i + 1 < T) score(i + 1);
-        const int g = gi + i;
-        if (!ok || !wait(&sh.p_full[g & 1], (g >> 1) & 1)) break;
-        const int stage = it % Sh::kStages;
-        if (!wait(&sh.full[stage], (it / Sh::kStages) & 1)) break;
-        const uint32_t v_lo = at_desc_mn(ring0 + stage * Sh::kStage);
-        const uint32_t a = tmem + (g & 1) * AT_TOKENS, d = tmem + 2 * AT_TOKENS;
+      while (ok) {
+        const int si = segs % AT_SEGS;
+        if (!arrived(&sh.seg_full[si], (segs / AT_SEGS) & 1)) break;
+        const int request = sh.seg[si].request, T = sh.seg[si].t1 - sh.seg[si].t0;
+        const int rows = sh.seg[si].count * p.group - sh.seg[si].block * Sh::kRows;
+        __syncwarp();
+        if (one) mbar_arrive(&sh.seg_empty[si]);
+        if (request < 0) break;
+        if (!arrived(&sh.q_full, segs & 1)) break;
+        ++segs;
+        const int blocks = WIDE && rows > AT_ROWS ? 2 : 1;
+        // S of tile i for block r.  The tensor core takes products in the order in
+        // which they are issued, so a wide block's S may follow the product that reads
+        // the P in its place.
+        auto score = [&](int r, int i) {
+          const int gt = g + i, buf = WIDE ? r : gt & 1;
+          if (!WIDE && gt >= 2 && !arrived(&sh.pv_done[buf], ((gt >> 1) - 1) & 1)) return;
+          const int stage = gt % Sh::kK;
+          if (r == 0 && !arrived(&sh.k_full[stage], (gt / Sh::kK) & 1)) return;
+          const uint32_t a = q_lo + r * (Sh::kQ >> 4);
+          const uint32_t b = at_desc_k(k0 + stage * Sh::kTile);
 #pragma unroll
-        for (int kk = 0; kk < AT_TOKENS / 16; ++kk)
-          umma_ts(one, d, a + kk * 8, v_lo + kk * 128, kAtDescHi, idesc_o, i | kk);
-        umma_commit_one(one, &sh.empty[stage]);
-        umma_commit_one(one, &sh.pv_done[g & 1]);
-        ++it;
+          for (int kk = 0; kk < HD / 16; ++kk)
+            umma_ss(one, tmem + buf * TOK, a + (kk / 4) * (AT_ROWS * 128 >> 4) + (kk % 4) * 2,
+                    b + (kk / 4) * (Sh::kBox >> 4) + (kk % 4) * 2, kAtDescHi, idesc_s, kk);
+          if (r == blocks - 1) umma_commit_one(one, &sh.k_empty[stage]);
+          umma_commit_one(one, &sh.s_full[buf]);
+        };
+        auto value = [&](int r, int i) {
+          const int gt = g + i, buf = WIDE ? r : gt & 1;
+          const uint32_t turn = WIDE ? turns[r] + i : gt >> 1;
+          if (!arrived(&sh.p_full[buf], turn & 1)) return;
+          const int stage = gt % Sh::kV;
+          if (r == 0 && !arrived(&sh.v_full[stage], (gt / Sh::kV) & 1)) return;
+          const uint32_t b = at_desc_mn(v0 + stage * Sh::kTile, Sh::kBox);
+#pragma unroll
+          for (int kk = 0; kk < TOK / 16; ++kk)
+            umma_ts(one, tmem + Sh::kO + r * HD, tmem + buf * TOK + kk * 8, b + kk * 128,
+                    kAtDescHi, idesc_o, i | kk);
+          if (r == blocks - 1) umma_commit_one(one, &sh.v_empty[stage]);
+          umma_commit_one(one, &sh.pv_done[buf]);
+        };
+        if constexpr (WIDE) {
+          for (int r = 0; ok && r < blocks; ++r) score(r, 0);
+          for (int i = 0; ok && i < T; ++i)
+            for (int r = 0; ok && r < blocks; ++r) {
+              value(r, i);
+              if (ok && i + 1 < T) score(r, i + 1);
+            }
+          for (int r = 0; r < blocks; ++r) turns[r] += T;
+        } else {
+          score(0, 0);
+          for (int i = 0; ok && i < T; ++i) {
+            if (i + 1 < T) score(0, i + 1);
+            if (ok) value(0, i);
+          }
+        }
+        g += T;
       }
-      gi += T;
     }
     if (!ok) {
-      // products in flight end before their memory is given back
+      // copies and products in flight end before their memory is given back
       const uint64_t t0 = global_timer_ns();
       while (global_timer_ns() - t0 < 20000000ull) __nanosleep(1000);
     }
     __syncwarp();
   } else {
     // ------------------------------------------------------------- softmax
-    const uint32_t lanes = static_cast<uint32_t>(warp * 32) << 16;
-    const uint32_t o_tmem = tmem + lanes + 2 * AT_TOKENS;
+    if constexpr (Sh::kSplitRegs) registers_up<Sh::kSoftmaxRegs>();
+    const int block = WIDE ? warp >> 2 : 0;  // of rows
+    const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
+    const uint32_t o_tmem = tmem + lanes + Sh::kO + block * HD;
     const int row = warp * 32 + lane;
     const float c = p.scale_log2;
+    const uint64_t c2 = pair_f32(__float_as_uint(c), __float_as_uint(c));
     bool ok = true;
-    int it = 0, gi = 0, segs = 0, scans = 0;
+    int g = 0, turn = 0, segs = 0, scans = 0;  // tiles, this block's, segments
     auto wait = [&](uint64_t *bar, uint32_t parity) {
       ok = ok && __all_sync(0xFFFFFFFFu, wait_bounded(bar, parity, abort_flag, p.status));
       return ok;
@@ -565,7 +667,7 @@ __global__ void __launch_bounds__(AT_THREADS, AtShape<HD>::kCtas)
       if (lane == 0) mbar_arrive(&sh.seg_empty[si]);
       if (s.request < 0) break;
       const int T = s.t1 - s.t0;
-      const int m = s.block * AT_ROWS + row, j = m / p.group;
+      const int m = s.block * Sh::kRows + row, j = m / p.group;
       const int head = s.head * p.group + (m - j * p.group);
       const bool mine = j < s.count;
       const bool any = __any_sync(0xFFFFFFFFu, mine);
@@ -574,11 +676,11 @@ __global__ void __launch_bounds__(AT_THREADS, AtShape<HD>::kCtas)
       if (mine) {
         const __nv_bfloat16 *src = static_cast<const __nv_bfloat16 *>(p.q.p) +
                                    q_row * p.q.stride + head * p.q.head_stride;
-        const uint32_t dst = smem_u32(smem) + row * 128;
+        const uint32_t dst = smem_u32(smem) + block * Sh::kQ + (row & (AT_ROWS - 1)) * 128;
 #pragma unroll 4
-        for (int c = 0; c < HD / 8; ++c) {
-          const uint32_t at = dst + (c / 8) * (AT_ROWS * 128) + (((c & 7) ^ (row & 7)) << 4);
-          if (c * 8 < p.d) cp_async_16(at, src + c * 8);
+        for (int e = 0; e < HD / 8; ++e) {
+          const uint32_t at = dst + (e / 8) * (AT_ROWS * 128) + (((e & 7) ^ (row & 7)) << 4);
+          if (e * 8 < p.d) cp_async_16(at, src + e * 8);
           else st_shared_zero16(at);
         }
         cp_async_wait_all();
@@ -586,57 +688,68 @@ __global__ void __launch_bounds__(AT_THREADS, AtShape<HD>::kCtas)
       fence_proxy_async_smem();
       __syncwarp();
       if (lane == 0) mbar_arrive(&sh.q_full);
+      ++segs;
+      // the second block may have no rows; the products leave it out too
+      if (WIDE && block == 1 && s.count * p.group - s.block * Sh::kRows <= AT_ROWS) {
+        g += T;
+        if (s.t1 * TOK > s.ctx + (s.tree ? 0 : s.block * Sh::kRows / p.group + 1)) ++scans;
+        continue;
+      }
 
       // ---- tokens
       const uint64_t bits =
           s.tree && mine ? tree_bits(p.tree, p.tree_width, s.request, j, s.count) : 0ull;
-      const int first_j = s.block * AT_ROWS / p.group;
+      const int upto = s.ctx + j + 1;
       // before this token every row attends every token
-      const int common = s.ctx + (s.tree ? 0 : first_j + 1);
-      uint64_t(&poison)[4][3] = sh.poison[segs & 1];
-      if (lane < 3) poison[warp][lane] = 0ull;
+      const int common = s.ctx + (s.tree ? 0 : s.block * Sh::kRows / p.group + 1);
+      uint32_t(&poison)[4][3] = sh.poison[segs & 1];
+      if (block == 0 && lane < 3) poison[warp][lane] = 0u;
       __syncwarp();
-      const bool scans_here = s.t1 * AT_TOKENS > common;
+      const bool scans_here = s.t1 * TOK > common;
       float top = -INFINITY, sum = 0.0f;
       for (int i = 0; i < T; ++i) {
-        const int g = gi + i, tile = s.t0 + i, token = tile * AT_TOKENS;
-        if (!wait(&sh.info_full[g % AT_INFOS], (g / AT_INFOS) & 1)) break;
-        const uint64_t valid = sh.valid[g % AT_INFOS];
-        const bool inner = token + AT_TOKENS <= common;
-        if (!wait(&sh.s_full[g & 1], (g >> 1) & 1)) break;
+        const int gt = g + i, token = (s.t0 + i) * TOK;
+        const int buf = WIDE ? block : gt & 1;
+        const uint32_t phase = WIDE ? turn & 1 : (gt >> 1) & 1;
+        ++turn;
+        if (!wait(&sh.info_full[gt % AT_INFOS], (gt / AT_INFOS) & 1)) break;
+        uint64_t valid[WORDS];
+        bool whole = true;
+#pragma unroll
+        for (int w = 0; w < WORDS; ++w) {
+          valid[w] = sh.valid[gt % AT_INFOS][w];
+          whole = whole && valid[w] == ~0ull;
+        }
+        const bool inner = token + TOK <= common;
+        if (!wait(&sh.s_full[buf], phase)) break;
         tc_fence_after();
         if (any) {
-          uint32_t s0[32], s1[32];
-          const uint32_t s_tmem = tmem + lanes + (g & 1) * AT_TOKENS;
-          tmem_ld_32x32b_x32(s_tmem, s0);
-          tmem_ld_32x32b_x32(s_tmem + 32, s1);
-          tmem_ld_wait(s0);
-          tmem_ld_wait(s1);
-          if (!inner || valid != ~0ull) {
-            uint64_t seen;
-            if (s.tree) {
-              const int shift = s.ctx - token;
-              seen = low_bits(shift);
-              if (shift >= 0 && shift < 64) seen |= bits << shift;
-              else if (shift < 0 && shift > -64) seen |= bits >> -shift;
-            } else {
-              seen = low_bits(s.ctx + j + 1 - token);
-            }
-            seen &= valid;
-            const uint32_t lo = static_cast<uint32_t>(seen), hi = static_cast<uint32_t>(seen >> 32);
+          uint32_t x[TOK / 32][32];
+          const uint32_t s_tmem = tmem + lanes + buf * TOK;
 #pragma unroll
-            for (int e = 0; e < 32; ++e) {
-              s0[e] = (lo >> e & 1u) ? s0[e] : 0xFF800000u;
-              s1[e] = (hi >> e & 1u) ? s1[e] : 0xFF800000u;
+          for (int k = 0; k < TOK / 32; ++k) tmem_ld_32x32b_x32(s_tmem + 32 * k, x[k]);
+#pragma unroll
+          for (int k = 0; k < TOK / 32; ++k) tmem_ld_wait(x[k]);
+          if (!inner || !whole) {
+#pragma unroll
+            for (int w = 0; w < WORDS; ++w) {
+              const uint64_t seen = at_seen(s, bits, upto, token + 64 * w) & valid[w];
+#pragma unroll
+              for (int k = 0; k < 2; ++k) {
+                const uint32_t half = static_cast<uint32_t>(seen >> (32 * k));
+#pragma unroll
+                for (int e = 0; e < 32; ++e)
+                  x[2 * w + k][e] = (half >> e & 1u) ? x[2 * w + k][e] : 0xFF800000u;
+              }
             }
           }
-          float t0 = -INFINITY, t1 = -INFINITY;
+          float highs[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-          for (int e = 0; e < 32; ++e) {
-            t0 = fmaxf(t0, __uint_as_float(s0[e]));
-            t1 = fmaxf(t1, __uint_as_float(s1[e]));
-          }
-          const float high = fmaxf(t0, t1);
+          for (int k = 0; k < TOK / 32; ++k)
+#pragma unroll
+            for (int e = 0; e < 32; ++e)
+              highs[e & 3] = fmaxf(highs[e & 3], __uint_as_float(x[k][e]));
+          const float high = fmaxf(fmaxf(highs[0], highs[1]), fmaxf(highs[2], highs[3]));
           const bool grow =
               mine && ((high - top) * c > kRescale || (top == -INFINITY && high > top));
           if (__any_sync(0xFFFFFFFFu, grow)) {
@@ -647,10 +760,11 @@ __global__ void __launch_bounds__(AT_THREADS, AtShape<HD>::kCtas)
             }
             __syncwarp();
             if (i > 0) {
-              // O holds the tiles before once their product is through
-              if (!wait(&sh.pv_done[(g - 1) & 1], ((g - 1) >> 1) & 1)) break;
+              // O holds the tiles before once their product is through; a wide block's
+              // S was issued after it
+              if (!WIDE && !wait(&sh.pv_done[(gt - 1) & 1], ((gt - 1) >> 1) & 1)) break;
               tc_fence_after();
-#pragma unroll
+#pragma unroll 1
               for (int at = 0; at < HD; at += 32) {
                 uint32_t o[32];
                 tmem_ld_32x32b_x32(o_tmem + at, o);
@@ -662,59 +776,69 @@ __global__ void __launch_bounds__(AT_THREADS, AtShape<HD>::kCtas)
               tmem_st_wait();
             }
           }
-          const float m = top == -INFINITY ? 0.0f : top;
-          float base = __fmul_rn(m, c);
+          const float off = top == -INFINITY ? 0.0f : top;
+          float base = __fmul_rn(off, c);
           const bool large = fabsf(base) > kLarge;
           if (__any_sync(0xFFFFFFFFu, large)) {
-            const float off = large ? m : 0.0f;  // a row's bits are its own affair
+            const float by = large ? off : 0.0f;  // a row's bits are its own affair
 #pragma unroll
-            for (int e = 0; e < 32; ++e) {
-              s0[e] = __float_as_uint(__uint_as_float(s0[e]) - off);
-              s1[e] = __float_as_uint(__uint_as_float(s1[e]) - off);
-            }
+            for (int k = 0; k < TOK / 32; ++k)
+#pragma unroll
+              for (int e = 0; e < 32; ++e)
+                x[k][e] = __float_as_uint(__uint_as_float(x[k][e]) - by);
             if (large) base = 0.0f;
           }
-          uint32_t pk[32];
-          float l0 = 0.0f, l1 = 0.0f;
+          const uint64_t base2 = pair_f32(__float_as_uint(-base), __float_as_uint(-base));
+          uint64_t sums[2] = {0ull, 0ull};
 #pragma unroll
-          for (int e = 0; e < 32; ++e) {
-            const uint32_t(&x)[32] = e < 16 ? s0 : s1;
-            const float a = exp2_approx(fmaf(__uint_as_float(x[(2 * e) & 31]), c, -base));
-            const float b = exp2_approx(fmaf(__uint_as_float(x[(2 * e + 1) & 31]), c, -base));
-            l0 += a;
-            l1 += b;
-            asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(pk[e]) : "f"(b), "f"(a));
+          for (int k = 0; k < TOK / 64; ++k) {
+            uint32_t pk[32];
+#pragma unroll
+            for (int e = 0; e < 32; ++e) {
+              const uint32_t(&y)[32] = x[2 * k + e / 16];
+              float lo, hi;
+              unpair_f32(pair_fma(pair_f32(y[(2 * e) & 31], y[(2 * e + 1) & 31]), c2, base2), lo,
+                         hi);
+              lo = exp2_approx(lo);
+              hi = exp2_approx(hi);
+              sums[e & 1] = pair_add(sums[e & 1], pair_f32(__float_as_uint(lo), __float_as_uint(hi)));
+              asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(pk[e]) : "f"(hi), "f"(lo));
+            }
+            tmem_st_32x32b_x32(s_tmem + 32 * k, pk);
           }
-          sum += l0 + l1;
-          tmem_st_32x32b_x32(s_tmem, pk);
+          float lo, hi;
+          unpair_f32(pair_add(sums[0], sums[1]), lo, hi);
+          sum += lo + hi;
           tmem_st_wait();
           tc_fence_before();
         }
         // ---- values of tokens that are not there are 0, and those that are not
         // finite where not every row attends them: 0 times them would be NaN
-        if (valid != ~0ull || !inner) {
-          const int x = it + (i < T - 1 ? 2 * i + 2 : 2 * T - 1);
-          const int stage = x % Sh::kStages;
-          if (!wait(&sh.full[stage], (x / Sh::kStages) & 1)) break;
-          const uint32_t v = smem_u32(ring + stage * Sh::kStage);
+        if (block == 0 && (!whole || !inner)) {
+          const int stage = gt % Sh::kV;
+          if (!wait(&sh.v_full[stage], (gt / Sh::kV) & 1)) break;
+          const uint32_t v = smem_u32(v_ring + stage * Sh::kTile);
+          constexpr int MINE = TOK / 4;  // tokens of a warp
+          const uint32_t there =
+              static_cast<uint32_t>(valid[warp * MINE / 64] >> (warp * MINE % 64));
           uint32_t bad = 0u;
-          for (int k = lane; k < 16 * (HD / 8); k += 32) {
-            const int r = k / (HD / 8), c = k - r * (HD / 8), tr = warp * 16 + r;
-            const uint32_t at = v + (c / 8) * (AT_TOKENS * 128) + tr * 128 + ((c & 7) << 4);
-            if ((valid >> tr & 1ull) == 0ull) {
+          for (int k = lane; k < MINE * (HD / 8); k += 32) {
+            const int r = k / (HD / 8), e = k - r * (HD / 8), tr = warp * MINE + r;
+            const uint32_t at = v + (e / 8) * Sh::kBox + tr * 128 + ((e & 7) << 4);
+            if ((there >> r & 1u) == 0u) {
               st_shared_zero16(at);
             } else if (!inner) {
               uint4 w = ld_shared_v4(at);
-              uint32_t *e = &w.x;
+              uint32_t *u = &w.x;
               bool found = false;
 #pragma unroll
               for (int q = 0; q < 4; ++q) {
-                if ((e[q] & 0x7F80u) == 0x7F80u) {
-                  e[q] &= 0xFFFF0000u;
+                if ((u[q] & 0x7F80u) == 0x7F80u) {
+                  u[q] &= 0xFFFF0000u;
                   found = true;
                 }
-                if ((e[q] & 0x7F800000u) == 0x7F800000u) {
-                  e[q] &= 0xFFFFu;
+                if ((u[q] & 0x7F800000u) == 0x7F800000u) {
+                  u[q] &= 0xFFFFu;
                   found = true;
                 }
               }
@@ -725,145 +849,145 @@ __global__ void __launch_bounds__(AT_THREADS, AtShape<HD>::kCtas)
             }
           }
           bad = __reduce_or_sync(0xFFFFFFFFu, bad);
-          if (!inner && lane == 0)
-            poison[warp][tile - common / AT_TOKENS] = static_cast<uint64_t>(bad) << (warp * 16);
+          if (!inner && lane == 0) poison[warp][s.t0 + i - common / TOK] = bad;
           fence_proxy_async_smem();
         }
         __syncwarp();
-        if (lane == 0) mbar_arrive(&sh.p_full[g & 1]);
+        if (lane == 0) mbar_arrive(&sh.p_full[buf]);
       }
       if (!ok) break;
-      gi += T;
-      it += 2 * T;
+      g += T;
       if (scans_here) {
         __syncwarp();
-        if (lane == 0) mbar_arrive(&sh.scanned);
+        if (block == 0 && lane == 0) mbar_arrive(&sh.scanned);
         if (!wait(&sh.scanned, scans & 1)) break;
         ++scans;
       }
       // ---- the item's rows, or what is to be joined
-      if (!wait(&sh.pv_done[(gi - 1) & 1], ((gi - 1) >> 1) & 1)) break;
+      const int buf = WIDE ? block : (g - 1) & 1;
+      if (!wait(&sh.pv_done[buf], WIDE ? (turn - 1) & 1 : ((g - 1) >> 1) & 1)) break;
       tc_fence_after();
-      uint64_t nonfinite[3] = {0ull, 0ull, 0ull};
-      if (scans_here) {
-        for (int k = 0; k < 3; ++k) {
-          const int token = (common / AT_TOKENS + k) * AT_TOKENS;
-          uint64_t x = poison[0][k] | poison[1][k] | poison[2][k] | poison[3][k];
-          if (s.tree) {
-            const int shift = s.ctx - token;
-            uint64_t seen = low_bits(shift);
-            if (shift >= 0 && shift < 64) seen |= bits << shift;
-            else if (shift < 0 && shift > -64) seen |= bits >> -shift;
-            x &= seen;
-          } else {
-            x &= low_bits(s.ctx + j + 1 - token);
-          }
-          nonfinite[k] = x;
+      // the tokens with values that are not finite that this row attends: by warp and
+      // tile, as they were found
+      uint32_t hit = 0u;
+      if (scans_here && mine) {
+        for (int k = 0; k < 12; ++k) {
+          if (poison[k / 3][k % 3] == 0u) continue;
+          const int token = (common / TOK + k % 3) * TOK + k / 3 * (TOK / 4);
+          if ((poison[k / 3][k % 3] & static_cast<uint32_t>(at_seen(s, bits, upto, token))) != 0u)
+            hit |= 1u << k;
         }
       }
       if (any) {
         const float by = sum == 0.0f ? 0.0f : 1.0f / sum;
 #pragma unroll 1
-        for (int c = 0; c < HD; c += 32) {
+        for (int at = 0; at < HD; at += 32) {
           uint32_t o[32];
-          tmem_ld_32x32b_x32(o_tmem + c, o);
+          tmem_ld_32x32b_x32(o_tmem + at, o);
           tmem_ld_wait(o);
-          if (mine && c < p.d) {
-          if ((nonfinite[0] | nonfinite[1] | nonfinite[2]) != 0ull) {
-            for (int k = 0; k < 3; ++k) {
-              for (uint64_t x = nonfinite[k]; x != 0ull; x &= x - 1ull) {
-                const int token = (common / AT_TOKENS + k) * AT_TOKENS + __ffsll(x) - 1;
+          if (mine && at < p.d) {
+            for (uint32_t left = hit; left != 0u; left &= left - 1u) {
+              const int k = __ffs(left) - 1;
+              const int first = (common / TOK + k % 3) * TOK + k / 3 * (TOK / 4);
+              uint32_t tokens = poison[k / 3][k % 3] &
+                                static_cast<uint32_t>(at_seen(s, bits, upto, first));
+              for (; tokens != 0u; tokens &= tokens - 1u) {
+                const int token = first + __ffs(tokens) - 1;
                 const int id = p.block_table[s.request * p.table_stride + (token >> p.page_shift)];
                 const __nv_bfloat16 *v =
                     p.v_cache + id * p.page_stride +
                     (token & ((1 << p.page_shift) - 1)) * p.token_stride +
-                    s.head * p.head_stride;
+                    s.head * p.head_stride + at;
 #pragma unroll
                 for (int e = 0; e < 32; ++e) {
-                  if (c + e < p.d) {
-                    const float f = __bfloat162float(v[c + e]);
+                  if (at + e < p.d) {
+                    const float f = __bfloat162float(v[e]);
                     if (!(fabsf(f) < INFINITY))
                       o[e] = __float_as_uint(__uint_as_float(o[e]) + f);
                   }
                 }
               }
             }
-          }
-          if (s.part < 0) {
-            __nv_bfloat16 *dst = static_cast<__nv_bfloat16 *>(p.out.p) + q_row * p.out.stride +
-                                 head * p.out.head_stride + c;
+            if (s.part < 0) {
+              __nv_bfloat16 *dst = static_cast<__nv_bfloat16 *>(p.out.p) + q_row * p.out.stride +
+                                   head * p.out.head_stride + at;
 #pragma unroll
-            for (int e = 0; e < 32; e += 8) {
-              if (c + e >= p.d) break;
-              uint4 w;
-              uint32_t *u = &w.x;
+              for (int e = 0; e < 32; e += 8) {
+                uint4 w;
+                uint32_t *u = &w.x;
 #pragma unroll
-              for (int q = 0; q < 4; ++q)
-                asm("cvt.rn.bf16x2.f32 %0, %1, %2;"
-                    : "=r"(u[q])
-                    : "f"(__uint_as_float(o[e + 2 * q + 1]) * by),
-                      "f"(__uint_as_float(o[e + 2 * q]) * by));
-              *reinterpret_cast<uint4 *>(dst + e) = w;
+                for (int q = 0; q < 4; ++q)
+                  asm("cvt.rn.bf16x2.f32 %0, %1, %2;"
+                      : "=r"(u[q])
+                      : "f"(__uint_as_float(o[e + 2 * q + 1]) * by),
+                        "f"(__uint_as_float(o[e + 2 * q]) * by));
+                if (at + e < p.d) *reinterpret_cast<uint4 *>(dst + e) = w;
+              }
+            } else {
+              float *dst =
+                  p.parts.o + (static_cast<int64_t>(s.part) * p.parts.rows + row) * HD + at;
+#pragma unroll
+              for (int e = 0; e < 32; e += 4)
+                *reinterpret_cast<uint4 *>(dst + e) =
+                    make_uint4(o[e], o[e + 1], o[e + 2], o[e + 3]);
             }
-          } else {
-            float *dst =
-                p.part_o + (static_cast<int64_t>(s.part) * p.tile_rows + row) * HD + c;
-#pragma unroll
-            for (int e = 0; e < 32; e += 4)
-              *reinterpret_cast<uint4 *>(dst + e) = make_uint4(o[e], o[e + 1], o[e + 2], o[e + 3]);
-          }
           }
           __syncwarp();
         }
         if (mine && s.part >= 0)
-          p.part_ml[static_cast<int64_t>(s.part) * p.tile_rows + row] = make_float2(top, sum);
+          p.parts.ml[static_cast<int64_t>(s.part) * p.parts.rows + row] = make_float2(top, sum);
         else if (mine && p.lse != nullptr)
           p.lse[q_row * (p.Hk * p.group) + head] =
               sum == 0.0f ? -INFINITY : at_base(top, c) * kLn2 + logf(sum);
       }
       tc_fence_before();
-      ++segs;
     }
   }
   if (lane == 0 && *abort_flag) raise_status(p.status, DSPARK_DEV_TIMEOUT);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  if (warp == 5) tmem_dealloc(tmem, Sh::kTmem);
+  if (warp == SOFTMAX + 2) tmem_dealloc(tmem, Sh::kTmem);
 }
 
 // Joins the pieces of the items that were cut: a warp a row.
 template <int HD>
-__global__ void __launch_bounds__(256) attention_join_kernel(const AtParams p) {
+__global__ void __launch_bounds__(256)
+    attention_join_kernel(const AtParams p, const AtParts narrow, const AtParts wide) {
   wait_for_earlier_kernel();
-  const int cta = static_cast<int>(blockIdx.x), lane = threadIdx.x & 31;
-  const int row = blockIdx.y * 8 + (threadIdx.x >> 5);
-  const AtMeta meta = p.meta[cta];
-  const int m = meta.block * AT_ROWS + row, j = m / p.group;
-  if (meta.last == 0 || row >= AT_ROWS || j >= meta.count) return;
+  const bool second = static_cast<int>(blockIdx.x) >= narrow.ctas;
+  const AtParts &parts = second ? wide : narrow;
+  const int cta = static_cast<int>(blockIdx.x) - (second ? narrow.ctas : 0);
+  const int lane = threadIdx.x & 31, row = blockIdx.y * 8 + (threadIdx.x >> 5);
+  const AtMeta meta = parts.meta[cta];
+  const int m = meta.block * (second ? 2 * AT_ROWS : AT_ROWS) + row, j = m / p.group;
+  if (meta.last == 0 || row >= parts.rows || j >= meta.count) return;
   const int head = meta.head * p.group + (m - j * p.group);
   const int pieces = meta.last - cta + 1;
   // the first piece is in the CTA's second slot, the others in first ones
   auto slot = [&](int k) {
-    return (static_cast<int64_t>(k == 0 ? 2 * cta + 1 : 2 * (cta + k))) * p.tile_rows + row;
+    return (static_cast<int64_t>(k == 0 ? 2 * cta + 1 : 2 * (cta + k))) * parts.rows + row;
   };
   float top = -INFINITY;
-  for (int k = lane; k < pieces; k += 32) top = fmaxf(top, p.part_ml[slot(k)].x);
+  for (int k = lane; k < pieces; k += 32) top = fmaxf(top, parts.ml[slot(k)].x);
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, o));
   const float above = top == -INFINITY ? 0.0f : top;
   constexpr int E = HD / 32;
   float acc[E] = {}, sum = 0.0f;
+#pragma unroll 4
   for (int k = 0; k < pieces; ++k) {
-    const float2 ml = p.part_ml[slot(k)];
+    const float2 ml = parts.ml[slot(k)];
+    const float *o = parts.o + slot(k) * HD + lane * E;
+    float2 v[E / 2];
+#pragma unroll
+    for (int e = 0; e < E / 2; ++e) v[e] = *reinterpret_cast<const float2 *>(o + 2 * e);
     const float w = exp2_approx(at_difference(ml.x, above, p.scale_log2));
-    const float *o = p.part_o + slot(k) * HD + lane * E;
     sum = fmaf(w, ml.y, sum);
 #pragma unroll
     for (int e = 0; e < E; e += 2) {
-      const float2 v = *reinterpret_cast<const float2 *>(o + e);
-      acc[e] = fmaf(w, v.x, acc[e]);
-      acc[e + 1] = fmaf(w, v.y, acc[e + 1]);
+      acc[e] = fmaf(w, v[e / 2].x, acc[e]);
+      acc[e + 1] = fmaf(w, v[e / 2].y, acc[e + 1]);
     }
   }
   const int64_t q_row = meta.first + j;
@@ -886,30 +1010,50 @@ __global__ void __launch_bounds__(256) attention_join_kernel(const AtParams p) {
 // host side
 // ==========================================================================
 static int padded_head(int32_t d) { return d <= 64 ? 64 : d <= 128 ? 128 : 256; }
-static int tile_rows(int32_t max_len, int32_t group) {
-  return static_cast<int>(
-      std::min<int64_t>(AT_ROWS, (static_cast<int64_t>(max_len) * group + 7) / 8 * 8));
+
+// Rows of a slot, and the workspace: status, then each kernel's meta, sums and O.
+struct AtLayout {
+  int narrow_rows, wide_rows;  // wide_rows 0: that kernel does not run
+  size_t meta[2], ml[2], o[2], total;
+};
+static AtLayout at_layout(int32_t max_len, int32_t group, int32_t d) {
+  AtLayout l = {};
+  const int64_t packed = (static_cast<int64_t>(max_len) * group + 7) / 8 * 8;
+  const int hd = padded_head(d);
+  l.narrow_rows = static_cast<int>(std::min<int64_t>(AT_ROWS, packed));
+  l.wide_rows = static_cast<int64_t>(max_len) * group > AT_ROWS && hd <= 128
+                    ? static_cast<int>(std::min<int64_t>(2 * AT_ROWS, packed))
+                    : 0;
+  size_t at = 256;
+  auto take = [&](size_t bytes) {
+    const size_t here = at;
+    at += (bytes + 255) / 256 * 256;
+    return here;
+  };
+  const int rows[2] = {l.narrow_rows, l.wide_rows}, ctas[2] = {AT_MAX_NARROW, AT_MAX_WIDE};
+  for (int k = 0; k < 2; ++k) {
+    const size_t slots = static_cast<size_t>(2 * ctas[k]) * rows[k];
+    l.meta[k] = take(ctas[k] * sizeof(AtMeta));
+    l.ml[k] = take(slots * sizeof(float2));
+    l.o[k] = take(slots * hd * sizeof(float));
+  }
+  l.total = at;
+  return l;
 }
-constexpr size_t kAtMetaOffset = 256;
-constexpr size_t kAtPartOffset = kAtMetaOffset + (AT_MAX_CTAS * sizeof(AtMeta) + 255) / 256 * 256;
 
 size_t attention_workspace_bytes(int32_t max_len, int32_t Hq, int32_t Hk, int32_t d) {
-  return kAtPartOffset + static_cast<size_t>(2 * AT_MAX_CTAS) * tile_rows(max_len, Hq / Hk) *
-                             (8 + 4 * static_cast<size_t>(padded_head(d)));
+  return at_layout(max_len, Hq / Hk, d).total;
 }
 
-static std::mutex g_at_mu;
-static bool g_at_attr[3][128];
-
 static bool encode_cache(EncodeTiledFn enc, CUtensorMap *map, const void *p,
-                         const AttentionArgs &a) {
+                         const AttentionArgs &a, int tokens) {
   cuuint64_t dims[4] = {static_cast<cuuint64_t>(a.d), static_cast<cuuint64_t>(a.Hk),
                         static_cast<cuuint64_t>(1) << a.page_shift,
                         static_cast<cuuint64_t>(a.num_pages)};
   cuuint64_t strides[3] = {static_cast<cuuint64_t>(a.head_stride) * 2,
                            static_cast<cuuint64_t>(a.token_stride) * 2,
                            static_cast<cuuint64_t>(a.page_stride) * 2};
-  cuuint32_t box[4] = {64, 1, static_cast<cuuint32_t>(std::min(1 << a.page_shift, AT_TOKENS)), 1};
+  cuuint32_t box[4] = {64, 1, static_cast<cuuint32_t>(std::min(1 << a.page_shift, tokens)), 1};
   cuuint32_t es[4] = {1, 1, 1, 1};
   return enc(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void *>(p), dims, strides, box,
              es, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
@@ -917,24 +1061,38 @@ static bool encode_cache(EncodeTiledFn enc, CUtensorMap *map, const void *p,
          CUDA_SUCCESS;
 }
 
-template <int HD>
-static dspark_status launch(const AttentionArgs &a, int which, int dev, int sms,
-                            cudaStream_t stream) {
-  using Sh = AtShape<HD>;
+static std::mutex g_at_mu;
+
+template <int HD, bool WIDE>
+static dspark_status launch_one(const AttentionArgs &a, const AtParams &p, int dev,
+                                cudaStream_t stream) {
+  using Sh = AtShape<HD, WIDE>;
+  constexpr int bytes = Sh::kTiles + static_cast<int>(sizeof(AtShared<HD, WIDE>));
+  static_assert(Sh::kCtas * (bytes + 1024) <= 228 * 1024, "shared memory of an SM");
+  static bool attr[128];
   {
     std::lock_guard<std::mutex> lk(g_at_mu);
-    if (!g_at_attr[which][dev]) {
-      if (cudaFuncSetAttribute(attention_kernel<HD>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                               Sh::kBytes) != cudaSuccess)
+    if (!attr[dev]) {
+      if (cudaFuncSetAttribute(attention_kernel<HD, WIDE>,
+                               cudaFuncAttributeMaxDynamicSharedMemorySize, bytes) != cudaSuccess)
         return DSPARK_ERR_CUDA;
-      g_at_attr[which][dev] = true;
+      attr[dev] = true;
     }
   }
   EncodeTiledFn enc = encode_tiled_fn();
   if (enc == nullptr) return DSPARK_ERR_CUDA;
   CUtensorMap k_map, v_map;
-  if (!encode_cache(enc, &k_map, a.k_cache, a) || !encode_cache(enc, &v_map, a.v_cache, a))
+  if (!encode_cache(enc, &k_map, a.k_cache, a, Sh::kTokens) ||
+      !encode_cache(enc, &v_map, a.v_cache, a, Sh::kTokens))
     return DSPARK_ERR_INVALID_ARG;
+  return launch_overlapped(attention_kernel<HD, WIDE>, dim3(p.parts.ctas), dim3(Sh::kThreads),
+                           bytes, stream, k_map, v_map, p) == cudaSuccess
+             ? DSPARK_OK
+             : DSPARK_ERR_CUDA;
+}
+
+template <int HD>
+static dspark_status launch(const AttentionArgs &a, int dev, int sms, cudaStream_t stream) {
   AtParams p = {};
   p.q = a.q;
   p.out = a.out;
@@ -957,21 +1115,39 @@ static dspark_status launch(const AttentionArgs &a, int which, int dev, int sms,
   p.page_shift = a.page_shift;
   p.num_pages = a.num_pages;
   p.max_pages = a.max_pages;
-  p.least_tiles = 4;
-  p.tile_rows = tile_rows(a.max_len, p.group);
   p.scale_log2 = a.scale * kLog2e;
   p.lse = a.lse;
   p.status = reinterpret_cast<uint32_t *>(a.workspace);
-  p.meta = reinterpret_cast<AtMeta *>(a.workspace + kAtMetaOffset);
-  p.part_o = reinterpret_cast<float *>(a.workspace + kAtPartOffset);
-  p.part_ml = reinterpret_cast<float2 *>(
-      p.part_o + static_cast<size_t>(2 * AT_MAX_CTAS) * p.tile_rows * HD);
-  const int grid = std::min(AT_MAX_CTAS, Sh::kCtas * sms);
-  if (launch_overlapped(attention_kernel<HD>, dim3(grid), dim3(AT_THREADS), Sh::kBytes, stream,
-                        k_map, v_map, p) != cudaSuccess)
-    return DSPARK_ERR_CUDA;
-  return launch_overlapped(attention_join_kernel<HD>, dim3(grid, (p.tile_rows + 7) / 8),
-                           dim3(256), 0, stream, p) == cudaSuccess
+  const AtLayout l = at_layout(a.max_len, p.group, a.d);
+  auto parts = [&](int k, int rows, int ctas) {
+    AtParts x;
+    x.meta = reinterpret_cast<AtMeta *>(a.workspace + l.meta[k]);
+    x.ml = reinterpret_cast<float2 *>(a.workspace + l.ml[k]);
+    x.o = reinterpret_cast<float *>(a.workspace + l.o[k]);
+    x.rows = rows;
+    x.ctas = ctas;
+    return x;
+  };
+  const AtParts narrow = parts(
+      0, l.narrow_rows, std::min(AT_MAX_NARROW, AtShape<HD, false>::kCtas * sms));
+  const AtParts wide = parts(1, l.wide_rows, l.wide_rows > 0 ? std::min(AT_MAX_WIDE, sms) : 0);
+  p.both = l.wide_rows > 0;
+  p.parts = narrow;
+  p.least_tiles = 4;
+  dspark_status s = launch_one<HD, false>(a, p, dev, stream);
+  if (s != DSPARK_OK) return s;
+  if constexpr (HD <= 128) {
+    if (l.wide_rows > 0) {
+      p.parts = wide;
+      p.least_tiles = 2;
+      s = launch_one<HD, true>(a, p, dev, stream);
+      if (s != DSPARK_OK) return s;
+    }
+  }
+  const int rows = std::max(l.narrow_rows, l.wide_rows);
+  return launch_overlapped(attention_join_kernel<HD>,
+                           dim3(narrow.ctas + wide.ctas, (rows + 7) / 8), dim3(256), 0, stream, p,
+                           narrow, wide) == cudaSuccess
              ? DSPARK_OK
              : DSPARK_ERR_CUDA;
 }
@@ -983,11 +1159,11 @@ dspark_status attention_launch(const AttentionArgs &a, cudaStream_t stream) {
   if (sms <= 0) return DSPARK_ERR_CUDA;
   switch (padded_head(a.d)) {
     case 64:
-      return launch<64>(a, 0, dev, sms, stream);
+      return launch<64>(a, dev, sms, stream);
     case 128:
-      return launch<128>(a, 1, dev, sms, stream);
+      return launch<128>(a, dev, sms, stream);
     default:
-      return launch<256>(a, 2, dev, sms, stream);
+      return launch<256>(a, dev, sms, stream);
   }
 }
 
