@@ -23,8 +23,9 @@
 //
 // Work is split by tiles of tokens, not by rows: all (request, head, block) items
 // laid end to end are cut into equal runs, one a CTA, so that one long context
-// occupies the whole GPU and short ones leave no tail.  A cut item leaves its O, m and
-// l in the workspace and a last kernel joins them, in order.
+// occupies the whole GPU and short ones leave no tail.  An item counts as some tiles
+// more than it has, for its queries' way in and its results' way out.  A cut item
+// leaves its O, m and l in the workspace and a last kernel joins them, in order.
 #include <algorithm>
 #include <cuda_bf16.h>
 #include <mutex>
@@ -67,6 +68,7 @@ struct AtShape {
   static constexpr int kO = 2 * kTokens;                         // where O begins
   static constexpr int kTiles = kGroups * kQ + (kK + kV) * kTile;
   static constexpr int kThreads = kGroups * 128 + 128;           // softmax; K, V, products
+  static constexpr int kItem = 2;                                // tiles that an item costs besides
   // registers of the two kinds of warpgroups: together at most the launch's
   static constexpr int kLaunchRegs = kCtas == 1 ? 168 : 128;
   static constexpr int kSoftmaxRegs = WIDE ? 208 : 176;
@@ -269,15 +271,15 @@ struct AtPlan {
   static __device__ __forceinline__ int tiles(int end) {
     return (end + Sh::kTokens - 1) / Sh::kTokens;
   }
-  // the tiles of one head
-  static __device__ __forceinline__ int64_t head_tiles(const AtParams &p, const AtRequest &r) {
+  // what one head costs, in tiles
+  static __device__ __forceinline__ int64_t head_units(const AtParams &p, const AtRequest &r) {
     int64_t sum = 0;
-    for (int b = 0; b < r.blocks; ++b) sum += tiles(end(p, r, b));
+    for (int b = 0; b < r.blocks; ++b) sum += Sh::kItem + tiles(end(p, r, b));
     return sum;
   }
 };
 
-// The CTAs' equal shares of all tiles.
+// The CTAs' equal shares of all units: each item's kItem, then its tiles.
 struct AtShares {
   int64_t units;
   int ctas;
@@ -386,7 +388,7 @@ __global__ void __launch_bounds__(AtShape<HD, WIDE>::kThreads, AtShape<HD, WIDE>
                                static_cast<int64_t>(p.max_pages) << p.page_shift)
           raise_status(p.status, DSPARK_DEV_PAGE_OOR);
       }
-      mine += p.Hk * Plan::head_tiles(p, r);
+      mine += p.Hk * Plan::head_units(p, r);
     }
     int64_t x = mine;
 #pragma unroll
@@ -408,7 +410,7 @@ __global__ void __launch_bounds__(AtShape<HD, WIDE>::kThreads, AtShape<HD, WIDE>
       int64_t rest = shares.begin(cta) - before;
       if (rest >= 0 && rest < mine) {
         for (int n = n0; n < n1; ++n) {
-          const int64_t units = p.Hk * Plan::head_tiles(p, Plan::request(p, n));
+          const int64_t units = p.Hk * Plan::head_units(p, Plan::request(p, n));
           if (rest < units) {
             sh.start_request = n;
             sh.start_rest = rest;
@@ -505,15 +507,15 @@ __global__ void __launch_bounds__(AtShape<HD, WIDE>::kThreads, AtShape<HD, WIDE>
         int64_t rest = sh.start_rest;
         for (; ok && unit < end_unit && n < p.N; ++n, rest = 0) {
           const AtRequest r = Plan::request(p, n);
-          const int64_t a_head = Plan::head_tiles(p, r);
+          const int64_t a_head = Plan::head_units(p, r);
           if (a_head == 0) continue;
           // the items before the first one of this run
           int h = static_cast<int>(rest / a_head), b = 0;
           rest -= h * a_head;
           for (; b < r.blocks; ++b) {
-            const int t = Plan::tiles(Plan::end(p, r, b));
-            if (rest < t) break;
-            rest -= t;
+            const int units = Sh::kItem + Plan::tiles(Plan::end(p, r, b));
+            if (rest < units) break;
+            rest -= units;
           }
           for (; ok && h < p.Hk && unit < end_unit; ++h, b = 0) {
             for (; ok && b < r.blocks && unit < end_unit; ++b) {
@@ -527,10 +529,13 @@ __global__ void __launch_bounds__(AtShape<HD, WIDE>::kThreads, AtShape<HD, WIDE>
               s.tree = r.tree;
               s.end = Plan::end(p, r, b);
               const int tiles = Plan::tiles(s.end);
-              s.t0 = static_cast<int>(rest);
-              s.t1 = static_cast<int>(min(static_cast<int64_t>(tiles), rest + (end_unit - unit)));
+              const int64_t stop =
+                  min(static_cast<int64_t>(Sh::kItem + tiles), rest + (end_unit - unit));
+              s.t0 = static_cast<int>(max(rest - Sh::kItem, static_cast<int64_t>(0)));
+              s.t1 = static_cast<int>(max(stop - Sh::kItem, static_cast<int64_t>(0)));
+              unit += stop - rest;
               rest = 0;
-              unit += s.t1 - s.t0;
+              if (s.t1 == s.t0) continue;  // this run ends before its first tile
               s.part = -1;
               if (s.t0 > 0) {
                 s.part = 2 * cta;
@@ -659,23 +664,20 @@ __global__ void __launch_bounds__(AtShape<HD, WIDE>::kThreads, AtShape<HD, WIDE>
       ok = ok && __all_sync(0xFFFFFFFFu, wait_bounded(bar, parity, abort_flag, p.status));
       return ok;
     };
-    while (ok) {
+    // The next segment, and its Q on the way to shared memory: each thread its row.
+    AtSeg next;
+    auto fetch = [&] {
       const int si = segs % AT_SEGS;
-      if (!wait(&sh.seg_full[si], (segs / AT_SEGS) & 1)) break;
-      const AtSeg s = sh.seg[si];
+      if (!wait(&sh.seg_full[si], (segs / AT_SEGS) & 1)) return;
+      next = sh.seg[si];
       __syncwarp();
       if (lane == 0) mbar_arrive(&sh.seg_empty[si]);
-      if (s.request < 0) break;
-      const int T = s.t1 - s.t0;
-      const int m = s.block * Sh::kRows + row, j = m / p.group;
-      const int head = s.head * p.group + (m - j * p.group);
-      const bool mine = j < s.count;
-      const bool any = __any_sync(0xFFFFFFFFu, mine);
-      const int64_t q_row = s.first + j;
-      // ---- Q: each thread its row
-      if (mine) {
+      ++segs;
+      const int m = next.block * Sh::kRows + row, j = m / p.group;
+      if (next.request >= 0 && j < next.count) {
+        const int head = next.head * p.group + (m - j * p.group);
         const __nv_bfloat16 *src = static_cast<const __nv_bfloat16 *>(p.q.p) +
-                                   q_row * p.q.stride + head * p.q.head_stride;
+                                   (next.first + j) * p.q.stride + head * p.q.head_stride;
         const uint32_t dst = smem_u32(smem) + block * Sh::kQ + (row & (AT_ROWS - 1)) * 128;
 #pragma unroll 4
         for (int e = 0; e < HD / 8; ++e) {
@@ -683,16 +685,28 @@ __global__ void __launch_bounds__(AtShape<HD, WIDE>::kThreads, AtShape<HD, WIDE>
           if (e * 8 < p.d) cp_async_16(at, src + e * 8);
           else st_shared_zero16(at);
         }
-        cp_async_wait_all();
       }
+    };
+    fetch();
+    while (ok) {
+      const AtSeg s = next;
+      if (s.request < 0) break;
+      const int T = s.t1 - s.t0;
+      const int m = s.block * Sh::kRows + row, j = m / p.group;
+      const int head = s.head * p.group + (m - j * p.group);
+      const bool mine = j < s.count;
+      const bool any = __any_sync(0xFFFFFFFFu, mine);
+      const int64_t q_row = s.first + j;
+      // ---- Q, on its way since the segment before
+      cp_async_wait_all();
       fence_proxy_async_smem();
       __syncwarp();
       if (lane == 0) mbar_arrive(&sh.q_full);
-      ++segs;
       // the second block may have no rows; the products leave it out too
       if (WIDE && block == 1 && s.count * p.group - s.block * Sh::kRows <= AT_ROWS) {
         g += T;
         if (s.t1 * TOK > s.ctx + (s.tree ? 0 : s.block * Sh::kRows / p.group + 1)) ++scans;
+        fetch();
         continue;
       }
 
@@ -702,7 +716,7 @@ __global__ void __launch_bounds__(AtShape<HD, WIDE>::kThreads, AtShape<HD, WIDE>
       const int upto = s.ctx + j + 1;
       // before this token every row attends every token
       const int common = s.ctx + (s.tree ? 0 : s.block * Sh::kRows / p.group + 1);
-      uint32_t(&poison)[4][3] = sh.poison[segs & 1];
+      uint32_t(&poison)[4][3] = sh.poison[segs & 1];  // segs is one ahead for all warps
       if (block == 0 && lane < 3) poison[warp][lane] = 0u;
       __syncwarp();
       const bool scans_here = s.t1 * TOK > common;
@@ -857,6 +871,8 @@ __global__ void __launch_bounds__(AtShape<HD, WIDE>::kThreads, AtShape<HD, WIDE>
       }
       if (!ok) break;
       g += T;
+      fetch();  // the last scores are there, so Q has been read
+      if (!ok) break;
       if (scans_here) {
         __syncwarp();
         if (block == 0 && lane == 0) mbar_arrive(&sh.scanned);
