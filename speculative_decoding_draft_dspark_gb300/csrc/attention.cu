@@ -41,7 +41,6 @@ constexpr int AT_ROWS = 128;       // rows of a product
 constexpr int AT_MAX_NARROW = 320;  // CTAs that leave partial results
 constexpr int AT_MAX_WIDE = 160;
 constexpr int AT_SEGS = 4;         // segments told ahead
-constexpr int AT_INFOS = 16;       // tiles told ahead: more than the K ring and the scores are
 constexpr float kRescale = 8.0f;   // log2 of what the maximum may grow by
 // Up to this a maximum is taken off as fma(s, c, -round(m c)): whatever m c was rounded
 // to is in lse too, so nothing is lost.  A larger m is taken off first, (s - m) c: at
@@ -88,8 +87,8 @@ struct AtMeta {
 struct AtParts {
   AtMeta *meta;
   float2 *ml;  // [slot][rows]: maximum, sum
-  float *o;    // [slot][rows][HD]
-  int32_t rows, ctas;
+  float *o;    // [slot][rows / 8][HD / 4][8][4]: eight rows' pieces side by side
+  int32_t rows, ctas;  // rows: a multiple of 8
 };
 
 struct AtParams {
@@ -101,6 +100,7 @@ struct AtParams {
   const __nv_bfloat16 *v_cache;
   int64_t page_stride, token_stride, head_stride;
   int32_t tree_width, N, R, max_len, Hk, group, d;
+  uint32_t group_magic, group_shift;  // for divisions by group
   int32_t page_shift, num_pages, max_pages, least_tiles;
   int32_t both;  // both kernels run: each takes its requests
   float scale_log2;
@@ -195,6 +195,34 @@ __device__ __forceinline__ void tmem_st_wait() {
   asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
 }
 
+__device__ __forceinline__ void tmem_st_32x32b_x16(uint32_t taddr, const uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], "
+      "{%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16};" ::"r"(taddr),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]),
+      "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]),
+      "r"(r[15])
+      : "memory");
+}
+// adds to one column of the warp's lanes
+__device__ __forceinline__ void tmem_add(uint32_t taddr, float by) {
+  float v;
+  asm volatile("tcgen05.ld.sync.aligned.32x32b.x1.b32 {%0}, [%1];" : "=f"(v) : "r"(taddr) : "memory");
+  asm volatile("tcgen05.wait::ld.sync.aligned;" : "+f"(v)::"memory");
+  v += by;
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x1.b32 [%0], {%1};" ::"r"(taddr), "f"(v) : "memory");
+  tmem_st_wait();
+}
+
+__device__ __forceinline__ uint32_t ld_shared_u32(uint32_t addr) {
+  uint32_t v;
+  asm volatile("ld.shared.u32 %0, [%1];" : "=r"(v) : "r"(addr) : "memory");
+  return v;
+}
+__device__ __forceinline__ void st_shared_u32(uint32_t addr, uint32_t v) {
+  asm volatile("st.shared.u32 [%0], %1;" ::"r"(addr), "r"(v) : "memory");
+}
+
 __device__ __forceinline__ float exp2_approx(float x) {
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
@@ -240,10 +268,18 @@ __device__ __forceinline__ uint64_t pair_add(uint64_t a, uint64_t b) {
   return r;
 }
 
+// m / group for m below 2^29
+__device__ __forceinline__ int at_token(const AtParams &p, int m) {
+  return p.group == 1 ? m
+                      : static_cast<int>(__umulhi(static_cast<uint32_t>(m), p.group_magic) >>
+                                         p.group_shift);
+}
+
 // ----------------------------------------------------------------- planning
 struct AtRequest {
   int first, count, ctx, blocks;
   bool tree;
+  uint32_t flags;  // what is wrong with its lengths
 };
 
 template <int HD, bool WIDE>
@@ -257,6 +293,10 @@ struct AtPlan {
     r.count = min(rows.count, p.max_len);
     r.ctx = max(p.ctx_len[n], 0);
     r.tree = is_tree(p.tree, p.tree_width, n, rows.count);
+    r.flags = rows.count > p.max_len ? DSPARK_DEV_LEN_OOR : 0u;
+    if (r.count > 0 && static_cast<int64_t>(r.ctx) + r.count >
+                           static_cast<int64_t>(p.max_pages) << p.page_shift)
+      r.flags |= DSPARK_DEV_PAGE_OOR;
     const int packed = r.count * p.group;
     r.blocks = p.both && (packed > AT_ROWS) != WIDE ? 0 : (packed + Sh::kRows - 1) / Sh::kRows;
     return r;
@@ -264,7 +304,7 @@ struct AtPlan {
   // Tokens that some row of a block attends, as an end: those in the cache and the
   // step's, up to the block's last row where the request is a chain.
   static __device__ __forceinline__ int end(const AtParams &p, const AtRequest &r, int b) {
-    const int last = r.tree ? r.count : min(r.count, ((b + 1) * Sh::kRows - 1) / p.group + 1);
+    const int last = r.tree ? r.count : min(r.count, at_token(p, (b + 1) * Sh::kRows - 1) + 1);
     const int64_t e = static_cast<int64_t>(r.ctx) + last;
     return static_cast<int>(min(e, static_cast<int64_t>(p.max_pages) << p.page_shift));
   }
@@ -279,12 +319,38 @@ struct AtPlan {
   }
 };
 
-// The CTAs' equal shares of all units: each item's kItem, then its tiles.
+// The CTAs' equal shares of all units (each item's kItem, then its tiles): the first
+// `more` CTAs have one more.
 struct AtShares {
-  int64_t units;
-  int ctas;
-  __device__ __forceinline__ int64_t begin(int c) const { return units * c / ctas; }
+  int64_t each;
+  int more, ctas;
+  __device__ __forceinline__ void split(int64_t units, int most, int least) {
+    ctas = static_cast<int>(min(static_cast<int64_t>(most), (units + least - 1) / least));
+    each = ctas > 0 ? units / ctas : 0;
+    more = static_cast<int>(units - each * ctas);
+  }
+  __device__ __forceinline__ int64_t begin(int c) const { return each * c + min(c, more); }
+  __device__ __forceinline__ int holder(int64_t unit) const {
+    const int64_t first = begin(more);
+    return unit < first ? static_cast<int>(unit / (each + 1))
+                        : more + static_cast<int>((unit - first) / each);
+  }
 };
+
+// A bounded wait (see common.cuh) in few instructions: what a CTA that gave up has to say
+// is said once, at its end.
+__device__ __forceinline__ bool at_wait(uint64_t *bar, uint32_t parity,
+                                        volatile uint32_t *abort_flag) {
+  if (mbar_try_wait(bar, parity)) return true;
+  const uint64_t t0 = global_timer_ns();
+  while (!mbar_try_wait_sleep(bar, parity, 20000u)) {
+    if (*abort_flag != 0u || global_timer_ns() - t0 > kWaitLimitNs) {
+      *abort_flag = 1u;
+      return false;
+    }
+  }
+  return true;
+}
 
 // Shared state besides the tiles
 template <int HD, bool WIDE>
@@ -292,18 +358,25 @@ struct AtShared {
   using Sh = AtShape<HD, WIDE>;
   uint64_t k_full[Sh::kK], k_empty[Sh::kK], v_full[Sh::kV], v_empty[Sh::kV];
   // by block of rows (wide) or by tile, in turn (narrow)
-  uint64_t s_full[2], p_full[2], pv_done[2];
+  uint64_t s_full[2], p_full[2][Sh::kWords], pv_done[2];  // p: 64 tokens at a time
   uint64_t q_full, scanned;
   uint64_t seg_full[AT_SEGS], seg_empty[AT_SEGS];
-  uint64_t info_full[AT_INFOS];
-  uint64_t valid[AT_INFOS][Sh::kWords];  // a tile's tokens that are there
   uint32_t poison[2][4][3];              // tokens whose values are not finite: warp, tile
   AtSeg seg[AT_SEGS];
   int64_t scan[Sh::kThreads / 32];
+  AtRequest start;
   int64_t start_rest;
   int32_t start_request;
   uint32_t tmem, abort;
 };
+
+// A partial O's four columns from `column` on, of one row; the next four are eight further.
+template <int HD>
+__device__ __forceinline__ float4 *at_part(const AtParts &parts, int slot, int row, int column) {
+  return reinterpret_cast<float4 *>(parts.o) +
+         (static_cast<int64_t>(slot) * (parts.rows / 8) + row / 8) * (2 * HD) + column / 4 * 8 +
+         (row & 7);
+}
 
 // The tokens of a tile's word that a row attends: of the cache, and of the step's rows
 // (`bits` in a tree, the first `upto` tokens in a chain).
@@ -342,7 +415,7 @@ __global__ void __launch_bounds__(AtShape<HD, WIDE>::kThreads, AtShape<HD, WIDE>
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(&sh.s_full[i], 1);
-      mbar_init(&sh.p_full[i], 4);
+      for (int w = 0; w < WORDS; ++w) mbar_init(&sh.p_full[i][w], 4);
       mbar_init(&sh.pv_done[i], 1);
     }
     mbar_init(&sh.q_full, SOFTMAX);
@@ -351,9 +424,7 @@ __global__ void __launch_bounds__(AtShape<HD, WIDE>::kThreads, AtShape<HD, WIDE>
       mbar_init(&sh.seg_full[i], 1);
       mbar_init(&sh.seg_empty[i], SOFTMAX + 2);
     }
-    for (int i = 0; i < AT_INFOS; ++i) mbar_init(&sh.info_full[i], 1);
     sh.abort = 0u;
-    sh.start_request = -1;
     fence_mbarrier_init();
     fence_proxy_async_smem();
   }
@@ -378,17 +449,13 @@ __global__ void __launch_bounds__(AtShape<HD, WIDE>::kThreads, AtShape<HD, WIDE>
   {
     const int C = (p.N + Sh::kThreads - 1) / Sh::kThreads;
     const int n0 = min(p.N, tid * C), n1 = min(p.N, n0 + C);
-    int64_t mine = 0;
+    int64_t mine = 0, last = 0;  // units of these requests, and of the last of them
+    AtRequest r;
     for (int n = n0; n < n1; ++n) {
-      const AtRequest r = Plan::request(p, n);
-      if (cta == 0 && !WIDE) {
-        if (row_span(p.cu_rows, n, p.R).count > p.max_len)
-          raise_status(p.status, DSPARK_DEV_LEN_OOR);
-        if (r.count > 0 && static_cast<int64_t>(r.ctx) + r.count >
-                               static_cast<int64_t>(p.max_pages) << p.page_shift)
-          raise_status(p.status, DSPARK_DEV_PAGE_OOR);
-      }
-      mine += p.Hk * Plan::head_units(p, r);
+      r = Plan::request(p, n);
+      last = p.Hk * Plan::head_units(p, r);
+      mine += last;
+      if (cta == 0 && !WIDE && r.flags != 0u) raise_status(p.status, r.flags);
     }
     int64_t x = mine;
 #pragma unroll
@@ -399,25 +466,27 @@ __global__ void __launch_bounds__(AtShape<HD, WIDE>::kThreads, AtShape<HD, WIDE>
     if (lane == 31) sh.scan[warp] = x;
     __syncthreads();
     int64_t before = x - mine, total = 0;
+#pragma unroll 1
     for (int w = 0; w < Sh::kThreads / 32; ++w) {
       if (w < warp) before += sh.scan[w];
       total += sh.scan[w];
     }
-    shares.units = total;
-    shares.ctas = static_cast<int>(min(static_cast<int64_t>(gridDim.x),
-                                       (total + p.least_tiles - 1) / p.least_tiles));
+    shares.split(total, static_cast<int>(gridDim.x), p.least_tiles);
     if (cta < shares.ctas) {
       int64_t rest = shares.begin(cta) - before;
       if (rest >= 0 && rest < mine) {
-        for (int n = n0; n < n1; ++n) {
-          const int64_t units = p.Hk * Plan::head_units(p, Plan::request(p, n));
-          if (rest < units) {
-            sh.start_request = n;
-            sh.start_rest = rest;
-            break;
+        int n = n1 - 1;
+        if (n > n0) {  // several requests: which
+          for (n = n0; n < n1; ++n) {
+            r = Plan::request(p, n);
+            const int64_t units = p.Hk * Plan::head_units(p, r);
+            if (rest < units) break;
+            rest -= units;
           }
-          rest -= units;
         }
+        sh.start = r;
+        sh.start_request = n;
+        sh.start_rest = rest;
       }
     }
     __syncthreads();
@@ -429,97 +498,62 @@ __global__ void __launch_bounds__(AtShape<HD, WIDE>::kThreads, AtShape<HD, WIDE>
     bool ok = true;
     int g = 0, segs = 0;  // tiles and segments so far
     auto wait = [&](uint64_t *bar, uint32_t parity) {
-      ok = ok && __all_sync(0xFFFFFFFFu, wait_bounded(bar, parity, abort_flag, p.status));
+      ok = ok && __all_sync(0xFFFFFFFFu, at_wait(bar, parity, abort_flag));
       return ok;
     };
-    // A segment's K or V tiles, through its pages: a lane each, 32 at a time.
-    const int box_rows = min(1 << p.page_shift, TOK);
-    auto load_tiles = [&](const AtSeg &s, bool is_v) {
-      const int64_t table = static_cast<int64_t>(s.request) * p.table_stride;
+    if (warp <= SOFTMAX + 1) {
+      // ------------------------------- segments and K (one warp), V (the other)
+      const bool is_v = warp != SOFTMAX;
       const int stages = is_v ? Sh::kV : Sh::kK;
       uint64_t *full = is_v ? sh.v_full : sh.k_full, *empty = is_v ? sh.v_empty : sh.k_empty;
       const uint32_t ring = smem_u32(is_v ? v_ring : k_ring);
       const CUtensorMap *map = is_v ? &v_map : &k_map;
-      int base = -1, ids = -1;
-      uint32_t good = 0u;  // of these pages, the ones that there are
-      for (int t = s.t0; t < s.t1; ++t, ++g) {
-        const int token = t * TOK, page0 = token >> p.page_shift;
-        if (base != (page0 & ~31)) {
-          base = page0 & ~31;
-          const int k = base + lane;
-          ids = k < p.max_pages ? p.block_table[table + k] : -1;
-          good = __ballot_sync(0xFFFFFFFFu, ids >= 0 && ids < p.num_pages);
-        }
-        const int stage = g % stages;
-        if (!wait(&empty[stage], ((g / stages) & 1) ^ 1u)) return;
-        const int boxes = (min(TOK, s.end - token) + box_rows - 1) / box_rows;
-        const uint32_t here = (good >> (page0 & 31)) & ((1u << boxes) - 1u);
-        if (!is_v) {
-          uint64_t valid[WORDS];
-#pragma unroll
-          for (int w = 0; w < WORDS; ++w) {
-            valid[w] = low_bits(s.end - token - 64 * w);
-            if (here != (1u << boxes) - 1u)
-              for (int k = 0; k < boxes; ++k)
-                if ((here >> k & 1u) == 0u)
-                  valid[w] &= ~(low_bits((k + 1) * box_rows - 64 * w) & ~low_bits(k * box_rows - 64 * w));
-          }
-          if (one) {
-#pragma unroll
-            for (int w = 0; w < WORDS; ++w) sh.valid[g % AT_INFOS][w] = valid[w];
-            mbar_arrive(&sh.info_full[g % AT_INFOS]);
-            if (here != (1u << boxes) - 1u) raise_status(p.status, DSPARK_DEV_PAGE_OOR);
-          }
-        }
-        if (one)
-          mbar_arrive_expect_tx(&full[stage], __popc(here) * Sh::kBoxes * box_rows * 128);
-        __syncwarp();
-        uint32_t dst = ring + stage * Sh::kTile;
-        const int offset = token & ((1 << p.page_shift) - 1);
-#pragma unroll 1
-        for (int k = 0; k < boxes; ++k, dst += box_rows * 128) {
-          const int id = __shfl_sync(0xFFFFFFFFu, ids, (page0 + k) & 31);
-          const uint32_t go = here >> k & 1u ? one : 0u;
-#pragma unroll
-          for (int c = 0; c < Sh::kBoxes; ++c)
-            tma_load_page(go, dst + c * Sh::kBox, map, &full[stage], c * 64, s.head, offset, id);
-        }
-      }
-    };
-
-    if (warp == SOFTMAX) {
-      // ---------------------------------------------- segments, and their K
+      const int box_rows = min(1 << p.page_shift, TOK);
+      // where this CTA's run has got to: request n (r), head h, block b, `rest` units in
       AtMeta meta = {};
-      auto place = [&](const AtSeg &s) {
-        const int i = segs % AT_SEGS;
-        if (!wait(&sh.seg_empty[i], ((segs / AT_SEGS) & 1) ^ 1u)) return;
-        if (one) {
-          sh.seg[i] = s;
-          mbar_arrive(&sh.seg_full[i]);
-        }
-        __syncwarp();
-        ++segs;
-      };
-      if (cta < shares.ctas) {
-        const int64_t end_unit = shares.begin(cta + 1);
-        int64_t unit = shares.begin(cta);
-        int n = sh.start_request;
-        int64_t rest = sh.start_rest;
-        for (; ok && unit < end_unit && n < p.N; ++n, rest = 0) {
-          const AtRequest r = Plan::request(p, n);
-          const int64_t a_head = Plan::head_units(p, r);
-          if (a_head == 0) continue;
-          // the items before the first one of this run
-          int h = static_cast<int>(rest / a_head), b = 0;
-          rest -= h * a_head;
-          for (; b < r.blocks; ++b) {
-            const int units = Sh::kItem + Plan::tiles(Plan::end(p, r, b));
-            if (rest < units) break;
-            rest -= units;
-          }
-          for (; ok && h < p.Hk && unit < end_unit; ++h, b = 0) {
-            for (; ok && b < r.blocks && unit < end_unit; ++b) {
-              AtSeg s;
+      AtRequest r = sh.start;
+      const int64_t end_unit = cta < shares.ctas ? shares.begin(cta + 1) : 0;
+      int64_t unit = cta < shares.ctas ? shares.begin(cta) : 0, rest = sh.start_rest;
+      int n = sh.start_request, h = 0, b = 0;
+      if (!is_v && unit < end_unit) {
+        const int64_t a_head = Plan::head_units(p, r);
+        h = static_cast<int>(rest / a_head);
+        rest -= h * a_head;
+      }
+      uint32_t stage = 0, turn = 0;  // of the ring
+      while (ok) {
+        const int si = segs % AT_SEGS;
+        AtSeg s;
+        if (is_v) {
+          if (!wait(&sh.seg_full[si], (segs / AT_SEGS) & 1)) break;
+          s = sh.seg[si];
+          __syncwarp();
+          if (one) mbar_arrive(&sh.seg_empty[si]);
+        } else {
+          s.request = -1;
+          while (unit < end_unit) {
+            if (b >= r.blocks) {
+              b = 0;
+              if (++h >= p.Hk) {
+                h = 0;
+                if (++n >= p.N) break;
+                r = Plan::request(p, n);
+              }
+              continue;
+            }
+            const int end = Plan::end(p, r, b), tiles = Plan::tiles(end);
+            if (rest >= Sh::kItem + tiles) {  // before this run
+              rest -= Sh::kItem + tiles;
+              ++b;
+              continue;
+            }
+            const int64_t stop =
+                min(static_cast<int64_t>(Sh::kItem + tiles), rest + (end_unit - unit));
+            s.t0 = static_cast<int>(max(rest - Sh::kItem, static_cast<int64_t>(0)));
+            s.t1 = static_cast<int>(max(stop - Sh::kItem, static_cast<int64_t>(0)));
+            unit += stop - rest;
+            rest = 0;
+            if (s.t1 > s.t0) {  // else this run ends before its first tile
               s.request = n;
               s.first = r.first;
               s.count = r.count;
@@ -527,50 +561,65 @@ __global__ void __launch_bounds__(AtShape<HD, WIDE>::kThreads, AtShape<HD, WIDE>
               s.head = h;
               s.block = b;
               s.tree = r.tree;
-              s.end = Plan::end(p, r, b);
-              const int tiles = Plan::tiles(s.end);
-              const int64_t stop =
-                  min(static_cast<int64_t>(Sh::kItem + tiles), rest + (end_unit - unit));
-              s.t0 = static_cast<int>(max(rest - Sh::kItem, static_cast<int64_t>(0)));
-              s.t1 = static_cast<int>(max(stop - Sh::kItem, static_cast<int64_t>(0)));
-              unit += stop - rest;
-              rest = 0;
-              if (s.t1 == s.t0) continue;  // this run ends before its first tile
+              s.end = end;
               s.part = -1;
               if (s.t0 > 0) {
                 s.part = 2 * cta;
               } else if (s.t1 < tiles) {
                 s.part = 2 * cta + 1;
-                const int64_t last_unit = unit + (tiles - s.t1) - 1;
-                int c = static_cast<int>(last_unit * shares.ctas / shares.units);
-                while (c + 1 < shares.ctas && shares.begin(c + 1) <= last_unit) ++c;
-                while (shares.begin(c) > last_unit) --c;
-                meta = {c, n, s.first, s.count, h, b};
+                meta = {shares.holder(unit + (tiles - s.t1) - 1), n, s.first, s.count, h, b};
               }
-              place(s);
-              if (ok) load_tiles(s, false);
             }
+            ++b;
+            if (s.request >= 0) break;
+          }
+          if (!wait(&sh.seg_empty[si], ((segs / AT_SEGS) & 1) ^ 1u)) break;
+          if (one) {
+            sh.seg[si] = s;
+            mbar_arrive(&sh.seg_full[si]);
+          }
+          __syncwarp();
+        }
+        ++segs;
+        if (s.request < 0) break;
+        // the segment's tiles, through its pages: a lane each, 32 at a time
+        const int32_t *table = p.block_table + static_cast<int64_t>(s.request) * p.table_stride;
+        int base = -1, ids = -1;
+        uint32_t good = 0u;  // of these pages, the ones that there are
+#pragma unroll 1
+        for (int t = s.t0; t < s.t1; ++t) {
+          const int token = t * TOK, page0 = token >> p.page_shift;
+          if (base != (page0 & ~31)) {
+            base = page0 & ~31;
+            const int k = base + lane;
+            ids = k < p.max_pages ? table[k] : -1;
+            good = __ballot_sync(0xFFFFFFFFu, ids >= 0 && ids < p.num_pages);
+          }
+          if (!wait(&empty[stage], turn ^ 1u)) break;
+          const int boxes = (min(TOK, s.end - token) + box_rows - 1) / box_rows;
+          const uint32_t here = (good >> (page0 & 31)) & ((1u << boxes) - 1u);
+          if (!is_v && one && here != (1u << boxes) - 1u)
+            raise_status(p.status, DSPARK_DEV_PAGE_OOR);
+          if (one)
+            mbar_arrive_expect_tx(&full[stage], __popc(here) * Sh::kBoxes * box_rows * 128);
+          __syncwarp();
+          uint32_t dst = ring + stage * Sh::kTile;
+          const int offset = token & ((1 << p.page_shift) - 1);
+#pragma unroll 1
+          for (int k = 0; k < boxes; ++k, dst += box_rows * 128) {
+            const int id = __shfl_sync(0xFFFFFFFFu, ids, (page0 + k) & 31);
+            const uint32_t go = here >> k & 1u ? one : 0u;
+#pragma unroll
+            for (int c = 0; c < Sh::kBoxes; ++c)
+              tma_load_page(go, dst + c * Sh::kBox, map, &full[stage], c * 64, s.head, offset, id);
+          }
+          if (++stage == static_cast<uint32_t>(stages)) {
+            stage = 0;
+            turn ^= 1u;
           }
         }
       }
-      if (ok) {
-        AtSeg s = {};
-        s.request = -1;
-        place(s);
-      }
-      if (one) p.parts.meta[cta] = meta;
-    } else if (warp == SOFTMAX + 1) {
-      // ------------------------------------------------------------------ V
-      while (ok) {
-        const int si = segs % AT_SEGS;
-        if (!wait(&sh.seg_full[si], (segs / AT_SEGS) & 1)) break;
-        const AtSeg s = sh.seg[si];
-        __syncwarp();
-        if (one) mbar_arrive(&sh.seg_empty[si]);
-        if (s.request < 0) break;
-        ++segs;
-        load_tiles(s, true);
-      }
+      if (!is_v && one) p.parts.meta[cta] = meta;
     } else if (warp == SOFTMAX + 2) {
       // ----------------------------------------------------------- products
       const uint32_t q_lo = at_desc_k(smem_u32(smem));
@@ -614,31 +663,34 @@ __global__ void __launch_bounds__(AtShape<HD, WIDE>::kThreads, AtShape<HD, WIDE>
         auto value = [&](int r, int i) {
           const int gt = g + i, buf = WIDE ? r : gt & 1;
           const uint32_t turn = WIDE ? turns[r] + i : gt >> 1;
-          if (!arrived(&sh.p_full[buf], turn & 1)) return;
           const int stage = gt % Sh::kV;
           if (r == 0 && !arrived(&sh.v_full[stage], (gt / Sh::kV) & 1)) return;
           const uint32_t b = at_desc_mn(v0 + stage * Sh::kTile, Sh::kBox);
 #pragma unroll
-          for (int kk = 0; kk < TOK / 16; ++kk)
-            umma_ts(one, tmem + Sh::kO + r * HD, tmem + buf * TOK + kk * 8, b + kk * 128,
-                    kAtDescHi, idesc_o, i | kk);
+          for (int w = 0; w < WORDS; ++w) {
+            if (!arrived(&sh.p_full[buf][w], turn & 1)) return;
+#pragma unroll
+            for (int kk = 4 * w; kk < 4 * w + 4; ++kk)
+              umma_ts(one, tmem + Sh::kO + r * HD, tmem + buf * TOK + kk * 8, b + kk * 128,
+                      kAtDescHi, idesc_o, i | kk);
+          }
           if (r == blocks - 1) umma_commit_one(one, &sh.v_empty[stage]);
           umma_commit_one(one, &sh.pv_done[buf]);
         };
-        if constexpr (WIDE) {
-          for (int r = 0; ok && r < blocks; ++r) score(r, 0);
-          for (int i = 0; ok && i < T; ++i)
-            for (int r = 0; ok && r < blocks; ++r) {
-              value(r, i);
-              if (ok && i + 1 < T) score(r, i + 1);
-            }
-          for (int r = 0; r < blocks; ++r) turns[r] += T;
-        } else {
-          score(0, 0);
-          for (int i = 0; ok && i < T; ++i) {
-            if (i + 1 < T) score(0, i + 1);
-            if (ok) value(0, i);
+        // wide: P V and the next S of one block, then of the other; narrow: the next S
+        // before P V
+#pragma unroll 1
+        for (int i = -1; ok && i < T; ++i) {
+#pragma unroll 1
+          for (int r = 0; ok && r < blocks; ++r) {
+            if (WIDE && i >= 0) value(r, i);
+            if (ok && i + 1 < T) score(r, i + 1);
+            if (!WIDE && ok && i >= 0) value(r, i);
           }
+        }
+        if (WIDE) {
+          turns[0] += T;
+          if (blocks == 2) turns[1] += T;
         }
         g += T;
       }
@@ -658,111 +710,147 @@ __global__ void __launch_bounds__(AtShape<HD, WIDE>::kThreads, AtShape<HD, WIDE>
     const int row = warp * 32 + lane;
     const float c = p.scale_log2;
     const uint64_t c2 = pair_f32(__float_as_uint(c), __float_as_uint(c));
-    bool ok = true;
+    const int box_shift = min(p.page_shift, WIDE ? 7 : 6);  // pages, or tiles within one
+    bool ok = true, have = false;
     int g = 0, turn = 0, segs = 0, scans = 0;  // tiles, this block's, segments
     auto wait = [&](uint64_t *bar, uint32_t parity) {
-      ok = ok && __all_sync(0xFFFFFFFFu, wait_bounded(bar, parity, abort_flag, p.status));
+      ok = ok && __all_sync(0xFFFFFFFFu, at_wait(bar, parity, abort_flag));
       return ok;
     };
-    // The next segment, and its Q on the way to shared memory: each thread its row.
-    AtSeg next;
-    auto fetch = [&] {
-      const int si = segs % AT_SEGS;
-      if (!wait(&sh.seg_full[si], (segs / AT_SEGS) & 1)) return;
-      next = sh.seg[si];
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&sh.seg_empty[si]);
-      ++segs;
-      const int m = next.block * Sh::kRows + row, j = m / p.group;
-      if (next.request >= 0 && j < next.count) {
-        const int head = next.head * p.group + (m - j * p.group);
-        const __nv_bfloat16 *src = static_cast<const __nv_bfloat16 *>(p.q.p) +
-                                   (next.first + j) * p.q.stride + head * p.q.head_stride;
-        const uint32_t dst = smem_u32(smem) + block * Sh::kQ + (row & (AT_ROWS - 1)) * 128;
-#pragma unroll 4
-        for (int e = 0; e < HD / 8; ++e) {
-          const uint32_t at = dst + (e / 8) * (AT_ROWS * 128) + (((e & 7) ^ (row & 7)) << 4);
-          if (e * 8 < p.d) cp_async_16(at, src + e * 8);
-          else st_shared_zero16(at);
-        }
-      }
-    };
-    fetch();
-    while (ok) {
-      const AtSeg s = next;
-      if (s.request < 0) break;
-      const int T = s.t1 - s.t0;
-      const int m = s.block * Sh::kRows + row, j = m / p.group;
-      const int head = s.head * p.group + (m - j * p.group);
-      const bool mine = j < s.count;
-      const bool any = __any_sync(0xFFFFFFFFu, mine);
-      const int64_t q_row = s.first + j;
-      // ---- Q, on its way since the segment before
-      cp_async_wait_all();
-      fence_proxy_async_smem();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&sh.q_full);
+    AtSeg s = {};
+    while (true) {
+      // ---- tokens of segment s
+      const int T = s.t1 - s.t0, m = s.block * Sh::kRows + row, j = at_token(p, m);
+      const bool mine = have && j < s.count;
       // the second block may have no rows; the products leave it out too
-      if (WIDE && block == 1 && s.count * p.group - s.block * Sh::kRows <= AT_ROWS) {
-        g += T;
-        if (s.t1 * TOK > s.ctx + (s.tree ? 0 : s.block * Sh::kRows / p.group + 1)) ++scans;
-        fetch();
-        continue;
-      }
-
-      // ---- tokens
+      const bool active =
+          have && !(block == 1 && s.count * p.group - s.block * Sh::kRows <= AT_ROWS);
+      const bool any = __any_sync(0xFFFFFFFFu, mine);
       const uint64_t bits =
-          s.tree && mine ? tree_bits(p.tree, p.tree_width, s.request, j, s.count) : 0ull;
+          mine && s.tree ? tree_bits(p.tree, p.tree_width, s.request, j, s.count) : 0ull;
       const int upto = s.ctx + j + 1;
       // before this token every row attends every token
-      const int common = s.ctx + (s.tree ? 0 : s.block * Sh::kRows / p.group + 1);
-      uint32_t(&poison)[4][3] = sh.poison[segs & 1];  // segs is one ahead for all warps
-      if (block == 0 && lane < 3) poison[warp][lane] = 0u;
-      __syncwarp();
-      const bool scans_here = s.t1 * TOK > common;
+      const int common = s.ctx + (s.tree ? 0 : at_token(p, s.block * Sh::kRows) + 1);
+      const bool scans_here = have && s.t1 * TOK > common;
+      uint32_t(&poison)[4][3] = sh.poison[segs & 1];
       float top = -INFINITY, sum = 0.0f;
-      for (int i = 0; i < T; ++i) {
-        const int gt = g + i, token = (s.t0 + i) * TOK;
-        const int buf = WIDE ? block : gt & 1;
-        const uint32_t phase = WIDE ? turn & 1 : (gt >> 1) & 1;
-        ++turn;
-        if (!wait(&sh.info_full[gt % AT_INFOS], (gt / AT_INFOS) & 1)) break;
-        uint64_t valid[WORDS];
-        bool whole = true;
+      if (active) {
+        if (block == 0 && lane < 3) poison[warp][lane] = 0u;
+        __syncwarp();
+        const int32_t *table = p.block_table + static_cast<int64_t>(s.request) * p.table_stride;
+        int base_page = -1;
+        uint32_t good = 0u;  // of 32 pages, the ones that there are
+#pragma unroll 1
+        for (int i = 0; i < T; ++i) {
+          const int gt = g + i, token = (s.t0 + i) * TOK;
+          const int buf = WIDE ? block : gt & 1;
+          const uint32_t phase = WIDE ? turn & 1 : (gt >> 1) & 1;
+          ++turn;
+          const int page0 = token >> p.page_shift;
+          if (base_page != (page0 & ~31)) {
+            base_page = page0 & ~31;
+            const int id = base_page + lane < p.max_pages ? table[base_page + lane] : -1;
+            good = __ballot_sync(0xFFFFFFFFu, id >= 0 && id < p.num_pages);
+          }
+          const uint32_t all = (1u << (TOK >> box_shift)) - 1u;
+          const uint32_t here = good >> (page0 & 31);
+          const bool whole = (here & all) == all && token + TOK <= s.end;
+          const bool inner = token + TOK <= common;
+          // of 32 tokens from the tile's 32 k on, the ones that there are
+          auto there = [&](int k) {
+            const uint32_t lo = here >> (32 * k >> box_shift) & 1u ? 0xFFFFu : 0u;
+            const uint32_t hi = here >> ((32 * k + 16) >> box_shift) & 1u ? 0xFFFF0000u : 0u;
+            return (lo | hi) & static_cast<uint32_t>(low_bits(s.end - token - 32 * k));
+          };
+          // Values of tokens that are not there are 0, and those that are not finite
+          // where not every row attends them: 0 times them would be NaN.
+          if (block == 0 && (!whole || !inner)) {
+            const int stage = gt % Sh::kV;
+            if (!wait(&sh.v_full[stage], (gt / Sh::kV) & 1)) break;
+            constexpr int MINE = TOK / 4;  // tokens of a warp
+            constexpr uint32_t ALL = MINE == 32 ? 0xFFFFFFFFu : (1u << (MINE & 31)) - 1u;
+            const uint32_t mine_there =
+                (MINE == 32 ? there(warp) : there(warp >> 1) >> (16 * (warp & 1))) & ALL;
+            const uint32_t v = smem_u32(v_ring + stage * Sh::kTile) + warp * MINE * 128;
+            // k: a row, then 16 bytes of it
+            auto chunk = [&](int k) {
+              const int r = k / (HD / 8), e = k % (HD / 8);
+              return v + (e / 8) * Sh::kBox + r * 128 + ((e & 7) << 4);
+            };
+            uint32_t bad = 0u;
+            if (mine_there != ALL) {
+#pragma unroll 1
+              for (int k = lane; k < MINE * (HD / 8); k += 32)
+                if ((mine_there >> (k / (HD / 8)) & 1u) == 0u) st_shared_zero16(chunk(k));
+              __syncwarp();
+            }
+            if (!inner) {
+              // 0 times a number is 0, 0 times anything else is NaN
+              const __nv_bfloat162 zero = __float2bfloat162_rn(0.0f);
+              __nv_bfloat162 none = zero;
+#pragma unroll 4
+              for (int k = lane; k < MINE * (HD / 8); k += 32) {
+                const uint4 w = ld_shared_v4(chunk(k));
+                const uint32_t *u = &w.x;
 #pragma unroll
-        for (int w = 0; w < WORDS; ++w) {
-          valid[w] = sh.valid[gt % AT_INFOS][w];
-          whole = whole && valid[w] == ~0ull;
-        }
-        const bool inner = token + TOK <= common;
-        if (!wait(&sh.s_full[buf], phase)) break;
-        tc_fence_after();
-        if (any) {
-          uint32_t x[TOK / 32][32];
+                for (int q = 0; q < 4; ++q)
+                  none = __hfma2(*reinterpret_cast<const __nv_bfloat162 *>(u + q), zero, none);
+              }
+              if (__any_sync(0xFFFFFFFFu, __hisnan(none.x) || __hisnan(none.y))) {
+#pragma unroll 1
+                for (int k = lane; k < 4 * MINE * (HD / 8); k += 32) {  // two at a time
+                  const uint32_t at = chunk(k >> 2) + (k & 3) * 4;
+                  const uint32_t w = ld_shared_u32(at);
+                  const uint32_t keep = ((w & 0x7F80u) == 0x7F80u ? 0u : 0xFFFFu) |
+                                        ((w & 0x7F800000u) == 0x7F800000u ? 0u : 0xFFFF0000u);
+                  if (keep != 0xFFFFFFFFu) {
+                    st_shared_u32(at, w & keep);
+                    bad |= 1u << ((k >> 2) / (HD / 8));
+                  }
+                }
+              }
+              bad = __reduce_or_sync(0xFFFFFFFFu, bad);
+              if (lane == 0) poison[warp][s.t0 + i - common / TOK] = bad;
+            }
+            fence_proxy_async_smem();
+          }
+          if (!wait(&sh.s_full[buf], phase)) break;
+          tc_fence_after();
+          if (!any) {
+            __syncwarp();
+            if (lane < WORDS) mbar_arrive(&sh.p_full[buf][lane]);
+            continue;
+          }
           const uint32_t s_tmem = tmem + lanes + buf * TOK;
+          if (!inner || !whole) {
+            // scores of what a row does not attend: -inf
+#pragma unroll 1
+            for (int k = 0; k < TOK / 32; ++k) {
+              const uint32_t seen =
+                  static_cast<uint32_t>(at_seen(s, bits, upto, token + 32 * k)) & there(k);
+              uint32_t x[32];
+              tmem_ld_32x32b_x32(s_tmem + 32 * k, x);
+              tmem_ld_wait(x);
+#pragma unroll
+              for (int e = 0; e < 32; ++e) x[e] = (seen >> e & 1u) ? x[e] : 0xFF800000u;
+              tmem_st_32x32b_x32(s_tmem + 32 * k, x);
+            }
+            tmem_st_wait();
+          }
+          uint32_t x[TOK / 32][32];
 #pragma unroll
           for (int k = 0; k < TOK / 32; ++k) tmem_ld_32x32b_x32(s_tmem + 32 * k, x[k]);
 #pragma unroll
           for (int k = 0; k < TOK / 32; ++k) tmem_ld_wait(x[k]);
-          if (!inner || !whole) {
-#pragma unroll
-            for (int w = 0; w < WORDS; ++w) {
-              const uint64_t seen = at_seen(s, bits, upto, token + 64 * w) & valid[w];
-#pragma unroll
-              for (int k = 0; k < 2; ++k) {
-                const uint32_t half = static_cast<uint32_t>(seen >> (32 * k));
-#pragma unroll
-                for (int e = 0; e < 32; ++e)
-                  x[2 * w + k][e] = (half >> e & 1u) ? x[2 * w + k][e] : 0xFF800000u;
-              }
-            }
-          }
           float highs[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
           for (int k = 0; k < TOK / 32; ++k)
 #pragma unroll
-            for (int e = 0; e < 32; ++e)
-              highs[e & 3] = fmaxf(highs[e & 3], __uint_as_float(x[k][e]));
+            for (int e = 0; e < 32; e += 8)
+#pragma unroll
+              for (int q = 0; q < 4; ++q)  // three operands at a time
+                highs[q] = fmaxf(fmaxf(highs[q], __uint_as_float(x[k][e + q])),
+                                 __uint_as_float(x[k][e + 4 + q]));
           const float high = fmaxf(fmaxf(highs[0], highs[1]), fmaxf(highs[2], highs[3]));
           const bool grow =
               mine && ((high - top) * c > kRescale || (top == -INFINITY && high > top));
@@ -779,13 +867,13 @@ __global__ void __launch_bounds__(AtShape<HD, WIDE>::kThreads, AtShape<HD, WIDE>
               if (!WIDE && !wait(&sh.pv_done[(gt - 1) & 1], ((gt - 1) >> 1) & 1)) break;
               tc_fence_after();
 #pragma unroll 1
-              for (int at = 0; at < HD; at += 32) {
-                uint32_t o[32];
-                tmem_ld_32x32b_x32(o_tmem + at, o);
+              for (int at = 0; at < HD; at += 16) {
+                uint32_t o[16];
+                tmem_ld_32x32b_x16(o_tmem + at, o);
                 tmem_ld_wait(o);
 #pragma unroll
-                for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * by);
-                tmem_st_32x32b_x32(o_tmem + at, o);
+                for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * by);
+                tmem_st_32x32b_x16(o_tmem + at, o);
               }
               tmem_st_wait();
             }
@@ -805,7 +893,7 @@ __global__ void __launch_bounds__(AtShape<HD, WIDE>::kThreads, AtShape<HD, WIDE>
           const uint64_t base2 = pair_f32(__float_as_uint(-base), __float_as_uint(-base));
           uint64_t sums[2] = {0ull, 0ull};
 #pragma unroll
-          for (int k = 0; k < TOK / 64; ++k) {
+          for (int k = 0; k < WORDS; ++k) {
             uint32_t pk[32];
 #pragma unroll
             for (int e = 0; e < 32; ++e) {
@@ -815,138 +903,157 @@ __global__ void __launch_bounds__(AtShape<HD, WIDE>::kThreads, AtShape<HD, WIDE>
                          hi);
               lo = exp2_approx(lo);
               hi = exp2_approx(hi);
-              sums[e & 1] = pair_add(sums[e & 1], pair_f32(__float_as_uint(lo), __float_as_uint(hi)));
+              sums[e & 1] =
+                  pair_add(sums[e & 1], pair_f32(__float_as_uint(lo), __float_as_uint(hi)));
               asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(pk[e]) : "f"(hi), "f"(lo));
             }
             tmem_st_32x32b_x32(s_tmem + 32 * k, pk);
+            tmem_st_wait();
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&sh.p_full[buf][k]);
           }
           float lo, hi;
           unpair_f32(pair_add(sums[0], sums[1]), lo, hi);
           sum += lo + hi;
-          tmem_st_wait();
-          tc_fence_before();
         }
-        // ---- values of tokens that are not there are 0, and those that are not
-        // finite where not every row attends them: 0 times them would be NaN
-        if (block == 0 && (!whole || !inner)) {
-          const int stage = gt % Sh::kV;
-          if (!wait(&sh.v_full[stage], (gt / Sh::kV) & 1)) break;
-          const uint32_t v = smem_u32(v_ring + stage * Sh::kTile);
-          constexpr int MINE = TOK / 4;  // tokens of a warp
-          const uint32_t there =
-              static_cast<uint32_t>(valid[warp * MINE / 64] >> (warp * MINE % 64));
-          uint32_t bad = 0u;
-          for (int k = lane; k < MINE * (HD / 8); k += 32) {
-            const int r = k / (HD / 8), e = k - r * (HD / 8), tr = warp * MINE + r;
-            const uint32_t at = v + (e / 8) * Sh::kBox + tr * 128 + ((e & 7) << 4);
-            if ((there >> r & 1u) == 0u) {
-              st_shared_zero16(at);
-            } else if (!inner) {
-              uint4 w = ld_shared_v4(at);
-              uint32_t *u = &w.x;
-              bool found = false;
-#pragma unroll
-              for (int q = 0; q < 4; ++q) {
-                if ((u[q] & 0x7F80u) == 0x7F80u) {
-                  u[q] &= 0xFFFF0000u;
-                  found = true;
-                }
-                if ((u[q] & 0x7F800000u) == 0x7F800000u) {
-                  u[q] &= 0xFFFFu;
-                  found = true;
-                }
-              }
-              if (found) {
-                st_shared_v4(at, w);
-                bad |= 1u << r;
-              }
-            }
-          }
-          bad = __reduce_or_sync(0xFFFFFFFFu, bad);
-          if (!inner && lane == 0) poison[warp][s.t0 + i - common / TOK] = bad;
-          fence_proxy_async_smem();
-        }
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&sh.p_full[buf]);
+        if (!ok) break;
       }
-      if (!ok) break;
       g += T;
-      fetch();  // the last scores are there, so Q has been read
-      if (!ok) break;
-      if (scans_here) {
+      // ---- the next segment, and its Q on the way to shared memory (the last scores of
+      // this one are there, so its own has been read): a warp its 32 rows, row after row,
+      // so that neighbouring lanes read neighbouring bytes
+      AtSeg next;
+      {
+        const int si = segs % AT_SEGS;
+        if (!wait(&sh.seg_full[si], (segs / AT_SEGS) & 1)) break;
+        next = sh.seg[si];
         __syncwarp();
-        if (block == 0 && lane == 0) mbar_arrive(&sh.scanned);
-        if (!wait(&sh.scanned, scans & 1)) break;
+        if (lane == 0) mbar_arrive(&sh.seg_empty[si]);
+        ++segs;
+        const int nm = next.block * Sh::kRows + row, nj = at_token(p, nm);
+        const __nv_bfloat16 *src = nullptr;
+        if (next.request >= 0 && nj < next.count)
+          src = static_cast<const __nv_bfloat16 *>(p.q.p) + (next.first + nj) * p.q.stride +
+                (next.head * p.group + nm - nj * p.group) * p.q.head_stride;
+        const uint32_t dst = smem_u32(smem) + block * Sh::kQ + (warp & 3) * 32 * 128;
+        constexpr int CHUNKS = HD / 8;  // of 16 bytes, a row
+#pragma unroll 2
+        for (int k = lane; k < 32 * CHUNKS; k += 32) {
+          const int r = k / CHUNKS, e = k % CHUNKS;
+          const __nv_bfloat16 *from = reinterpret_cast<const __nv_bfloat16 *>(
+              __shfl_sync(0xFFFFFFFFu, reinterpret_cast<uint64_t>(src), r));
+          const uint32_t at =
+              dst + (e / 8) * (AT_ROWS * 128) + r * 128 + (((e & 7) ^ (r & 7)) << 4);
+          if (from != nullptr) {
+            if (e * 8 < p.d) cp_async_16(at, from + e * 8);
+            else st_shared_zero16(at);
+          }
+        }
+      }
+      // ---- this segment's rows, or what is to be joined
+      if (scans_here) {
+        if (active) {
+          if (block == 0 && lane == 0) mbar_arrive(&sh.scanned);
+          if (!wait(&sh.scanned, scans & 1)) break;
+        }
         ++scans;
       }
-      // ---- the item's rows, or what is to be joined
-      const int buf = WIDE ? block : (g - 1) & 1;
-      if (!wait(&sh.pv_done[buf], WIDE ? (turn - 1) & 1 : ((g - 1) >> 1) & 1)) break;
-      tc_fence_after();
-      // the tokens with values that are not finite that this row attends: by warp and
-      // tile, as they were found
-      uint32_t hit = 0u;
-      if (scans_here && mine) {
-        for (int k = 0; k < 12; ++k) {
-          if (poison[k / 3][k % 3] == 0u) continue;
-          const int token = (common / TOK + k % 3) * TOK + k / 3 * (TOK / 4);
-          if ((poison[k / 3][k % 3] & static_cast<uint32_t>(at_seen(s, bits, upto, token))) != 0u)
-            hit |= 1u << k;
-        }
+      if (active) {
+        const int buf = WIDE ? block : (g - 1) & 1;
+        if (!wait(&sh.pv_done[buf], WIDE ? (turn - 1) & 1 : ((g - 1) >> 1) & 1)) break;
+        tc_fence_after();
       }
-      if (any) {
+      if (active && any) {
+        const int head = s.head * p.group + (m - j * p.group);
+        const int64_t q_row = s.first + j;
+        // the tokens with values that are not finite that this row attends: by warp and
+        // tile, as they were found
+        uint32_t hit = 0u;
+        auto found = [&](int k) {
+          const int token = (common / TOK + k % 3) * TOK + k / 3 * (TOK / 4);
+          return poison[k / 3][k % 3] & static_cast<uint32_t>(at_seen(s, bits, upto, token));
+        };
+        if (scans_here && mine) {
+#pragma unroll 1
+          for (int k = 0; k < 12; ++k)
+            if (found(k) != 0u) hit |= 1u << k;
+        }
+        if (__any_sync(0xFFFFFFFFu, hit != 0u)) {
+#pragma unroll 1
+          for (int at = 0; at < p.d; ++at) {
+            float f = 0.0f;
+            for (uint32_t left = hit; left != 0u; left &= left - 1u) {
+              const int k = __ffs(left) - 1;
+              for (uint32_t tokens = found(k); tokens != 0u; tokens &= tokens - 1u) {
+                const int token =
+                    (common / TOK + k % 3) * TOK + k / 3 * (TOK / 4) + __ffs(tokens) - 1;
+                const int id =
+                    p.block_table[s.request * p.table_stride + (token >> p.page_shift)];
+                const float v = __bfloat162float(
+                    p.v_cache[id * p.page_stride +
+                              (token & ((1 << p.page_shift) - 1)) * p.token_stride +
+                              s.head * p.head_stride + at]);
+                if (!(fabsf(v) < INFINITY)) f += v;
+              }
+            }
+            __syncwarp();
+            tmem_add(o_tmem + at, f);
+          }
+        }
         const float by = sum == 0.0f ? 0.0f : 1.0f / sum;
+        // where this lane's four rows go: 0 for none
+        uint64_t rows_out[4];
+        {
+          const uint64_t mine_out =
+              mine ? reinterpret_cast<uint64_t>(static_cast<__nv_bfloat16 *>(p.out.p) +
+                                                q_row * p.out.stride + head * p.out.head_stride)
+                   : 0ull;
+#pragma unroll
+          for (int q = 0; q < 4; ++q)
+            rows_out[q] = __shfl_sync(0xFFFFFFFFu, mine_out, (lane & ~3) + q);
+        }
 #pragma unroll 1
         for (int at = 0; at < HD; at += 32) {
           uint32_t o[32];
           tmem_ld_32x32b_x32(o_tmem + at, o);
           tmem_ld_wait(o);
-          if (mine && at < p.d) {
-            for (uint32_t left = hit; left != 0u; left &= left - 1u) {
-              const int k = __ffs(left) - 1;
-              const int first = (common / TOK + k % 3) * TOK + k / 3 * (TOK / 4);
-              uint32_t tokens = poison[k / 3][k % 3] &
-                                static_cast<uint32_t>(at_seen(s, bits, upto, first));
-              for (; tokens != 0u; tokens &= tokens - 1u) {
-                const int token = first + __ffs(tokens) - 1;
-                const int id = p.block_table[s.request * p.table_stride + (token >> p.page_shift)];
-                const __nv_bfloat16 *v =
-                    p.v_cache + id * p.page_stride +
-                    (token & ((1 << p.page_shift) - 1)) * p.token_stride +
-                    s.head * p.head_stride + at;
+          if (s.part < 0) {
+            // Four lanes exchange their 16-byte pieces, so that each stores one of every
+            // row: 64 neighbouring bytes a row and store instead of 16.
+            uint32_t w[4][4];
 #pragma unroll
-                for (int e = 0; e < 32; ++e) {
-                  if (at + e < p.d) {
-                    const float f = __bfloat162float(v[e]);
-                    if (!(fabsf(f) < INFINITY))
-                      o[e] = __float_as_uint(__uint_as_float(o[e]) + f);
-                  }
+            for (int q = 0; q < 16; ++q)
+              asm("cvt.rn.bf16x2.f32 %0, %1, %2;"
+                  : "=r"(w[q >> 2][q & 3])
+                  : "f"(__uint_as_float(o[2 * q + 1]) * by), "f"(__uint_as_float(o[2 * q]) * by));
+#pragma unroll
+            for (int step = 1; step <= 2; step *= 2) {
+              const bool upper = (lane & step) != 0;
+#pragma unroll
+              for (int q = 0; q < 4; ++q) {
+                if ((q & step) != 0) continue;
+#pragma unroll
+                for (int u = 0; u < 4; ++u) {
+                  const uint32_t got =
+                      __shfl_xor_sync(0xFFFFFFFFu, upper ? w[q][u] : w[q + step][u], step);
+                  if (upper) w[q][u] = got;
+                  else w[q + step][u] = got;
                 }
               }
             }
-            if (s.part < 0) {
-              __nv_bfloat16 *dst = static_cast<__nv_bfloat16 *>(p.out.p) + q_row * p.out.stride +
-                                   head * p.out.head_stride + at;
+            const int column = at + (lane & 3) * 8;
 #pragma unroll
-              for (int e = 0; e < 32; e += 8) {
-                uint4 w;
-                uint32_t *u = &w.x;
+            for (int q = 0; q < 4; ++q)
+              if (rows_out[q] != 0 && column < p.d)
+                *reinterpret_cast<uint4 *>(rows_out[q] + 2 * column) =
+                    make_uint4(w[q][0], w[q][1], w[q][2], w[q][3]);
+          } else if (mine) {
+            float4 *dst = at_part<HD>(p.parts, s.part, row, at);
 #pragma unroll
-                for (int q = 0; q < 4; ++q)
-                  asm("cvt.rn.bf16x2.f32 %0, %1, %2;"
-                      : "=r"(u[q])
-                      : "f"(__uint_as_float(o[e + 2 * q + 1]) * by),
-                        "f"(__uint_as_float(o[e + 2 * q]) * by));
-                if (at + e < p.d) *reinterpret_cast<uint4 *>(dst + e) = w;
-              }
-            } else {
-              float *dst =
-                  p.parts.o + (static_cast<int64_t>(s.part) * p.parts.rows + row) * HD + at;
-#pragma unroll
-              for (int e = 0; e < 32; e += 4)
-                *reinterpret_cast<uint4 *>(dst + e) =
-                    make_uint4(o[e], o[e + 1], o[e + 2], o[e + 3]);
-            }
+            for (int e = 0; e < 8; ++e)
+              dst[8 * e] = make_float4(__uint_as_float(o[4 * e]), __uint_as_float(o[4 * e + 1]),
+                                       __uint_as_float(o[4 * e + 2]), __uint_as_float(o[4 * e + 3]));
           }
           __syncwarp();
         }
@@ -957,6 +1064,13 @@ __global__ void __launch_bounds__(AtShape<HD, WIDE>::kThreads, AtShape<HD, WIDE>
               sum == 0.0f ? -INFINITY : at_base(top, c) * kLn2 + logf(sum);
       }
       tc_fence_before();
+      if (next.request < 0) break;
+      s = next;
+      have = true;
+      cp_async_wait_all();
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&sh.q_full);
     }
   }
   if (lane == 0 && *abort_flag) raise_status(p.status, DSPARK_DEV_TIMEOUT);
@@ -966,58 +1080,88 @@ __global__ void __launch_bounds__(AtShape<HD, WIDE>::kThreads, AtShape<HD, WIDE>
   if (warp == SOFTMAX + 2) tmem_dealloc(tmem, Sh::kTmem);
 }
 
-// Joins the pieces of the items that were cut: a warp a row.
+// Joins the pieces of the items that were cut: a CTA eight rows, a thread four columns of
+// one of them, every blockDim.y-th piece.  The pieces' maxima and sums are read once for
+// the CTA, AT_JOIN pieces at a time.
+constexpr int AT_JOIN = 64;
 template <int HD>
-__global__ void __launch_bounds__(256)
+__global__ void __launch_bounds__(HD == 64 ? 512 : 1024)
     attention_join_kernel(const AtParams p, const AtParts narrow, const AtParts wide) {
+  __shared__ float2 ml[AT_JOIN][8];      // maximum, sum
+  __shared__ float4 others[3][2 * HD];   // of the threads (., y > 0)
   wait_for_earlier_kernel();
   const bool second = static_cast<int>(blockIdx.x) >= narrow.ctas;
   const AtParts &parts = second ? wide : narrow;
   const int cta = static_cast<int>(blockIdx.x) - (second ? narrow.ctas : 0);
-  const int lane = threadIdx.x & 31, row = blockIdx.y * 8 + (threadIdx.x >> 5);
   const AtMeta meta = parts.meta[cta];
-  const int m = meta.block * (second ? 2 * AT_ROWS : AT_ROWS) + row, j = m / p.group;
-  if (meta.last == 0 || row >= parts.rows || j >= meta.count) return;
-  const int head = meta.head * p.group + (m - j * p.group);
+  const int row0 = blockIdx.y * 8, m0 = meta.block * (second ? 2 * AT_ROWS : AT_ROWS) + row0;
+  if (meta.last == 0 || row0 >= parts.rows || m0 >= meta.count * p.group) return;
+  const int row = row0 + (threadIdx.x & 7), column = (threadIdx.x >> 3) * 4;
   const int pieces = meta.last - cta + 1;
   // the first piece is in the CTA's second slot, the others in first ones
-  auto slot = [&](int k) {
-    return (static_cast<int64_t>(k == 0 ? 2 * cta + 1 : 2 * (cta + k))) * parts.rows + row;
+  auto slot = [&](int k) { return k == 0 ? 2 * cta + 1 : 2 * (cta + k); };
+  const int threads = blockDim.x * blockDim.y, thread = threadIdx.y * blockDim.x + threadIdx.x;
+  float4 acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+  float sum = 0.0f, top = -INFINITY;
+  auto add = [&](float w, const float4 &v) {
+    acc.x = fmaf(w, v.x, acc.x);
+    acc.y = fmaf(w, v.y, acc.y);
+    acc.z = fmaf(w, v.z, acc.z);
+    acc.w = fmaf(w, v.w, acc.w);
   };
-  float top = -INFINITY;
-  for (int k = lane; k < pieces; k += 32) top = fmaxf(top, parts.ml[slot(k)].x);
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, o));
-  const float above = top == -INFINITY ? 0.0f : top;
-  constexpr int E = HD / 32;
-  float acc[E] = {}, sum = 0.0f;
+  for (int k0 = 0; k0 < pieces; k0 += AT_JOIN) {
+    const int n = min(AT_JOIN, pieces - k0);
+    if (k0 > 0) __syncthreads();
+    for (int k = thread; k < 8 * n; k += threads)
+      ml[k >> 3][k & 7] =
+          parts.ml[static_cast<int64_t>(slot(k0 + (k >> 3))) * parts.rows + row0 + (k & 7)];
+    __syncthreads();
+    float high = top;
+#pragma unroll 8
+    for (int k = 0; k < n; ++k) high = fmaxf(high, ml[k][threadIdx.x & 7].x);
+    const float above = high == -INFINITY ? 0.0f : high;
+    if (k0 > 0) {
+      const float by = exp2_approx(at_difference(top, above, p.scale_log2));
+      sum *= by;
+      acc = make_float4(acc.x * by, acc.y * by, acc.z * by, acc.w * by);
+    }
+    top = high;
 #pragma unroll 4
-  for (int k = 0; k < pieces; ++k) {
-    const float2 ml = parts.ml[slot(k)];
-    const float *o = parts.o + slot(k) * HD + lane * E;
-    float2 v[E / 2];
-#pragma unroll
-    for (int e = 0; e < E / 2; ++e) v[e] = *reinterpret_cast<const float2 *>(o + 2 * e);
-    const float w = exp2_approx(at_difference(ml.x, above, p.scale_log2));
-    sum = fmaf(w, ml.y, sum);
-#pragma unroll
-    for (int e = 0; e < E; e += 2) {
-      acc[e] = fmaf(w, v[e / 2].x, acc[e]);
-      acc[e + 1] = fmaf(w, v[e / 2].y, acc[e + 1]);
+    for (int k = threadIdx.y; k < n; k += blockDim.y) {
+      const float4 v = *at_part<HD>(parts, slot(k0 + k), row, column);
+      const float2 x = ml[k][threadIdx.x & 7];
+      const float w = exp2_approx(at_difference(x.x, above, p.scale_log2));
+      sum = fmaf(w, x.y, sum);
+      add(w, v);
     }
   }
+  if (blockDim.y > 1) {
+    // each in its turn, so that the sums have one order
+    __shared__ float sums[3][2 * HD];
+    if (threadIdx.y > 0) {
+      others[threadIdx.y - 1][threadIdx.x] = acc;
+      sums[threadIdx.y - 1][threadIdx.x] = sum;
+    }
+    __syncthreads();
+    if (threadIdx.y > 0) return;
+    for (int y = 0; y < static_cast<int>(blockDim.y) - 1; ++y) {
+      add(1.0f, others[y][threadIdx.x]);
+      sum += sums[y][threadIdx.x];
+    }
+  }
+  const int m = m0 + (threadIdx.x & 7), j = m / p.group;
+  if (j >= meta.count) return;
+  const int head = meta.head * p.group + (m - j * p.group);
   const int64_t q_row = meta.first + j;
   const float by = sum == 0.0f ? 0.0f : 1.0f / sum;
-  __nv_bfloat16 *dst = static_cast<__nv_bfloat16 *>(p.out.p) + q_row * p.out.stride +
-                       head * p.out.head_stride + lane * E;
-#pragma unroll
-  for (int e = 0; e < E; e += 2)
-    if (lane * E + e < p.d) {
-      uint32_t w;
-      asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(w) : "f"(acc[e + 1] * by), "f"(acc[e] * by));
-      *reinterpret_cast<uint32_t *>(dst + e) = w;
-    }
-  if (lane == 0 && p.lse != nullptr)
+  if (column < p.d) {
+    uint2 w;
+    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(w.x) : "f"(acc.y * by), "f"(acc.x * by));
+    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(w.y) : "f"(acc.w * by), "f"(acc.z * by));
+    *reinterpret_cast<uint2 *>(static_cast<__nv_bfloat16 *>(p.out.p) + q_row * p.out.stride +
+                               head * p.out.head_stride + column) = w;
+  }
+  if (column == 0 && p.lse != nullptr)
     p.lse[q_row * (p.Hk * p.group) + head] =
         sum == 0.0f ? -INFINITY : at_base(top, p.scale_log2) * kLn2 + logf(sum);
 }
@@ -1128,6 +1272,11 @@ static dspark_status launch(const AttentionArgs &a, int dev, int sms, cudaStream
   p.Hk = a.Hk;
   p.group = a.Hq / a.Hk;
   p.d = a.d;
+  while ((1 << p.group_shift) < p.group) ++p.group_shift;
+  if (p.group > 1) {
+    --p.group_shift;
+    p.group_magic = static_cast<uint32_t>(((1ull << (32 + p.group_shift)) + p.group - 1) / p.group);
+  }
   p.page_shift = a.page_shift;
   p.num_pages = a.num_pages;
   p.max_pages = a.max_pages;
@@ -1161,8 +1310,10 @@ static dspark_status launch(const AttentionArgs &a, int dev, int sms, cudaStream
     }
   }
   const int rows = std::max(l.narrow_rows, l.wide_rows);
+  // few rows: more threads for an item's pieces
+  const int share = rows <= 16 ? (HD == 256 ? 2 : 4) : rows <= 64 && HD <= 128 ? 2 : 1;
   return launch_overlapped(attention_join_kernel<HD>,
-                           dim3(narrow.ctas + wide.ctas, (rows + 7) / 8), dim3(256), 0, stream, p,
+                           dim3(narrow.ctas + wide.ctas, rows / 8), dim3(2 * HD, share), 0, stream, p,
                            narrow, wide) == cudaSuccess
              ? DSPARK_OK
              : DSPARK_ERR_CUDA;
