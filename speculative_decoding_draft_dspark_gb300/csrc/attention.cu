@@ -41,6 +41,7 @@ constexpr int AT_ROWS = 128;       // rows of a product
 constexpr int AT_MAX_NARROW = 320;  // CTAs that leave partial results
 constexpr int AT_MAX_WIDE = 160;
 constexpr int AT_SEGS = 4;         // segments told ahead
+constexpr int AT_POISON = 8;       // segments looked over ahead: more than AT_SEGS + 1
 constexpr float kRescale = 8.0f;   // log2 of what the maximum may grow by
 // Up to this a maximum is taken off as fma(s, c, -round(m c)): whatever m c was rounded
 // to is in lse too, so nothing is lost.  A larger m is taken off first, (s - m) c: at
@@ -67,7 +68,7 @@ struct AtShape {
   static constexpr int kO = 2 * kTokens;                         // where O begins
   static constexpr int kTiles = kGroups * kQ + (kK + kV) * kTile;
   static constexpr int kThreads = kGroups * 128 + 128;           // softmax; K, V, products
-  static constexpr int kItem = 2;                                // tiles that an item costs besides
+  static constexpr int kItem = WIDE ? 4 : 3;                                // tiles that an item costs besides
   // registers of the two kinds of warpgroups: together at most the launch's
   static constexpr int kLaunchRegs = kCtas == 1 ? 168 : 128;
   static constexpr int kSoftmaxRegs = WIDE ? 208 : 176;
@@ -356,12 +357,13 @@ __device__ __forceinline__ bool at_wait(uint64_t *bar, uint32_t parity,
 template <int HD, bool WIDE>
 struct AtShared {
   using Sh = AtShape<HD, WIDE>;
-  uint64_t k_full[Sh::kK], k_empty[Sh::kK], v_full[Sh::kV], v_empty[Sh::kV];
+  uint64_t k_full[Sh::kK], k_empty[Sh::kK], v_full[Sh::kV], v_ready[Sh::kV],
+      v_empty[Sh::kV];
   // by block of rows (wide) or by tile, in turn (narrow)
   uint64_t s_full[2], p_full[2][Sh::kWords], pv_done[2];  // p: 64 tokens at a time
-  uint64_t q_full, scanned;
+  uint64_t q_full, scanned[AT_POISON];
   uint64_t seg_full[AT_SEGS], seg_empty[AT_SEGS];
-  uint32_t poison[2][4][3];              // tokens whose values are not finite: warp, tile
+  uint32_t poison[AT_POISON][3][Sh::kTokens / 32];  // tokens with values that are not finite
   AtSeg seg[AT_SEGS];
   int64_t scan[Sh::kThreads / 32];
   AtRequest start;
@@ -389,6 +391,44 @@ __device__ __forceinline__ uint64_t at_seen(const AtSeg &s, uint64_t bits, int u
   return seen;
 }
 
+// Before this token every row of a segment's block attends every token.
+template <class Sh>
+__device__ __forceinline__ int at_common(const AtParams &p, const AtSeg &s) {
+  return s.ctx + (s.tree ? 0 : at_token(p, s.block * Sh::kRows) + 1);
+}
+
+// A segment's pages, 32 at a time: which of them there are.
+struct AtPages {
+  const int32_t *table;
+  int base = -1, page0;
+  uint32_t good = 0u;
+  __device__ __forceinline__ AtPages(const AtParams &p, const AtSeg &s)
+      : table(p.block_table + static_cast<int64_t>(s.request) * p.table_stride),
+        shift(p.page_shift) {}
+  int shift;
+  // by the whole warp, for every tile in turn: those of the tile at this token
+  __device__ __forceinline__ void at(const AtParams &p, int token) {
+    page0 = token >> shift;
+    if (base == (page0 & ~31)) return;
+    base = page0 & ~31;
+    const int k = base + static_cast<int>(threadIdx.x & 31);
+    const int id = k < p.max_pages ? table[k] : -1;
+    good = __ballot_sync(0xFFFFFFFFu, id >= 0 && id < p.num_pages);
+  }
+  // of 32 tokens from the tile's 32 q on, the ones that there are
+  __device__ __forceinline__ uint32_t there(const AtSeg &s, int token, int q) const {
+    const int from = token + 32 * q;
+    const uint32_t lo = good >> (from >> shift & 31) & 1u ? 0xFFFFu : 0u;
+    const uint32_t hi = good >> ((from + 16) >> shift & 31) & 1u ? 0xFFFF0000u : 0u;
+    return (lo | hi) & static_cast<uint32_t>(low_bits(s.end - from));
+  }
+  template <int TOK>
+  __device__ __forceinline__ bool whole(const AtSeg &s, int token) const {
+    const uint32_t all = (1u << (TOK >> shift > 1 ? TOK >> shift : 1)) - 1u;
+    return token + TOK <= s.end && (good >> (page0 & 31) & all) == all;
+  }
+};
+
 template <int HD, bool WIDE>
 __global__ void __launch_bounds__(AtShape<HD, WIDE>::kThreads, AtShape<HD, WIDE>::kCtas)
     attention_kernel(const __grid_constant__ CUtensorMap k_map,
@@ -411,6 +451,7 @@ __global__ void __launch_bounds__(AtShape<HD, WIDE>::kThreads, AtShape<HD, WIDE>
     }
     for (int i = 0; i < Sh::kV; ++i) {
       mbar_init(&sh.v_full[i], 1);
+      mbar_init(&sh.v_ready[i], 1);
       mbar_init(&sh.v_empty[i], 1);
     }
     for (int i = 0; i < 2; ++i) {
@@ -419,10 +460,10 @@ __global__ void __launch_bounds__(AtShape<HD, WIDE>::kThreads, AtShape<HD, WIDE>
       mbar_init(&sh.pv_done[i], 1);
     }
     mbar_init(&sh.q_full, SOFTMAX);
-    mbar_init(&sh.scanned, 4);
+    for (int i = 0; i < AT_POISON; ++i) mbar_init(&sh.scanned[i], 1);
     for (int i = 0; i < AT_SEGS; ++i) {
       mbar_init(&sh.seg_full[i], 1);
-      mbar_init(&sh.seg_empty[i], SOFTMAX + 2);
+      mbar_init(&sh.seg_empty[i], SOFTMAX + 3);
     }
     sh.abort = 0u;
     fence_mbarrier_init();
@@ -436,7 +477,11 @@ __global__ void __launch_bounds__(AtShape<HD, WIDE>::kThreads, AtShape<HD, WIDE>
     prefetch_tensormap(&k_map);
     prefetch_tensormap(&v_map);
   }
-  wait_for_earlier_kernel();
+  // The narrow kernel after the wide one takes other requests' rows, and what it reads
+  // was there before the wide one, whose CTAs had all waited when this one was let in: it
+  // waits at its end only, for whoever comes after both.
+  const bool follows = !WIDE && p.both != 0;
+  if (!follows) wait_for_earlier_kernel();
   allow_next_kernel();
   tc_fence_before();
   __syncthreads();
@@ -664,7 +709,7 @@ __global__ void __launch_bounds__(AtShape<HD, WIDE>::kThreads, AtShape<HD, WIDE>
           const int gt = g + i, buf = WIDE ? r : gt & 1;
           const uint32_t turn = WIDE ? turns[r] + i : gt >> 1;
           const int stage = gt % Sh::kV;
-          if (r == 0 && !arrived(&sh.v_full[stage], (gt / Sh::kV) & 1)) return;
+          if (r == 0 && !arrived(&sh.v_ready[stage], (gt / Sh::kV) & 1)) return;
           const uint32_t b = at_desc_mn(v0 + stage * Sh::kTile, Sh::kBox);
 #pragma unroll
           for (int w = 0; w < WORDS; ++w) {
@@ -695,6 +740,88 @@ __global__ void __launch_bounds__(AtShape<HD, WIDE>::kThreads, AtShape<HD, WIDE>
         g += T;
       }
     }
+    if (warp == SOFTMAX + 3) {
+      // ---------------------------------------------------------- V, looked over
+      // Values of tokens that are not there are 0, and those that are not finite where
+      // not every row attends them: 0 times them would be NaN.
+      uint32_t stage = 0, phase = 0;
+      while (ok) {
+        const int si = segs % AT_SEGS;
+        if (!wait(&sh.seg_full[si], (segs / AT_SEGS) & 1)) break;
+        const AtSeg s = sh.seg[si];
+        __syncwarp();
+        if (one) mbar_arrive(&sh.seg_empty[si]);
+        if (s.request < 0) break;
+        const int slot = segs++ % AT_POISON;
+        const int common = at_common<Sh>(p, s);
+        uint32_t(&poison)[3][TOK / 32] = sh.poison[slot];
+        if (lane < 3 * (TOK / 32)) poison[lane / (TOK / 32)][lane % (TOK / 32)] = 0u;
+        __syncwarp();
+        AtPages pages(p, s);
+#pragma unroll 1
+        for (int t = s.t0; t < s.t1; ++t) {
+          const int token = t * TOK;
+          pages.at(p, token);
+          if (!wait(&sh.v_full[stage], phase)) break;
+          const bool inner = token + TOK <= common;
+          if (!inner || !pages.whole<TOK>(s, token)) {
+            const uint32_t v = smem_u32(v_ring) + stage * Sh::kTile;
+            constexpr int CHUNKS = HD / 8;
+#pragma unroll 1
+            for (int q = 0; q < TOK / 32; ++q) {  // 32 tokens at a time
+              const uint32_t there = pages.there(s, token, q), v_q = v + q * 32 * 128;
+              // k: a row, then 16 bytes of it
+              auto chunk = [&](int k) {
+                const int r = k / CHUNKS, e = k % CHUNKS;
+                return v_q + (e / 8) * Sh::kBox + r * 128 + ((e & 7) << 4);
+              };
+              if (there != 0xFFFFFFFFu) {
+#pragma unroll 1
+                for (int k = lane; k < 32 * CHUNKS; k += 32)
+                  if ((there >> (k / CHUNKS) & 1u) == 0u) st_shared_zero16(chunk(k));
+                __syncwarp();
+              }
+              if (inner) continue;
+              // 0 times a number is 0, 0 times anything else is NaN
+              const __nv_bfloat162 zero = __float2bfloat162_rn(0.0f);
+              __nv_bfloat162 none = zero;
+#pragma unroll 4
+              for (int k = lane; k < 32 * CHUNKS; k += 32) {
+                const uint4 w = ld_shared_v4(chunk(k));
+                const uint32_t *u = &w.x;
+#pragma unroll
+                for (int h = 0; h < 4; ++h)
+                  none = __hfma2(*reinterpret_cast<const __nv_bfloat162 *>(u + h), zero, none);
+              }
+              if (!__any_sync(0xFFFFFFFFu, __hisnan(none.x) || __hisnan(none.y))) continue;
+              uint32_t bad = 0u;
+#pragma unroll 1
+              for (int k = lane; k < 4 * 32 * CHUNKS; k += 32) {  // two values at a time
+                const uint32_t at = chunk(k >> 2) + (k & 3) * 4;
+                const uint32_t w = ld_shared_u32(at);
+                const uint32_t keep = ((w & 0x7F80u) == 0x7F80u ? 0u : 0xFFFFu) |
+                                      ((w & 0x7F800000u) == 0x7F800000u ? 0u : 0xFFFF0000u);
+                if (keep != 0xFFFFFFFFu) {
+                  st_shared_u32(at, w & keep);
+                  bad |= 1u << ((k >> 2) / CHUNKS);
+                }
+              }
+              bad = __reduce_or_sync(0xFFFFFFFFu, bad);
+              if (lane == 0) poison[t - common / TOK][q] = bad;
+            }
+            fence_proxy_async_smem();
+            __syncwarp();
+          }
+          if (one) mbar_arrive(&sh.v_ready[stage]);
+          if (++stage == Sh::kV) {
+            stage = 0;
+            phase ^= 1u;
+          }
+        }
+        __syncwarp();
+        if (one) mbar_arrive(&sh.scanned[slot]);
+      }
+    }
     if (!ok) {
       // copies and products in flight end before their memory is given back
       const uint64_t t0 = global_timer_ns();
@@ -710,9 +837,8 @@ __global__ void __launch_bounds__(AtShape<HD, WIDE>::kThreads, AtShape<HD, WIDE>
     const int row = warp * 32 + lane;
     const float c = p.scale_log2;
     const uint64_t c2 = pair_f32(__float_as_uint(c), __float_as_uint(c));
-    const int box_shift = min(p.page_shift, WIDE ? 7 : 6);  // pages, or tiles within one
     bool ok = true, have = false;
-    int g = 0, turn = 0, segs = 0, scans = 0;  // tiles, this block's, segments
+    int g = 0, turn = 0, segs = 0;  // tiles, this block's, segments
     auto wait = [&](uint64_t *bar, uint32_t parity) {
       ok = ok && __all_sync(0xFFFFFFFFu, at_wait(bar, parity, abort_flag));
       return ok;
@@ -730,90 +856,19 @@ __global__ void __launch_bounds__(AtShape<HD, WIDE>::kThreads, AtShape<HD, WIDE>
           mine && s.tree ? tree_bits(p.tree, p.tree_width, s.request, j, s.count) : 0ull;
       const int upto = s.ctx + j + 1;
       // before this token every row attends every token
-      const int common = s.ctx + (s.tree ? 0 : at_token(p, s.block * Sh::kRows) + 1);
-      const bool scans_here = have && s.t1 * TOK > common;
-      uint32_t(&poison)[4][3] = sh.poison[segs & 1];
+      const int common = at_common<Sh>(p, s);
+      const int this_seg = segs - 1;
       float top = -INFINITY, sum = 0.0f;
       if (active) {
-        if (block == 0 && lane < 3) poison[warp][lane] = 0u;
-        __syncwarp();
-        const int32_t *table = p.block_table + static_cast<int64_t>(s.request) * p.table_stride;
-        int base_page = -1;
-        uint32_t good = 0u;  // of 32 pages, the ones that there are
+        AtPages pages(p, s);
 #pragma unroll 1
         for (int i = 0; i < T; ++i) {
           const int gt = g + i, token = (s.t0 + i) * TOK;
           const int buf = WIDE ? block : gt & 1;
           const uint32_t phase = WIDE ? turn & 1 : (gt >> 1) & 1;
           ++turn;
-          const int page0 = token >> p.page_shift;
-          if (base_page != (page0 & ~31)) {
-            base_page = page0 & ~31;
-            const int id = base_page + lane < p.max_pages ? table[base_page + lane] : -1;
-            good = __ballot_sync(0xFFFFFFFFu, id >= 0 && id < p.num_pages);
-          }
-          const uint32_t all = (1u << (TOK >> box_shift)) - 1u;
-          const uint32_t here = good >> (page0 & 31);
-          const bool whole = (here & all) == all && token + TOK <= s.end;
-          const bool inner = token + TOK <= common;
-          // of 32 tokens from the tile's 32 k on, the ones that there are
-          auto there = [&](int k) {
-            const uint32_t lo = here >> (32 * k >> box_shift) & 1u ? 0xFFFFu : 0u;
-            const uint32_t hi = here >> ((32 * k + 16) >> box_shift) & 1u ? 0xFFFF0000u : 0u;
-            return (lo | hi) & static_cast<uint32_t>(low_bits(s.end - token - 32 * k));
-          };
-          // Values of tokens that are not there are 0, and those that are not finite
-          // where not every row attends them: 0 times them would be NaN.
-          if (block == 0 && (!whole || !inner)) {
-            const int stage = gt % Sh::kV;
-            if (!wait(&sh.v_full[stage], (gt / Sh::kV) & 1)) break;
-            constexpr int MINE = TOK / 4;  // tokens of a warp
-            constexpr uint32_t ALL = MINE == 32 ? 0xFFFFFFFFu : (1u << (MINE & 31)) - 1u;
-            const uint32_t mine_there =
-                (MINE == 32 ? there(warp) : there(warp >> 1) >> (16 * (warp & 1))) & ALL;
-            const uint32_t v = smem_u32(v_ring + stage * Sh::kTile) + warp * MINE * 128;
-            // k: a row, then 16 bytes of it
-            auto chunk = [&](int k) {
-              const int r = k / (HD / 8), e = k % (HD / 8);
-              return v + (e / 8) * Sh::kBox + r * 128 + ((e & 7) << 4);
-            };
-            uint32_t bad = 0u;
-            if (mine_there != ALL) {
-#pragma unroll 1
-              for (int k = lane; k < MINE * (HD / 8); k += 32)
-                if ((mine_there >> (k / (HD / 8)) & 1u) == 0u) st_shared_zero16(chunk(k));
-              __syncwarp();
-            }
-            if (!inner) {
-              // 0 times a number is 0, 0 times anything else is NaN
-              const __nv_bfloat162 zero = __float2bfloat162_rn(0.0f);
-              __nv_bfloat162 none = zero;
-#pragma unroll 4
-              for (int k = lane; k < MINE * (HD / 8); k += 32) {
-                const uint4 w = ld_shared_v4(chunk(k));
-                const uint32_t *u = &w.x;
-#pragma unroll
-                for (int q = 0; q < 4; ++q)
-                  none = __hfma2(*reinterpret_cast<const __nv_bfloat162 *>(u + q), zero, none);
-              }
-              if (__any_sync(0xFFFFFFFFu, __hisnan(none.x) || __hisnan(none.y))) {
-#pragma unroll 1
-                for (int k = lane; k < 4 * MINE * (HD / 8); k += 32) {  // two at a time
-                  const uint32_t at = chunk(k >> 2) + (k & 3) * 4;
-                  const uint32_t w = ld_shared_u32(at);
-                  const uint32_t keep = ((w & 0x7F80u) == 0x7F80u ? 0u : 0xFFFFu) |
-                                        ((w & 0x7F800000u) == 0x7F800000u ? 0u : 0xFFFF0000u);
-                  if (keep != 0xFFFFFFFFu) {
-                    st_shared_u32(at, w & keep);
-                    bad |= 1u << ((k >> 2) / (HD / 8));
-                  }
-                }
-              }
-              bad = __reduce_or_sync(0xFFFFFFFFu, bad);
-              if (lane == 0) poison[warp][s.t0 + i - common / TOK] = bad;
-            }
-            fence_proxy_async_smem();
-          }
+          pages.at(p, token);
+          const bool inner = token + TOK <= common && pages.whole<TOK>(s, token);
           if (!wait(&sh.s_full[buf], phase)) break;
           tc_fence_after();
           if (!any) {
@@ -822,12 +877,13 @@ __global__ void __launch_bounds__(AtShape<HD, WIDE>::kThreads, AtShape<HD, WIDE>
             continue;
           }
           const uint32_t s_tmem = tmem + lanes + buf * TOK;
-          if (!inner || !whole) {
+          if (!inner) {
             // scores of what a row does not attend: -inf
 #pragma unroll 1
             for (int k = 0; k < TOK / 32; ++k) {
               const uint32_t seen =
-                  static_cast<uint32_t>(at_seen(s, bits, upto, token + 32 * k)) & there(k);
+                  static_cast<uint32_t>(at_seen(s, bits, upto, token + 32 * k)) &
+                  pages.there(s, token, k);
               uint32_t x[32];
               tmem_ld_32x32b_x32(s_tmem + 32 * k, x);
               tmem_ld_wait(x);
@@ -952,13 +1008,6 @@ __global__ void __launch_bounds__(AtShape<HD, WIDE>::kThreads, AtShape<HD, WIDE>
         }
       }
       // ---- this segment's rows, or what is to be joined
-      if (scans_here) {
-        if (active) {
-          if (block == 0 && lane == 0) mbar_arrive(&sh.scanned);
-          if (!wait(&sh.scanned, scans & 1)) break;
-        }
-        ++scans;
-      }
       if (active) {
         const int buf = WIDE ? block : (g - 1) & 1;
         if (!wait(&sh.pv_done[buf], WIDE ? (turn - 1) & 1 : ((g - 1) >> 1) & 1)) break;
@@ -967,17 +1016,19 @@ __global__ void __launch_bounds__(AtShape<HD, WIDE>::kThreads, AtShape<HD, WIDE>
       if (active && any) {
         const int head = s.head * p.group + (m - j * p.group);
         const int64_t q_row = s.first + j;
-        // the tokens with values that are not finite that this row attends: by warp and
-        // tile, as they were found
+        // the tokens with values that are not finite that this row attends, by 32
         uint32_t hit = 0u;
+        const uint32_t(&poison)[3][TOK / 32] = sh.poison[this_seg % AT_POISON];
+        auto first_token = [&](int k) { return common / TOK * TOK + 32 * k; };
         auto found = [&](int k) {
-          const int token = (common / TOK + k % 3) * TOK + k / 3 * (TOK / 4);
-          return poison[k / 3][k % 3] & static_cast<uint32_t>(at_seen(s, bits, upto, token));
+          return poison[k / (TOK / 32)][k % (TOK / 32)] &
+                 static_cast<uint32_t>(at_seen(s, bits, upto, first_token(k)));
         };
-        if (scans_here && mine) {
+        if (s.t1 * TOK > common) {
+          if (!wait(&sh.scanned[this_seg % AT_POISON], (this_seg / AT_POISON) & 1)) break;
 #pragma unroll 1
-          for (int k = 0; k < 12; ++k)
-            if (found(k) != 0u) hit |= 1u << k;
+          for (int k = 0; k < 3 * (TOK / 32); ++k)
+            if (mine && found(k) != 0u) hit |= 1u << k;
         }
         if (__any_sync(0xFFFFFFFFu, hit != 0u)) {
 #pragma unroll 1
@@ -986,8 +1037,7 @@ __global__ void __launch_bounds__(AtShape<HD, WIDE>::kThreads, AtShape<HD, WIDE>
             for (uint32_t left = hit; left != 0u; left &= left - 1u) {
               const int k = __ffs(left) - 1;
               for (uint32_t tokens = found(k); tokens != 0u; tokens &= tokens - 1u) {
-                const int token =
-                    (common / TOK + k % 3) * TOK + k / 3 * (TOK / 4) + __ffs(tokens) - 1;
+                const int token = first_token(k) + __ffs(tokens) - 1;
                 const int id =
                     p.block_table[s.request * p.table_stride + (token >> p.page_shift)];
                 const float v = __bfloat162float(
@@ -1078,6 +1128,7 @@ __global__ void __launch_bounds__(AtShape<HD, WIDE>::kThreads, AtShape<HD, WIDE>
   __syncthreads();
   tc_fence_after();
   if (warp == SOFTMAX + 2) tmem_dealloc(tmem, Sh::kTmem);
+  if (follows) wait_for_earlier_kernel();
 }
 
 // Joins the pieces of the items that were cut: a CTA eight rows, a thread four columns of
@@ -1297,18 +1348,17 @@ static dspark_status launch(const AttentionArgs &a, int dev, int sms, cudaStream
       0, l.narrow_rows, std::min(AT_MAX_NARROW, AtShape<HD, false>::kCtas * sms));
   const AtParts wide = parts(1, l.wide_rows, l.wide_rows > 0 ? std::min(AT_MAX_WIDE, sms) : 0);
   p.both = l.wide_rows > 0;
-  p.parts = narrow;
-  p.least_tiles = 4;
-  dspark_status s = launch_one<HD, false>(a, p, dev, stream);
-  if (s != DSPARK_OK) return s;
+  dspark_status s;
   if constexpr (HD <= 128) {
     if (l.wide_rows > 0) {
       p.parts = wide;
       p.least_tiles = 2;
-      s = launch_one<HD, true>(a, p, dev, stream);
-      if (s != DSPARK_OK) return s;
+      if ((s = launch_one<HD, true>(a, p, dev, stream)) != DSPARK_OK) return s;
     }
   }
+  p.parts = narrow;
+  p.least_tiles = 4;
+  if ((s = launch_one<HD, false>(a, p, dev, stream)) != DSPARK_OK) return s;
   const int rows = std::max(l.narrow_rows, l.wide_rows);
   // few rows: more threads for an item's pieces
   const int share = rows <= 16 ? (HD == 256 ? 2 : 4) : rows <= 64 && HD <= 128 ? 2 : 1;

@@ -215,15 +215,17 @@ def test_the_types_lowest_values():
 @pytest.mark.parametrize("tree", [None, 12])
 @pytest.mark.parametrize("ctx", [0, 30, 64])
 @pytest.mark.parametrize("value", [math.nan, math.inf, -math.inf])
-def test_what_is_not_attended_has_no_effect(tree, ctx, value):
+@pytest.mark.parametrize("heads", [6, 32])
+def test_what_is_not_attended_has_no_effect(tree, ctx, value, heads):
     """A token of the step with bad keys and values changes the rows that attend it,
-    and no bit of the others."""
+    and no bit of the others; with 36 packed rows, and with 192."""
     requests = [(ctx, 12), (ctx + 3, 12)]
-    c = Case(requests, tree=tree, heads=6, kv=2, d=128)
+    half = heads // 2
+    c = Case(requests, tree=tree, heads=heads, kv=2, d=128)
     clean = c.call(c.gpu())
     for which in ("k", "v", "both"):
         for j in (0, 4, 11):
-            d = Case(requests, tree=tree, heads=6, kv=2, d=128)
+            d = Case(requests, tree=tree, heads=heads, kv=2, d=128)
             t = ctx + j
             id = int(d.table[0, t // 16])
             if which != "v":
@@ -237,10 +239,10 @@ def test_what_is_not_attended_has_no_effect(tree, ctx, value):
                 if not hit:
                     assert torch.equal(s["out"][r], clean["out"][r]) and torch.equal(s["lse"][r], clean["lse"][r])
                 else:
-                    assert torch.equal(s["out"][r, 3:], clean["out"][r, 3:])     # the other key head
+                    assert torch.equal(s["out"][r, half:], clean["out"][r, half:])     # the other key head
                     if which == "v":
-                        assert not s["out"][r, :3, 7].isfinite().any()
-                        assert torch.equal(s["out"][r, :3, 8:], clean["out"][r, :3, 8:])
+                        assert not s["out"][r, :half, 7].isfinite().any()
+                        assert torch.equal(s["out"][r, :half, 8:], clean["out"][r, :half, 8:])
                         assert torch.equal(s["lse"][r], clean["lse"][r])
 
 
@@ -254,8 +256,9 @@ def test_bad_values_in_the_context_reach_every_row():
     assert s["out"][:5, :, other].isfinite().all()
 
 
-def test_pages_that_are_not_there_are_left_out():
-    c = Case([(200, 4), (90, 2)])
+@pytest.mark.parametrize("heads,kv,page", [(4, 2, 16), (48, 1, 16), (96, 1, 64)])
+def test_pages_that_are_not_there_are_left_out(heads, kv, page):
+    c = Case([(page * 12, 4), (page * 5 + 10, 2)], heads=heads, kv=kv, page=page)
     c.table[0, 3], c.table[0, 7], c.table[1, 0] = -1, len(c.k), 1 << 30
     c.run(status=T.DEV_PAGE_OOR)
     c = Case([(40, 3)])
@@ -379,3 +382,42 @@ def test_a_run_of_decoding_steps_matches_a_chunk():
         c.call(one, max_len=1)
         assert ((one["lse"][0] - s["lse"][j]).abs() < 2 * c.score_error()).all()
         assert ((one["out"][0].float() - s["out"][j].float()).abs() <= 4 * HALF * (1 + s["out"][j].float().abs())).all()
+
+
+@pytest.mark.parametrize("requests,heads,kv,d,tree,page", [
+    ([(3000, 1), (500, 40), (0, 200), (64, 8), (900, 33)], 8, 2, 128, None, 16),
+    ([(300, 25), (0, 25), (64, 3), (127, 25)], 32, 1, 64, 25, 32),
+    ([(5000, 64), (10, 64)], 32, 4, 128, 64, 64),
+    ([(130, 17), (2000, 2)], 128, 1, 80, None, 256),
+    ([(2500, 300)], 1, 1, 64, None, 128)])
+def test_few_and_many_packed_rows_together(requests, heads, kv, d, tree, page):
+    """Requests for both kernels in one call, and cut items of both."""
+    Case(requests, heads=heads, kv=kv, d=d, tree=tree, page=page).run()
+
+
+def test_many_packed_rows_the_same_bits_every_time():
+    """Blocks of rows whose products follow each other in tensor memory."""
+    c = Case([(700, 130), (64, 40), (0, 90), (2000, 3)], heads=16, kv=4, d=128)
+    s = c.call(c.gpu())
+    c.check(s)
+    first = s["out"].clone(), s["lse"].clone()
+    for _ in range(300):
+        s["out"].fill_(5.0)
+        c.call(s)
+        assert torch.equal(first[0], s["out"]) and torch.equal(first[1], s["lse"])
+
+
+def test_bad_values_in_a_chunk_of_a_prompt():
+    """Rows before a token with bad values are as they were, bit for bit, in a chunk
+    that takes several blocks."""
+    requests = [(70, 150)]
+    clean = Case(requests, heads=8, kv=2)
+    a = clean.call(clean.gpu())
+    for j in (0, 63, 64, 100, 149):
+        c = Case(requests, heads=8, kv=2)
+        t = 70 + j
+        c.v[int(c.table[0, t // 16]), t % 16, 1, 3] = math.nan
+        s = c.call(c.gpu())
+        assert torch.equal(s["out"][:j], a["out"][:j])
+        assert s["out"][j:150, 4:, 3].isnan().all() and s["out"][j:150, 4:, 4:].isfinite().all()
+        assert torch.equal(s["out"][:150, :4], a["out"][:150, :4]) and torch.equal(s["lse"], a["lse"])
