@@ -2,7 +2,8 @@
 //
 // mask_kernel streams what a mask forbids, 16 bytes at a time: in place, vectors that
 // are forbidden whole are written unread and those that are allowed whole are left
-// alone; elsewhere all are copied.
+// alone; elsewhere all are copied.  Logits pass through L2 as what is not used again, so
+// that the masks stay there for the second kernel.
 //
 // adjust_kernel changes the few entries of a row that can change otherwise: the tokens
 // of the request's history and drafts, and its biases.  A CTA counts the tokens of one
@@ -27,7 +28,7 @@ constexpr int MK_CHUNK = 32768;            // entries of a CTA
 constexpr int AJ_THREADS = 512;
 constexpr int AJ_SLICE = 8192;             // vocabulary entries of a CTA without hashing
 constexpr int AJ_MOST_SLOTS = 16384;       // of a hash table
-constexpr int AJ_CTAS = 2 * 152;           // aimed at, by giving a CTA fewer rows
+constexpr int AJ_CTAS = 2 * 152;           // that run at once: a CTA gets fewer rows up to there
 constexpr uint32_t kEmpty = 0xFFFFFFFFu;
 constexpr uint32_t kListed = 1u << 31;
 constexpr uint32_t kInPrompt = 1u << 30;
@@ -118,7 +119,7 @@ __global__ void __launch_bounds__(MK_THREADS) mask_kernel(const AdjustArgs p) {
     for (int u = 0; u < UNROLL; ++u) {
       const int v = v0 + u * MK_THREADS;
       if (v < vectors && keep[u] != 0u && (copies || keep[u] != ALL))
-        x[u] = *reinterpret_cast<const uint4 *>(src + lead + v * V);
+        x[u] = __ldcs(reinterpret_cast<const uint4 *>(src + lead + v * V));
     }
 #pragma unroll
     for (int u = 0; u < UNROLL; ++u) {
@@ -129,7 +130,7 @@ __global__ void __launch_bounds__(MK_THREADS) mask_kernel(const AdjustArgs p) {
       x[u].y = (x[u].y & m.y) | (NONE & ~m.y);
       x[u].z = (x[u].z & m.z) | (NONE & ~m.z);
       x[u].w = (x[u].w & m.w) | (NONE & ~m.w);
-      *reinterpret_cast<uint4 *>(dst + lead + v * V) = x[u];
+      __stcs(reinterpret_cast<uint4 *>(dst + lead + v * V), x[u]);
     }
   }
   const int held = vectors * V;
@@ -251,47 +252,72 @@ __global__ void __launch_bounds__(AJ_THREADS, 2)
   const bool tree = is_tree(p.tree, p.tree_width, n, rows.count);
   if (after_masks) wait_for_earlier_kernel();
 
-  // Entries that are allowed: in place their logits are as they were.
+  // Entries that are allowed: in place their logits are as they were.  Four at a time, so
+  // that their loads (a mask's row, its word, the logit) overlap.
   const int total = entries * (j1 - j0);
-  for (int x = tid; x < total; x += AJ_THREADS) {
-    const int r = x / entries, j = j0 + r, s = list[x - r * entries];
-    const int t = HASH ? static_cast<int>(key[s]) : lo + s;
-    const int64_t row = rows.first + j;
-    float v = logit_f32(static_cast<const T *>(p.logits)[row * p.stride + t]);
-    if (p.mask != nullptr) {
-      const int64_t m = p.mask_index != nullptr ? p.mask_index[row] : row;
-      if (m >= 0 && m < p.mask_rows &&
-          (p.mask[m * p.mask_stride + (t >> 5)] >> (t & 31) & 1u) == 0u)
-        continue;
+  constexpr int ITEMS = 4;
+  for (int x0 = tid; x0 < total; x0 += ITEMS * AJ_THREADS) {
+    int slot[ITEMS], row_j[ITEMS], token[ITEMS];
+    int64_t mask_row[ITEMS];
+    float logit[ITEMS];
+    bool allowed[ITEMS];
+#pragma unroll
+    for (int u = 0; u < ITEMS; ++u) {
+      const int x = x0 + u * AJ_THREADS;
+      allowed[u] = x < total;
+      if (!allowed[u]) continue;
+      const int r = x / entries;
+      row_j[u] = j0 + r;
+      slot[u] = list[x - r * entries];
+      token[u] = HASH ? static_cast<int>(key[slot[u]]) : lo + slot[u];
+      const int64_t row = rows.first + row_j[u];
+      mask_row[u] = p.mask == nullptr ? -1 : p.mask_index != nullptr ? p.mask_index[row] : row;
     }
-    const uint32_t word = count[s];
-    uint32_t c = word & kCount;
-    if ((word & kDraft) != 0u) {
-      // on row j's path: the rows that it attends, without row 0
-      const uint64_t path =
-          tree ? tree_bits(p.tree, p.tree_width, n, j, rows.count) : low_bits(j + 1);
-      for (int i = 1; i <= drafts; ++i)
-        if (draft[i] == t) c += static_cast<uint32_t>(path >> i) & 1u;
-    }
-    if (c != 0u || (word & kInPrompt) != 0u) v = v > 0.0f ? __fdiv_rn(v, rep) : __fmul_rn(v, rep);
-    if (c != 0u) {
-      v = __fsub_rn(v, __fmul_rn(freq, static_cast<float>(c)));
-      v = __fsub_rn(v, pres);
-    }
-    if ((word & kBiases) != 0u) {
-      // several: their sum, in order
-      bool any = false;
-      float sum = 0.0f;
-      for (int i = 0; i < biases; ++i) {
-        if (bias_token[i] != t) continue;
-        sum = any ? __fadd_rn(sum, bias_value[i]) : bias_value[i];
-        any = true;
+#pragma unroll
+    for (int u = 0; u < ITEMS; ++u)
+      if (allowed[u] && mask_row[u] >= 0 && mask_row[u] < p.mask_rows)
+        allowed[u] = (p.mask[mask_row[u] * p.mask_stride + (token[u] >> 5)] >> (token[u] & 31) &
+                      1u) != 0u;
+#pragma unroll
+    for (int u = 0; u < ITEMS; ++u)
+      if (allowed[u])
+        logit[u] = logit_f32(
+            static_cast<const T *>(p.logits)[(rows.first + row_j[u]) * p.stride + token[u]]);
+#pragma unroll
+    for (int u = 0; u < ITEMS; ++u) {
+      if (!allowed[u]) continue;
+      const int s = slot[u], t = token[u], j = row_j[u];
+      float v = logit[u];
+      const uint32_t word = count[s];
+      uint32_t c = word & kCount;
+      if ((word & kDraft) != 0u) {
+        // on row j's path: the rows that it attends, without row 0
+        const uint64_t path =
+            tree ? tree_bits(p.tree, p.tree_width, n, j, rows.count) : low_bits(j + 1);
+        for (int i = 1; i <= drafts; ++i)
+          if (draft[i] == t) c += static_cast<uint32_t>(path >> i) & 1u;
       }
-      v = __fadd_rn(v, sum);
-    } else if ((word & kBiased) != 0u) {
-      v = __fadd_rn(v, bias_value[bias_at[s]]);
+      if (c != 0u || (word & kInPrompt) != 0u)
+        v = v > 0.0f ? __fdiv_rn(v, rep) : __fmul_rn(v, rep);
+      if (c != 0u) {
+        v = __fsub_rn(v, __fmul_rn(freq, static_cast<float>(c)));
+        v = __fsub_rn(v, pres);
+      }
+      if ((word & kBiases) != 0u) {
+        // several: their sum, in order
+        bool any = false;
+        float sum = 0.0f;
+        for (int i = 0; i < biases; ++i) {
+          if (bias_token[i] != t) continue;
+          sum = any ? __fadd_rn(sum, bias_value[i]) : bias_value[i];
+          any = true;
+        }
+        v = __fadd_rn(v, sum);
+      } else if ((word & kBiased) != 0u) {
+        v = __fadd_rn(v, bias_value[bias_at[s]]);
+      }
+      logit_set(v, static_cast<T *>(p.out) + (rows.first + j) * p.out_stride + t);
     }
-    logit_set(v, static_cast<T *>(p.out) + row * p.out_stride + t);
   }
   if (flags != 0u) raise_status(p.status, flags);
 }
@@ -309,7 +335,7 @@ static dspark_status launch_adjust(const AdjustArgs &a, const AdjustShape &shape
   // rows a request, as far as the host knows
   const int64_t rows = (static_cast<int64_t>(a.R) + a.N - 1) / a.N;
   const int64_t each = static_cast<int64_t>(shape.slices) * a.N;
-  const int64_t shares = std::min(rows, (AJ_CTAS + each - 1) / each);
+  const int64_t shares = std::max<int64_t>(1, std::min(rows, AJ_CTAS / each));
   const dim3 grid(shape.slices, a.N, static_cast<unsigned>(shares));
   return launch_overlapped(adjust_kernel<T, HASH>, grid, dim3(AJ_THREADS),
                            shape.bytes(HASH, biases), stream, a, shape) == cudaSuccess

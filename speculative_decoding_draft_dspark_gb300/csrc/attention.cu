@@ -1357,7 +1357,7 @@ static dspark_status launch(const AttentionArgs &a, int dev, int sms, cudaStream
     }
   }
   p.parts = narrow;
-  p.least_tiles = 4;
+  p.least_tiles = 8;
   if ((s = launch_one<HD, false>(a, p, dev, stream)) != DSPARK_OK) return s;
   const int rows = std::max(l.narrow_rows, l.wide_rows);
   // few rows: more threads for an item's pieces

@@ -81,9 +81,10 @@ def _sizes(name, t, dims):
     """Shape of a tensor of so many dimensions, each below 2^31."""
     if t is None or t.dim() != dims:
         raise ValueError(f"{name} must be {dims}-D")
-    if any(s > _I32_MAX for s in t.shape):
-        raise ValueError(f"{name}'s dimensions must be below 2^31, got {tuple(t.shape)}")
-    return t.shape
+    shape = t.shape
+    if max(shape) > _I32_MAX:
+        raise ValueError(f"{name}'s dimensions must be below 2^31, got {tuple(shape)}")
+    return shape
 
 
 def _int(name, value, low=0):
