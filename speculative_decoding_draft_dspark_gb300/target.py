@@ -103,30 +103,41 @@ def _heads(name, t, shape, dtype, dev):
     columns are contiguous."""
     if t is None or t.dtype is not dtype or t.shape != shape or t.get_device() != dev:
         _refuse(name, t, shape, dtype, dev)
+    rows, heads, d = shape
     row, head, one = t.stride()
-    if one != 1 and shape[2] > 1:
+    if one != 1 and d > 1:
         raise ValueError(f"{name} must be contiguous along its columns")
     # the stride of a dimension with one entry means nothing
-    head = head if shape[1] > 1 else shape[2]
-    return t.data_ptr(), row if shape[0] > 1 else max(1, shape[1]) * max(head, shape[2]), head
+    if heads <= 1:
+        head = d
+    if rows <= 1:
+        row = max(1, heads) * max(head, d)
+    return t.data_ptr(), row, head
 
 
 def _caches(k_cache, v_cache, heads, d, dtype, dev):
     """(pointers, strides, page size, pages) of a cache's keys and values."""
-    shape = pages, size, _, _ = _sizes("k_cache", k_cache, 4)
-    want = torch.Size((pages, size, heads, d))
-    for name, t in (("k_cache", k_cache), ("v_cache", v_cache)):
-        if t is None or t.dtype is not dtype or t.shape != want or t.get_device() != dev:
-            _refuse(name, t, want, dtype, dev)
-        if t.stride()[3] != 1 and d > 1:
-            raise ValueError(f"{name} must be contiguous along its columns")
-    if any(a != b for a, b, n in zip(k_cache.stride(), v_cache.stride(), shape) if n > 1):
+    shape = _sizes("k_cache", k_cache, 4)
+    if (k_cache.dtype is not dtype or shape[2] != heads or shape[3] != d
+            or k_cache.get_device() != dev):
+        _refuse("k_cache", k_cache, torch.Size((shape[0], shape[1], heads, d)), dtype, dev)
+    if (v_cache is None or v_cache.dtype is not dtype or v_cache.shape != shape
+            or v_cache.get_device() != dev):
+        _refuse("v_cache", v_cache, shape, dtype, dev)
+    strides = page, token, head, one = k_cache.stride()
+    if one != 1 and d > 1:
+        raise ValueError("k_cache must be contiguous along its columns")
+    pages, size = shape[0], shape[1]
+    if v_cache.stride() != strides and any(
+            a != b for a, b, n in zip(strides, v_cache.stride(), shape) if n > 1):
         raise ValueError("k_cache and v_cache must have the same strides")
-    page, token, head, _ = k_cache.stride()
     # as above, in an order that nests
-    head = head if heads > 1 else d
-    token = token if size > 1 else heads * head
-    page = page if pages > 1 else max(size * token, heads * head)
+    if heads <= 1:
+        head = d
+    if size <= 1:
+        token = heads * head
+    if pages <= 1:
+        page = max(size * token, heads * head)
     return (k_cache.data_ptr(), v_cache.data_ptr()), (page, token, head), size, pages
 
 
@@ -226,7 +237,9 @@ def dspark_rotary(q, k, position, turns, q_out, k_out, *, n_rows=None, interleav
         if a is None:
             sides.append(((None, 0, 0), 0, (None, 0, 0)))
             continue
-        shape = torch.Size((R, _sizes(na, a, 3)[1], d))
+        shape = _sizes(na, a, 3)
+        if shape[0] != R or shape[2] != d:
+            raise ValueError(f"{na} must be {(R, shape[1], d)}, got {tuple(shape)}")
         sides.append((_heads(na, a, shape, t, dev), shape[1], _heads(nb, b, shape, t, dev)))
     (pq, Hq, pqo), (pk, Hk, pko) = sides
     pt, rot = _turns(turns, dev)
@@ -247,7 +260,9 @@ def dspark_rotary_append(q, k, v, position, slot, turns, q_out, k_cache, v_cache
     Hk = _sizes("k", k, 3)[1]
     dev = _place("q", q)
     dt, t = _dtype("q", q), q.dtype
-    shape, kv = torch.Size((R, Hq, d)), torch.Size((R, Hk, d))
+    shape, kv = q.shape, k.shape
+    if kv[0] != R or kv[2] != d:
+        raise ValueError(f"k must be {(R, Hk, d)}, got {tuple(kv)}")
     caches, strides, page_size, pages = _caches(k_cache, v_cache, Hk, d, t, dev)
     pt, rot = _turns(turns, dev)
     code = (_lib or load()).dspark_rotary_append(
