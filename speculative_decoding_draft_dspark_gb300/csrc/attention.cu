@@ -320,21 +320,29 @@ struct AtPlan {
   }
 };
 
+// a / b for numbers of units, which hardly ever need 64 bits
+__device__ __forceinline__ int64_t at_divide(int64_t a, int64_t b) {
+  if (((a | b) >> 32) == 0)
+    return static_cast<uint32_t>(a) / static_cast<uint32_t>(b);
+  return a / b;
+}
+
 // The CTAs' equal shares of all units (each item's kItem, then its tiles): the first
 // `more` CTAs have one more.
 struct AtShares {
   int64_t each;
   int more, ctas;
   __device__ __forceinline__ void split(int64_t units, int most, int least) {
-    ctas = static_cast<int>(min(static_cast<int64_t>(most), (units + least - 1) / least));
-    each = ctas > 0 ? units / ctas : 0;
+    ctas = static_cast<int>(
+        min(static_cast<int64_t>(most), at_divide(units + least - 1, least)));
+    each = ctas > 0 ? at_divide(units, ctas) : 0;
     more = static_cast<int>(units - each * ctas);
   }
   __device__ __forceinline__ int64_t begin(int c) const { return each * c + min(c, more); }
   __device__ __forceinline__ int holder(int64_t unit) const {
     const int64_t first = begin(more);
-    return unit < first ? static_cast<int>(unit / (each + 1))
-                        : more + static_cast<int>((unit - first) / each);
+    return unit < first ? static_cast<int>(at_divide(unit, each + 1))
+                        : more + static_cast<int>(at_divide(unit - first, each));
   }
 };
 
@@ -562,7 +570,7 @@ __global__ void __launch_bounds__(AtShape<HD, WIDE>::kThreads, AtShape<HD, WIDE>
       int n = sh.start_request, h = 0, b = 0;
       if (!is_v && unit < end_unit) {
         const int64_t a_head = Plan::head_units(p, r);
-        h = static_cast<int>(rest / a_head);
+        h = static_cast<int>(at_divide(rest, a_head));
         rest -= h * a_head;
       }
       uint32_t stage = 0, turn = 0;  // of the ring
@@ -576,6 +584,7 @@ __global__ void __launch_bounds__(AtShape<HD, WIDE>::kThreads, AtShape<HD, WIDE>
           if (one) mbar_arrive(&sh.seg_empty[si]);
         } else {
           s.request = -1;
+          int64_t cut = -1;  // the last unit of an item that begins here and is cut
           while (unit < end_unit) {
             if (b >= r.blocks) {
               b = 0;
@@ -612,7 +621,8 @@ __global__ void __launch_bounds__(AtShape<HD, WIDE>::kThreads, AtShape<HD, WIDE>
                 s.part = 2 * cta;
               } else if (s.t1 < tiles) {
                 s.part = 2 * cta + 1;
-                meta = {shares.holder(unit + (tiles - s.t1) - 1), n, s.first, s.count, h, b};
+                meta = {0, n, s.first, s.count, h, b};
+                cut = unit + (tiles - s.t1) - 1;
               }
             }
             ++b;
@@ -624,6 +634,7 @@ __global__ void __launch_bounds__(AtShape<HD, WIDE>::kThreads, AtShape<HD, WIDE>
             mbar_arrive(&sh.seg_full[si]);
           }
           __syncwarp();
+          if (cut >= 0) meta.last = shares.holder(cut);
         }
         ++segs;
         if (s.request < 0) break;
