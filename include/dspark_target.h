@@ -175,7 +175,8 @@ DSPARK_API dspark_status dspark_rotary_append(
  * on it, NaN and infinities included; nor have tokens on pages outside [0,
  * num_pages) or past the table (left out, DSPARK_DEV_PAGE_OOR).
  *
- * q, out     bf16 [R, Hq, d], row and head strides in elements.
+ * q, out     bf16 [R, Hq, d], row and head strides in elements; out overlaps nothing
+ *            that is read.
  * k_cache, v_cache  bf16, element (page, offset, head, column) as in
  *            dspark_rotary_append.
  * block_table [N, max_pages], rows table_stride apart.   ctx_len [N] (negative: 0).
@@ -219,7 +220,8 @@ DSPARK_API dspark_status dspark_tree_attention(
  * path: draft_tokens[n, i-1] for every row i >= 1 that row j attends (see Trees).
  *
  * logits, out  [R, vocab] of dtype (DSPARK_BF16 or DSPARK_F32), rows stride elements
- *              apart.  out may be logits: then only what changes is written.
+ *              apart.  out may be logits: then only what changes is written; else
+ *              they do not overlap.
  * cu_rows      [N+1]: the requests' rows among the logits' (cu_out of
  *              dspark_step_rows).  Rows past cu_rows[N] are left as they are.
  * tokens       [N, tokens_width], rows tokens_stride apart.  hist_len [N]; prompt_len

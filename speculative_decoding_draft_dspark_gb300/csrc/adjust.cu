@@ -16,6 +16,7 @@
 // with masks in the same kernel.)
 #include <algorithm>
 #include <cuda_bf16.h>
+#include <mutex>
 
 #include "common.cuh"
 #include "launch.cuh"
@@ -322,16 +323,28 @@ __global__ void __launch_bounds__(AJ_THREADS, 2)
   if (flags != 0u) raise_status(p.status, flags);
 }
 
+static std::mutex g_aj_mu;
+
 template <typename T, bool HASH>
 static dspark_status launch_adjust(const AdjustArgs &a, const AdjustShape &shape,
                                    cudaStream_t stream) {
   const bool biases = a.bias_width > 0;
   const AdjustShape most = {HASH ? AJ_MOST_SLOTS : AJ_SLICE, 1};
-  if (cudaFuncSetAttribute(adjust_kernel<T, HASH>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                           most.bytes(HASH, true)) != cudaSuccess ||
-      cudaFuncSetAttribute(adjust_kernel<T, HASH>, cudaFuncAttributePreferredSharedMemoryCarveout,
-                           cudaSharedmemCarveoutMaxShared) != cudaSuccess)
-    return DSPARK_ERR_CUDA;
+  static bool attr[128];
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 128) return DSPARK_ERR_CUDA;
+  {
+    std::lock_guard<std::mutex> lk(g_aj_mu);
+    if (!attr[dev]) {
+      if (cudaFuncSetAttribute(adjust_kernel<T, HASH>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                               most.bytes(HASH, true)) != cudaSuccess ||
+          cudaFuncSetAttribute(adjust_kernel<T, HASH>,
+                               cudaFuncAttributePreferredSharedMemoryCarveout,
+                               cudaSharedmemCarveoutMaxShared) != cudaSuccess)
+        return DSPARK_ERR_CUDA;
+      attr[dev] = true;
+    }
+  }
   // rows a request, as far as the host knows
   const int64_t rows = (static_cast<int64_t>(a.R) + a.N - 1) / a.N;
   const int64_t each = static_cast<int64_t>(shape.slices) * a.N;

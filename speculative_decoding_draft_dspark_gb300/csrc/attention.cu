@@ -292,11 +292,11 @@ struct AtPlan {
     const RowSpan rows = row_span(p.cu_rows, n, p.R);
     r.first = rows.first;
     r.count = min(rows.count, p.max_len);
-    r.ctx = max(p.ctx_len[n], 0);
+    const int64_t room = static_cast<int64_t>(p.max_pages) << p.page_shift;
+    r.ctx = static_cast<int>(min(static_cast<int64_t>(max(p.ctx_len[n], 0)), room));
     r.tree = is_tree(p.tree, p.tree_width, n, rows.count);
     r.flags = rows.count > p.max_len ? DSPARK_DEV_LEN_OOR : 0u;
-    if (r.count > 0 && static_cast<int64_t>(r.ctx) + r.count >
-                           static_cast<int64_t>(p.max_pages) << p.page_shift)
+    if (r.count > 0 && r.ctx + static_cast<int64_t>(r.count) > room)
       r.flags |= DSPARK_DEV_PAGE_OOR;
     const int packed = r.count * p.group;
     r.blocks = p.both && (packed > AT_ROWS) != WIDE ? 0 : (packed + Sh::kRows - 1) / Sh::kRows;

@@ -157,7 +157,8 @@ __global__ void __launch_bounds__(RW_THREADS) rows_kernel(const RowsArgs p) {
     if (is_tree(p.tree, p.tree_width, n, count))
       depth = __popcll(tree_bits(p.tree, p.tree_width, n, j, count) & ~(1ull << j));
     p.row_request[r] = n;
-    p.position[r] = ctx + depth;
+    p.position[r] = static_cast<int>(min(static_cast<int64_t>(ctx) + depth,
+                                         static_cast<int64_t>(INT32_MAX)));
 
     // the page of this row's token: an old one, or one popped off the free list
     const int64_t index = static_cast<int64_t>(ctx) + j;

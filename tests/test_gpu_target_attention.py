@@ -421,3 +421,30 @@ def test_bad_values_in_a_chunk_of_a_prompt():
         assert torch.equal(s["out"][:j], a["out"][:j])
         assert s["out"][j:150, 4:, 3].isnan().all() and s["out"][j:150, 4:, 4:].isfinite().all()
         assert torch.equal(s["out"][:150, :4], a["out"][:150, :4]) and torch.equal(s["lse"], a["lse"])
+
+
+def test_no_rows_at_all():
+    c = Case([(5, 0), (0, 0), (100, 0)], heads=8, kv=2)
+    s = c.call(c.gpu())
+    assert (s["out"] == 5.0).all() and (s["lse"] == 5.0).all() and D.dspark_read_status(s["ws"]) == 0
+
+
+def test_thousands_of_requests():
+    c = Case([(i % 23, 1 + (i % 50 == 0)) for i in range(4000)], heads=2, kv=1, d=64)
+    c.run()
+
+
+def test_the_largest_length():
+    """ctx_len at the end of 32 bits: as one that fills the table."""
+    c = Case([(150, 3), (20, 2)])
+    full = Case([(150, 3), (20, 2)])
+    for x in (c.k, c.v, full.k, full.v):
+        x.nan_to_num_(0.0)            # what no request wrote counts here
+    s, t = c.gpu(), full.gpu()
+    s["ctx"][0] = (1 << 31) - 1
+    t["ctx"][0] = c.table.shape[1] * 16
+    c.call(s)
+    full.call(t)
+    assert D.dspark_read_status(s["ws"]) == D.dspark_read_status(t["ws"]) == T.DEV_PAGE_OOR
+    assert torch.equal(s["out"], t["out"]) and torch.equal(s["lse"], t["lse"])
+    assert s["out"].isfinite().all()
