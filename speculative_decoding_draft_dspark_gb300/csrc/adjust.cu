@@ -11,9 +11,14 @@
 // request's rows, entry by entry.  The counts are whole numbers, so their order does
 // not matter.  They are in a hash table where one holds every token that a request can
 // have; longer histories go through the vocabulary a slice at a time, a CTA each,
-// with a word for every entry.  (A slice costs the whole history again: at 262144
-// entries and 256 requests of up to 4096 tokens 32 slices took 490 us, in place and
-// with masks in the same kernel.)
+// with a word for every entry.  (A slice costs the whole history again: with 262144
+// entries, 256 requests x 8 rows and histories of up to 4096 tokens, 32 slices, and
+// their masks in the same kernel, took 322 us.)
+//
+// Measured on a GB300, that case, in place with half of the rows masked: 194-196 us, of
+// which masks 147 (0.74 of HBM's cycles: 537 MB written, half of it read) and entries
+// 49 (some 600000 single logits, a sector each).  561 rows x 50003 fp32 elsewhere:
+// 45 us, 0.75 of measured HBM.
 #include <algorithm>
 #include <cuda_bf16.h>
 #include <mutex>
