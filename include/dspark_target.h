@@ -120,7 +120,7 @@ DSPARK_API dspark_status dspark_step_rows(
  * q, q_out   [R, Hq, d] of dtype (DSPARK_BF16 or DSPARK_F32): row strides and head
  *            strides in elements, columns contiguous.  k, k_out [R, Hk, d] alike.
  *            q with Hq = 0, or k with Hk = 0, may be NULL.  The outputs may be the
- *            inputs themselves.
+ *            inputs themselves, with the same strides; else they do not overlap.
  * position   [R] int32, taken as it is (negative ones turn backwards).
  * n_rows     device scalar or NULL (R): rows from it on are left as they are.
  * turns      [rot / 2] uint64 device memory.
@@ -186,7 +186,7 @@ DSPARK_API dspark_status dspark_rotary_append(
  * lse        out fp32 [R, Hq], contiguous, or NULL.
  * workspace  >= dspark_attention_workspace_size(N, max_len, Hq, Hk, d) bytes,
  *            256-byte aligned.
- * scale      positive (and a normal number).
+ * scale      positive, a normal number below 2^127.
  * All strides multiples of 8, all bases 16-byte aligned.
  * Limits: 1 <= N <= 16384, 1 <= R <= 2^22, Hq a multiple of Hk, Hq / Hk <= 128, Hq <=
  * 1024, d a multiple of 8 in [8, 256], num_pages * page_size < 2^31, max_pages *

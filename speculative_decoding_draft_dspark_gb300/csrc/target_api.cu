@@ -74,6 +74,13 @@ bool heads_out_ok(const HeadRows &t, int32_t rows, int32_t heads, int32_t d, uin
                         distinct(d, rows, t.stride, heads, t.head_stride));
 }
 
+// In place: every element where it was.
+bool in_place_ok(const HeadRows &in, const HeadRows &out, int32_t rows, int32_t heads) {
+  return heads == 0 || in.p != out.p ||
+         ((rows == 1 || in.stride == out.stride) &&
+          (heads == 1 || in.head_stride == out.head_stride));
+}
+
 // The strides of a cache: any order of pages, tokens and heads, one element a place.
 bool cache_ok(int64_t page_stride, int64_t token_stride, int64_t head_stride, int32_t num_pages,
               int32_t page_size, int32_t heads, int32_t d, int64_t multiple) {
@@ -92,7 +99,7 @@ dspark_status check_rotary(const RotaryArgs &a, int32_t dtype) {
   if (a.R == 0) return DSPARK_OK;  // an empty tensor has no pointer
   const int e = dtype == DSPARK_F32 ? 4 : 2;
   if (!heads_ok(a.q.p, a.q.stride, a.q.head_stride, a.Hq, a.d, e, 1) ||
-      !heads_out_ok(a.q_out, a.R, a.Hq, a.d, e, 1) ||
+      !heads_out_ok(a.q_out, a.R, a.Hq, a.d, e, 1) || !in_place_ok(a.q, a.q_out, a.R, a.Hq) ||
       !heads_ok(a.k.p, a.k.stride, a.k.head_stride, a.Hk, a.d, e, 1))
     return DSPARK_ERR_INVALID_ARG;
   if (!given(a.position, 4) || !given(a.turns, 8) || !optional(a.n_rows, 4) ||
@@ -242,7 +249,8 @@ dspark_status dspark_rotary(const void *q, int64_t q_stride, int64_t q_head_stri
   a.amplitude = amplitude;
   const dspark_status s = check_rotary(a, dtype);
   if (s != DSPARK_OK || R == 0) return s;
-  if (!heads_out_ok(a.k_out, R, Hk, d, a.f32 ? 4 : 2, 1)) return DSPARK_ERR_INVALID_ARG;
+  if (!heads_out_ok(a.k_out, R, Hk, d, a.f32 ? 4 : 2, 1) || !in_place_ok(a.k, a.k_out, R, Hk))
+    return DSPARK_ERR_INVALID_ARG;
   return rotary_launch(a, reinterpret_cast<cudaStream_t>(stream));
 }
 
@@ -331,7 +339,7 @@ dspark_status dspark_tree_attention(
     return DSPARK_ERR_UNSUPPORTED;
   if (!given(block_table, 4) || table_stride < max_pages || !given(ctx_len, 4) ||
       !given(cu_rows, 4) || !optional(lse, 4) || !(scale > 0.0f) ||
-      !std::isnormal(scale))
+      !std::isnormal(scale) || !std::isfinite(scale * 2.0f))
     return DSPARK_ERR_INVALID_ARG;
   if ((s = check_ws(workspace, workspace_bytes, attention_workspace_bytes(max_len, Hq, Hk, d))) !=
       DSPARK_OK)

@@ -94,6 +94,8 @@ I, U, W = D.ERR_INVALID_ARG, D.ERR_UNSUPPORTED, D.ERR_WORKSPACE
     ("dspark_rotary", dict(position=None), I),
     ("dspark_rotary", dict(amplitude=math.nan), I),
     ("dspark_rotary", dict(qos=64), I),              # rows of the output overlap
+    ("dspark_rotary", dict(qos=576), I),             # in place, rows elsewhere
+    ("dspark_rotary", dict(koh=128, kos=256), I),
     ("dspark_rotary", dict(qh=63), I),
     ("dspark_rotary_append", dict(v=None), I),
     ("dspark_rotary_append", dict(slot=None), I),
@@ -114,6 +116,8 @@ I, U, W = D.ERR_INVALID_ARG, D.ERR_UNSUPPORTED, D.ERR_WORKSPACE
     ("dspark_tree_attention", dict(scale=math.inf), I),
     ("dspark_tree_attention", dict(scale=-1.0), I),
     ("dspark_tree_attention", dict(scale=0.0), I),
+    ("dspark_tree_attention", dict(scale=1e-40), I),
+    ("dspark_tree_attention", dict(scale=3e38), I),
     ("dspark_tree_attention", dict(max_len=0), I),
     ("dspark_tree_attention", dict(R=0), I),
     ("dspark_tree_attention", dict(N=16385), U),
