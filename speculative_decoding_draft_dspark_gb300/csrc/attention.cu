@@ -1021,8 +1021,11 @@ __global__ void __launch_bounds__(AtShape<HD, WIDE>::kThreads, AtShape<HD, WIDE>
                 (next.head * p.group + nm - nj * p.group) * p.q.head_stride;
         const uint32_t dst = smem_u32(smem) + block * Sh::kQ + (warp & 3) * 32 * 128;
         constexpr int CHUNKS = HD / 8;  // of 16 bytes, a row
+        // of the rows that there are
+        const int left = next.request < 0 ? 0 : next.count * p.group - (nm - lane);
+        const int chunks = min(max(left, 0), 32) * CHUNKS;
 #pragma unroll 2
-        for (int k = lane; k < 32 * CHUNKS; k += 32) {
+        for (int k = lane; k - lane < chunks; k += 32) {
           const int r = k / CHUNKS, e = k % CHUNKS;
           const __nv_bfloat16 *from = reinterpret_cast<const __nv_bfloat16 *>(
               __shfl_sync(0xFFFFFFFFu, reinterpret_cast<uint64_t>(src), r));
