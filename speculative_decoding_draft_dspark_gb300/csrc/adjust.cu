@@ -353,7 +353,9 @@ static dspark_status launch_adjust(const AdjustArgs &a, const AdjustShape &shape
   // rows a request, as far as the host knows
   const int64_t rows = (static_cast<int64_t>(a.R) + a.N - 1) / a.N;
   const int64_t each = static_cast<int64_t>(shape.slices) * a.N;
-  const int64_t shares = std::max<int64_t>(1, std::min(rows, AJ_CTAS / each));
+  // one request may have all rows: a CTA's entries are counted in 31 bits
+  const int64_t least = (static_cast<int64_t>(a.R) * shape.slots >> 30) + 1;
+  const int64_t shares = std::max(least, std::min(rows, AJ_CTAS / each));
   const dim3 grid(shape.slices, a.N, static_cast<unsigned>(shares));
   return launch_overlapped(adjust_kernel<T, HASH>, grid, dim3(AJ_THREADS),
                            shape.bytes(HASH, biases), stream, a, shape) == cudaSuccess

@@ -193,3 +193,24 @@ def test_rows_past_32_bits():
     s["logits"] = s["out"] = big
     c.call(s)
     c.check(s)
+
+
+def test_a_request_with_most_of_the_rows():
+    """Its rows times its distinct tokens, one CTA's work by the average request, are
+    more than 2^31.  A single fp32 subtraction: exact but for the rounding to bf16."""
+    N, rows, vocab = 304, 270000, 8192
+    R = rows + N - 1
+    g = torch.Generator(device="cuda").manual_seed(0)
+    s = {"logits": torch.empty(R, vocab, dtype=BF16, device="cuda").normal_(generator=g)}
+    before, s["out"], s["ws"] = s["logits"].clone(), s["logits"], T.new_workspace(256)
+    s["cu"] = torch.cat([torch.zeros(1), torch.arange(N) + rows]).to(I32).cuda()
+    s["tokens"] = torch.randperm(vocab, generator=g, device="cuda").to(I32).expand(N, vocab).contiguous()
+    s["hist_len"] = torch.full((N,), vocab, dtype=I32, device="cuda")
+    s["prompt_len"] = s["draft_tokens"] = s["tree"] = None
+    s["presence"] = torch.linspace(0.5, 1.5, N, device="cuda")
+    Case.call(None, s)
+    assert D.dspark_read_status(s["ws"]) == 0
+    pres = torch.cat([s["presence"][:1].expand(rows), s["presence"][1:]])
+    for a in range(0, R, 30000):
+        b = slice(a, min(R, a + 30000))
+        assert torch.equal(s["out"][b], (before[b].float() - pres[b, None]).to(BF16))
