@@ -169,24 +169,18 @@ __global__ void __launch_bounds__(AJ_THREADS, 2)
   __shared__ int listed;
   __shared__ int32_t draft[kMaxStepDrafts + 1];  // [i]: the token of the request's row i
   const int tid = threadIdx.x;
-  // What is read up to the wait below was there before mask_kernel, whose CTAs had all
-  // waited for it when this kernel was let in; without mask_kernel this is the first.
-  const bool after_masks = p.out != p.logits || p.mask != nullptr;
-  if (!after_masks) wait_for_earlier_kernel();
   const int n = blockIdx.y;
   for (int i = tid; i < shape.slots / 4; i += AJ_THREADS) {
     reinterpret_cast<uint4 *>(count)[i] = make_uint4(0u, 0u, 0u, 0u);
     if (HASH) reinterpret_cast<uint4 *>(key)[i] = make_uint4(kEmpty, kEmpty, kEmpty, kEmpty);
   }
   if (tid == 0) listed = 0;
+  wait_for_earlier_kernel();
   const RowSpan rows = row_span(p.cu_rows, n, p.R);
   // this CTA's share of them
   const int share = (rows.count + gridDim.z - 1) / gridDim.z;
   const int j0 = blockIdx.z * share, j1 = min(rows.count, j0 + share);
-  if (j0 >= j1) {
-    if (after_masks) wait_for_earlier_kernel();
-    return;
-  }
+  if (j0 >= j1) return;
   int hist = p.hist_len[n];
   const int prompt = p.prompt_len != nullptr ? p.prompt_len[n] : 0;
   const int biases = p.bias_width > 0 ? min(max(p.bias_count[n], 0), p.bias_width) : 0;
@@ -256,7 +250,6 @@ __global__ void __launch_bounds__(AJ_THREADS, 2)
   const float freq = p.frequency != nullptr ? p.frequency[n] : 0.0f;
   const float pres = p.presence != nullptr ? p.presence[n] : 0.0f;
   const bool tree = is_tree(p.tree, p.tree_width, n, rows.count);
-  if (after_masks) wait_for_earlier_kernel();
 
   // Entries that are allowed: in place their logits are as they were.  Four at a time, so
   // that their loads (a mask's row, its word, the logit) overlap.
