@@ -493,19 +493,17 @@ __global__ void __launch_bounds__(AtShape<HD, WIDE>::kThreads, AtShape<HD, WIDE>
     fence_mbarrier_init();
     fence_proxy_async_smem();
   }
-  if (warp == SOFTMAX + 2) {
-    tmem_alloc(&sh.tmem, Sh::kTmem);
-    tmem_relinquish();
-  }
   if (warp == SOFTMAX && lane == 0) {
     prefetch_tensormap(&k_map);
     prefetch_tensormap(&v_map);
   }
-  // The narrow kernel after the wide one takes other requests' rows, and what it reads
-  // was there before the wide one, whose CTAs had all waited when this one was let in: it
-  // waits at its end only, for whoever comes after both.
-  const bool follows = !WIDE && p.both != 0;
-  if (!follows) wait_for_earlier_kernel();
+  // Tensor memory after the wait: what waits for an earlier kernel holds none that a CTA
+  // of that kernel may still ask for.
+  wait_for_earlier_kernel();
+  if (warp == SOFTMAX + 2) {
+    tmem_alloc(&sh.tmem, Sh::kTmem);
+    tmem_relinquish();
+  }
   allow_next_kernel();
   tc_fence_before();
   __syncthreads();
@@ -1158,7 +1156,6 @@ __global__ void __launch_bounds__(AtShape<HD, WIDE>::kThreads, AtShape<HD, WIDE>
   __syncthreads();
   tc_fence_after();
   if (warp == SOFTMAX + 2) tmem_dealloc(tmem, Sh::kTmem);
-  if (follows) wait_for_earlier_kernel();
 }
 
 // Joins the pieces of the items that were cut: a CTA eight rows, a thread four columns of

@@ -32,7 +32,7 @@ def kernels(name):
         i += 1
 
 
-@pytest.mark.parametrize("name", ["adjust.cu", "rotary.cu", "norm.cu", "head_loss.cu"])
+@pytest.mark.parametrize("name", ["adjust.cu", "attention.cu", "rotary.cu", "norm.cu", "head_loss.cu"])
 def test_every_thread_waits_before_it_reads(name):
     found = list(kernels(name))
     with open(os.path.join(CSRC, name)) as f:
