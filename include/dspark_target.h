@@ -112,8 +112,9 @@ DSPARK_API dspark_status dspark_step_rows(
  *     DSPARK_ROPE_LINEAR    f_i / factor
  *     DSPARK_ROPE_BY_PARTS  f_i (1 - w) + f_i / factor w, w a ramp over i from 0 at
  *                           lo = max(floor e(high), 0) to 1 at
- *                           hi = min(ceil e(low), rot / 2 - 1), with
- *                           e(b) = rot ln(original / (2 pi b)) / (2 ln base)
+ *                           hi = min(ceil e(low), rot - 1), with
+ *                           e(b) = rot ln(original / (2 pi b)) / (2 ln base); a step
+ *                           after lo where hi <= lo
  *     DSPARK_ROPE_BY_TURNS  f_i s + f_i / factor (1 - s), s = (u - low) / (high -
  *                           low) clamped to [0, 1], u = original f_i / (2 pi)
  *

@@ -201,7 +201,8 @@ dspark_status dspark_rotary_table(int32_t rot, double base, int32_t scaling, dou
       return rot * std::log(original / (b * kTwoPi)) / (2.0 * std::log(base));
     };
     first = std::fmax(std::floor(edge(high)), 0.0);
-    last = std::fmin(std::ceil(edge(low)), rot / 2 - 1.0);
+    // the end may lie behind the last pair, which is then within the ramp
+    last = std::fmin(std::ceil(edge(low)), rot - 1.0);
   }
   for (int32_t i = 0; i < rot / 2; ++i) {
     double f = std::pow(base, -2.0 * i / rot);

@@ -213,3 +213,22 @@ def test_rotary_table_refusals(lib, rot, base, kw):
 
 def test_c_entry_survives_null(lib):
     assert lib.dspark_rotary_table(8, ctypes.c_double(1e4), 0, 1.0, 0.0, 0.0, 0.0, None) == I
+
+
+@pytest.mark.parametrize("rot,base,original,factor,low,high,kept", [
+    (128, 10000.0, 65536, 4.0, 1, 32, 0.31),         # the ramp ends two pairs behind the last
+    (64, 10000.0, 65536, 4.0, 1, 32, None), (64, 100.0, 4096, 8.0, 1, 32, None), (16, 10000.0, 131072, 16.0, 1, 32, None)])
+def test_a_ramp_that_ends_behind_the_last_pair(lib, rot, base, original, factor, low, high, kept):
+    """The ramp's end is cut at rot - 1, not at the last pair, whose frequency is then
+    stretched in part only."""
+    got = T.dspark_rotary_table(rot, base, scaling=T.ROPE_BY_PARTS, factor=factor, original=original, low=low,
+                                high=high).tolist()
+    edge = lambda b: rot * math.log(original / (2 * math.pi * b)) / (2 * math.log(base))  # noqa: E731
+    lo, hi = max(0, math.floor(edge(high))), min(rot - 1, math.ceil(edge(low)))
+    assert lo < rot // 2 - 1 < hi
+    for i, x in enumerate(got):
+        f, w = base ** (-2.0 * i / rot), min(1.0, max(0.0, (i - lo) / (hi - lo)))
+        assert abs(x / 2.0 ** 64 - turns_of(f * (1 - w) + f / factor * w)) <= 2.0 ** -50
+    if kept:
+        last = base ** (-2.0 * (rot // 2 - 1) / rot) / (2 * math.pi)
+        assert abs(got[-1] / 2.0 ** 64 / last - kept) < 1e-6
