@@ -2,7 +2,7 @@
 //
 // A pair's angle is position * f_i.  f_i comes as a fraction of a turn in units of
 // 2^-64, so that the product's low 64 bits are the angle's fraction of a turn, exact
-// at any position; its upper 32 bits, signed, go to sincospi.  A CTA takes a few rows:
+// at any position; signed, and rounded to fp32, it goes to sincospi.  A CTA takes a few rows:
 // their sines and cosines are computed once, an angle a thread, into shared memory, and
 // serve all heads.  The rest is a copy, bound by memory: 8192 rows of 32 + 2 x 8 heads x
 // 128 columns in 37 us, 5.4 TB/s, 0.81 of measured HBM (GB300).  A row a CTA, its first
@@ -141,9 +141,10 @@ __global__ void __launch_bounds__(RT_THREADS, 6)
     int pair;
     const int r = r0 + shape.half(i, pair);
     const uint64_t pos = static_cast<uint64_t>(static_cast<int64_t>(p.position[r]));
-    const int32_t t = static_cast<int32_t>((pos * p.turns[pair]) >> 32);
+    // signed, and all 64 bits to the nearest float: a small angle keeps its 24 bits
+    const int64_t t = static_cast<int64_t>(pos * p.turns[pair]);
     float s, c;
-    sincospif(static_cast<float>(t) * 0x1p-31f, &s, &c);
+    sincospif(static_cast<float>(t) * 0x1p-63f, &s, &c);
     turn[i] = make_float2(c * p.amplitude, (p.inverse ? -s : s) * p.amplitude);
   }
   if (p.slot != nullptr && tid < rows) {
