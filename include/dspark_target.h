@@ -117,6 +117,7 @@ DSPARK_API dspark_status dspark_step_rows(
  *                           after lo where hi <= lo
  *     DSPARK_ROPE_BY_TURNS  f_i s + f_i / factor (1 - s), s = (u - low) / (high -
  *                           low) clamped to [0, 1], u = original f_i / (2 pi)
+ * A factor so small that f_i is not finite is refused.
  *
  * q, q_out   [R, Hq, d] of dtype (DSPARK_BF16 or DSPARK_F32): row strides and head
  *            strides in elements, columns contiguous.  k, k_out [R, Hk, d] alike.

@@ -218,6 +218,7 @@ dspark_status dspark_rotary_table(int32_t rot, double base, int32_t scaling, dou
       f = f * s + f / factor * (1.0 - s);
     }
     const double t = f / kTwoPi;
+    if (!std::isfinite(t)) return DSPARK_ERR_INVALID_ARG;  // a factor too small for f / factor
     turns[i] = static_cast<uint64_t>(std::ldexp(t - std::floor(t), 64));
   }
   return DSPARK_OK;

@@ -232,3 +232,10 @@ def test_a_ramp_that_ends_behind_the_last_pair(lib, rot, base, original, factor,
     if kept:
         last = base ** (-2.0 * (rot // 2 - 1) / rot) / (2 * math.pi)
         assert abs(got[-1] / 2.0 ** 64 / last - kept) < 1e-6
+
+
+@pytest.mark.parametrize("scaling", [T.ROPE_LINEAR, T.ROPE_BY_PARTS, T.ROPE_BY_TURNS])
+def test_a_frequency_that_overflows_is_refused(lib, scaling):
+    """1 / 1e-310 is no number in 64 bits, and has no fraction of a turn."""
+    with pytest.raises(D.DsparkError):
+        T.dspark_rotary_table(8, 1e4, scaling=scaling, factor=1e-310, original=4096, low=1, high=32)
