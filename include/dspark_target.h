@@ -63,7 +63,9 @@ extern "C" {
  * tokens         [N, tokens_width], rows tokens_stride apart, or NULL: each
  *                request's committed tokens by index, the last one (not in the
  *                cache yet) at ctx_len[n].  draft_tokens [N, K].
- * page_count     [N]; free_pages [free_max]; free_count device scalar.
+ * page_count     [N], within [0, max_pages]; free_pages [free_max]; free_count device
+ *                scalar, within [0, free_max].  Counts outside are clamped,
+ *                DSPARK_DEV_LEN_OOR.
  * block_table    [N, max_pages], rows table_stride apart: entries from
  *                page_count[n] on are written where pages are added.
  * page_count_out [N], free_count_out scalar: after the step's pages are taken; may

@@ -95,7 +95,8 @@ __global__ void __launch_bounds__(RW_THREADS) rows_kernel(const RowsArgs p) {
   // pages, and the rows of sampling requests
   uint32_t pages = 0u, outs = 0u;
   auto need_of = [&](int n) -> uint32_t {
-    const int have = min(max(p.page_count[n], 0), p.max_pages);
+    const int said = p.page_count[n], have = min(max(said, 0), p.max_pages);
+    if (have != said) flags |= DSPARK_DEV_LEN_OOR;
     owned[n] = have;
     const int count = cu[n + 1] - cu[n];
     if (count == 0) return 0u;
@@ -116,7 +117,8 @@ __global__ void __launch_bounds__(RW_THREADS) rows_kernel(const RowsArgs p) {
   uint32_t all_pages, all_outs;
   uint32_t page_at = scan_block(pages, warp_sums, &all_pages);
   uint32_t out_at = scan_block(outs, warp_sums, &all_outs);
-  const int have_free = min(max(*p.free_count, 0), p.free_max);
+  const int said_free = *p.free_count, have_free = min(max(said_free, 0), p.free_max);
+  if (have_free != said_free) flags |= DSPARK_DEV_LEN_OOR;
   if (all_pages > static_cast<uint32_t>(have_free)) flags |= DSPARK_DEV_PAGES_SHORT;
   for (int n = n0; n < n1; ++n) {
     first_page[n] = static_cast<int32_t>(page_at);

@@ -1,0 +1,48 @@
+"""Counts, lengths and pages out of range: what is left out or clamped is said in the
+status word, as well where everything else goes on."""
+import pytest
+
+torch = pytest.importorskip("torch")
+
+import test_gpu_target_rows as steps  # noqa: E402
+from speculative_decoding_draft_dspark_gb300 import dspark as D  # noqa: E402
+from speculative_decoding_draft_dspark_gb300 import target as T  # noqa: E402
+
+pytestmark = pytest.mark.gpu
+I32 = torch.int32
+
+
+def step(change, status, in_place=False):
+    c = steps.make(6, 3, 16, 8, 2, prompts=0.0, ctx=50)
+    change(c)
+    want, table = steps.expected(c)
+    s = steps.put(c)
+    if "free_count" in c:
+        s["free_count"].fill_(c["free_count"])
+    out = dict(page_count_out=s["page_count"], free_count_out=s["free_count"]) if in_place else {}
+    steps.call(c, s, **out)
+    steps.same(c, s, want, table, *(("page_count", "free_count") if in_place else ()))
+    assert D.dspark_read_status(s["ws"]) == status
+
+
+@pytest.mark.parametrize("in_place", [False, True])
+@pytest.mark.parametrize("count", [-1, -(1 << 31), 9, (1 << 31) - 1])
+def test_page_counts(count, in_place):
+    def change(c):
+        c["page_count"][2] = count
+        # so many pages are in its row of the table, or none
+        c["table"][2] = [k % 5 for k in range(8)] if count > 0 else [steps.LEFT] * 8
+    step(change, T.DEV_LEN_OOR, in_place)
+
+
+@pytest.mark.parametrize("in_place", [False, True])
+def test_a_free_count_past_the_list(in_place):
+    step(lambda c: c.update(free_count=len(c["free"]) + 1), T.DEV_LEN_OOR, in_place)
+
+
+def test_a_negative_free_count():
+    def change(c):
+        c["free"], c["free_count"] = [], -3
+        c["page_count"] = [8] * 6
+        c["table"] = [[k for k in range(8)] for _ in range(6)]
+    step(change, T.DEV_LEN_OOR)
