@@ -54,7 +54,8 @@ extern "C" {
  * page_count[n] it has are popped off the end of free_pages, request by request
  * (the first one popped is free_pages[free_count - 1]), and written to
  * block_table.  Pages that are not there are -1 (DSPARK_DEV_PAGES_SHORT), as are
- * the slots of their rows.
+ * the slots of their rows; so are the slots of rows on a page outside [0, num_pages),
+ * whose number stays in the table (DSPARK_DEV_PAGE_OOR).
  *
  * draft_len      [N]; sampling_mask [N] uint8 or NULL (all sample); chunk_len [N]
  *                or NULL (0).

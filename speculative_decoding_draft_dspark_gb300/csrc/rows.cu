@@ -169,7 +169,10 @@ __global__ void __launch_bounds__(RW_THREADS) rows_kernel(const RowsArgs p) {
     int32_t *table = p.block_table + static_cast<int64_t>(n) * p.table_stride;
     auto fresh = [&](int64_t k) {
       const int64_t pick = static_cast<int64_t>(have_free) - 1 - first_page[n] - (k - owned[n]);
-      return pick >= 0 ? p.free_pages[pick] : -1;
+      if (pick < 0) return -1;  // the list ran out, which has a bit of its own
+      const int id = p.free_pages[pick];
+      if (id < 0 || id >= p.num_pages) flags |= DSPARK_DEV_PAGE_OOR;
+      return id;
     };
     const int64_t k = index >> p.page_shift;
     int id = -1;

@@ -46,3 +46,15 @@ def test_a_negative_free_count():
         c["page_count"] = [8] * 6
         c["table"] = [[k for k in range(8)] for _ in range(6)]
     step(change, T.DEV_LEN_OOR)
+
+
+@pytest.mark.parametrize("bad", [-7, -1, -(1 << 31), "num_pages", (1 << 31) - 1])
+@pytest.mark.parametrize("own", [True, False])
+def test_a_free_list_with_pages_that_are_not_there(bad, own):
+    """Popped for a row, or for a page before the request's first row."""
+    def change(c):
+        c["ctx_len"] = [16, 5, 5, 5, 5, 5]
+        c["page_count"] = [1 if own else 0, 1, 1, 1, 1, 1]
+        c["table"] = [[n if k < c["page_count"][n] else steps.LEFT for k in range(8)] for n in range(6)]
+        c["free"][-1] = c["num_pages"] if bad == "num_pages" else bad
+    step(change, T.DEV_PAGE_OOR)
