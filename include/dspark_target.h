@@ -231,7 +231,9 @@ DSPARK_API dspark_status dspark_tree_attention(
  *              dspark_step_rows).  Rows past cu_rows[N] are left as they are.
  * tokens       [N, tokens_width], rows tokens_stride apart.  hist_len [N]; prompt_len
  *              [N] or NULL (0).  draft_tokens [N, K] or NULL (K = 0).  A token
- *              outside [0, vocab) is skipped, DSPARK_DEV_TOKEN_OOR.
+ *              outside [0, vocab) is skipped, DSPARK_DEV_TOKEN_OOR.  hist_len outside
+ *              [0, tokens_width] and bias_count outside [0, bias_width] are clamped,
+ *              DSPARK_DEV_LEN_OOR.
  * repetition, frequency, presence  [N] fp32, each may be NULL (1, 0, 0).
  * bias_token [N, bias_width], bias_value fp32, bias_count [N]; or NULL, bias_width 0.
  *              A token more than once: its values are added up in order first.

@@ -183,14 +183,15 @@ __global__ void __launch_bounds__(AJ_THREADS, 2)
   if (j0 >= j1) return;
   int hist = p.hist_len[n];
   const int prompt = p.prompt_len != nullptr ? p.prompt_len[n] : 0;
-  const int biases = p.bias_width > 0 ? min(max(p.bias_count[n], 0), p.bias_width) : 0;
+  const int said = p.bias_width > 0 ? p.bias_count[n] : 0;
+  const int biases = min(max(said, 0), p.bias_width);
   const int32_t *bias_token = p.bias_token + static_cast<int64_t>(n) * p.bias_width;
   const float *bias_value = p.bias_value + static_cast<int64_t>(n) * p.bias_width;
   const int drafts = min(p.K, rows.count - 1);
   const int lo = HASH ? 0 : blockIdx.x * AJ_SLICE;
   const int size = HASH ? p.vocab : min(AJ_SLICE, p.vocab - lo);
   uint32_t flags = 0u;
-  if (hist < 0 || hist > p.tokens_width) flags |= DSPARK_DEV_LEN_OOR;
+  if (hist < 0 || hist > p.tokens_width || said != biases) flags |= DSPARK_DEV_LEN_OOR;
   hist = min(max(hist, 0), p.tokens_width);
   __syncthreads();
 

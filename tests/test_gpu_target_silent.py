@@ -4,6 +4,7 @@ import pytest
 
 torch = pytest.importorskip("torch")
 
+import test_gpu_target_adjust as logits  # noqa: E402
 import test_gpu_target_rows as steps  # noqa: E402
 from speculative_decoding_draft_dspark_gb300 import dspark as D  # noqa: E402
 from speculative_decoding_draft_dspark_gb300 import target as T  # noqa: E402
@@ -58,3 +59,13 @@ def test_a_free_list_with_pages_that_are_not_there(bad, own):
         c["table"] = [[n if k < c["page_count"][n] else steps.LEFT for k in range(8)] for n in range(6)]
         c["free"][-1] = c["num_pages"] if bad == "num_pages" else bad
     step(change, T.DEV_PAGE_OOR)
+
+
+@pytest.mark.parametrize("dtype", [logits.BF16, logits.F32])
+@pytest.mark.parametrize("count,as_if", [(-1, 0), (-(1 << 31), 0), (6, 5), ((1 << 31) - 1, 5)])
+def test_bias_counts(count, as_if, dtype):
+    c = logits.Case([3, 2], 700, dtype)
+    c.a["bias_count"] = torch.tensor([2, count], dtype=I32)
+    s = c.call(c.gpu())
+    c.a["bias_count"][1] = as_if
+    c.check(s, status=T.DEV_LEN_OOR)
