@@ -184,7 +184,8 @@ DSPARK_API dspark_status dspark_rotary_append(
  *            that is read.
  * k_cache, v_cache  bf16, element (page, offset, head, column) as in
  *            dspark_rotary_append.
- * block_table [N, max_pages], rows table_stride apart.   ctx_len [N] (negative: 0).
+ * block_table [N, max_pages], rows table_stride apart.   ctx_len [N] (negative: 0,
+ *            DSPARK_DEV_LEN_OOR).
  * cu_rows    [N+1]: as written by dspark_step_rows; rows past cu_rows[N] are left as
  *            they are.
  * max_len    no request has more rows (more: left as they are, DSPARK_DEV_LEN_OOR).

@@ -309,9 +309,10 @@ struct AtPlan {
     r.first = rows.first;
     r.count = min(rows.count, p.max_len);
     const int64_t room = static_cast<int64_t>(p.max_pages) << p.page_shift;
-    r.ctx = static_cast<int>(min(static_cast<int64_t>(max(p.ctx_len[n], 0)), room));
+    const int ctx = p.ctx_len[n];
+    r.ctx = static_cast<int>(min(static_cast<int64_t>(max(ctx, 0)), room));
     r.tree = is_tree(p.tree, p.tree_width, n, rows.count);
-    r.flags = rows.count > p.max_len ? DSPARK_DEV_LEN_OOR : 0u;
+    r.flags = rows.count > p.max_len || (ctx < 0 && rows.count > 0) ? DSPARK_DEV_LEN_OOR : 0u;
     if (r.count > 0 && r.ctx + static_cast<int64_t>(r.count) > room)
       r.flags |= DSPARK_DEV_PAGE_OOR;
     const int packed = r.count * p.group;

@@ -5,6 +5,7 @@ import pytest
 torch = pytest.importorskip("torch")
 
 import test_gpu_target_adjust as logits  # noqa: E402
+import test_gpu_target_attention as attention  # noqa: E402
 import test_gpu_target_rows as steps  # noqa: E402
 from speculative_decoding_draft_dspark_gb300 import dspark as D  # noqa: E402
 from speculative_decoding_draft_dspark_gb300 import target as T  # noqa: E402
@@ -69,3 +70,18 @@ def test_bias_counts(count, as_if, dtype):
     s = c.call(c.gpu())
     c.a["bias_count"][1] = as_if
     c.check(s, status=T.DEV_LEN_OOR)
+
+
+@pytest.mark.parametrize("heads", [4, 96])      # few packed rows, and more than a block
+@pytest.mark.parametrize("ctx", [-1, -(1 << 31)])
+def test_negative_lengths(ctx, heads):
+    c = attention.Case([(0, 3), (40, 2), (0, 0)], heads=heads, kv=2)
+    s = c.gpu()
+    s["ctx"][0] = ctx
+    c.call(s)
+    c.check(s, status=T.DEV_LEN_OOR)
+    c = attention.Case([(40, 2), (0, 0)])        # of a request without rows: no matter
+    s = c.gpu()
+    s["ctx"][1] = ctx
+    c.call(s)
+    c.check(s)
