@@ -214,3 +214,40 @@ def test_a_request_with_most_of_the_rows():
     for a in range(0, R, 30000):
         b = slice(a, min(R, a + 30000))
         assert torch.equal(s["out"][b], (before[b].float() - pres[b, None]).to(BF16))
+
+
+@pytest.mark.parametrize("in_place", [True, False])
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("counts,kw", [
+    ([64, 1, 30], dict(K=63, tree=True)), ([64, 1, 30], dict(K=63)), ([8], dict(width=5000, few=900)),
+    ([4, 1], dict(width=20000, few=2900, bias=50)), ([4, 9], dict(width=20000, few=2900, tree=True)),
+    ([1] * 300, dict(K=1)), ([40], dict(K=5)), ([0, 0, 3], dict(K=2))])
+def test_rows_of_a_request(counts, kw, dtype, in_place):
+    c = Case(counts, 3001, dtype, **kw)
+    c.check(c.call(c.gpu(in_place)), in_place)
+
+
+@pytest.mark.parametrize("in_place", [True, False])
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("bias", [0, 5])
+def test_infinities_and_overflows(bias, dtype, in_place):
+    """Every entry: infinities and NaN as in 64 bits; what is past the type's largest
+    value by more than half a step, an infinity of its sign; all else to the usual bounds.
+    Between them, within the 16 * 2^-24 of fp32's operations, either."""
+    c = Case([4], 640, dtype, masked=True, bias=bias, few=600, width=400)
+    top = torch.finfo(dtype)
+    c.logits[:, ::7], c.logits[:, 1::7], c.logits[:, 2::7] = math.nan, math.inf, -math.inf
+    c.logits[:, 3::7], c.logits[:, 4::14] = top.min, top.max
+    s = c.call(c.gpu(in_place))
+    want, size = ref.adjust(c.logits, c.cu, **c.a)
+    got, want, size = s["out"][:4].cpu().double(), want[:4], size[:4]
+    assert torch.equal(got.isnan(), want.isnan())
+    cut = want.isinf()
+    assert cut.any() and torch.equal(got[cut], want[cut])
+    edge = top.max * (1.0 + top.eps / 4)                    # half a step past the largest value
+    finite = want.isfinite()
+    past, within = finite & (want.abs() > edge * (1 + 2.0 ** -20)), finite & (want.abs() < edge * (1 - 2.0 ** -20))
+    assert past.any() and within.any()
+    assert torch.equal(got[past], want[past].sign() * math.inf)
+    tol = want.abs() * top.eps / 2 + 16 * 2.0 ** -24 * size
+    assert ((got - want).abs() <= tol)[within].all()

@@ -193,3 +193,34 @@ def test_in_a_graph():
     gpos.add_(5)
     graph.replay()
     close(out, ref.rotate(q, pos + 5, freq, 64, False), q, BF16)
+
+
+# rows from which a CTA takes 2, 4 or 8 of them, and CTAs that end in part
+@pytest.mark.parametrize("R", [1215, 1216, 1217, 2435, 4871])
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("interleaved", [False, True])
+@pytest.mark.parametrize("Hq,Hk,d,rot", [(2, 1, 64, 64), (3, 2, 75, 50), (2, 2, 80, 40), (1, 1, 128, 128), (3, 1, 40, 2)])
+def test_several_rows_of_a_cta(R, Hq, Hk, d, rot, interleaved, dtype):
+    (q, k, v), (gq, gk, gv), pos, turns, freq = case(R, Hq, Hk, d, rot, dtype, seed=R)
+    want = [ref.rotate(x, pos, freq, rot, interleaved, 1.25) for x in (q, k)]
+    kw = dict(interleaved=interleaved, amplitude=1.25)
+    page, gpos = 16, pos.cuda()
+    pages = R // page + 2
+    slot = torch.randperm(pages * page, generator=torch.Generator().manual_seed(R))[:R].int()
+    slot[5], slot[R - 2], slot[R // 2] = -1, pages * page, -(1 << 31)
+    for n in (None, R - 1, R - 9, 4, 1, 0):             # that end in and between CTAs
+        last = R if n is None else n
+        n_rows = None if n is None else torch.tensor([n], dtype=torch.int32, device="cuda")
+        qo, ko = (torch.full(x.shape, 7.0, dtype=dtype, device="cuda") for x in (q, k))
+        T.dspark_rotary(gq, gk, gpos, turns, qo, ko, n_rows=n_rows, **kw)
+        for y, w, x in ((qo, want[0], q), (ko, want[1], k)):
+            close(y[:last], w[:last], x[:last] * 1.25, dtype)
+            assert (y[last:] == 7.0).all()
+        kc, vc = (torch.full((pages, page, Hk, d), 7.0, dtype=dtype, device="cuda") for _ in range(2))
+        q2 = torch.full(q.shape, 7.0, dtype=dtype, device="cuda")
+        T.dspark_rotary_append(gq, gk, gv, gpos, slot.cuda(), turns, q2, kc, vc, n_rows=n_rows, **kw)
+        assert torch.equal(q2, qo)
+        wk, wv = (torch.full((pages * page, Hk, d), 7.0, dtype=dtype) for _ in range(2))
+        there = (slot >= 0) & (slot < pages * page) & (torch.arange(R) < last)
+        wk[slot[there].long()], wv[slot[there].long()] = ko.cpu()[there], v[there]
+        assert torch.equal(kc.cpu().view(-1, Hk, d), wk) and torch.equal(vc.cpu().view(-1, Hk, d), wv)
