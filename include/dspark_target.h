@@ -230,7 +230,9 @@ DSPARK_API dspark_status dspark_tree_attention(
  *              they do not overlap.
  * cu_rows      [N+1]: the requests' rows among the logits' (cu_out of
  *              dspark_step_rows).  Rows past cu_rows[N] are left as they are.
- * tokens       [N, tokens_width], rows tokens_stride apart.  hist_len [N]; prompt_len
+ * tokens       [N, tokens_width], rows tokens_stride apart: the buffer's first columns,
+ *              as many as hist_len may reach (more than 10900 less K and bias_width take
+ *              a slower way, whatever hist_len).  hist_len [N]; prompt_len
  *              [N] or NULL (0).  draft_tokens [N, K] or NULL (K = 0).  A token
  *              outside [0, vocab) is skipped, DSPARK_DEV_TOKEN_OOR.  hist_len outside
  *              [0, tokens_width] and bias_count outside [0, bias_width] are clamped,

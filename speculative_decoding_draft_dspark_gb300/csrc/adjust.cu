@@ -10,15 +10,17 @@
 // request in shared memory, lists the distinct ones, and then takes a share of the
 // request's rows, entry by entry.  The counts are whole numbers, so their order does
 // not matter.  They are in a hash table where one holds every token that a request can
-// have; longer histories go through the vocabulary a slice at a time, a CTA each,
-// with a word for every entry.  (A slice costs the whole history again: with 262144
-// entries, 256 requests x 8 rows and histories of up to 4096 tokens, 32 slices, and
-// their masks in the same kernel, took 322 us.)
+// have, which the host knows by the text buffer's width; wider buffers go through the
+// vocabulary a slice at a time, a CTA each, with a word for every entry, whatever the
+// histories in them.  (A slice costs the whole history again.  262144 entries, 256
+// requests x 8 rows, half of them masked, in place, in a graph: with a buffer of 4096
+// tokens and histories up to that 207 us, up to 100 tokens 176; with a buffer of 131072
+// 289 and 272, and 417 with histories up to 32768.)
 //
-// Measured on a GB300, that case, in place with half of the rows masked: 194-196 us, of
-// which masks 147 (0.74 of HBM's cycles: 537 MB written, half of it read) and entries
-// 49 (some 600000 single logits, a sector each).  561 rows x 50003 fp32 elsewhere:
-// 45 us, 0.75 of measured HBM.
+// Measured on a GB300, that case with a buffer of 4096, call after call: 197-199 us, of
+// which masks 143 (0.74 of HBM's cycles: 537 MB written, half of it read), then counts
+// and entries 42 (some 600000 single logits, a sector each).  561 rows x 50003 fp32
+// elsewhere: 49 us, the copy 37 (0.91 of measured HBM), counts and entries 10.
 #include <algorithm>
 #include <cuda_bf16.h>
 #include <mutex>

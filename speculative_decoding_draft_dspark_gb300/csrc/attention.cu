@@ -34,10 +34,10 @@
 // Measured on a GB300, 32 query heads, 8 key heads, 128 columns: 64 requests x 8 rows
 // over up to 8192 tokens 180-184 us, 5.9-6.0 TB/s, 0.87-0.89 of measured HBM.  One token
 // over 8192: 22 us, of which the cache's bytes are 5; starting, planning and joining are
-// chains of dependent loads.  16 chunks of 512 rows: 484-500 us, 1.12 PFLOP/s, 0.58 of
-// measured bf16; a tile's 3000 cycles are a block's softmax (1800) and its two products
+// chains of dependent loads.  16 chunks of 512 rows: 477-500 us, 1.10-1.15 PFLOP/s, 0.57-0.60
+// of measured bf16; a tile's 3000 cycles are a block's softmax (1800) and its two products
 // (1024), which tensor memory has no room to overlap within the block.  256 trees of 25
-// rows, 24 query heads, 4 key heads, 64 columns: 134-136 us, 2.3 TB/s; tiles of 2500
+// rows, 24 query heads, 4 key heads, 64 columns: 135-138 us, 2.2-2.3 TB/s; tiles of 2500
 // cycles where the products need 1024, 22 of the second block's 128 rows in use, and
 // some 10000 cycles around an item's eight tiles.
 #include <algorithm>

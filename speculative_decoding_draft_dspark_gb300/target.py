@@ -313,7 +313,8 @@ def dspark_adjust_logits(logits, cu_rows, tokens, hist_len, prompt_len, draft_to
                          mask_index=None, stream=None, raise_on_error=True) -> int:
     """Penalties, biases and masks on logits [R, vocab] (bf16 or fp32; rows may be
     apart) into out (logits itself: in place).  cu_rows [N + 1], tokens [N, width]
-    int32 (rows may be apart), hist_len [N], prompt_len [N] or None, draft_tokens
+    int32 (rows may be apart: of a long buffer, pass the columns that hist_len may
+    reach), hist_len [N], prompt_len [N] or None, draft_tokens
     [N, K] or None, tree [N, width] int64 masks or None; repetition, frequency and
     presence [N] fp32 or None; bias_token [N, most] int32, bias_value fp32 and
     bias_count [N], or None; mask [rows, words] int32 (rows may be apart), 1 =

@@ -251,3 +251,18 @@ def test_infinities_and_overflows(bias, dtype, in_place):
     assert torch.equal(got[past], want[past].sign() * math.inf)
     tol = want.abs() * top.eps / 2 + 16 * 2.0 ** -24 * size
     assert ((got - want).abs() <= tol)[within].all()
+
+
+@pytest.mark.parametrize("in_place", [True, False])
+def test_columns_of_a_wide_text_buffer(in_place):
+    """As many as the histories may reach, and all of them: the same bits."""
+    c = Case([3, 8, 1], 20011, width=300)
+    outs = []
+    for narrow in (True, False):
+        s = c.gpu(in_place)
+        wide = torch.full((3, 20000), 77, dtype=I32, device="cuda")
+        wide[:, :300] = s["tokens"]
+        s["tokens"] = wide[:, :300] if narrow else wide
+        c.check(c.call(s), in_place)
+        outs.append(s["out"].clone())
+    assert torch.equal(*outs)
